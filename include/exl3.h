@@ -74,7 +74,8 @@ typedef enum {
     EXL3_ERR_CUDA = 6,               /* a CUDA runtime call or a launch failed */
     EXL3_ERR_DEVICE_TIMEOUT = 7,     /* a kernel gave up a bounded wait (see exl3_get_device_status) */
     EXL3_ERR_NOALLOC_TOO_LARGE = 8,  /* the problem needs more scratch than the fixed no-alloc buffer holds */
-    EXL3_ERR_OUT_OF_BOUNDS = 9       /* bounds-checked build only: a kernel's index left its buffer */
+    EXL3_ERR_OUT_OF_BOUNDS = 9,      /* bounds-checked build only: a kernel's index left its buffer */
+    EXL3_ERR_DEVICE_INDEX = 10       /* a page number, length or row range read on the device is out of range */
 } exl3_status;
 
 typedef enum { EXL3_F16 = 0, EXL3_F32 = 1 } exl3_dtype;
@@ -271,8 +272,10 @@ exl3_status exl3_logits_masked(const void *x, int64_t M, int64_t K, const uint16
  * Synchronises `stream`, then reads and clears the current device's error
  * word, which holds the first device-side error since the last read:
  * EXL3_ERR_DEVICE_TIMEOUT if a kernel gave up one of its bounded waits,
- * EXL3_ERR_OUT_OF_BOUNDS if a check of the bounds-checked build failed;
- * EXL3_OK otherwise.
+ * EXL3_ERR_OUT_OF_BOUNDS if a check of the bounds-checked build failed,
+ * EXL3_ERR_DEVICE_INDEX if a serving call met a page number, length or row
+ * range on the device that its buffers do not hold (what it names was
+ * skipped); EXL3_OK otherwise.
  * The word is one per device, shared by every stream and workspace on it
  * (some entry points that wait on the device have no workspace): with
  * several streams, a timeout is reported to whichever caller reads first.
@@ -365,6 +368,176 @@ exl3_status exl3_selftest_bounds(int *units_reported, int *units_total, void *st
 exl3_status exl3_linear_decode_noalloc(const void *x, int64_t M, int64_t K, const uint16_t *trellis,
                                        int bits, int64_t n_stored, int64_t n_gemm, const void *su,
                                        const void *sv, void *y, int y_dtype, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Serving operators: what a decode step needs between the projections (an
+ * 8-bit paged key/value cache and the attention that reads it) and after the
+ * logits (penalties, biases and a grammar mask before a token is chosen).
+ * Everything sizes depend on per step (lengths, rows of each sequence, page
+ * numbers) lives on the device, so a captured graph serves every step whose
+ * bounds (rows, max_rows, max_pages) it was captured with.
+ * ---------------------------------------------------------------------------
+ *
+ * Matrices (codes, q, k, v, out, logits) and `weight` are 16-byte aligned;
+ * scales, lse and integer arrays by their elements (4 bytes). A NULL or
+ * misaligned pointer returns EXL3_ERR_ALIGNMENT.
+ *
+ * The cache holds E4M3 codes in blocks (pages) of 64 tokens. A block holds,
+ * for each key/value head, 64 x head_dim codes and ONE scale, a power of two;
+ * keys and values have blocks of the same number in two buffers:
+ *     value[page][head][token][d] = code * scale[page][head].
+ * A block's scale is 2^e, e the smallest integer in -32 .. 8 with
+ * max |x| <= 448 * 2^e over the finite values it holds (448 is E4M3's largest
+ * value; every finite fp16 fits), and never smaller than it was while the
+ * block held older tokens. Powers of two make a change of scale exact except
+ * where a code becomes subnormal.
+ */
+#define EXL3_KV8_BLOCK 64
+
+typedef struct {
+    void *k, *v;             /* E4M3, n_pages x n_kv_heads x 64 x head_dim */
+    float *k_scale, *v_scale;/* n_pages x n_kv_heads */
+    float *weight;           /* n_pages x n_kv_heads x 64: accumulated attention weight, or NULL */
+    int64_t n_pages;         /* n_pages * n_kv_heads * 64 < 2^31 */
+    int32_t n_kv_heads;      /* 1 .. 1024 */
+    int32_t head_dim;        /* 64 or 128 */
+} exl3_kv8_cache;
+
+/*
+ * The sequences of one call. Row r of a call's q / k / v matrices belongs to
+ * the sequence s with q_start[s] <= r < q_start[s + 1]; its rows are the last
+ * tokens of the sequence: row q_start[s] + i stands at position
+ * kv_len[s] - (q_start[s + 1] - q_start[s]) + i. kv_len counts this call's
+ * own tokens too.
+ */
+typedef struct {
+    const int32_t *page_table; /* n_seqs x max_pages: page of tokens 64 j .. 64 j + 63 of a sequence */
+    const int32_t *kv_len;     /* n_seqs, each at most 64 * max_pages */
+    const int32_t *q_start;    /* n_seqs + 1, not decreasing, from 0 to rows */
+    int32_t n_seqs;            /* 0 .. 65535 */
+    int32_t max_pages;
+    int32_t rows;              /* rows of this call, all sequences */
+    int32_t max_rows;          /* the most rows that one sequence has */
+} exl3_kv8_batch;
+
+/*
+ * exl3_kv8_append: quantizes this call's keys and values into the cache.
+ *   k, v: rows x (n_kv_heads * head_dim) fp16, leading dimensions ldk, ldv
+ *         (elements, multiples of 8, at least the width): column ranges of
+ *         one fused projection's output will do.
+ * Each block that receives tokens gets the scale above. Where it grows, the
+ * older tokens' codes are rescaled, E4M3(code * 2^(e_old - e)); new codes are
+ * E4M3(x * 2^-e), both rounded to nearest even. Infinities saturate at
+ * +-448 * 2^e; NaN is stored as NaN (E4M3 has one) and takes no part in the
+ * scale. Slots past a sequence's length keep what they held. The cache's
+ * `weight` of the new tokens is set to 0 where the cache has one.
+ * Blocks that receive tokens must not be shared between sequences.
+ */
+exl3_status exl3_kv8_append(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, const void *k, int64_t ldk,
+                            const void *v, int64_t ldv, void *stream);
+
+/*
+ * exl3_kv8_attention: attention of this call's rows over the cached tokens.
+ *     s[t] = scale * sum_d q[d] key[t][d];  s = softcap * tanh(s / softcap) if softcap > 0
+ *     out  = sum_t softmax(s)[t] value[t]
+ * over the positions t that the row sees: those up to its own (causal != 0)
+ * or the whole sequence.
+ *   q:    rows x (n_heads * head_dim) fp16, leading dimension ldq (multiple
+ *         of 8). n_heads is a multiple of n_kv_heads; query head h reads
+ *         key/value head h / (n_heads / n_kv_heads).
+ *   out:  rows x (n_heads * head_dim) fp16 (RNE of fp32), leading dimension
+ *         ldo (multiple of 8).
+ *   lse:  rows x n_heads fp32, log sum_t exp(s[t]); or NULL.
+ * A row that sees no token gives out = 0 and lse = -inf. What lies past a
+ * sequence's length in its last block is never used, whatever its bytes are.
+ * A NaN among the values of a sequence may reach every row that attends to
+ * the sequence in this call, also rows before its position.
+ * Sums, maxima and the softmax are fp32; the probabilities enter the product
+ * with the values as fp16.
+ *   scale: finite; softcap: finite, 0 (off) or more.
+ *   workspace: exl3_kv8_attention_workspace_bytes bytes (0 for invalid
+ *         arguments), contents undefined before and after.
+ */
+size_t exl3_kv8_attention_workspace_bytes(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, int32_t n_heads);
+exl3_status exl3_kv8_attention(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, const void *q, int64_t ldq,
+                               int32_t n_heads, float scale, float softcap, int causal, void *out, int64_t ldo,
+                               float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * exl3_kv8_weigh: adds to the cache's `weight` of every token that a row of
+ * this call sees the attention that it gets,
+ *     weight[t] += sum over rows and query heads of the group: exp(s[t] - lse),
+ * with s as in exl3_kv8_attention and lse as that call returned it (rows whose
+ * lse is -inf add nothing). Each token's sum is formed in a fixed order: the
+ * result does not depend on scheduling.
+ */
+exl3_status exl3_kv8_weigh(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, const void *q, int64_t ldq,
+                           int32_t n_heads, float scale, float softcap, int causal, const float *lse, void *stream);
+
+/*
+ * exl3_kv8_evict: cuts sequences back to `budget` tokens. For each sequence
+ * and key/value head it keeps the last min(recent, kv_len) tokens and, of the
+ * others, those with the largest `weight` (ties: the lower position; a NaN
+ * weight counts as the lowest) until min(budget, kv_len) are kept, and writes
+ * them, in their order, to the blocks of dst_pages.
+ *   batch:     page_table, kv_len, n_seqs and max_pages of the sequences as
+ *              they are (q_start, rows and max_rows are not read).
+ *   dst_pages: n_seqs x ceil(budget / 64) page numbers, none of them a page
+ *              of `batch` and none twice: the sequences' new page table. The
+ *              old pages are the caller's to reuse after this call.
+ *   kept:      n_seqs x n_kv_heads x budget int32: the positions kept, then -1.
+ *   new_len:   n_seqs int32: min(budget, kv_len).
+ * A new block's scale is the largest of its tokens' scales (their codes are
+ * rescaled, E4M3(code * 2^(e_old - e))); weights move along; slots past
+ * new_len keep what they held. 1 <= budget, 0 <= recent <= budget.
+ * Positions are a sequence's own afterwards: a later append continues at
+ * new_len.
+ */
+exl3_status exl3_kv8_evict(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, const int32_t *dst_pages,
+                           int32_t budget, int32_t recent, int32_t *kept, int32_t *new_len, void *stream);
+
+/*
+ * exl3_logits_adjust: penalties, biases and a grammar mask on logits, and the
+ * greedy choice from what is left. For row m and token t < n, with c the times
+ * that t occurs in the generated part of the row's history and `seen` whether
+ * it occurs in it at all:
+ *     l = seen ? (l > 0 ? l / repetition : l * repetition) : l
+ *     l = l - (frequency * c + (c > 0 ? presence : 0))
+ *     l = l + bias[t]
+ *     l = -inf where the mask forbids t
+ * in fp32, each operation rounded by itself.
+ */
+typedef struct {
+    const int32_t *history;        /* token ids of all rows; ids outside 0 .. n-1 are ignored */
+    const int32_t *history_start;  /* M + 1: row m's ids are history[history_start[m]] ... (both NULL: no history) */
+    const int32_t *generated_from; /* M: index in the row's history of the first generated token, or NULL (0) */
+    const float *repetition;       /* M, each > 0, or NULL (1) */
+    const float *presence;         /* M, or NULL (0) */
+    const float *frequency;        /* M, or NULL (0) */
+    const int32_t *bias_id;        /* token ids; entries of the same id add up in their order */
+    const float *bias_value;
+    const int32_t *bias_start;     /* M + 1 (all three NULL: no biases) */
+    const uint32_t *allowed;       /* M x ceil(n / 32) words, bit t % 32 of word t / 32 set: allowed; or NULL */
+    int32_t history_size;          /* entries of `history` */
+    int32_t bias_size;             /* entries of `bias_id` */
+} exl3_logits_rules;
+
+/*
+ *   logits, out: M x n fp32, leading dimensions ldl, ldo (multiples of 4, at
+ *          least n): exl3_logits_masked's logits with n = n_decodable. They may
+ *          be the same buffer. Columns from n on are neither read nor written.
+ *   argmax: M int32: the first index of the row's maximum (a NaN is never
+ *          the maximum); -1 where no token is left (all -inf or NaN).
+ *   1 <= n <= 2^19, 0 <= M <= 65535.
+ */
+exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules *rules,
+                               float *out, int64_t ldo, int32_t *argmax, void *stream);
+
+/*
+ * exl3_selftest_bounds, for the translation units of the serving operators.
+ */
+exl3_status exl3_selftest_bounds_serving(int *units_reported, int *units_total, void *stream);
 
 #ifdef __cplusplus
 }

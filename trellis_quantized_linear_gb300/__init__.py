@@ -25,7 +25,9 @@ __all__ = [
     "exl3_linear", "exl3_logits_masked", "exl3_get_device_status", "exl3_selftest_wait_timeout",
     "exl3_linear_decode_noalloc", "exl3_silu_mul", "exl3_reconstruct_rotated",
     "exl3_weight_rotated_workspace_bytes", "exl3_linear_weight_rotated", "exl3_bounds_checked",
-    "exl3_selftest_bounds", "HEADER_SYMBOLS", "BOUNDS_CHECKED",
+    "exl3_selftest_bounds", "EXL3_KV8_BLOCK", "Exl3Kv8Cache", "Exl3Kv8Batch", "exl3_kv8_append",
+    "exl3_kv8_attention_workspace_bytes", "exl3_kv8_attention", "exl3_kv8_weigh", "exl3_kv8_evict",
+    "exl3_logits_adjust", "exl3_selftest_bounds_serving", "HEADER_SYMBOLS", "BOUNDS_CHECKED",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -38,11 +40,13 @@ EXL3_LAYOUT_KN = 0
 EXL3_LAYOUT_NK = 1
 EXL3_RECONSTRUCT_CHUNK_COLS = 32768
 EXL3_NOALLOC_SCRATCH_BYTES = 24 << 20
+EXL3_KV8_BLOCK = 64
 
 STATUS_NAMES = {
     0: "EXL3_OK", 1: "EXL3_ERR_INVALID_ARG", 2: "EXL3_ERR_ALIGNMENT", 3: "EXL3_ERR_UNSUPPORTED_BITS",
     4: "EXL3_ERR_WORKSPACE_TOO_SMALL", 5: "EXL3_ERR_NOT_INITIALIZED", 6: "EXL3_ERR_CUDA",
     7: "EXL3_ERR_DEVICE_TIMEOUT", 8: "EXL3_ERR_NOALLOC_TOO_LARGE", 9: "EXL3_ERR_OUT_OF_BOUNDS",
+    10: "EXL3_ERR_DEVICE_INDEX",
 }
 
 # Every function include/exl3.h declares.
@@ -53,7 +57,8 @@ HEADER_SYMBOLS = (
     "exl3_logits_masked", "exl3_get_device_status", "exl3_selftest_wait_timeout",
     "exl3_linear_decode_noalloc", "exl3_silu_mul", "exl3_reconstruct_rotated",
     "exl3_weight_rotated_workspace_bytes", "exl3_linear_weight_rotated", "exl3_bounds_checked",
-    "exl3_selftest_bounds",
+    "exl3_selftest_bounds", "exl3_kv8_append", "exl3_kv8_attention_workspace_bytes", "exl3_kv8_attention",
+    "exl3_kv8_weigh", "exl3_kv8_evict", "exl3_logits_adjust", "exl3_selftest_bounds_serving",
 )
 
 
@@ -67,7 +72,61 @@ class Exl3Error(RuntimeError):
 _lib = None
 _lock = threading.Lock()
 _i64 = ctypes.c_int64
+_i32 = ctypes.c_int32
 _vp = ctypes.c_void_p
+
+
+class Exl3Kv8Cache(ctypes.Structure):
+    """exl3_kv8_cache over the caller's tensors (kept alive by this object):
+    k, v n_pages x n_kv_heads x 64 x head_dim (torch.float8_e4m3fn or uint8),
+    k_scale, v_scale n_pages x n_kv_heads fp32, weight n_pages x n_kv_heads x
+    64 fp32 or None; all contiguous."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("weight", _vp), ("n_pages", _i64),
+                ("n_kv_heads", _i32), ("head_dim", _i32)]
+
+    def __init__(self, k, v, k_scale, v_scale, weight=None):
+        if k.dim() != 4 or k.shape[2] != EXL3_KV8_BLOCK or v.shape != k.shape or k.element_size() != 1 or v.element_size() != 1:
+            raise ValueError("Exl3Kv8Cache: k and v are n_pages x n_kv_heads x 64 x head_dim, one byte an element")
+        if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2] or (weight is not None and weight.shape != k.shape[:3]):
+            raise ValueError("Exl3Kv8Cache: scales are n_pages x n_kv_heads, weight n_pages x n_kv_heads x 64")
+        _require_f32_contiguous("Exl3Kv8Cache", k_scale, v_scale, weight)
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("Exl3Kv8Cache: k and v are contiguous")
+        super().__init__(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), k.shape[0], k.shape[1], k.shape[3])
+        self._keep = (k, v, k_scale, v_scale, weight)
+        self._ref = ctypes.byref(self)
+
+
+class Exl3Kv8Batch(ctypes.Structure):
+    """exl3_kv8_batch over the caller's int32 tensors (kept alive by this
+    object): page_table n_seqs x max_pages, kv_len n_seqs, q_start n_seqs + 1;
+    their contents may change between calls. rows and max_rows bound this
+    call's rows, in total and for one sequence."""
+    _fields_ = [("page_table", _vp), ("kv_len", _vp), ("q_start", _vp), ("n_seqs", _i32), ("max_pages", _i32),
+                ("rows", _i32), ("max_rows", _i32)]
+
+    def __init__(self, page_table, kv_len, q_start=None, rows=0, max_rows=0):
+        n = page_table.shape[0]
+        if page_table.dim() != 2 or kv_len.numel() != n or (q_start is not None and q_start.numel() != n + 1):
+            raise ValueError("Exl3Kv8Batch: page_table is n_seqs x max_pages, kv_len n_seqs, q_start n_seqs + 1")
+        for t in (page_table, kv_len, q_start):
+            if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()):
+                raise ValueError("Exl3Kv8Batch: tensors are contiguous int32")
+        super().__init__(_ptr(page_table), _ptr(kv_len), _ptr(q_start), n, page_table.shape[1], rows, max_rows)
+        self._keep = (page_table, kv_len, q_start)
+        self._ref = ctypes.byref(self)
+
+
+class _LogitsRules(ctypes.Structure):
+    _fields_ = [("history", _vp), ("history_start", _vp), ("generated_from", _vp), ("repetition", _vp),
+                ("presence", _vp), ("frequency", _vp), ("bias_id", _vp), ("bias_value", _vp), ("bias_start", _vp),
+                ("allowed", _vp), ("history_size", _i32), ("bias_size", _i32)]
+
+
+def _require_f32_contiguous(where, *tensors):
+    for t in tensors:
+        if t is not None and (t.element_size() != 4 or not t.is_floating_point() or not t.is_contiguous()):
+            raise ValueError(f"{where}: expected contiguous fp32 tensors")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -115,6 +174,16 @@ def load():
                                                           _vp, ctypes.c_int, _vp, ctypes.c_size_t, _vp]),
             "exl3_bounds_checked": (ctypes.c_int, []),
             "exl3_selftest_bounds": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int), _vp]),
+            "exl3_kv8_append": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp]),
+            "exl3_kv8_attention_workspace_bytes": (ctypes.c_size_t, [_vp, _vp, _i32]),
+            "exl3_kv8_attention": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, ctypes.c_float, ctypes.c_float,
+                                                  ctypes.c_int, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp]),
+            "exl3_kv8_weigh": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, ctypes.c_float, ctypes.c_float, ctypes.c_int,
+                                              _vp, _vp]),
+            "exl3_kv8_evict": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp]),
+            "exl3_logits_adjust": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp]),
+            "exl3_selftest_bounds_serving": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int),
+                                                            ctypes.POINTER(ctypes.c_int), _vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -287,3 +356,62 @@ def exl3_silu_mul(gate, up, out, n: int | None = None, stream=None) -> None:
     """out = fp16(silu(gate) * up), the dense-MLP glue between projections."""
     n = gate.numel() if n is None else n
     _check(load().exl3_silu_mul(_ptr(gate), _ptr(up), _ptr(out), int(n), _stream(stream)), "exl3_silu_mul")
+
+
+def exl3_kv8_append(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, k, v, stream=None) -> None:
+    """Quantizes rows of keys and values (fp16, rows x n_kv_heads * head_dim,
+    any row stride) into the 8-bit cache."""
+    _check(load().exl3_kv8_append(cache._ref, batch._ref, _ptr(k), k.stride(0), _ptr(v), v.stride(0),
+                                  _stream(stream)), "exl3_kv8_append")
+
+
+def exl3_kv8_attention_workspace_bytes(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, n_heads: int) -> int:
+    return int(load().exl3_kv8_attention_workspace_bytes(cache._ref, batch._ref, int(n_heads)))
+
+
+def exl3_kv8_attention(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, q, n_heads: int, scale: float, out, workspace,
+                       softcap: float = 0.0, causal: bool = True, lse=None, workspace_bytes: int | None = None,
+                       stream=None) -> None:
+    """Attention of q (fp16, rows x n_heads * head_dim, any row stride) over the
+    8-bit cache into out (fp16, same shape); lse: rows x n_heads fp32 or None."""
+    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check(load().exl3_kv8_attention(cache._ref, batch._ref, _ptr(q), q.stride(0), n_heads, scale, softcap, causal,
+                                     _ptr(out), out.stride(0), _ptr(lse), _ptr(workspace), nbytes, _stream(stream)),
+           "exl3_kv8_attention")
+
+
+def exl3_kv8_weigh(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, q, n_heads: int, scale: float, lse, softcap: float = 0.0,
+                   causal: bool = True, stream=None) -> None:
+    """Adds the attention that q's rows give each cached token to cache.weight;
+    lse as exl3_kv8_attention returned it."""
+    _check(load().exl3_kv8_weigh(cache._ref, batch._ref, _ptr(q), q.stride(0), n_heads, scale, softcap, causal,
+                                 _ptr(lse), _stream(stream)), "exl3_kv8_weigh")
+
+
+def exl3_kv8_evict(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, dst_pages, budget: int, recent: int, kept, new_len,
+                   stream=None) -> None:
+    """Moves each sequence's last `recent` and heaviest other tokens, `budget` in
+    all, to dst_pages (int32, n_seqs x ceil(budget / 64)); kept (int32, n_seqs x
+    n_kv_heads x budget) and new_len (int32, n_seqs) receive what was kept."""
+    _check(load().exl3_kv8_evict(cache._ref, batch._ref, _ptr(dst_pages), budget, recent, _ptr(kept), _ptr(new_len),
+                                 _stream(stream)), "exl3_kv8_evict")
+
+
+def exl3_logits_adjust(logits, n: int, out, argmax, history=None, history_start=None, generated_from=None,
+                       repetition=None, presence=None, frequency=None, bias_id=None, bias_value=None, bias_start=None,
+                       allowed=None, stream=None) -> None:
+    """Penalties, biases and a grammar mask on the first n columns of logits
+    (fp32, M x ld) into out (may be logits), and the greedy choice."""
+    rules = _LogitsRules(_ptr(history), _ptr(history_start), _ptr(generated_from), _ptr(repetition), _ptr(presence),
+                         _ptr(frequency), _ptr(bias_id), _ptr(bias_value), _ptr(bias_start), _ptr(allowed),
+                         0 if history is None else history.numel(), 0 if bias_id is None else bias_id.numel())
+    _check(load().exl3_logits_adjust(_ptr(logits), logits.stride(0), logits.shape[0], n, ctypes.byref(rules), _ptr(out),
+                                     out.stride(0), _ptr(argmax), _stream(stream)), "exl3_logits_adjust")
+
+
+def exl3_selftest_bounds_serving(stream=None) -> tuple[int, int]:
+    """exl3_selftest_bounds for the serving operators' translation units."""
+    rep, tot = ctypes.c_int(0), ctypes.c_int(0)
+    _check(load().exl3_selftest_bounds_serving(ctypes.byref(rep), ctypes.byref(tot), _stream(stream)),
+           "exl3_selftest_bounds_serving")
+    return rep.value, tot.value

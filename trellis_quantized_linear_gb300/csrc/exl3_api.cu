@@ -10,6 +10,7 @@
 #include "../../include/exl3.h"
 #include "exl3_common.cuh"
 #include "exl3_internal.h"
+#include "exl3_serve.h"
 
 // Device error word: kernels record in it the first bounded wait they gave
 // up (and, in the bounds-checked build, the first failed bounds check).
@@ -247,7 +248,9 @@ exl3_status exl3_init(int device) {
   if (init_rotate_kernels(info.status) != cudaSuccess || init_reconstruct_kernels(info.status) != cudaSuccess ||
       init_reconstruct_rotated_kernels(info.status) != cudaSuccess ||
       init_decode_kernels(info.status) != cudaSuccess || init_prefill_kernels(info.status) != cudaSuccess ||
-      init_fused_kernels(info.status) != cudaSuccess || init_fused_prefill_kernels(info.status) != cudaSuccess)
+      init_fused_kernels(info.status) != cudaSuccess || init_fused_prefill_kernels(info.status) != cudaSuccess ||
+      init_kv8_cache_kernels(info.status) != cudaSuccess || init_kv8_attention_kernels(info.status) != cudaSuccess ||
+      init_logits_adjust_kernels(info.status) != cudaSuccess)
     return EXL3_ERR_CUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return EXL3_ERR_CUDA;
   info.ready = true;
@@ -267,6 +270,7 @@ const char *exl3_status_string(int status) {
     case EXL3_ERR_DEVICE_TIMEOUT: return "a kernel gave up a bounded wait on the device";
     case EXL3_ERR_NOALLOC_TOO_LARGE: return "problem needs more scratch than the fixed no-alloc buffer holds";
     case EXL3_ERR_OUT_OF_BOUNDS: return "a bounds check of the bounds-checked build failed on the device";
+    case EXL3_ERR_DEVICE_INDEX: return "a page number, length or row range read on the device is out of range";
     default: return "unknown status";
   }
 }

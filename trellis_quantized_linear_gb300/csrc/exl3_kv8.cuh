@@ -1,0 +1,103 @@
+// Device helpers of the 8-bit key/value cache (layout in include/exl3.h).
+#pragma once
+
+#include <stdint.h>
+
+#include "exl3_common.cuh"
+#include "exl3_serve.h"
+
+namespace exl3 {
+
+constexpr int kKvBlock = EXL3_KV8_BLOCK;
+constexpr int kMinExp = -32, kMaxExp = 8;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ void report_index(int *status) {
+  atomicCAS(status, 0, (int)EXL3_ERR_DEVICE_INDEX);
+}
+
+// What the device buffers say of one sequence, checked against what the call
+// declared: lengths and row ranges outside it are reported, and the sequence
+// is then empty.
+struct KvSeq {
+  int row0, rows, len;
+};
+__device__ __forceinline__ int kv_length(const KvView &kv, int s) {
+  const int len = kv.kv_len[s];
+  if (len < 0 || len > kv.max_pages * (int64_t)kKvBlock) {
+    report_index(kv.status);
+    return 0;
+  }
+  return len;
+}
+__device__ __forceinline__ KvSeq kv_sequence(const KvView &kv, int s) {
+  KvSeq q{kv.q_start[s], 0, kv_length(kv, s)};
+  q.rows = kv.q_start[s + 1] - q.row0;
+  if (q.row0 < 0 || q.rows < 0 || q.rows > kv.max_rows || q.row0 + (int64_t)q.rows > kv.rows) {
+    report_index(kv.status);
+    q = KvSeq{0, 0, 0};
+  }
+  return q;
+}
+
+// Page of block b of sequence s, or -1 (reported) when the table's entry names
+// no page. b < max_pages.
+__device__ __forceinline__ int kv_page(const KvView &kv, int s, int b) {
+  const int p = kv.page_table[(int64_t)s * kv.max_pages + b];
+  if (p < 0 || p >= kv.n_pages) {
+    report_index(kv.status);
+    return -1;
+  }
+  return p;
+}
+
+// 2^e for -126 <= e <= 127, and the exponent of a power of two.
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int pow2_exponent(float s) { return ((__float_as_int(s) >> 23) & 255) - 127; }
+
+// Smallest e in kMinExp .. kMaxExp with a <= 448 * 2^e, for an fp16 value a >= 0.
+// With a = m 2^x, m in [1/2, 1), and 448 = 7/8 * 2^9: x - 9, one more when m > 7/8.
+__device__ __forceinline__ int block_exponent(float a) {
+  const int b = __float_as_int(a);
+  const int e = (b >> 23) - 126 - 9 + ((b & 0x7FFFFF) > 0x600000 ? 1 : 0);
+  return min(max(e, kMinExp), kMaxExp);
+}
+
+// Two fp32 values to two E4M3 codes (a in the low byte): nearest even,
+// saturating, NaN to NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// Two E4M3 codes to two fp16 values, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
+// Eight codes times 2^d, rounded to nearest even.
+__device__ __forceinline__ uint2 rescale_codes(uint2 c, float factor) {
+  const uint32_t w[2] = {c.x, c.y};
+  uint32_t o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = e4m3x2_to_half2((uint16_t)(w[i] & 0xFFFF)), hi = e4m3x2_to_half2((uint16_t)(w[i] >> 16));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    o[i] = to_e4m3x2(a.x * factor, a.y * factor) | (to_e4m3x2(b.x * factor, b.y * factor) << 16);
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+// softcap * tanh(s / softcap) through 1 - 2 / (exp(2 x) + 1): an absolute error
+// near softcap * 2^-23, which a direct tanh approximation (relative error 2^-11
+// of a score near the cap) would not give. exp overflows to inf: tanh is then 1.
+__device__ __forceinline__ float soft_cap(float s, float cap, float inv_cap) {
+  return cap - cap * __fdividef(2.0f, 1.0f + exp2f(s * inv_cap * (2.0f * kLog2e)));
+}
+
+}  // namespace exl3
