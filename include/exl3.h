@@ -399,7 +399,7 @@ typedef struct {
     void *k, *v;             /* E4M3, n_pages x n_kv_heads x 64 x head_dim */
     float *k_scale, *v_scale;/* n_pages x n_kv_heads */
     float *weight;           /* n_pages x n_kv_heads x 64: accumulated attention weight, or NULL */
-    int64_t n_pages;         /* n_pages * n_kv_heads * 64 < 2^31 */
+    int64_t n_pages;         /* at least 1; n_pages * n_kv_heads * 64 < 2^31 */
     int32_t n_kv_heads;      /* 1 .. 1024 */
     int32_t head_dim;        /* 64 or 128 */
 } exl3_kv8_cache;

@@ -1,153 +1,853 @@
 // Attention over the 8-bit key/value cache, and the accumulated attention weight
 // of its tokens. Formulas in include/exl3.h.
+//
+// Stream kernel. All work is cut into units of 32 cached tokens; the units of
+// every (sequence, key/value head, row tile) lie one behind the other, and each
+// warp of a persistent grid takes one equal, contiguous range of them, whatever
+// the sequences' lengths are (they are read on the device). A warp keeps its own
+// ring of TMA copies in flight and its own running maximum, sum and output, so
+// warps never wait for one another. Where a range ends inside a segment, the
+// warp leaves its partial result in the workspace and a second kernel joins the
+// partials in the order of the warps.
+//
+// The bound is the cache stream: D + D bytes a token and head. The tensor core's
+// narrow side takes the rows (S^T = K Q^T and O^T = V^T P^T, m16n8k16): 8 rows
+// of a group cost half the products and registers that 16 would, and the
+// transposed probabilities come from one movmatrix each. Codes become fp16
+// exactly. The dimension is permuted so that a lane's 16 bytes of a key serve
+// four k-steps and its 16 bytes of a value four rows of the output, without a
+// shuffle.
+#include <cuda.h>
+
 #include "exl3_internal.h"
 #include "exl3_kv8.cuh"
+#include "exl3_tcgen05.cuh"
 
 namespace exl3 {
 
 namespace {
 
-// Sequence of row r: the last s with q_start[s] <= r.
-__device__ __forceinline__ int sequence_of_row(const KvView &kv, int r) {
-  int lo = 0, hi = kv.n_seqs - 1;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kUnit = 32;         // tokens
+constexpr int kMaxSeqs = 1024;    // sequences of one launch
+
+template <int D, bool WEIGH>
+struct StreamCfg {
+  static constexpr int kHalf = kUnit * D;                     // bytes of a unit's keys (or values)
+  static constexpr int kStage = WEIGH ? kHalf : 2 * kHalf;
+  static constexpr int kStages = 24 * 1024 / kStage;          // 24 KB of copies in flight per warp
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kOffPrefix = kRing;                    // int64 prefix[kMaxSeqs + 1], warp sums
+  static constexpr int kOffBar = kOffPrefix + (kMaxSeqs + 1 + kWarps) * 8;
+  static constexpr int kSmem = 1024 + kOffBar + kWarps * kStages * 8;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+struct StreamParams {
+  KvAttention a;
+  int group;      // query heads of a key/value head
+  float *part_o;  // warps x 2 x tile rows x D
+  float *part_ml; // warps x 2 x tile rows x 2 (maximum in log2 units, sum)
+  int warps;      // of the stream grid
+  int64_t part_rows;  // 2 * warps * tile rows
+};
+
+__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+
+// Units of all sequences before sequence s, prefix[s], for s = 0 .. n_seqs; row
+// tiles of `tile` rows (0: the rows are not tiled). Every thread of the CTA takes
+// part; ends with a barrier.
+__device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile, int64_t *prefix) {
+  int64_t *warp_sum = prefix + kMaxSeqs + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  int64_t carry = 0;
+  if (threadIdx.x == 0) prefix[0] = 0;
+  for (int c = 0; c < kv.n_seqs; c += blockDim.x) {
+    const int s = c + (int)threadIdx.x;
+    int64_t n = 0;
+    if (s < kv.n_seqs) {
+      const KvSeq q = kv_sequence(kv, s);
+      if (q.rows > 0)
+        n = (int64_t)units_of(q.len) * kv.n_kv_heads * (tile ? ((int64_t)q.rows * group + tile - 1) / tile : 1);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += o;
+    }
+    if (lane == 31) warp_sum[warp] = n;
+    __syncthreads();
+    for (int w = 0; w < nwarps; ++w) {
+      if (w < warp) n += warp_sum[w];
+    }
+    if (s < kv.n_seqs) prefix[s + 1] = carry + n;
+    int64_t total = 0;
+    for (int w = 0; w < nwarps; ++w) total += warp_sum[w];
+    carry += total;
+    __syncthreads();
+  }
+  __syncthreads();
+}
+
+// First unit of warp w of W over T units, and the warp that owns unit z.
+__device__ __forceinline__ int64_t range_start(int64_t w, int64_t W, int64_t T) { return w * T / W; }
+__device__ __forceinline__ int64_t range_owner(int64_t z, int64_t W, int64_t T) { return ((z + 1) * W - 1) / T; }
+
+// A place in the unit order.
+struct Cursor {
+  KvSeq q;
+  int s, h, rt, u;    // sequence, key/value head, row tile, unit of the segment
+  int units, tiles;   // of this sequence's segments
+};
+__device__ __forceinline__ void enter_sequence(const KvView &kv, int group, int tile, Cursor &c) {
+  c.q = kv_sequence(kv, c.s);
+  c.units = units_of(c.q.len);
+  c.tiles = tile ? (int)(((int64_t)c.q.rows * group + tile - 1) / tile) : 1;
+}
+__device__ __forceinline__ Cursor locate(const KvView &kv, int group, int tile, const int64_t *prefix, int64_t z) {
+  Cursor c;
+  int lo = 0, hi = kv.n_seqs - 1;  // the s with prefix[s] <= z < prefix[s + 1]
   while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (kv.q_start[mid] <= r) lo = mid;
-    else hi = mid - 1;
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid + 1] > z) hi = mid;
+    else lo = mid + 1;
   }
-  return lo;
+  c.s = lo;
+  enter_sequence(kv, group, tile, c);
+  const int64_t rem = z - prefix[lo];
+  const int64_t seg = rem / c.units;
+  c.u = (int)(rem - seg * c.units);
+  c.h = (int)(seg / c.tiles);
+  c.rt = (int)(seg - (int64_t)c.h * c.tiles);
+  return c;
+}
+__device__ __forceinline__ void advance(const KvView &kv, int group, int tile, const int64_t *prefix, Cursor &c) {
+  if (++c.u < c.units) return;
+  c.u = 0;
+  if (++c.rt < c.tiles) return;
+  c.rt = 0;
+  if (++c.h < kv.n_kv_heads) return;
+  c.h = 0;
+  do ++c.s;
+  while (c.s < kv.n_seqs && prefix[c.s + 1] == prefix[c.s]);
+  if (c.s < kv.n_seqs) enter_sequence(kv, group, tile, c);
 }
 
-// This lane's D / 32 elements of a token's codes.
-template <int D>
-__device__ __forceinline__ void load_codes(const uint8_t *p, int lane, float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    const uint32_t h = e4m3x2_to_half2(*reinterpret_cast<const uint16_t *>(p + lane * E + 2 * i));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+// Page numbers and scales of 32 consecutive blocks of one (sequence, head), one
+// block a lane.
+struct Blocks {
+  int s = -1, h = -1, base = 0;
+  int page = -1;
+  float ks = 0.f, vs = 0.f;
+  __device__ __forceinline__ bool holds(const Cursor &c) const {
+    const int b = c.u >> 1;
+    return c.s == s && c.h == h && b >= base && b < base + 32;
   }
-}
+  template <bool WEIGH>
+  __device__ __forceinline__ void load(const KvView &kv, const Cursor &c, int lane) {
+    s = c.s;
+    h = c.h;
+    base = c.u >> 1;
+    page = -1;
+    ks = 0.f;
+    vs = 0.f;
+    const int b = base + lane;
+    if (b * 2 < c.units) page = kv_page(kv, s, b);
+    if (page >= 0) {
+      const int64_t slab = (int64_t)page * kv.n_kv_heads + h;
+      ks = kv.k_scale[slab];
+      if (!WEIGH) vs = kv.v_scale[slab];
+    }
+  }
+};
 
-template <int D>
-__device__ __forceinline__ float warp_dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
-  float r = 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) r = fmaf(a[i], b[i], r);
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) r += __shfl_xor_sync(0xffffffffu, r, m);
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
-template <int D>
-__device__ __forceinline__ void load_row(const __half *q, int lane, float (&x)[D / 32]) {
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) x[i] = __half2float(q[lane * (D / 32) + i]);
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One warp per (row, query head), one token at a time: running maximum, sum and
-// output, all fp32.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t lo_codes(uint32_t w) { return e4m3x2_to_half2((uint16_t)(w & 0xFFFFu)); }
+__device__ __forceinline__ uint32_t hi_codes(uint32_t w) { return e4m3x2_to_half2((uint16_t)(w >> 16)); }
+
+// Address of 16-byte piece c of token row r in a copied tile (128-byte swizzle
+// for 128-byte rows, 64-byte swizzle for 64-byte rows).
 template <int D>
-__global__ void __launch_bounds__(128) kv8_attention_kernel(KvAttention p) {
-  const KvView &kv = p.kv;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (w >= (int64_t)kv.rows * p.n_heads) return;
-  const int r = (int)(w / p.n_heads), head = (int)(w % p.n_heads);
-  const int s = sequence_of_row(kv, r), h = head / (p.n_heads / kv.n_kv_heads);
-  const KvSeq q = kv_sequence(kv, s);
-  const int limit = min(q.len, p.causal ? q.len - q.rows + (r - q.row0) + 1 : q.len);
-  constexpr int E = D / 32;
-  float qx[E], o[E] = {};
-  load_row<D>(static_cast<const __half *>(p.q) + r * p.ldq + (int64_t)head * D, lane, qx);
-  float top = -INFINITY, total = 0.f;
-  for (int b = 0; b * kKvBlock < limit; ++b) {
-    const int page = kv_page(kv, s, b);
-    if (page < 0) continue;
-    const int64_t slab = (int64_t)page * kv.n_kv_heads + h;
-    const float ks = kv.k_scale[slab] * p.scale, vs = kv.v_scale[slab];
-    for (int t = 0; t < kKvBlock && b * kKvBlock + t < limit; ++t) {
-      float kx[E], vx[E];
-      load_codes<D>(kv.k + (slab * kKvBlock + t) * D, lane, kx);
-      load_codes<D>(kv.v + (slab * kKvBlock + t) * D, lane, vx);
-      float x = warp_dot<D>(qx, kx) * ks;
-      if (p.softcap > 0.f) x = soft_cap(x, p.softcap, 1.0f / p.softcap);
-      const float now = fmaxf(top, x);
-      const float keep = exp2f((top - now) * kLog2e), e = exp2f((x - now) * kLog2e);
-      total = total * keep + e;
+__device__ __forceinline__ uint32_t piece(uint32_t base, int r, int c) {
+  return D == 128 ? base + r * 128 + ((c ^ (r & 7)) << 4) : base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+template <int W>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t *w) {
+  if (!EXL3_SMEM(addr, 4 * W)) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = o[i] * keep + e * vs * vx[i];
-      top = now;
+    for (int i = 0; i < W; ++i) w[i] = 0;
+    return;
+  }
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+
+// The B operand of S^T: this lane's D / 4 elements of row j (lane / 4) of the tile.
+template <int D>
+__device__ __forceinline__ void load_query(const StreamParams &p, const Cursor &c, int j, int lane, uint32_t (&qf)[D / 8]) {
+  const int t = lane & 3;
+  const int i = j / p.group;
+#pragma unroll
+  for (int k = 0; k < D / 8; ++k) qf[k] = 0;
+  if (i >= c.q.rows) return;
+  const int64_t off = (int64_t)(c.q.row0 + i) * p.a.ldq + (int64_t)(c.h * p.group + j - i * p.group) * D + t * (D / 4);
+  const __half *q = static_cast<const __half *>(p.a.q) + off;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k)
+    if (EXL3_SPAN(off + 8 * k, 8, (int64_t)(p.a.kv.rows - 1) * p.a.ldq + (int64_t)p.a.n_heads * D)) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q) + k);
+      qf[4 * k] = v.x;
+      qf[4 * k + 1] = v.y;
+      qf[4 * k + 2] = v.z;
+      qf[4 * k + 3] = v.w;
+    }
+}
+
+// Tokens that row j of a segment sees: 0 for rows past the last.
+__device__ __forceinline__ int row_limit(const StreamParams &p, const Cursor &c, int j) {
+  const int i = j / p.group;
+  if (i >= c.q.rows) return 0;
+  return p.a.causal ? c.q.len - c.q.rows + i + 1 : c.q.len;
+}
+
+// The A operands of S^T for 16 tokens from r0 on: D / 16 k-steps.
+template <int D>
+__device__ __forceinline__ void load_keys(uint32_t base, int r0, int lane, uint32_t (&a)[D / 16][4]) {
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t w[2][D / 16];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) lds<4>(piece<D>(base, r0 + g + 8 * r, (D / 64) * t + x), &w[r][4 * x]);
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    a[j][0] = lo_codes(w[0][j]);
+    a[j][1] = lo_codes(w[1][j]);
+    a[j][2] = hi_codes(w[0][j]);
+    a[j][3] = hi_codes(w[1][j]);
+  }
+}
+
+// Scores in log2 units. ks: key scale * softmax scale (* log2 e without a cap).
+template <bool CAP>
+__device__ __forceinline__ float score(float acc, float ks, float cap, float inv_cap) {
+  if constexpr (CAP) return soft_cap(acc * ks, cap, inv_cap) * kLog2e;
+  return acc * ks;
+}
+
+// A warp's ring of copies: issues the keys (and values) of units in order.
+template <int D, bool WEIGH>
+struct Ring {
+  using Cfg = StreamCfg<D, WEIGH>;
+  uint32_t base, bars;
+  int put = 0, get = 0;
+  uint32_t get_phase = 0;
+  int in_flight = 0;
+
+  __device__ __forceinline__ void issue(const CUtensorMap *tk, const CUtensorMap *tv, const KvView &kv, const Cursor &c,
+                                        int page, int lane) {
+    if (lane == 0) {
+      const uint32_t bar = bars + 8 * put, dst = base + put * Cfg::kStage;
+      const int64_t row = ((int64_t)max(page, 0) * kv.n_kv_heads + c.h) * kKvBlock + (c.u & 1) * kUnit;
+      // a page that the table does not name: nothing is copied, the consumer skips the unit
+      const bool ok = page >= 0 && EXL3_SPAN(row, kUnit, kv.n_pages * kv.n_kv_heads * kKvBlock) &&
+                      EXL3_SMEM(dst, Cfg::kStage) && EXL3_SMEM(bar, 8);
+      mbar_arrive_expect_tx(bar, ok ? Cfg::kStage : 0);
+      if (ok) {
+        tma_load_2d(dst, tk, bar, 0, (int)row);
+        if (!WEIGH) tma_load_2d(dst + Cfg::kHalf, tv, bar, 0, (int)row);
+      }
+    }
+    if (++put == Cfg::kStages) put = 0;
+    ++in_flight;
+  }
+  __device__ __forceinline__ uint32_t stage() const { return base + get * Cfg::kStage; }
+  __device__ __forceinline__ bool wait(int *status) {
+    return __all_sync(0xffffffffu, mbar_wait(bars + 8 * get, get_phase, status));
+  }
+  __device__ __forceinline__ void next() {
+    if (++get == Cfg::kStages) {
+      get = 0;
+      get_phase ^= 1u;
+    }
+    --in_flight;
+  }
+  // After a wait that ran out: the copies still in flight land before the CTA leaves.
+  __device__ __forceinline__ void drain() {
+    while (in_flight > 0) {
+      mbar_wait_short(bars + 8 * get, get_phase);
+      next();
     }
   }
-  const float inv = total > 0.f ? 1.0f / total : (total == total ? 0.f : total);
-  __half *out = static_cast<__half *>(p.out) + r * p.ldo + (int64_t)head * D + lane * E;
+};
+
+template <int D, int NT>
+struct RowState {
+  float o[NT][D / 16][4];  // O^T in units of 2^e_v: d by lane / 4, rows 2 t, 2 t + 1
+  float m[NT][2], l[NT][2];
+  int ev;                  // exponent of the value scale that o is in units of
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < E; ++i) out[i] = __float2half_rn(o[i] * inv);
-  if (p.lse && lane == 0) p.lse[(int64_t)r * p.n_heads + head] = total == 0.f ? -INFINITY : top + logf(total);
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n][i][k] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+    ev = 0;
+  }
+};
+
+// One unit: scores, running maximum and sum, O^T += V^T P^T.
+template <int D, int NT, bool CAP>
+__device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stage, int pos0, int len, float ks, float vs,
+                                            const uint32_t (&qf)[NT][D / 8], const int (&limit)[NT][2], int min_limit,
+                                            float inv_cap, int lane, RowState<D, NT> &st) {
+  const int g = lane >> 2, t = lane & 3;
+  float s[NT][2][4];
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi) {
+    uint32_t a[D / 16][4];
+    load_keys<D>(stage, 16 * mi, lane, a);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[n][mi][k] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) mma_16816(s[n][mi], a[j][0], a[j][1], a[j][2], a[j][3], qf[n][2 * j], qf[n][2 * j + 1]);
+    }
+  }
+  const float c = ks * p.a.scale * (CAP ? 1.0f : kLog2e);
+  const bool masked = pos0 + kUnit > min_limit;  // some row does not see the whole unit
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s[n][mi][k] = score<CAP>(s[n][mi][k], c, p.a.softcap, inv_cap);
+        if (masked && pos0 + 16 * mi + g + 8 * (k >> 1) >= limit[n][k & 1]) s[n][mi][k] = -INFINITY;
+      }
+  const int ev = pow2_exponent(vs);
+  const float unit = pow2i(max(min(st.ev - ev, 127), -126));  // exact: O in the new unit
+  uint32_t b[NT][2][2];
+  float alpha[NT][2];
+  bool still = ev == st.ev;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int col = 0; col < 2; ++col) {
+      float top = fmaxf(fmaxf(s[n][0][col], s[n][0][2 + col]), fmaxf(s[n][1][col], s[n][1][2 + col]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      const float now = fmaxf(st.m[n][col], top);
+      const float ref = now == -INFINITY ? 0.f : now;
+      const float keep = ex2(st.m[n][col] - ref);
+      still = still && (keep == 1.0f || st.m[n][col] == -INFINITY);
+      float sum = 0.f;
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float e = ex2(s[n][mi][2 * r + col] - ref);
+          s[n][mi][2 * r + col] = e;
+          sum += e;
+        }
+      st.m[n][col] = now;
+      st.l[n][col] = st.l[n][col] * keep + sum;
+      alpha[n][col] = keep * unit;
+    }
+    // fp16 probabilities: relative error 2^-12 on average, the size of the result's own rounding
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const __half2 h = __floats2half2_rn(s[n][mi][2 * r], s[n][mi][2 * r + 1]);
+        b[n][mi][r] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&h));
+      }
+  }
+  if (!__all_sync(0xffffffffu, still)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st.o[n][i][k] *= alpha[n][k & 1];
+    st.ev = ev;
+  }
+  const bool tail = pos0 + kUnit > len;
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi) {
+    constexpr int W = D / 32;  // words of a lane's piece of a token
+    uint32_t v[4][W];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tok = 16 * mi + 2 * t + (r & 1) + 8 * (r >> 1);
+      if constexpr (D == 128) lds<4>(piece<D>(stage + StreamCfg<D, false>::kHalf, tok, g), v[r]);
+      else lds<2>(piece<D>(stage + StreamCfg<D, false>::kHalf, tok, g >> 1) + (g & 1) * 8, v[r]);
+      if (tail && pos0 + tok >= len) {  // whatever lies past the length (a NaN times 0 is a NaN)
+#pragma unroll
+        for (int w = 0; w < W; ++w) v[r][w] = 0;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const uint32_t x = __byte_perm(v[0][w], v[1][w], 0x5140), y = __byte_perm(v[2][w], v[3][w], 0x5140);
+      const uint32_t z = __byte_perm(v[0][w], v[1][w], 0x7362), u = __byte_perm(v[2][w], v[3][w], 0x7362);
+      const uint32_t a0 = lo_codes(x), a1 = hi_codes(x), a2 = lo_codes(y), a3 = hi_codes(y);
+      const uint32_t c0 = lo_codes(z), c1 = hi_codes(z), c2 = lo_codes(u), c3 = hi_codes(u);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_16816(st.o[n][2 * w], a0, a1, a2, a3, b[n][mi][0], b[n][mi][1]);
+        mma_16816(st.o[n][2 * w + 1], c0, c1, c2, c3, b[n][mi][0], b[n][mi][1]);
+      }
+    }
+  }
 }
 
-// One warp per (cached token, sequence, key/value head): all rows of the
-// sequence in order.
+// Writes a finished row's D / 8 consecutive outputs of this lane.
 template <int D>
-__global__ void __launch_bounds__(128) kv8_weigh_kernel(KvAttention p) {
-  const KvView &kv = p.kv;
-  const int lane = threadIdx.x & 31, s = blockIdx.y, h = blockIdx.z;
-  const int t = blockIdx.x * (int)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  const KvSeq q = kv_sequence(kv, s);
-  if (t >= q.len || q.rows == 0) return;
-  const int page = kv_page(kv, s, t / kKvBlock);
-  if (page < 0) return;
-  const int64_t slab = (int64_t)page * kv.n_kv_heads + h;
-  const int64_t at = slab * kKvBlock + t % kKvBlock;
-  const float ks = kv.k_scale[slab] * p.scale;
-  float kx[D / 32], qx[D / 32], add = 0.f;
-  load_codes<D>(kv.k + at * D, lane, kx);
-  const int group = p.n_heads / kv.n_kv_heads;
-  const int from = p.causal ? max(0, t - (q.len - q.rows)) : 0;
-  for (int i = from; i < q.rows; ++i)
-    for (int g = 0; g < group; ++g) {
-      const int head = h * group + g;
-      const int64_t r = q.row0 + i;
-      const float lse = p.lse[r * p.n_heads + head];
-      load_row<D>(static_cast<const __half *>(p.q) + r * p.ldq + (int64_t)head * D, lane, qx);
-      float x = warp_dot<D>(qx, kx) * ks;
-      if (p.softcap > 0.f) x = soft_cap(x, p.softcap, 1.0f / p.softcap);
-      if (lse != -INFINITY) add += exp2f((x - lse) * kLog2e);
+__device__ __forceinline__ void store_out(const KvAttention &a, int64_t row, int head, int d0, const float (&v)[D / 8]) {
+  const int64_t off = row * a.ldo + (int64_t)head * D + d0;
+  if (!EXL3_SPAN(off, D / 8, (int64_t)(a.kv.rows - 1) * a.ldo + (int64_t)a.n_heads * D)) return;
+  __half *out = static_cast<__half *>(a.out) + off;
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
-  if (lane == 0) kv.weight[at] += add;
+    reinterpret_cast<uint4 *>(out)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The end of a warp's part of a segment: the result where the part is the whole
+// segment, else a partial (slot 0: the segment began before this warp's range,
+// slot 1: it began in it).
+template <int D, int NT>
+__device__ __forceinline__ void finish_part(const StreamParams &p, const Cursor &c, bool whole, int64_t slot, int lane,
+                                            RowState<D, NT> &st) {
+  const int g = lane >> 2, t = lane & 3;
+  const float unit = pow2i(st.ev);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int col = 0; col < 2; ++col) {
+      float l = st.l[n][col];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int jt = 8 * n + 2 * t + col, j = c.rt * 8 * NT + jt, i = j / p.group;
+      float v[D / 8];
+      const float f = whole ? (l == 0.f ? 0.f : unit / l) : unit;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        v[2 * k] = st.o[n][k][col] * f;
+        v[2 * k + 1] = st.o[n][k][2 + col] * f;
+      }
+      if (i >= c.q.rows) continue;
+      const int head = c.h * p.group + j - i * p.group;
+      if (whole) {
+        store_out<D>(p.a, c.q.row0 + i, head, g * (D / 8), v);
+        if (p.a.lse && g == 0)
+          p.a.lse[(int64_t)(c.q.row0 + i) * p.a.n_heads + head] = l == 0.f ? -INFINITY : (st.m[n][col] + __log2f(l)) * kLn2;
+      } else {
+        const int64_t at = slot * 8 * NT + jt;
+        if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
+        float4 *o = reinterpret_cast<float4 *>(p.part_o + at * D + g * (D / 8));
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) o[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        if (g == 0) reinterpret_cast<float2 *>(p.part_ml)[at] = make_float2(st.m[n][col], l);
+      }
+    }
+}
+
+template <int D, int NT, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_stream_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const StreamParams p) {
+  using Cfg = StreamCfg<D, false>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const KvView &kv = p.a.kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t *prefix = reinterpret_cast<int64_t *>(smem + Cfg::kOffPrefix);
+  Ring<D, false> ring;
+  ring.base = smem_u32(smem) + warp * Cfg::kStages * Cfg::kStage;
+  ring.bars = smem_u32(smem + Cfg::kOffBar) + warp * Cfg::kStages * 8;
+  if (lane == 0) {
+    for (int i = 0; i < Cfg::kStages; ++i) mbar_init(ring.bars + 8 * i, 1);
+    fence_barrier_init();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int tile = 8 * NT;
+  build_plan(kv, p.group, tile, prefix);
+  const int64_t T = prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+  if (w >= W) return;
+  int64_t z = range_start(w, W, T), zp = z;
+  const int64_t z1 = range_start(w + 1, W, T);
+  Cursor c = locate(kv, p.group, tile, prefix, z), cp = c;
+  Blocks ahead, now;
+  const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
+
+  uint32_t qf[NT][D / 8];
+  int limit[NT][2], min_limit = 0;  // tokens that this lane's rows see, and the tile's first row
+  RowState<D, NT> st;
+  bool fresh = true, began = false;
+  for (; z < z1; ++z) {
+    while (zp < z1 && ring.in_flight < Cfg::kStages) {
+      if (!ahead.holds(cp)) ahead.load<false>(kv, cp, lane);
+      ring.issue(&tk, &tv, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
+      ++zp;
+      advance(kv, p.group, tile, prefix, cp);
+    }
+    if (!now.holds(c)) {
+      if (ahead.holds(c)) now = ahead;
+      else now.load<false>(kv, c, lane);
+    }
+    const int at = (c.u >> 1) - now.base;
+    const int page = __shfl_sync(0xffffffffu, now.page, at);
+    const float ks = __shfl_sync(0xffffffffu, now.ks, at), vs = __shfl_sync(0xffffffffu, now.vs, at);
+    if (fresh) {
+      fresh = false;
+      began = c.u == 0;
+      st.clear();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        load_query<D>(p, c, c.rt * tile + 8 * n + (lane >> 2), lane, qf[n]);
+        limit[n][0] = row_limit(p, c, c.rt * tile + 8 * n + 2 * (lane & 3));
+        limit[n][1] = row_limit(p, c, c.rt * tile + 8 * n + 2 * (lane & 3) + 1);
+      }
+      min_limit = row_limit(p, c, c.rt * tile);  // rows come in order: the first sees the least
+    }
+    if (!ring.wait(kv.status)) {
+      ring.drain();
+      return;
+    }
+    if (page >= 0)
+      attend_unit<D, NT, CAP>(p, ring.stage(), c.u * kUnit, c.q.len, ks, vs, qf, limit, min_limit, inv_cap, lane, st);
+    __syncwarp();  // every lane is done with the stage before it is filled again
+    ring.next();
+    const bool end = c.u + 1 == c.units;
+    if (end || z + 1 == z1) {
+      finish_part<D, NT>(p, c, began && end, 2 * w + (began ? 1 : 0), lane, st);
+      fresh = true;
+    }
+    advance(kv, p.group, tile, prefix, c);
+  }
+}
+
+// Joins the partials of the segments that several warps worked on, in the order
+// of the warps, and writes the rows of segments without tokens. One CTA of D
+// threads per (sequence, key/value head, row tile) and row of the tile.
+template <int D, int NT>
+__global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
+  __shared__ int64_t prefix[kMaxSeqs + 1 + kWarps];
+  const KvView &kv = p.a.kv;
+  constexpr int tile = 8 * NT;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Cursor c;
+  c.s = blockIdx.y;
+  c.h = blockIdx.z;
+  c.rt = blockIdx.x / tile;
+  enter_sequence(kv, p.group, tile, c);
+  const int j = blockIdx.x, i = j / p.group;
+  build_plan(kv, p.group, tile, prefix);
+  if (i >= c.q.rows) return;
+  const int head = c.h * p.group + j - i * p.group;
+  const int64_t row = c.q.row0 + i;
+  __half *out = static_cast<__half *>(p.a.out) + row * p.a.ldo + (int64_t)head * D + threadIdx.x;
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  if (c.units > 0) {
+    const int64_t T = prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
+    const int64_t z = prefix[c.s] + ((int64_t)c.h * c.tiles + c.rt) * c.units;
+    const int64_t w0 = range_owner(z, W, T), w1 = range_owner(z + c.units - 1, W, T);
+    if (w0 == w1) return;  // the warp wrote the result
+    for (int64_t w = w0; w <= w1; ++w) {
+      const int64_t at = (2 * w + (w == w0 ? 1 : 0)) * tile + j % tile;
+      if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
+      const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
+      const float x = p.part_o[at * D + threadIdx.x];
+      const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+      const float a = ex2(m - ref), b = ex2(ml.x - ref);
+      l = l * a + ml.y * b;
+      o = o * a + x * b;
+      m = top;
+    }
+  }
+  *out = __float2half_rn(l == 0.f ? 0.f : o / l);
+  if (p.a.lse && threadIdx.x == 0) p.a.lse[row * p.a.n_heads + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
+// Accumulated weight: the same stream over the keys alone; a unit's weights are
+// the sums over all rows of the sequence, formed by the warp that owns the unit.
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_weigh_kernel(const __grid_constant__ CUtensorMap tk, const StreamParams p) {
+  using Cfg = StreamCfg<D, true>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const KvView &kv = p.a.kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  int64_t *prefix = reinterpret_cast<int64_t *>(smem + Cfg::kOffPrefix);
+  Ring<D, true> ring;
+  ring.base = smem_u32(smem) + warp * Cfg::kStages * Cfg::kStage;
+  ring.bars = smem_u32(smem + Cfg::kOffBar) + warp * Cfg::kStages * 8;
+  if (lane == 0) {
+    for (int i = 0; i < Cfg::kStages; ++i) mbar_init(ring.bars + 8 * i, 1);
+    fence_barrier_init();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  build_plan(kv, p.group, 0, prefix);
+  const int64_t T = prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+  if (w >= W) return;
+  int64_t z = range_start(w, W, T), zp = z;
+  const int64_t z1 = range_start(w + 1, W, T);
+  Cursor c = locate(kv, p.group, 0, prefix, z), cp = c;
+  Blocks ahead, now;
+  const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
+  uint32_t qf[D / 8];
+  int limit[2];
+  float lse[2];  // in log2 units
+  int held_s = -1, held_h = -1, held_j = -1;
+
+  for (; z < z1; ++z) {
+    while (zp < z1 && ring.in_flight < Cfg::kStages) {
+      if (!ahead.holds(cp)) ahead.load<true>(kv, cp, lane);
+      ring.issue(&tk, nullptr, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
+      ++zp;
+      advance(kv, p.group, 0, prefix, cp);
+    }
+    if (!now.holds(c)) {
+      if (ahead.holds(c)) now = ahead;
+      else now.load<true>(kv, c, lane);
+    }
+    const int at = (c.u >> 1) - now.base;
+    const int page = __shfl_sync(0xffffffffu, now.page, at);
+    const float ks = __shfl_sync(0xffffffffu, now.ks, at) * p.a.scale * (CAP ? 1.0f : kLog2e);
+    if (!ring.wait(kv.status)) {
+      ring.drain();
+      return;
+    }
+    if (page >= 0) {
+      uint32_t a[2][D / 16][4];
+      load_keys<D>(ring.stage(), 0, lane, a[0]);
+      load_keys<D>(ring.stage(), 16, lane, a[1]);
+      const int pos0 = c.u * kUnit, J = c.q.rows * p.group;
+      // the first row that sees a token of the unit
+      const int first = p.a.causal ? max(0, pos0 - (c.q.len - c.q.rows)) * p.group : 0;
+      float sum[2][2] = {}, part[2][2] = {};
+      int n = 0;
+      for (int j0 = first & ~7; j0 < J; j0 += 8) {
+        if (held_s != c.s || held_h != c.h || held_j != j0) {
+          held_s = c.s;
+          held_h = c.h;
+          held_j = j0;
+          load_query<D>(p, c, j0 + g, lane, qf);
+#pragma unroll
+          for (int col = 0; col < 2; ++col) {
+            const int j = j0 + 2 * t + col, i = j / p.group;
+            limit[col] = row_limit(p, c, j);
+            lse[col] = limit[col] > 0 ? p.a.lse[(int64_t)(c.q.row0 + i) * p.a.n_heads + c.h * p.group + j - i * p.group] : 0.f;
+            if (lse[col] == -INFINITY) limit[col] = 0;
+            lse[col] *= kLog2e;
+          }
+        }
+#pragma unroll
+        for (int mi = 0; mi < 2; ++mi) {
+          float s[4] = {};
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) mma_16816(s, a[mi][k][0], a[mi][k][1], a[mi][k][2], a[mi][k][3], qf[2 * k], qf[2 * k + 1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (pos0 + 16 * mi + g + 8 * (k >> 1) < limit[k & 1])
+              part[mi][k >> 1] += ex2(score<CAP>(s[k], ks, p.a.softcap, inv_cap) - lse[k & 1]);
+        }
+        // sums of sums: 16 tiles to a part, so that long chunks do not lose bits
+        if ((++n & 15) == 0 || j0 + 8 >= J) {
+#pragma unroll
+          for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              sum[mi][r] += part[mi][r];
+              part[mi][r] = 0.f;
+            }
+        }
+      }
+      const int64_t slab = (int64_t)page * kv.n_kv_heads + c.h;
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float x = sum[mi][r];
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          const int tok = 16 * mi + g + 8 * r;
+          const int64_t off = slab * kKvBlock + (c.u & 1) * kUnit + tok;
+          if (t == 0 && pos0 + tok < c.q.len && EXL3_SPAN(off, 1, kv.n_pages * kv.n_kv_heads * kKvBlock)) kv.weight[off] += x;
+        }
+    }
+    __syncwarp();
+    ring.next();
+    advance(kv, p.group, 0, prefix, c);
+  }
+}
+
+// A launch that may start while the kernel before it in the stream is ending
+// (the kernels wait before they touch memory).
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Up to 8 rows of a (sequence, head) in one tile: half the registers and
+// products of the 16-row tile.
+bool narrow(int64_t tile_rows) { return tile_rows <= 8; }
+
+template <int D>
+bool cache_map(CUtensorMap *m, const KvView &kv, const uint8_t *codes) {
+  const uint64_t rows = (uint64_t)kv.n_pages * kv.n_kv_heads * kKvBlock;
+  return encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, D, rows, D, D, kUnit,
+                              D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int D, int NT>
+cudaError_t run_stream(const CUtensorMap &tk, const CUtensorMap &tv, const StreamParams &p, cudaStream_t st) {
+  const int grid = p.warps / kWarps;
+  const size_t smem = StreamCfg<D, false>::kSmem;
+  const cudaError_t e =
+      p.a.softcap > 0.f ? launch_overlapped(kv8_stream_kernel<D, NT, true>, grid, kThreads, smem, st, tk, tv, p)
+                        : launch_overlapped(kv8_stream_kernel<D, NT, false>, grid, kThreads, smem, st, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  const dim3 join((unsigned)(p.a.kv.max_rows * (int64_t)p.group), p.a.kv.n_seqs, p.a.kv.n_kv_heads);
+  return launch_overlapped(kv8_join_kernel<D, NT>, join, D, 0, st, p);
+}
+
+// The sequences [s0, s0 + n) of a call.
+KvView slice(const KvView &kv, int s0, int n) {
+  KvView v = kv;
+  v.page_table += (int64_t)s0 * kv.max_pages;
+  v.kv_len += s0;
+  v.q_start += s0;
+  v.n_seqs = n;
+  return v;
+}
+
+int64_t part_rows(int64_t tile_rows, int num_sms) { return (int64_t)num_sms * kWarps * 2 * (narrow(tile_rows) ? 8 : 16); }
+
+template <int D>
+cudaError_t attention(const KvAttention &a, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  if (!cache_map<D>(&tk, a.kv, a.kv.k) || !cache_map<D>(&tv, a.kv, a.kv.v)) return cudaErrorInvalidValue;
+  StreamParams p;
+  p.a = a;
+  p.group = a.n_heads / a.kv.n_kv_heads;
+  p.warps = a.num_sms * kWarps;
+  const int64_t rows = (int64_t)a.kv.max_rows * p.group;
+  p.part_rows = part_rows(rows, a.num_sms);
+  p.part_o = static_cast<float *>(a.workspace);
+  p.part_ml = p.part_o + p.part_rows * D;
+  for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kMaxSeqs) {
+    p.a.kv = slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
+    const cudaError_t e = narrow(rows) ? run_stream<D, 1>(tk, tv, p, st) : run_stream<D, 2>(tk, tv, p, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int D>
+cudaError_t weigh(const KvAttention &a, cudaStream_t st) {
+  CUtensorMap tk;
+  if (!cache_map<D>(&tk, a.kv, a.kv.k)) return cudaErrorInvalidValue;
+  StreamParams p{};
+  p.a = a;
+  p.group = a.n_heads / a.kv.n_kv_heads;
+  p.warps = a.num_sms * kWarps;
+  const size_t smem = StreamCfg<D, true>::kSmem;
+  for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kMaxSeqs) {
+    p.a.kv = slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
+    const cudaError_t e = a.softcap > 0.f ? launch_overlapped(kv8_weigh_kernel<D, true>, a.num_sms, kThreads, smem, st, tk, p)
+                                          : launch_overlapped(kv8_weigh_kernel<D, false>, a.num_sms, kThreads, smem, st, tk, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int D>
+cudaError_t init_dim() {
+  cudaError_t e = cudaSuccess;
+  cudaFuncAttributes attr;
+  for (const void *f : {(const void *)kv8_stream_kernel<D, 1, false>, (const void *)kv8_stream_kernel<D, 1, true>,
+                        (const void *)kv8_stream_kernel<D, 2, false>, (const void *)kv8_stream_kernel<D, 2, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, false>::kSmem);
+  for (const void *f : {(const void *)kv8_weigh_kernel<D, false>, (const void *)kv8_weigh_kernel<D, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, true>::kSmem);
+  for (const void *f : {(const void *)kv8_join_kernel<D, 1>, (const void *)kv8_join_kernel<D, 2>})
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, f);
+  return e;
 }
 
 }  // namespace
 
-size_t kv8_attention_workspace_bytes(const exl3_kv8_cache &, const exl3_kv8_batch &, int, int) { return 16; }
-
-cudaError_t launch_kv8_attention(const KvAttention &p, cudaStream_t st) {
-  const int64_t warps = (int64_t)p.kv.rows * p.n_heads;
-  if (warps == 0 || p.kv.n_seqs == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)ceil_div(warps, 4);
-  if (p.kv.head_dim == 64) kv8_attention_kernel<64><<<grid, 128, 0, st>>>(p);
-  else kv8_attention_kernel<128><<<grid, 128, 0, st>>>(p);
-  return cudaGetLastError();
+size_t kv8_attention_workspace_bytes(const exl3_kv8_cache &c, const exl3_kv8_batch &b, int n_heads, int num_sms) {
+  if (b.rows == 0 || b.n_seqs == 0 || b.max_rows == 0) return 16;
+  return (size_t)part_rows((int64_t)b.max_rows * (n_heads / c.n_kv_heads), num_sms) * (c.head_dim + 2) * sizeof(float);
 }
 
-cudaError_t launch_kv8_weigh(const KvAttention &p, cudaStream_t st) {
-  if (p.kv.rows == 0 || p.kv.n_seqs == 0) return cudaSuccess;
-  const dim3 grid((unsigned)(p.kv.max_pages * (kKvBlock / 4)), p.kv.n_seqs, p.kv.n_kv_heads);
-  if (p.kv.head_dim == 64) kv8_weigh_kernel<64><<<grid, 128, 0, st>>>(p);
-  else kv8_weigh_kernel<128><<<grid, 128, 0, st>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_kv8_attention(const KvAttention &a, cudaStream_t st) {
+  if (a.kv.rows == 0 || a.kv.n_seqs == 0 || a.kv.max_rows == 0) return cudaSuccess;
+  return a.kv.head_dim == 64 ? attention<64>(a, st) : attention<128>(a, st);
+}
+
+cudaError_t launch_kv8_weigh(const KvAttention &a, cudaStream_t st) {
+  if (a.kv.rows == 0 || a.kv.n_seqs == 0 || a.kv.max_rows == 0) return cudaSuccess;
+  return a.kv.head_dim == 64 ? weigh<64>(a, st) : weigh<128>(a, st);
 }
 
 cudaError_t init_kv8_attention_kernels(int *status) {
   cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
-  cudaFuncAttributes a;
-  for (const void *f : {(const void *)kv8_attention_kernel<64>, (const void *)kv8_attention_kernel<128>,
-                        (const void *)kv8_weigh_kernel<64>, (const void *)kv8_weigh_kernel<128>})
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, f);
-  return e;
+  if (e == cudaSuccess) e = init_dim<64>();
+  return e == cudaSuccess ? init_dim<128>() : e;
 }
 
 #if EXL3_DEBUG_BOUNDS

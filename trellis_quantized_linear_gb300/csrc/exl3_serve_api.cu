@@ -17,7 +17,7 @@ bool aligned(const void *p, uintptr_t a) { return p != nullptr && (reinterpret_c
 exl3_status from_cuda(cudaError_t e) { return e == cudaSuccess ? EXL3_OK : EXL3_ERR_CUDA; }
 
 bool cache_shape_ok(const exl3_kv8_cache &c) {
-  return (c.head_dim == 64 || c.head_dim == 128) && c.n_kv_heads >= 1 && c.n_kv_heads <= 1024 && c.n_pages >= 0 &&
+  return (c.head_dim == 64 || c.head_dim == 128) && c.n_kv_heads >= 1 && c.n_kv_heads <= 1024 && c.n_pages >= 1 &&
          c.n_pages <= INT32_MAX && c.n_pages * c.n_kv_heads * EXL3_KV8_BLOCK <= INT32_MAX;
 }
 bool batch_shape_ok(const exl3_kv8_batch &b) {
