@@ -529,7 +529,7 @@ typedef struct {
  *          be the same buffer. Columns from n on are neither read nor written.
  *   argmax: M int32: the first index of the row's maximum (a NaN is never
  *          the maximum); -1 where no token is left (all -inf or NaN).
- *   1 <= n <= 2^19, 0 <= M <= 65535.
+ *   1 <= n <= 2^19, 0 <= M <= 65535; at most 2^29 history and 2^29 bias entries.
  */
 exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules *rules,
                                float *out, int64_t ldo, int32_t *argmax, void *stream);

@@ -3,6 +3,8 @@
 
 #include <stdint.h>
 
+#include <utility>
+
 #include "exl3_common.cuh"
 #include "exl3_serve.h"
 
@@ -98,6 +100,24 @@ __device__ __forceinline__ uint2 rescale_codes(uint2 c, float factor) {
 // of a score near the cap) would not give. exp overflows to inf: tanh is then 1.
 __device__ __forceinline__ float soft_cap(float s, float cap, float inv_cap) {
   return cap - cap * __fdividef(2.0f, 1.0f + exp2f(s * inv_cap * (2.0f * kLog2e)));
+}
+
+// A launch that may start while the kernel before it in the stream is ending.
+// The kernels wait (griddepcontrol.wait) before they touch memory, and read it
+// through ordinary loads: a read-only load could move above the wait.
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 }  // namespace exl3

@@ -216,7 +216,7 @@ __device__ __forceinline__ void load_query(const StreamParams &p, const Cursor &
 #pragma unroll
   for (int k = 0; k < D / 32; ++k)
     if (EXL3_SPAN(off + 8 * k, 8, (int64_t)(p.a.kv.rows - 1) * p.a.ldq + (int64_t)p.a.n_heads * D)) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q) + k);
+      const uint4 v = reinterpret_cast<const uint4 *>(q)[k];
       qf[4 * k] = v.x;
       qf[4 * k + 1] = v.y;
       qf[4 * k + 2] = v.z;
@@ -721,23 +721,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     ring.next();
     advance(kv, p.group, 0, prefix, c);
   }
-}
-
-// A launch that may start while the kernel before it in the stream is ending
-// (the kernels wait before they touch memory).
-template <typename... Params, typename... Args>
-cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args &&...args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // Up to 8 rows of a (sequence, head) in one tile: half the registers and

@@ -16,13 +16,15 @@ namespace {
 constexpr int kAppendThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(KvView kv, const __half *__restrict__ xk, int64_t ldk,
-                                                                    const __half *__restrict__ xv, int64_t ldv) {
+__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(KvView kv, const __half *xk, int64_t ldk,
+                                                                    const __half *xv, int64_t ldv) {
   constexpr int kVecs = D / 8;                       // 8-element pieces of a token
   constexpr int kTokens = kAppendThreads / kVecs;    // tokens per pass
   constexpr int kPasses = kKvBlock / kTokens;
   const int s = blockIdx.y, h = blockIdx.z >> 1;
   const bool is_k = (blockIdx.z & 1) == 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const KvSeq q = kv_sequence(kv, s);
   const int first = q.len - q.rows;                  // position of the first new token; < 0: the row has no place
   const int b = max(first, 0) / kKvBlock + (int)blockIdx.x;
@@ -47,7 +49,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(KvView kv, c
     if (pos >= first && pos < q.len) {
       const int64_t off = (int64_t)(q.row0 + pos - first) * ld + h * D + c * 8;
       if (EXL3_SPAN(off, 8, (int64_t)(kv.rows - 1) * ld + (int64_t)kv.n_kv_heads * D))
-        raw[i] = __ldg(reinterpret_cast<const uint4 *>(x + off));
+        raw[i] = *reinterpret_cast<const uint4 *>(x + off);
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -102,19 +104,26 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-__device__ __forceinline__ float token_weight(const KvView &kv, int s, int h, int pos) {
-  const int page = kv_page(kv, s, pos / kKvBlock);
-  return page < 0 ? 0.f : kv.weight[((int64_t)page * kv.n_kv_heads + h) * kKvBlock + pos % kKvBlock];
-}
+// One CTA per (sequence, head). The keys of the tokens to choose among are read
+// once into shared memory (those past what fits are read again from memory); a
+// radix selection, 11 bits a pass from the top, finds the key of the last token
+// that is kept, and each warp then writes the kept positions of one contiguous
+// part, ties to the lower positions. The first pass's bins hold the sign, the
+// exponent and two bits: few, so same-address adds dominate it.
+constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectKeys = 48 * 1024;  // held in shared memory
+constexpr int kBins = 2048;
+constexpr int kSelectSmem = (kSelectKeys + kBins) * 4;
 
-// One CTA per (sequence, head): a radix selection (8 bits a pass, from the top)
-// of the key of the last token that is kept, then one pass in position order
-// that writes the kept positions; ties take the lower positions.
-constexpr int kSelectThreads = 1024;
-
-__global__ void __launch_bounds__(kSelectThreads) kv8_select_kernel(KvView kv, int budget, int recent, int32_t *kept,
-                                                                    int32_t *new_len) {
-  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+__global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv, int budget, int recent, int32_t *kept,
+                                                                       int32_t *new_len) {
+  extern __shared__ __align__(16) uint32_t select_smem[];
+  uint32_t *keys = select_smem;
+  int *hist = reinterpret_cast<int *>(select_smem + kSelectKeys);
+  __shared__ int warp_count[kSelectWarps], warp_tie[kSelectWarps], s_bin, s_left;
+  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int len = kv_length(kv, s);
   const int keep = min(len, budget);
   if (h == 0 && tid == 0) new_len[s] = keep;
@@ -123,76 +132,115 @@ __global__ void __launch_bounds__(kSelectThreads) kv8_select_kernel(KvView kv, i
   const int early = len - min(recent, len);   // tokens that are kept by weight
   const int want = keep - (len - early);      // how many of them
   for (int i = early + tid; i < len; i += kSelectThreads) out[want + i - early] = i;
-
-  __shared__ int hist[256];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_left;
-  if (tid == 0) {
-    s_prefix = 0;
-    s_left = want;
+  if (want == 0) return;
+  if (want == early) {
+    for (int i = tid; i < early; i += kSelectThreads) out[i] = i;
+    return;
   }
-  if (want > 0 && want < early) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t prefix = s_prefix, above = shift == 24 ? 0u : ~0u << (shift + 8);
-      for (int i = tid; i < early; i += kSelectThreads) {
-        const uint32_t key = weight_key(token_weight(kv, s, h, i));
-        if ((key & above) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int left = s_left, d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        s_prefix = prefix | ((uint32_t)d << shift);
-        s_left = left;
-      }
-      __syncthreads();
+
+  auto read_key = [&](int i) {
+    const int page = kv_page(kv, s, i / kKvBlock);
+    return page < 0 ? 0u : weight_key(kv.weight[((int64_t)page * kv.n_kv_heads + h) * kKvBlock + i % kKvBlock]);
+  };
+  auto key_at = [&](int i) { return i < kSelectKeys ? keys[i] : read_key(i); };
+  const int held = min(early, kSelectKeys);
+  for (int i = tid; i < held; i += kSelectThreads * 4) {
+    uint32_t k[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * kSelectThreads < held) k[j] = read_key(i + j * kSelectThreads);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * kSelectThreads < held) keys[i + j * kSelectThreads] = k[j];
+  }
+
+  uint32_t threshold = 0;  // the bits of the threshold's key found so far
+  int left = want;         // tokens still to keep among those that share them
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u, above = pass == 0 ? 0u : ~0u << (shift + (pass == 2 ? 10 : 11));
+    hist[tid] = hist[tid + kSelectThreads] = 0;
+    __syncthreads();
+    for (int i = tid; i < early; i += kSelectThreads) {
+      const uint32_t key = key_at(i);
+      if ((key & above) == threshold) atomicAdd(&hist[(key >> shift) & mask], 1);
     }
+    __syncthreads();
+    // from the top: thread tid has bins 2047 - 2 tid and the one below
+    const int hi = kBins - 1 - 2 * tid, c1 = hist[hi], c0 = hist[hi - 1];
+    int sum = c1 + c0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    if (lane == 31) warp_count[warp] = sum;
+    __syncthreads();
+    int base = lane < warp ? warp_count[lane] : 0;
+    base = __reduce_add_sync(0xffffffffu, base);
+    const int before = base + sum - c1 - c0;  // tokens in the bins above
+    if (before < left && left <= before + c1) {
+      s_bin = hi;
+      s_left = left - before;
+    } else if (before + c1 < left && left <= before + c1 + c0) {
+      s_bin = hi - 1;
+      s_left = left - before - c1;
+    }
+    __syncthreads();
+    threshold |= (uint32_t)s_bin << shift;
+    left = s_left;
+  }
+
+  // `left` tokens of the threshold's key are kept, the first ones.
+  const int part = ((early + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+  const int i0 = min(warp * part, early), i1 = min(i0 + part, early);
+  int gt = 0, eq = 0;
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t key = key_at(i);
+    gt += key > threshold;
+    eq += key == threshold;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    warp_count[warp] = gt;
+    warp_tie[warp] = eq;
   }
   __syncthreads();
-  const uint32_t threshold = want >= early ? 0u : s_prefix;  // want >= early: all of them
-  int ties = want >= early ? INT_MAX : s_left;               // tokens of the threshold's key that are kept
-  if (want == 0) return;
-  __shared__ int warp_gt[kSelectThreads / 32], warp_eq[kSelectThreads / 32];
-  int done = 0;
-  for (int base = 0; base < early; base += kSelectThreads) {
-    const int i = base + tid;
-    const uint32_t key = i < early ? weight_key(token_weight(kv, s, h, i)) : 0u;
-    const bool gt = i < early && key > threshold, eq = i < early && key == threshold;
-    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-    const int w = tid >> 5;
-    if ((tid & 31) == 0) {
-      warp_gt[w] = __popc(mg);
-      warp_eq[w] = __popc(me);
-    }
-    __syncthreads();
-    int g = __popc(mg & ((1u << (tid & 31)) - 1)), e = __popc(me & ((1u << (tid & 31)) - 1)), tg = 0, te = 0;
-    for (int j = 0; j < kSelectThreads / 32; ++j) {
-      if (j < w) {
-        g += warp_gt[j];
-        e += warp_eq[j];
-      }
-      tg += warp_gt[j];
-      te += warp_eq[j];
-    }
-    __syncthreads();
-    if (gt || (eq && e < ties)) out[done + g + min(e, ties)] = i;
-    done += tg + min(te, ties);
-    ties -= min(te, ties);
+  int g = __reduce_add_sync(0xffffffffu, lane < warp ? warp_count[lane] : 0);
+  int e = __reduce_add_sync(0xffffffffu, lane < warp ? warp_tie[lane] : 0);
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const uint32_t key = i < i1 ? key_at(i) : 0u;
+    const bool is_gt = i < i1 && key > threshold, is_eq = i < i1 && key == threshold;
+    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
+    const uint32_t below = (1u << lane) - 1;
+    const int ties = e + __popc(me & below);
+    const int at = g + __popc(mg & below) + min(ties, left);
+    if ((is_gt || (is_eq && ties < left)) && EXL3_RANGE(at, 0, want)) out[at] = i;
+    g += __popc(mg);
+    e += __popc(me);
   }
 }
 
-// One CTA per (new block, sequence, head, keys or values): the block's scale is
-// the largest of its tokens' scales, so codes only ever shrink.
+// One CTA per (new block, sequence, head): its keys and values. The block's scale
+// is the largest of its tokens' scales, so codes only ever shrink. Bound by the
+// bytes moved; all of a thread's loads are in flight before its first store.
 constexpr int kMoveThreads = 256;
 
+__device__ __forceinline__ uint4 rescale_16(uint4 c, float factor) {
+  const uint2 a = rescale_codes(make_uint2(c.x, c.y), factor), b = rescale_codes(make_uint2(c.z, c.w), factor);
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) kv8_move_kernel(KvView kv, const int32_t *__restrict__ dst_pages,
-                                                                int dst_blocks, int budget,
-                                                                const int32_t *__restrict__ kept) {
-  const int b = blockIdx.x, s = blockIdx.y, h = blockIdx.z >> 1, tid = threadIdx.x;
-  const bool is_k = (blockIdx.z & 1) == 0;
+__global__ void __launch_bounds__(kMoveThreads) kv8_move_kernel(KvView kv, const int32_t *dst_pages,
+                                                                int dst_blocks, int budget, const int32_t *kept) {
+  const int b = blockIdx.x, s = blockIdx.y, h = blockIdx.z, tid = threadIdx.x;
+  __shared__ int64_t src[kKvBlock];  // slab * 64 + token, -1 where there is none
+  __shared__ int exps[2][kKvBlock], top[2][2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int len = kv_length(kv, s);
   const int n = min(min(len, budget) - b * kKvBlock, kKvBlock);
   if (n <= 0) return;
@@ -201,40 +249,51 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_move_kernel(KvView kv, const
     if (tid == 0) report_index(kv.status);
     return;
   }
-  uint8_t *codes = is_k ? kv.k : kv.v;
-  float *scales = is_k ? kv.k_scale : kv.v_scale;
-  __shared__ int64_t src[kKvBlock];  // slab * 64 + token, -1 where there is none
-  __shared__ int exps[kKvBlock], top[2];
+  const int64_t to = (int64_t)dst * kv.n_kv_heads + h;
   if (tid < kKvBlock) {
     int64_t at = -1;
-    int e = INT_MIN;
+    int ek = INT_MIN, ev = INT_MIN;
     if (tid < n) {
       const int pos = kept[((int64_t)s * kv.n_kv_heads + h) * budget + b * kKvBlock + tid];
       const int page = EXL3_RANGE(pos, 0, len) ? kv_page(kv, s, pos / kKvBlock) : -1;
       if (page >= 0) {
         const int64_t slab = (int64_t)page * kv.n_kv_heads + h;
         at = slab * kKvBlock + pos % kKvBlock;
-        e = pow2_exponent(scales[slab]);
+        ek = pow2_exponent(kv.k_scale[slab]);
+        ev = pow2_exponent(kv.v_scale[slab]);
+        kv.weight[to * kKvBlock + tid] = kv.weight[at];
       }
     }
     src[tid] = at;
-    exps[tid] = e;
-    const int m = __reduce_max_sync(0xffffffffu, e);
-    if ((tid & 31) == 0) top[tid >> 5] = m;
+    exps[0][tid] = ek;
+    exps[1][tid] = ev;
+    const int mk = __reduce_max_sync(0xffffffffu, ek), mv = __reduce_max_sync(0xffffffffu, ev);
+    if ((tid & 31) == 0) {
+      top[0][tid >> 5] = mk;
+      top[1][tid >> 5] = mv;
+    }
   }
   __syncthreads();
-  const int e = max(top[0], top[1]);
-  const int64_t to = (int64_t)dst * kv.n_kv_heads + h;
-  if (tid == 0 && e != INT_MIN) scales[to] = pow2i(e);
-  constexpr int kVecs = D / 8;
+  constexpr int kVecs = D / 16, kPasses = kKvBlock * kVecs / kMoveThreads;
+  uint4 v[2][kPasses];
 #pragma unroll
-  for (int i = tid; i < kKvBlock * kVecs; i += kMoveThreads) {
-    const int t = i / kVecs, c = i % kVecs;
-    if (src[t] < 0) continue;
-    uint2 v = __ldg(reinterpret_cast<const uint2 *>(codes + src[t] * D) + c);
-    if (exps[t] != e) v = rescale_codes(v, pow2i(max(exps[t] - e, -126)));
-    reinterpret_cast<uint2 *>(codes + (to * kKvBlock + t) * D)[c] = v;
-    if (is_k && c == 0) kv.weight[to * kKvBlock + t] = kv.weight[src[t]];
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t at = src[(i * kMoveThreads + tid) / kVecs];
+      if (at >= 0) v[x][i] = reinterpret_cast<const uint4 *>((x ? kv.v : kv.k) + at * D)[tid % kVecs];
+    }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int e = max(top[x][0], top[x][1]);
+    if (tid == 0 && e != INT_MIN) (x ? kv.v_scale : kv.k_scale)[to] = pow2i(e);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int t = (i * kMoveThreads + tid) / kVecs;
+      if (src[t] < 0) continue;
+      if (exps[x][t] != e) v[x][i] = rescale_16(v[x][i], pow2i(max(exps[x][t] - e, -126)));
+      reinterpret_cast<uint4 *>((x ? kv.v : kv.k) + (to * kKvBlock + t) * D)[tid % kVecs] = v[x][i];
+    }
   }
 }
 
@@ -245,29 +304,29 @@ cudaError_t launch_kv8_append(const KvView &kv, const void *k, int64_t ldk, cons
   // the most blocks that max_rows consecutive tokens touch
   const dim3 grid((unsigned)((kv.max_rows + (int64_t)2 * kKvBlock - 2) / kKvBlock), kv.n_seqs, 2 * kv.n_kv_heads);
   const __half *xk = static_cast<const __half *>(k), *xv = static_cast<const __half *>(v);
-  if (kv.head_dim == 64) kv8_append_kernel<64><<<grid, kAppendThreads, 0, st>>>(kv, xk, ldk, xv, ldv);
-  else kv8_append_kernel<128><<<grid, kAppendThreads, 0, st>>>(kv, xk, ldk, xv, ldv);
-  return cudaGetLastError();
+  return launch_overlapped(kv.head_dim == 64 ? kv8_append_kernel<64> : kv8_append_kernel<128>, grid, kAppendThreads, 0, st, kv,
+                           xk, ldk, xv, ldv);
 }
 
 cudaError_t launch_kv8_evict(const KvView &kv, const int32_t *dst_pages, int budget, int recent, int32_t *kept,
                              int32_t *new_len, cudaStream_t st) {
   if (kv.n_seqs == 0) return cudaSuccess;
-  kv8_select_kernel<<<dim3(kv.n_kv_heads, kv.n_seqs), kSelectThreads, 0, st>>>(kv, budget, recent, kept, new_len);
+  cudaError_t e = launch_overlapped(kv8_select_kernel, dim3(kv.n_kv_heads, kv.n_seqs), kSelectThreads, kSelectSmem, st, kv,
+                                    budget, recent, kept, new_len);
+  if (e != cudaSuccess) return e;
   const int blocks = (int)(((int64_t)budget + kKvBlock - 1) / kKvBlock);
-  const dim3 grid(blocks, kv.n_seqs, 2 * kv.n_kv_heads);
-  if (kv.head_dim == 64) kv8_move_kernel<64><<<grid, kMoveThreads, 0, st>>>(kv, dst_pages, blocks, budget, kept);
-  else kv8_move_kernel<128><<<grid, kMoveThreads, 0, st>>>(kv, dst_pages, blocks, budget, kept);
-  return cudaGetLastError();
+  const dim3 grid(blocks, kv.n_seqs, kv.n_kv_heads);
+  return launch_overlapped(kv.head_dim == 64 ? kv8_move_kernel<64> : kv8_move_kernel<128>, grid, kMoveThreads, 0, st, kv,
+                           dst_pages, blocks, budget, kept);
 }
 
 cudaError_t init_kv8_cache_kernels(int *status) {
   cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
   cudaFuncAttributes a;
   for (const void *f : {(const void *)kv8_append_kernel<64>, (const void *)kv8_append_kernel<128>,
-                        (const void *)kv8_select_kernel, (const void *)kv8_move_kernel<64>,
-                        (const void *)kv8_move_kernel<128>})
+                        (const void *)kv8_move_kernel<64>, (const void *)kv8_move_kernel<128>})
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, f);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
   return e;
 }
 

@@ -144,7 +144,7 @@ exl3_status exl3_kv8_evict(const exl3_kv8_cache *cache, const exl3_kv8_batch *ba
 exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules *rules,
                                float *out, int64_t ldo, int32_t *argmax, void *stream) {
   if (!rules || M < 0 || M > 65535 || n < 1 || n > (1 << 19) || ldl < n || ldl % 4 || ldo < n || ldo % 4 ||
-      rules->history_size < 0 || rules->bias_size < 0)
+      rules->history_size < 0 || rules->history_size > (1 << 29) || rules->bias_size < 0 || rules->bias_size > (1 << 29))
     return EXL3_ERR_INVALID_ARG;
   const exl3_logits_rules &r = *rules;
   // parts of a rule go together
