@@ -132,6 +132,8 @@ def _require_f32_contiguous(where, *tensors):
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compiles the library this process loads (libexl3.so, or libexl3_bounds.so
     under EXL3_BOUNDS_CHECKED=1) for sm_103a with nvcc (in-tree)."""
+    if _lib is not None and not force:
+        return LIB_PATH  # this process has loaded it
     from . import _build
     return _build.build(force=force, verbose=verbose, bounds_checked=BOUNDS_CHECKED)
 
@@ -139,6 +141,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 def load():
     """Loads the library (LIB_PATH); raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -214,10 +218,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            # the raw handle of torch's current stream: torch.cuda.current_stream() builds an object
+            # for it at every call, which takes longer than a launch
+            get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+            if get is None or device is None:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+            else:
+                _current_stream = lambda: get(device())  # noqa: E731
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

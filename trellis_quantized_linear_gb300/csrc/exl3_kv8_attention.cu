@@ -6,9 +6,10 @@
 // warp of a persistent grid takes one equal, contiguous range of them, whatever
 // the sequences' lengths are (they are read on the device). A warp keeps its own
 // ring of TMA copies in flight and its own running maximum, sum and output, so
-// warps never wait for one another. Where a range ends inside a segment, the
-// warp leaves its partial result in the workspace and a second kernel joins the
-// partials in the order of the warps.
+// warps do not wait for one another. Where ranges end inside a segment, the
+// partial results are joined in the order of the ranges: those of a CTA's warps
+// through shared memory when the CTA is done, those of several CTAs through the
+// workspace by a second kernel.
 //
 // The bound is the cache stream: D + D bytes a token and head. The tensor core's
 // narrow side takes the rows (S^T = K Q^T and O^T = V^T P^T, m16n8k16): 8 rows
@@ -46,10 +47,15 @@ struct StreamCfg {
 struct StreamParams {
   KvAttention a;
   int group;      // query heads of a key/value head
-  float *part_o;  // warps x 2 x tile rows x D
-  float *part_ml; // warps x 2 x tile rows x 2 (maximum in log2 units, sum)
-  int warps;      // of the stream grid
-  int64_t part_rows;  // 2 * warps * tile rows
+  // Workspace: partial results of the CTAs (slot 0: a segment that began before
+  // the CTA's range, slot 1: one that began in it and goes on after it), and the
+  // plan for the join.
+  float *part_o;      // CTAs x 2 x tile rows x D
+  float *part_ml;     // CTAs x 2 x tile rows x 2 (maximum in log2 units, sum)
+  float *first;       // warps x tile rows x (D + 2): see Parts
+  int64_t *plan;      // prefix of build_plan
+  int warps;          // of the stream grid
+  int64_t part_rows;  // 2 * CTAs * tile rows
 };
 
 __device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
@@ -447,14 +453,34 @@ __device__ __forceinline__ void store_out(const KvAttention &a, int64_t row, int
   }
 }
 
-// The end of a warp's part of a segment: the result where the part is the whole
-// segment, else a partial (slot 0: the segment began before this warp's range,
-// slot 1: it began in it).
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
+
+// Parts of segments that a CTA's warps do not cover alone, two a warp: 2 w, the
+// end of a segment that began before the warp's range (in the workspace), and
+// 2 w + 1, its last segment (in shared memory, the ring's).
+struct Part {
+  int s, h, rt;  // the segment; s < 0: no part
+  int begins, ends;
+};
 template <int D, int NT>
-__device__ __forceinline__ void finish_part(const StreamParams &p, const Cursor &c, bool whole, int64_t slot, int lane,
-                                            RowState<D, NT> &st) {
-  const int g = lane >> 2, t = lane & 3;
-  const float unit = pow2i(st.ev);
+struct Parts {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kFloats = kRows * (D + 2);  // output, then (maximum, sum) of each row
+  static constexpr int kHeads = kWarps * kFloats * 4;
+  static_assert(kHeads + 2 * kWarps * (int)sizeof(Part) <= StreamCfg<D, false>::kRing, "parts fit the ring");
+  uint8_t *smem;
+  float *first;  // workspace: CTAs x warps x kFloats
+  __device__ __forceinline__ float *o(int i) const {
+    return i & 1 ? reinterpret_cast<float *>(smem) + (i >> 1) * kFloats
+                 : first + ((int64_t)blockIdx.x * kWarps + (i >> 1)) * kFloats;
+  }
+  __device__ __forceinline__ float2 *ml(int i) const { return reinterpret_cast<float2 *>(o(i) + kRows * D); }
+  __device__ __forceinline__ Part *head(int i) const { return reinterpret_cast<Part *>(smem + kHeads) + i; }
+};
+
+// The sum of each row over the lanes that share it.
+template <int D, int NT>
+__device__ __forceinline__ void close_rows(RowState<D, NT> &st) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -463,29 +489,104 @@ __device__ __forceinline__ void finish_part(const StreamParams &p, const Cursor 
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
-      const int jt = 8 * n + 2 * t + col, j = c.rt * 8 * NT + jt, i = j / p.group;
+      st.l[n][col] = l;
+    }
+}
+
+// The result of a segment that one warp worked on alone.
+template <int D, int NT>
+__device__ __forceinline__ void write_rows(const StreamParams &p, const Cursor &c, int lane, const RowState<D, NT> &st) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int col = 0; col < 2; ++col) {
+      const float l = st.l[n][col], f = l == 0.f ? 0.f : pow2i(st.ev) / l;
+      const int j = c.rt * 8 * NT + 8 * n + 2 * t + col, i = j / p.group;
+      if (i >= c.q.rows) continue;
       float v[D / 8];
-      const float f = whole ? (l == 0.f ? 0.f : unit / l) : unit;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         v[2 * k] = st.o[n][k][col] * f;
         v[2 * k + 1] = st.o[n][k][2 + col] * f;
       }
-      if (i >= c.q.rows) continue;
       const int head = c.h * p.group + j - i * p.group;
-      if (whole) {
-        store_out<D>(p.a, c.q.row0 + i, head, g * (D / 8), v);
-        if (p.a.lse && g == 0)
-          p.a.lse[(int64_t)(c.q.row0 + i) * p.a.n_heads + head] = l == 0.f ? -INFINITY : (st.m[n][col] + __log2f(l)) * kLn2;
-      } else {
-        const int64_t at = slot * 8 * NT + jt;
-        if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
-        float4 *o = reinterpret_cast<float4 *>(p.part_o + at * D + g * (D / 8));
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) o[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        if (g == 0) reinterpret_cast<float2 *>(p.part_ml)[at] = make_float2(st.m[n][col], l);
-      }
+      store_out<D>(p.a, c.q.row0 + i, head, g * (D / 8), v);
+      if (p.a.lse && g == 0) p.a.lse[(int64_t)(c.q.row0 + i) * p.a.n_heads + head] = log_sum(st.m[n][col], l);
     }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void keep_part(float *part_o, float2 *part_ml, int lane, const RowState<D, NT> &st) {
+  const int g = lane >> 2, t = lane & 3;
+  const float unit = pow2i(st.ev);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int col = 0; col < 2; ++col) {
+      const int r = 8 * n + 2 * t + col;
+      float4 *o = reinterpret_cast<float4 *>(part_o + r * D + g * (D / 8));
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+        o[k] = make_float4(st.o[n][2 * k][col] * unit, st.o[n][2 * k][2 + col] * unit, st.o[n][2 * k + 1][col] * unit,
+                           st.o[n][2 * k + 1][2 + col] * unit);
+      if (g == 0) part_ml[r] = make_float2(st.m[n][col], st.l[n][col]);
+    }
+}
+
+// Joins the CTA's parts, in order. Every thread has four columns of some rows.
+template <int D, int NT>
+__device__ __forceinline__ void join_cta(const StreamParams &p, const Parts<D, NT> &parts) {
+  using P = Parts<D, NT>;
+  constexpr int kPerRow = D / 4, kStep = kThreads / kPerRow;  // threads of a row, rows at a time
+  const int d0 = threadIdx.x % kPerRow * 4;
+  for (int r = threadIdx.x / kPerRow; r < P::kRows; r += kStep) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool begins = false;
+    for (int i = 0; i < 2 * kWarps; ++i) {
+      const Part part = *parts.head(i);
+      if (part.s < 0) continue;
+      const float2 ml = parts.ml(i)[r];
+      const float4 x = *reinterpret_cast<const float4 *>(parts.o(i) + r * D + d0);
+      const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+      const float a = ex2(m - ref), b = ex2(ml.x - ref);
+      m = top;
+      l = l * a + ml.y * b;
+      o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
+      begins = begins || part.begins;
+      bool last = part.ends;  // the segment's last part in this CTA: it ends, or no other part follows
+      if (!last) {
+        last = true;
+        for (int k = i + 1; k < 2 * kWarps; ++k) last = last && parts.head(k)->s < 0;
+      }
+      if (!last) continue;
+      const KvSeq q = kv_sequence(p.a.kv, part.s);
+      const int j = part.rt * P::kRows + r, row = j / p.group;
+      if (row < q.rows) {
+        if (begins && part.ends) {
+          const int head = part.h * p.group + j - row * p.group;
+          const int64_t off = (int64_t)(q.row0 + row) * p.a.ldo + (int64_t)head * D + d0;
+          const float f = l == 0.f ? 0.f : 1.0f / l;
+          const __half2 lo = __floats2half2_rn(o.x * f, o.y * f), hi = __floats2half2_rn(o.z * f, o.w * f);
+          if (EXL3_SPAN(off, 4, (int64_t)(p.a.kv.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D))
+            *reinterpret_cast<uint2 *>(static_cast<__half *>(p.a.out) + off) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+          if (p.a.lse && d0 == 0) p.a.lse[(int64_t)(q.row0 + row) * p.a.n_heads + head] = log_sum(m, l);
+        } else {
+          const int64_t at = (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * P::kRows + r;
+          if (EXL3_SPAN(at, 1, p.part_rows)) {
+            *reinterpret_cast<float4 *>(p.part_o + at * D + d0) = o;
+            if (d0 == 0) reinterpret_cast<float2 *>(p.part_ml)[at] = make_float2(m, l);
+          }
+        }
+      }
+      m = -INFINITY;
+      l = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      begins = false;
+    }
+  }
 }
 
 template <int D, int NT, bool CAP>
@@ -510,89 +611,107 @@ __global__ void __launch_bounds__(kThreads, 1)
   build_plan(kv, p.group, tile, prefix);
   const int64_t T = prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
-  if (w >= W) return;
-  int64_t z = range_start(w, W, T), zp = z;
-  const int64_t z1 = range_start(w + 1, W, T);
-  Cursor c = locate(kv, p.group, tile, prefix, z), cp = c;
-  Blocks ahead, now;
-  const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
-
-  uint32_t qf[NT][D / 8];
-  int limit[NT][2], min_limit = 0;  // tokens that this lane's rows see, and the tile's first row
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= kv.n_seqs; i += kThreads) p.plan[i] = prefix[i];
+  if ((int64_t)blockIdx.x * kWarps >= W) return;
+  const Parts<D, NT> parts{smem, p.first};
+  Part first{-1}, last{-1};  // this warp's parts of segments that it does not cover
   RowState<D, NT> st;
-  bool fresh = true, began = false;
-  for (; z < z1; ++z) {
-    while (zp < z1 && ring.in_flight < Cfg::kStages) {
-      if (!ahead.holds(cp)) ahead.load<false>(kv, cp, lane);
-      ring.issue(&tk, &tv, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
-      ++zp;
-      advance(kv, p.group, tile, prefix, cp);
-    }
-    if (!now.holds(c)) {
-      if (ahead.holds(c)) now = ahead;
-      else now.load<false>(kv, c, lane);
-    }
-    const int at = (c.u >> 1) - now.base;
-    const int page = __shfl_sync(0xffffffffu, now.page, at);
-    const float ks = __shfl_sync(0xffffffffu, now.ks, at), vs = __shfl_sync(0xffffffffu, now.vs, at);
-    if (fresh) {
-      fresh = false;
-      began = c.u == 0;
-      st.clear();
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        load_query<D>(p, c, c.rt * tile + 8 * n + (lane >> 2), lane, qf[n]);
-        limit[n][0] = row_limit(p, c, c.rt * tile + 8 * n + 2 * (lane & 3));
-        limit[n][1] = row_limit(p, c, c.rt * tile + 8 * n + 2 * (lane & 3) + 1);
+  if (w < W) {
+    int64_t z = range_start(w, W, T), zp = z;
+    const int64_t z1 = range_start(w + 1, W, T);
+    Cursor c = locate(kv, p.group, tile, prefix, z), cp = c;
+    Blocks ahead, now;
+    const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
+    uint32_t qf[NT][D / 8];
+    int limit[NT][2], min_limit = 0;  // tokens that this lane's rows see, and the tile's first row
+    bool fresh = true, began = false;
+    for (; z < z1; ++z) {
+      while (zp < z1 && ring.in_flight < Cfg::kStages) {
+        if (!ahead.holds(cp)) ahead.load<false>(kv, cp, lane);
+        ring.issue(&tk, &tv, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
+        ++zp;
+        advance(kv, p.group, tile, prefix, cp);
       }
-      min_limit = row_limit(p, c, c.rt * tile);  // rows come in order: the first sees the least
+      if (!now.holds(c)) {
+        if (ahead.holds(c)) now = ahead;
+        else now.load<false>(kv, c, lane);
+      }
+      const int at = (c.u >> 1) - now.base;
+      const int page = __shfl_sync(0xffffffffu, now.page, at);
+      const float ks = __shfl_sync(0xffffffffu, now.ks, at), vs = __shfl_sync(0xffffffffu, now.vs, at);
+      if (fresh) {
+        fresh = false;
+        began = c.u == 0;
+        st.clear();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          load_query<D>(p, c, c.rt * tile + 8 * n + (lane >> 2), lane, qf[n]);
+          limit[n][0] = row_limit(p, c, c.rt * tile + 8 * n + 2 * (lane & 3));
+          limit[n][1] = row_limit(p, c, c.rt * tile + 8 * n + 2 * (lane & 3) + 1);
+        }
+        min_limit = row_limit(p, c, c.rt * tile);  // rows come in order: the first sees the least
+      }
+      if (!ring.wait(kv.status)) {
+        ring.drain();  // the call's outputs are undefined: the error word says so
+        break;
+      }
+      if (page >= 0)
+        attend_unit<D, NT, CAP>(p, ring.stage(), c.u * kUnit, c.q.len, ks, vs, qf, limit, min_limit, inv_cap, lane, st);
+      __syncwarp();  // every lane is done with the stage before it is filled again
+      ring.next();
+      const bool end = c.u + 1 == c.units;
+      if (end || z + 1 == z1) {
+        close_rows<D, NT>(st);
+        if (end && began) {
+          write_rows<D, NT>(p, c, lane, st);
+        } else if (z + 1 == z1) {
+          last = Part{c.s, c.h, c.rt, began, end};
+          break;  // kept in registers
+        } else {
+          // the end of a segment that began before this range: the first part of
+          // a range only, and the ring is in use, so it goes to the workspace
+          first = Part{c.s, c.h, c.rt, false, true};
+          keep_part<D, NT>(parts.o(2 * warp), parts.ml(2 * warp), lane, st);
+        }
+        fresh = true;
+      }
+      advance(kv, p.group, tile, prefix, c);
     }
-    if (!ring.wait(kv.status)) {
-      ring.drain();
-      return;
-    }
-    if (page >= 0)
-      attend_unit<D, NT, CAP>(p, ring.stage(), c.u * kUnit, c.q.len, ks, vs, qf, limit, min_limit, inv_cap, lane, st);
-    __syncwarp();  // every lane is done with the stage before it is filled again
-    ring.next();
-    const bool end = c.u + 1 == c.units;
-    if (end || z + 1 == z1) {
-      finish_part<D, NT>(p, c, began && end, 2 * w + (began ? 1 : 0), lane, st);
-      fresh = true;
-    }
-    advance(kv, p.group, tile, prefix, c);
   }
+  __syncthreads();  // no warp uses its ring any more
+  if (lane == 0) {
+    *parts.head(2 * warp) = first;
+    *parts.head(2 * warp + 1) = last;
+  }
+  if (last.s >= 0) keep_part<D, NT>(parts.o(2 * warp + 1), parts.ml(2 * warp + 1), lane, st);
+  __syncthreads();
+  join_cta<D, NT>(p, parts);
 }
 
-// Joins the partials of the segments that several warps worked on, in the order
-// of the warps, and writes the rows of segments without tokens. One CTA of D
-// threads per (sequence, key/value head, row tile) and row of the tile.
+// Joins the partials of the segments that several CTAs worked on, in the order of
+// the CTAs, and writes the rows of segments without tokens. One CTA of D threads
+// per (row of a group, sequence, key/value head).
 template <int D, int NT>
 __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
-  __shared__ int64_t prefix[kMaxSeqs + 1 + kWarps];
   const KvView &kv = p.a.kv;
   constexpr int tile = 8 * NT;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  Cursor c;
-  c.s = blockIdx.y;
-  c.h = blockIdx.z;
-  c.rt = blockIdx.x / tile;
-  enter_sequence(kv, p.group, tile, c);
-  const int j = blockIdx.x, i = j / p.group;
-  build_plan(kv, p.group, tile, prefix);
-  if (i >= c.q.rows) return;
-  const int head = c.h * p.group + j - i * p.group;
-  const int64_t row = c.q.row0 + i;
-  __half *out = static_cast<__half *>(p.a.out) + row * p.a.ldo + (int64_t)head * D + threadIdx.x;
+  const int s = blockIdx.y, h = blockIdx.z, j = blockIdx.x, i = j / p.group;
+  const int64_t z0 = p.plan[s], units_s = p.plan[s + 1] - z0, T = p.plan[kv.n_seqs], W = min((int64_t)p.warps, T);
+  const KvSeq q = kv_sequence(kv, s);
+  if (i >= q.rows) return;
+  const int head = h * p.group + j - i * p.group;
   float m = -INFINITY, l = 0.f, o = 0.f;
-  if (c.units > 0) {
-    const int64_t T = prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
-    const int64_t z = prefix[c.s] + ((int64_t)c.h * c.tiles + c.rt) * c.units;
-    const int64_t w0 = range_owner(z, W, T), w1 = range_owner(z + c.units - 1, W, T);
-    if (w0 == w1) return;  // the warp wrote the result
-    for (int64_t w = w0; w <= w1; ++w) {
-      const int64_t at = (2 * w + (w == w0 ? 1 : 0)) * tile + j % tile;
+  if (units_s > 0) {
+    const int tiles = (q.rows * p.group + tile - 1) / tile, units = units_of(q.len);
+    const int64_t z = z0 + ((int64_t)h * tiles + j / tile) * units;
+    const int64_t c0 = range_owner(z, W, T) / kWarps, c1 = range_owner(z + units - 1, W, T) / kWarps;
+    if (c0 == c1) return;  // the CTA wrote the result
+#pragma unroll 4
+    for (int64_t c = c0; c <= c1; ++c) {
+      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * tile + j % tile;
       if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
       const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
       const float x = p.part_o[at * D + threadIdx.x];
@@ -603,8 +722,10 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
       m = top;
     }
   }
-  *out = __float2half_rn(l == 0.f ? 0.f : o / l);
-  if (p.a.lse && threadIdx.x == 0) p.a.lse[row * p.a.n_heads + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+  const int64_t row = q.row0 + i, off = row * p.a.ldo + (int64_t)head * D + threadIdx.x;
+  if (EXL3_SPAN(off, 1, (int64_t)(kv.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D))
+    static_cast<__half *>(p.a.out)[off] = __float2half_rn(l == 0.f ? 0.f : o / l);
+  if (p.a.lse && threadIdx.x == 0) p.a.lse[row * p.a.n_heads + head] = log_sum(m, l);
 }
 
 // Accumulated weight: the same stream over the keys alone; a unit's weights are
@@ -714,7 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           x += __shfl_xor_sync(0xffffffffu, x, 2);
           const int tok = 16 * mi + g + 8 * r;
           const int64_t off = slab * kKvBlock + (c.u & 1) * kUnit + tok;
-          if (t == 0 && pos0 + tok < c.q.len && EXL3_SPAN(off, 1, kv.n_pages * kv.n_kv_heads * kKvBlock)) kv.weight[off] += x;
+          if (t == 0 && pos0 + tok < c.q.len && EXL3_SPAN(off, 1, kv.n_pages * kv.n_kv_heads * kKvBlock))
+            atomicAdd(&kv.weight[off], x);  // the only add to this token in the call: without a wait for the old value
         }
     }
     __syncwarp();
@@ -756,7 +878,20 @@ KvView slice(const KvView &kv, int s0, int n) {
   return v;
 }
 
-int64_t part_rows(int64_t tile_rows, int num_sms) { return (int64_t)num_sms * kWarps * 2 * (narrow(tile_rows) ? 8 : 16); }
+// Floats of the workspace's parts, in the order of StreamParams; the plan first.
+struct StreamWorkspace {
+  int64_t part_rows, o, ml, first, total;
+};
+StreamWorkspace stream_workspace(int64_t rows, int D, int num_sms) {
+  StreamWorkspace w;
+  const int64_t tile = narrow(rows) ? 8 : 16;
+  w.part_rows = num_sms * 2 * tile;
+  w.o = 2 * (kMaxSeqs + 8);  // the plan's int64
+  w.ml = w.o + w.part_rows * D;
+  w.first = w.ml + w.part_rows * 2;
+  w.total = w.first + (int64_t)num_sms * kWarps * tile * (D + 2);
+  return w;
+}
 
 template <int D>
 cudaError_t attention(const KvAttention &a, cudaStream_t st) {
@@ -767,9 +902,13 @@ cudaError_t attention(const KvAttention &a, cudaStream_t st) {
   p.group = a.n_heads / a.kv.n_kv_heads;
   p.warps = a.num_sms * kWarps;
   const int64_t rows = (int64_t)a.kv.max_rows * p.group;
-  p.part_rows = part_rows(rows, a.num_sms);
-  p.part_o = static_cast<float *>(a.workspace);
-  p.part_ml = p.part_o + p.part_rows * D;
+  const StreamWorkspace w = stream_workspace(rows, D, a.num_sms);
+  float *ws = static_cast<float *>(a.workspace);
+  p.part_rows = w.part_rows;
+  p.plan = reinterpret_cast<int64_t *>(ws);
+  p.part_o = ws + w.o;
+  p.part_ml = ws + w.ml;
+  p.first = ws + w.first;
   for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kMaxSeqs) {
     p.a.kv = slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
     const cudaError_t e = narrow(rows) ? run_stream<D, 1>(tk, tv, p, st) : run_stream<D, 2>(tk, tv, p, st);
@@ -814,7 +953,7 @@ cudaError_t init_dim() {
 
 size_t kv8_attention_workspace_bytes(const exl3_kv8_cache &c, const exl3_kv8_batch &b, int n_heads, int num_sms) {
   if (b.rows == 0 || b.n_seqs == 0 || b.max_rows == 0) return 16;
-  return (size_t)part_rows((int64_t)b.max_rows * (n_heads / c.n_kv_heads), num_sms) * (c.head_dim + 2) * sizeof(float);
+  return (size_t)stream_workspace((int64_t)b.max_rows * (n_heads / c.n_kv_heads), c.head_dim, num_sms).total * sizeof(float);
 }
 
 cudaError_t launch_kv8_attention(const KvAttention &a, cudaStream_t st) {

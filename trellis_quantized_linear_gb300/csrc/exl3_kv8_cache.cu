@@ -109,11 +109,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // radix selection, 11 bits a pass from the top, finds the key of the last token
 // that is kept, and each warp then writes the kept positions of one contiguous
 // part, ties to the lower positions. The first pass's bins hold the sign, the
-// exponent and two bits: few, so same-address adds dominate it.
+// exponent and two bits: weights fill few of them, so each bin has eight copies,
+// one for every eighth lane.
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectKeys = 48 * 1024;  // held in shared memory
-constexpr int kBins = 2048;
-constexpr int kSelectSmem = (kSelectKeys + kBins) * 4;
+constexpr int kSelectKeys = 38 * 1024;  // held in shared memory
+constexpr int kBins = 2048, kCopies = 8;
+constexpr int kSelectSmem = (kSelectKeys + kBins * kCopies) * 4;
 
 __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv, int budget, int recent, int32_t *kept,
                                                                        int32_t *new_len) {
@@ -144,13 +145,13 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv
   };
   auto key_at = [&](int i) { return i < kSelectKeys ? keys[i] : read_key(i); };
   const int held = min(early, kSelectKeys);
-  for (int i = tid; i < held; i += kSelectThreads * 4) {
-    uint32_t k[4];
+  for (int i = tid; i < held; i += kSelectThreads * 8) {
+    uint32_t k[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
       if (i + j * kSelectThreads < held) k[j] = read_key(i + j * kSelectThreads);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
       if (i + j * kSelectThreads < held) keys[i + j * kSelectThreads] = k[j];
   }
 
@@ -160,15 +161,20 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t mask = pass == 2 ? 1023u : 2047u, above = pass == 0 ? 0u : ~0u << (shift + (pass == 2 ? 10 : 11));
-    hist[tid] = hist[tid + kSelectThreads] = 0;
+    for (int i = tid; i < kBins * kCopies / 4; i += kSelectThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
     for (int i = tid; i < early; i += kSelectThreads) {
       const uint32_t key = key_at(i);
-      if ((key & above) == threshold) atomicAdd(&hist[(key >> shift) & mask], 1);
+      if ((key & above) == threshold) atomicAdd(&hist[((key >> shift) & mask) * kCopies + lane % kCopies], 1);
     }
     __syncthreads();
     // from the top: thread tid has bins 2047 - 2 tid and the one below
-    const int hi = kBins - 1 - 2 * tid, c1 = hist[hi], c0 = hist[hi - 1];
+    const int hi = kBins - 1 - 2 * tid;
+    auto bin = [&](int b) {
+      const int4 x = reinterpret_cast<const int4 *>(hist)[2 * b], y = reinterpret_cast<const int4 *>(hist)[2 * b + 1];
+      return x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
+    };
+    const int c1 = bin(hi), c0 = bin(hi - 1);
     int sum = c1 + c0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {

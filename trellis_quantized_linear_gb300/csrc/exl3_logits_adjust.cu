@@ -18,7 +18,6 @@ namespace exl3 {
 
 namespace {
 
-constexpr int kAdjustThreads = 512;
 constexpr int kAdjustVecs = 8;   // 4-token pieces that a thread holds at a time
 constexpr int kMaxCluster = 16;
 // A token's word: in the history at all, has a bias, times generated.
@@ -75,7 +74,8 @@ struct Best {
   }
 };
 
-__global__ void __launch_bounds__(kAdjustThreads) logits_adjust_kernel(const AdjustParams p) {
+template <int kAdjustThreads>
+__global__ void __launch_bounds__(kAdjustThreads, 768 / kAdjustThreads) logits_adjust_kernel(const AdjustParams p) {
   extern __shared__ __align__(16) uint32_t words[];  // one of each token of the range
   __shared__ float sb[kAdjustThreads / 32], cb[kMaxCluster];
   __shared__ int si[kAdjustThreads / 32], ci[kMaxCluster], duplicates;
@@ -221,15 +221,19 @@ __global__ void __launch_bounds__(kAdjustThreads) logits_adjust_kernel(const Adj
 }  // namespace
 
 cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules &r,
-                                 float *out, int64_t ldo, int32_t *argmax, int *status, cudaStream_t st) {
+                                 float *out, int64_t ldo, int32_t *argmax, int *status, int num_sms, cudaStream_t st) {
   if (M == 0) return cudaSuccess;
   // 2048 tokens (one piece a thread) to a CTA at least, up to 16 CTAs
   int ranks = 1;
   while (ranks < kMaxCluster && n > (int64_t)ranks * 2048) ranks *= 2;
   AdjustParams p{logits, out, argmax, status, ldl, ldo, M, (int)n, (int)(ceil_div(n, 128 * ranks) * 128), r};
+  // Few rows: every CTA has an SM to itself and 512 threads hold its whole range;
+  // many rows: three CTAs of 256 threads an SM, so that one streams while another counts.
+  const bool few = M * ranks <= num_sms;
+  const auto kernel = few ? logits_adjust_kernel<512> : logits_adjust_kernel<256>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(M * ranks));
-  cfg.blockDim = dim3(kAdjustThreads);
+  cfg.blockDim = dim3(few ? 512 : 256);
   cfg.dynamicSmemBytes = (size_t)p.range * 4;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -240,15 +244,16 @@ cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, in
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logits_adjust_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 cudaError_t init_logits_adjust_kernels(int *status) {
   cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
-  // the widest range: 2^19 tokens over 16 CTAs
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(logits_adjust_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (1 << 19) / kMaxCluster * 4);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(logits_adjust_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (const void *f : {(const void *)logits_adjust_kernel<256>, (const void *)logits_adjust_kernel<512>}) {
+    // the widest range: 2^19 tokens over 16 CTAs
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (1 << 19) / kMaxCluster * 4);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  }
   return e;
 }
 

@@ -47,7 +47,7 @@ cudaError_t launch_kv8_attention(const KvAttention &p, cudaStream_t st);
 // lse of the call that p describes; adds to p.kv.weight.
 cudaError_t launch_kv8_weigh(const KvAttention &p, cudaStream_t st);
 cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules &r,
-                                 float *out, int64_t ldo, int32_t *argmax, int *status, cudaStream_t st);
+                                 float *out, int64_t ldo, int32_t *argmax, int *status, int num_sms, cudaStream_t st);
 
 #if EXL3_DEBUG_BOUNDS
 cudaError_t bounds_probe_kv8_cache(cudaStream_t st);

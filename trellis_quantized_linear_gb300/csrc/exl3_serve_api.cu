@@ -159,7 +159,7 @@ exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int6
     if (p && !aligned(p, 4)) return EXL3_ERR_ALIGNMENT;
   const DeviceInfo *dev = initialized_device();
   if (!dev) return EXL3_ERR_NOT_INITIALIZED;
-  return from_cuda(launch_logits_adjust(logits, ldl, M, n, r, out, ldo, argmax, dev->status,
+  return from_cuda(launch_logits_adjust(logits, ldl, M, n, r, out, ldo, argmax, dev->status, dev->num_sms,
                                         static_cast<cudaStream_t>(stream)));
 }
 
