@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 __all__ = [
@@ -121,6 +122,9 @@ class _LogitsRules(ctypes.Structure):
     _fields_ = [("history", _vp), ("history_start", _vp), ("generated_from", _vp), ("repetition", _vp),
                 ("presence", _vp), ("frequency", _vp), ("bias_id", _vp), ("bias_value", _vp), ("bias_start", _vp),
                 ("allowed", _vp), ("history_size", _i32), ("bias_size", _i32)]
+
+
+_PACK_RULES = struct.Struct("@10P2i").pack  # a _LogitsRules' bytes, in a quarter of the time
 
 
 def _require_f32_contiguous(where, *tensors):
@@ -418,11 +422,11 @@ def exl3_logits_adjust(logits, n: int, out, argmax, history=None, history_start=
                        allowed=None, stream=None) -> None:
     """Penalties, biases and a grammar mask on the first n columns of logits
     (fp32, M x ld) into out (may be logits), and the greedy choice."""
-    rules = _LogitsRules(_ptr(history), _ptr(history_start), _ptr(generated_from), _ptr(repetition), _ptr(presence),
-                         _ptr(frequency), _ptr(bias_id), _ptr(bias_value), _ptr(bias_start), _ptr(allowed),
-                         0 if history is None else history.numel(), 0 if bias_id is None else bias_id.numel())
-    _check(load().exl3_logits_adjust(_ptr(logits), logits.stride(0), logits.shape[0], n, ctypes.byref(rules), _ptr(out),
-                                     out.stride(0), _ptr(argmax), _stream(stream)), "exl3_logits_adjust")
+    rules = _PACK_RULES(*[0 if t is None else t.data_ptr() for t in (
+        history, history_start, generated_from, repetition, presence, frequency, bias_id, bias_value, bias_start, allowed)],
+        0 if history is None else history.numel(), 0 if bias_id is None else bias_id.numel())
+    _check(load().exl3_logits_adjust(logits.data_ptr(), logits.stride(0), logits.size(0), n, rules, out.data_ptr(),
+                                     out.stride(0), argmax.data_ptr(), _stream(stream)), "exl3_logits_adjust")
 
 
 def exl3_selftest_bounds_serving(stream=None) -> tuple[int, int]:

@@ -28,18 +28,27 @@ namespace exl3 {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kUnit = 32;         // tokens
 constexpr int kMaxSeqs = 1024;    // sequences of one launch
+// What a warp spends on entering a segment (queries, page numbers and scales of
+// another head), in units: counted as that many units of no tokens in front of
+// each segment, so that ranges of many short sequences are not longer than the
+// others. 16 sequences of 61 to 8192 tokens: the slowest CTA 82K cycles of 59K on
+// average without it.
+constexpr int kEntry = 3;
 
-template <int D, bool WEIGH>
+// NT tiles of 8 rows. 8 rows leave room for 12 warps an SM (168 registers a
+// thread), 16 rows for 8; the kernel is bound by the latency of dependent
+// instructions until there are about 12.
+template <int D, int NT, bool WEIGH>
 struct StreamCfg {
+  static constexpr int kWarps = NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
   static constexpr int kHalf = kUnit * D;                     // bytes of a unit's keys (or values)
   static constexpr int kStage = WEIGH ? kHalf : 2 * kHalf;
-  static constexpr int kStages = 24 * 1024 / kStage;          // 24 KB of copies in flight per warp
+  static constexpr int kStages = 192 * 1024 / kWarps / kStage;  // 192 KB of copies in flight per SM
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kOffPrefix = kRing;                    // int64 prefix[kMaxSeqs + 1], warp sums
-  static constexpr int kOffBar = kOffPrefix + (kMaxSeqs + 1 + kWarps) * 8;
+  static constexpr int kOffPlan = kRing;
+  static constexpr int kOffBar = kOffPlan + (kMaxSeqs + 32) * 8 + (kMaxSeqs + 8) * 8;
   static constexpr int kSmem = 1024 + kOffBar + kWarps * kStages * 8;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -60,21 +69,33 @@ struct StreamParams {
 
 __device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
 
-// Units of all sequences before sequence s, prefix[s], for s = 0 .. n_seqs; row
-// tiles of `tile` rows (0: the rows are not tiled). Every thread of the CTA takes
-// part; ends with a barrier.
-__device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile, int64_t *prefix) {
-  int64_t *warp_sum = prefix + kMaxSeqs + 1;
+// The sequences of a launch in shared memory.
+struct Plan {
+  int64_t *prefix;  // kMaxSeqs + 1: units (with those of entering) of all sequences before each; then scratch
+  int2 *seq;        // kMaxSeqs + 1: first row and length of each sequence (length -1: not to be served)
+  __device__ __forceinline__ KvSeq at(int s) const {
+    const int2 a = seq[s];
+    return KvSeq{a.x, a.y < 0 ? 0 : seq[s + 1].x - a.x, a.y < 0 ? 0 : a.y};
+  }
+};
+
+__device__ __forceinline__ int64_t segment_units(int len) { return len > 0 ? units_of(len) + kEntry : 0; }
+
+// Row tiles of `tile` rows (0: the rows are not tiled). Every thread of the CTA
+// takes part; ends with a barrier.
+__device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile, const Plan &plan) {
+  int64_t *warp_sum = plan.prefix + kMaxSeqs + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
   int64_t carry = 0;
-  if (threadIdx.x == 0) prefix[0] = 0;
+  if (threadIdx.x == 0) plan.prefix[0] = 0;
   for (int c = 0; c < kv.n_seqs; c += blockDim.x) {
     const int s = c + (int)threadIdx.x;
     int64_t n = 0;
     if (s < kv.n_seqs) {
       const KvSeq q = kv_sequence(kv, s);
-      if (q.rows > 0)
-        n = (int64_t)units_of(q.len) * kv.n_kv_heads * (tile ? ((int64_t)q.rows * group + tile - 1) / tile : 1);
+      if (q.rows > 0) n = segment_units(q.len) * kv.n_kv_heads * (tile ? ((int64_t)q.rows * group + tile - 1) / tile : 1);
+      plan.seq[s] = make_int2(kv.q_start[s], q.rows > 0 ? q.len : -1);
+      if (s + 1 == kv.n_seqs) plan.seq[s + 1] = make_int2(kv.q_start[s + 1], -1);
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -83,12 +104,13 @@ __device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile
     }
     if (lane == 31) warp_sum[warp] = n;
     __syncthreads();
-    for (int w = 0; w < nwarps; ++w) {
-      if (w < warp) n += warp_sum[w];
-    }
-    if (s < kv.n_seqs) prefix[s + 1] = carry + n;
     int64_t total = 0;
-    for (int w = 0; w < nwarps; ++w) total += warp_sum[w];
+    for (int w = 0; w < nwarps; ++w) {
+      const int64_t x = warp_sum[w];
+      if (w < warp) n += x;
+      total += x;
+    }
+    if (s < kv.n_seqs) plan.prefix[s + 1] = carry + n;
     carry += total;
     __syncthreads();
   }
@@ -99,44 +121,53 @@ __device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile
 __device__ __forceinline__ int64_t range_start(int64_t w, int64_t W, int64_t T) { return w * T / W; }
 __device__ __forceinline__ int64_t range_owner(int64_t z, int64_t W, int64_t T) { return ((z + 1) * W - 1) / T; }
 
-// A place in the unit order.
+// A place in the unit order; u < 0: entering the segment.
 struct Cursor {
   KvSeq q;
   int s, h, rt, u;    // sequence, key/value head, row tile, unit of the segment
   int units, tiles;   // of this sequence's segments
 };
-__device__ __forceinline__ void enter_sequence(const KvView &kv, int group, int tile, Cursor &c) {
-  c.q = kv_sequence(kv, c.s);
+__device__ __forceinline__ void enter_sequence(const Plan &plan, int group, int tile, Cursor &c) {
+  c.q = plan.at(c.s);
   c.units = units_of(c.q.len);
-  c.tiles = tile ? (int)(((int64_t)c.q.rows * group + tile - 1) / tile) : 1;
+  c.tiles = tile ? (c.q.rows * group + tile - 1) / tile : 1;
 }
-__device__ __forceinline__ Cursor locate(const KvView &kv, int group, int tile, const int64_t *prefix, int64_t z) {
+__device__ __forceinline__ Cursor locate(const KvView &kv, int group, int tile, const Plan &plan, int64_t z) {
   Cursor c;
   int lo = 0, hi = kv.n_seqs - 1;  // the s with prefix[s] <= z < prefix[s + 1]
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (prefix[mid + 1] > z) hi = mid;
+    if (plan.prefix[mid + 1] > z) hi = mid;
     else lo = mid + 1;
   }
   c.s = lo;
-  enter_sequence(kv, group, tile, c);
-  const int64_t rem = z - prefix[lo];
-  const int64_t seg = rem / c.units;
-  c.u = (int)(rem - seg * c.units);
+  enter_sequence(plan, group, tile, c);
+  const int64_t rem = z - plan.prefix[lo];
+  const int64_t seg = rem / (c.units + kEntry);
+  c.u = (int)(rem - seg * (c.units + kEntry)) - kEntry;
   c.h = (int)(seg / c.tiles);
   c.rt = (int)(seg - (int64_t)c.h * c.tiles);
   return c;
 }
-__device__ __forceinline__ void advance(const KvView &kv, int group, int tile, const int64_t *prefix, Cursor &c) {
+// The next place; z moves with it.
+__device__ __forceinline__ void advance(const KvView &kv, int group, int tile, const Plan &plan, Cursor &c, int64_t &z) {
+  ++z;
   if (++c.u < c.units) return;
-  c.u = 0;
+  c.u = -kEntry;
   if (++c.rt < c.tiles) return;
   c.rt = 0;
   if (++c.h < kv.n_kv_heads) return;
   c.h = 0;
   do ++c.s;
-  while (c.s < kv.n_seqs && prefix[c.s + 1] == prefix[c.s]);
-  if (c.s < kv.n_seqs) enter_sequence(kv, group, tile, c);
+  while (c.s < kv.n_seqs && plan.prefix[c.s + 1] == plan.prefix[c.s]);
+  if (c.s < kv.n_seqs) enter_sequence(plan, group, tile, c);
+}
+// Past the places of entering.
+__device__ __forceinline__ void skip_entry(Cursor &c, int64_t &z) {
+  if (c.u < 0) {
+    z -= c.u;
+    c.u = 0;
+  }
 }
 
 // Page numbers and scales of 32 consecutive blocks of one (sequence, head), one
@@ -175,7 +206,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -183,7 +214,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -237,22 +268,46 @@ __device__ __forceinline__ int row_limit(const StreamParams &p, const Cursor &c,
   return p.a.causal ? c.q.len - c.q.rows + i + 1 : c.q.len;
 }
 
-// The A operands of S^T for 16 tokens from r0 on: D / 16 k-steps.
+// The keys of a unit: word j of w[mi][r] holds the A operands of k-step j for
+// token 16 mi + 8 r + lane / 4.
 template <int D>
-__device__ __forceinline__ void load_keys(uint32_t base, int r0, int lane, uint32_t (&a)[D / 16][4]) {
+__device__ __forceinline__ void load_keys(uint32_t base, int lane, uint32_t (&w)[2][2][D / 16]) {
   const int g = lane >> 2, t = lane & 3;
-  uint32_t w[2][D / 16];
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) lds<4>(piece<D>(base, r0 + g + 8 * r, (D / 64) * t + x), &w[r][4 * x]);
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    a[j][0] = lo_codes(w[0][j]);
-    a[j][1] = lo_codes(w[1][j]);
-    a[j][2] = hi_codes(w[0][j]);
-    a[j][3] = hi_codes(w[1][j]);
-  }
+      for (int x = 0; x < D / 64; ++x) lds<4>(piece<D>(base, 16 * mi + 8 * r + g, (D / 64) * t + x), &w[mi][r][4 * x]);
+}
+
+// S^T of a unit for NT tiles of 8 rows; the chains of the two 16-token halves and
+// of even and odd k-steps are independent.
+template <int D, int NT>
+__device__ __forceinline__ void score_products(const uint32_t (&w)[2][2][D / 16], const uint32_t (&qf)[NT][D / 8],
+                                               float (&s)[NT][2][4]) {
+  float odd[NT][2][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[n][mi][k] = odd[n][mi][k] = 0.f;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi) {
+      const uint32_t a0 = lo_codes(w[mi][0][j]), a1 = lo_codes(w[mi][1][j]);
+      const uint32_t a2 = hi_codes(w[mi][0][j]), a3 = hi_codes(w[mi][1][j]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_16816(j & 1 ? odd[n][mi] : s[n][mi], a0, a1, a2, a3, qf[n][2 * j], qf[n][2 * j + 1]);
+    }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[n][mi][k] += odd[n][mi][k];
 }
 
 // Scores in log2 units. ks: key scale * softmax scale (* log2 e without a cap).
@@ -263,9 +318,9 @@ __device__ __forceinline__ float score(float acc, float ks, float cap, float inv
 }
 
 // A warp's ring of copies: issues the keys (and values) of units in order.
-template <int D, bool WEIGH>
+template <int D, int NT, bool WEIGH>
 struct Ring {
-  using Cfg = StreamCfg<D, WEIGH>;
+  using Cfg = StreamCfg<D, NT, WEIGH>;
   uint32_t base, bars;
   int put = 0, get = 0;
   uint32_t get_phase = 0;
@@ -334,17 +389,10 @@ __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stag
                                             float inv_cap, int lane, RowState<D, NT> &st) {
   const int g = lane >> 2, t = lane & 3;
   float s[NT][2][4];
-#pragma unroll
-  for (int mi = 0; mi < 2; ++mi) {
-    uint32_t a[D / 16][4];
-    load_keys<D>(stage, 16 * mi, lane, a);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[n][mi][k] = 0.f;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) mma_16816(s[n][mi], a[j][0], a[j][1], a[j][2], a[j][3], qf[n][2 * j], qf[n][2 * j + 1]);
-    }
+  {
+    uint32_t w[2][2][D / 16];
+    load_keys<D>(stage, lane, w);
+    score_products<D, NT>(w, qf, s);
   }
   const float c = ks * p.a.scale * (CAP ? 1.0f : kLog2e);
   const bool masked = pos0 + kUnit > min_limit;  // some row does not see the whole unit
@@ -413,8 +461,8 @@ __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stag
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int tok = 16 * mi + 2 * t + (r & 1) + 8 * (r >> 1);
-      if constexpr (D == 128) lds<4>(piece<D>(stage + StreamCfg<D, false>::kHalf, tok, g), v[r]);
-      else lds<2>(piece<D>(stage + StreamCfg<D, false>::kHalf, tok, g >> 1) + (g & 1) * 8, v[r]);
+      if constexpr (D == 128) lds<4>(piece<D>(stage + kUnit * D, tok, g), v[r]);
+      else lds<2>(piece<D>(stage + kUnit * D, tok, g >> 1) + (g & 1) * 8, v[r]);
       if (tail && pos0 + tok >= len) {  // whatever lies past the length (a NaN times 0 is a NaN)
 #pragma unroll
         for (int w = 0; w < W; ++w) v[r][w] = 0;
@@ -464,10 +512,12 @@ struct Part {
 };
 template <int D, int NT>
 struct Parts {
+  using Cfg = StreamCfg<D, NT, false>;
+  static constexpr int kWarps = Cfg::kWarps;
   static constexpr int kRows = 8 * NT;
   static constexpr int kFloats = kRows * (D + 2);  // output, then (maximum, sum) of each row
   static constexpr int kHeads = kWarps * kFloats * 4;
-  static_assert(kHeads + 2 * kWarps * (int)sizeof(Part) <= StreamCfg<D, false>::kRing, "parts fit the ring");
+  static_assert(kHeads + 2 * kWarps * (int)sizeof(Part) <= Cfg::kRing, "parts fit the ring");
   uint8_t *smem;
   float *first;  // workspace: CTAs x warps x kFloats
   __device__ __forceinline__ float *o(int i) const {
@@ -538,15 +588,18 @@ __device__ __forceinline__ void keep_part(float *part_o, float2 *part_ml, int la
 template <int D, int NT>
 __device__ __forceinline__ void join_cta(const StreamParams &p, const Parts<D, NT> &parts) {
   using P = Parts<D, NT>;
-  constexpr int kPerRow = D / 4, kStep = kThreads / kPerRow;  // threads of a row, rows at a time
-  const int d0 = threadIdx.x % kPerRow * 4;
+  constexpr int kWarps = P::kWarps;
+  constexpr int kPerRow = D / 4, kStep = P::Cfg::kThreads / kPerRow;  // threads of a row, rows at a time
+  const int d0 = threadIdx.x % kPerRow * 4, lane = threadIdx.x & 31;
+  static_assert(2 * kWarps <= 32, "a bit for each part");
+  const uint32_t valid = __ballot_sync(0xffffffffu, lane < 2 * kWarps && parts.head(lane < 2 * kWarps ? lane : 0)->s >= 0);
   for (int r = threadIdx.x / kPerRow; r < P::kRows; r += kStep) {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     bool begins = false;
-    for (int i = 0; i < 2 * kWarps; ++i) {
+    for (uint32_t left = valid; left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
       const Part part = *parts.head(i);
-      if (part.s < 0) continue;
       const float2 ml = parts.ml(i)[r];
       const float4 x = *reinterpret_cast<const float4 *>(parts.o(i) + r * D + d0);
       const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
@@ -555,11 +608,8 @@ __device__ __forceinline__ void join_cta(const StreamParams &p, const Parts<D, N
       l = l * a + ml.y * b;
       o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
       begins = begins || part.begins;
-      bool last = part.ends;  // the segment's last part in this CTA: it ends, or no other part follows
-      if (!last) {
-        last = true;
-        for (int k = i + 1; k < 2 * kWarps; ++k) last = last && parts.head(k)->s < 0;
-      }
+      // the segment's last part in this CTA: it ends, or no other part follows
+      const bool last = part.ends || (left & (left - 1)) == 0;
       if (!last) continue;
       const KvSeq q = kv_sequence(p.a.kv, part.s);
       const int j = part.rt * P::kRows + r, row = j / p.group;
@@ -590,15 +640,16 @@ __device__ __forceinline__ void join_cta(const StreamParams &p, const Parts<D, N
 }
 
 template <int D, int NT, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
     kv8_stream_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const StreamParams p) {
-  using Cfg = StreamCfg<D, false>;
+  using Cfg = StreamCfg<D, NT, false>;
+  constexpr int kWarps = Cfg::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const KvView &kv = p.a.kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t *prefix = reinterpret_cast<int64_t *>(smem + Cfg::kOffPrefix);
-  Ring<D, false> ring;
+  const Plan plan{reinterpret_cast<int64_t *>(smem + Cfg::kOffPlan), reinterpret_cast<int2 *>(smem + Cfg::kOffPlan + (kMaxSeqs + 32) * 8)};
+  Ring<D, NT, false> ring;
   ring.base = smem_u32(smem) + warp * Cfg::kStages * Cfg::kStage;
   ring.bars = smem_u32(smem + Cfg::kOffBar) + warp * Cfg::kStages * 8;
   if (lane == 0) {
@@ -608,30 +659,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int tile = 8 * NT;
-  build_plan(kv, p.group, tile, prefix);
-  const int64_t T = prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
+  build_plan(kv, p.group, tile, plan);
+  const int64_t T = plan.prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= kv.n_seqs; i += kThreads) p.plan[i] = prefix[i];
+    for (int i = threadIdx.x; i <= kv.n_seqs; i += Cfg::kThreads) p.plan[i] = plan.prefix[i];
   if ((int64_t)blockIdx.x * kWarps >= W) return;
   const Parts<D, NT> parts{smem, p.first};
   Part first{-1}, last{-1};  // this warp's parts of segments that it does not cover
   RowState<D, NT> st;
   if (w < W) {
-    int64_t z = range_start(w, W, T), zp = z;
+    int64_t z = range_start(w, W, T);
     const int64_t z1 = range_start(w + 1, W, T);
-    Cursor c = locate(kv, p.group, tile, prefix, z), cp = c;
+    Cursor c = locate(kv, p.group, tile, plan, z);
+    skip_entry(c, z);
+    int64_t zp = z;
+    Cursor cp = c;
     Blocks ahead, now;
     const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
     uint32_t qf[NT][D / 8];
     int limit[NT][2], min_limit = 0;  // tokens that this lane's rows see, and the tile's first row
     bool fresh = true, began = false;
-    for (; z < z1; ++z) {
+    while (z < z1) {
       while (zp < z1 && ring.in_flight < Cfg::kStages) {
         if (!ahead.holds(cp)) ahead.load<false>(kv, cp, lane);
         ring.issue(&tk, &tv, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
-        ++zp;
-        advance(kv, p.group, tile, prefix, cp);
+        advance(kv, p.group, tile, plan, cp, zp);
+        skip_entry(cp, zp);
       }
       if (!now.holds(c)) {
         if (ahead.holds(c)) now = ahead;
@@ -661,11 +715,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();  // every lane is done with the stage before it is filled again
       ring.next();
       const bool end = c.u + 1 == c.units;
-      if (end || z + 1 == z1) {
+      const bool done = z + 1 == z1 || (end && z + 1 + kEntry >= z1);  // no unit of the range is left
+      if (end || done) {
         close_rows<D, NT>(st);
         if (end && began) {
           write_rows<D, NT>(p, c, lane, st);
-        } else if (z + 1 == z1) {
+        } else if (done) {
           last = Part{c.s, c.h, c.rt, began, end};
           break;  // kept in registers
         } else {
@@ -676,7 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fresh = true;
       }
-      advance(kv, p.group, tile, prefix, c);
+      advance(kv, p.group, tile, plan, c, z);
+      skip_entry(c, z);
     }
   }
   __syncthreads();  // no warp uses its ring any more
@@ -695,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int NT>
 __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
   const KvView &kv = p.a.kv;
-  constexpr int tile = 8 * NT;
+  constexpr int tile = 8 * NT, kWarps = StreamCfg<D, NT, false>::kWarps;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.y, h = blockIdx.z, j = blockIdx.x, i = j / p.group;
@@ -706,7 +762,7 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
   float m = -INFINITY, l = 0.f, o = 0.f;
   if (units_s > 0) {
     const int tiles = (q.rows * p.group + tile - 1) / tile, units = units_of(q.len);
-    const int64_t z = z0 + ((int64_t)h * tiles + j / tile) * units;
+    const int64_t z = z0 + ((int64_t)h * tiles + j / tile) * (units + kEntry) + kEntry;
     const int64_t c0 = range_owner(z, W, T) / kWarps, c1 = range_owner(z + units - 1, W, T) / kWarps;
     if (c0 == c1) return;  // the CTA wrote the result
 #pragma unroll 4
@@ -731,15 +787,16 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
 // Accumulated weight: the same stream over the keys alone; a unit's weights are
 // the sums over all rows of the sequence, formed by the warp that owns the unit.
 template <int D, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
     kv8_weigh_kernel(const __grid_constant__ CUtensorMap tk, const StreamParams p) {
-  using Cfg = StreamCfg<D, true>;
+  using Cfg = StreamCfg<D, 1, true>;
+  constexpr int kWarps = Cfg::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const KvView &kv = p.a.kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  int64_t *prefix = reinterpret_cast<int64_t *>(smem + Cfg::kOffPrefix);
-  Ring<D, true> ring;
+  const Plan plan{reinterpret_cast<int64_t *>(smem + Cfg::kOffPlan), reinterpret_cast<int2 *>(smem + Cfg::kOffPlan + (kMaxSeqs + 32) * 8)};
+  Ring<D, 1, true> ring;
   ring.base = smem_u32(smem) + warp * Cfg::kStages * Cfg::kStage;
   ring.bars = smem_u32(smem + Cfg::kOffBar) + warp * Cfg::kStages * 8;
   if (lane == 0) {
@@ -748,26 +805,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  build_plan(kv, p.group, 0, prefix);
-  const int64_t T = prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
+  build_plan(kv, p.group, 0, plan);
+  const int64_t T = plan.prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   if (w >= W) return;
-  int64_t z = range_start(w, W, T), zp = z;
+  int64_t z = range_start(w, W, T);
   const int64_t z1 = range_start(w + 1, W, T);
-  Cursor c = locate(kv, p.group, 0, prefix, z), cp = c;
+  Cursor c = locate(kv, p.group, 0, plan, z);
+  skip_entry(c, z);
+  int64_t zp = z;
+  Cursor cp = c;
   Blocks ahead, now;
   const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
-  uint32_t qf[D / 8];
+  uint32_t qf[1][D / 8];
   int limit[2];
   float lse[2];  // in log2 units
   int held_s = -1, held_h = -1, held_j = -1;
 
-  for (; z < z1; ++z) {
+  while (z < z1) {
     while (zp < z1 && ring.in_flight < Cfg::kStages) {
       if (!ahead.holds(cp)) ahead.load<true>(kv, cp, lane);
       ring.issue(&tk, nullptr, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
-      ++zp;
-      advance(kv, p.group, 0, prefix, cp);
+      advance(kv, p.group, 0, plan, cp, zp);
+      skip_entry(cp, zp);
     }
     if (!now.holds(c)) {
       if (ahead.holds(c)) now = ahead;
@@ -781,9 +841,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
     if (page >= 0) {
-      uint32_t a[2][D / 16][4];
-      load_keys<D>(ring.stage(), 0, lane, a[0]);
-      load_keys<D>(ring.stage(), 16, lane, a[1]);
+      uint32_t words[2][2][D / 16];
+      load_keys<D>(ring.stage(), lane, words);
       const int pos0 = c.u * kUnit, J = c.q.rows * p.group;
       // the first row that sees a token of the unit
       const int first = p.a.causal ? max(0, pos0 - (c.q.len - c.q.rows)) * p.group : 0;
@@ -794,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           held_s = c.s;
           held_h = c.h;
           held_j = j0;
-          load_query<D>(p, c, j0 + g, lane, qf);
+          load_query<D>(p, c, j0 + g, lane, qf[0]);
 #pragma unroll
           for (int col = 0; col < 2; ++col) {
             const int j = j0 + 2 * t + col, i = j / p.group;
@@ -804,16 +863,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             lse[col] *= kLog2e;
           }
         }
+        float s[1][2][4];
+        score_products<D, 1>(words, qf, s);
 #pragma unroll
-        for (int mi = 0; mi < 2; ++mi) {
-          float s[4] = {};
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) mma_16816(s, a[mi][k][0], a[mi][k][1], a[mi][k][2], a[mi][k][3], qf[2 * k], qf[2 * k + 1]);
+        for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (pos0 + 16 * mi + g + 8 * (k >> 1) < limit[k & 1])
-              part[mi][k >> 1] += ex2(score<CAP>(s[k], ks, p.a.softcap, inv_cap) - lse[k & 1]);
-        }
+              part[mi][k >> 1] += ex2(score<CAP>(s[0][mi][k], ks, p.a.softcap, inv_cap) - lse[k & 1]);
         // sums of sums: 16 tiles to a part, so that long chunks do not lose bits
         if ((++n & 15) == 0 || j0 + 8 >= J) {
 #pragma unroll
@@ -841,7 +898,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     ring.next();
-    advance(kv, p.group, 0, prefix, c);
+    advance(kv, p.group, 0, plan, c, z);
+    skip_entry(c, z);
   }
 }
 
@@ -857,15 +915,18 @@ bool cache_map(CUtensorMap *m, const KvView &kv, const uint8_t *codes) {
 }
 
 template <int D, int NT>
-cudaError_t run_stream(const CUtensorMap &tk, const CUtensorMap &tv, const StreamParams &p, cudaStream_t st) {
-  const int grid = p.warps / kWarps;
-  const size_t smem = StreamCfg<D, false>::kSmem;
+cudaError_t run_stream(const CUtensorMap &tk, const CUtensorMap &tv, const StreamParams &params, cudaStream_t st) {
+  using Cfg = StreamCfg<D, NT, false>;
+  StreamParams p = params;
+  const int grid = p.a.num_sms, kThreads = Cfg::kThreads;
+  p.warps = grid * Cfg::kWarps;
+  const size_t smem = Cfg::kSmem;
   const cudaError_t e =
-      p.a.softcap > 0.f ? launch_overlapped(kv8_stream_kernel<D, NT, true>, grid, kThreads, smem, st, tk, tv, p)
-                        : launch_overlapped(kv8_stream_kernel<D, NT, false>, grid, kThreads, smem, st, tk, tv, p);
+      p.a.softcap > 0.f ? launch_overlapped(kv8_stream_kernel<D, NT, true>, grid, kThreads, smem, st, 1, tk, tv, p)
+                        : launch_overlapped(kv8_stream_kernel<D, NT, false>, grid, kThreads, smem, st, 1, tk, tv, p);
   if (e != cudaSuccess) return e;
   const dim3 join((unsigned)(p.a.kv.max_rows * (int64_t)p.group), p.a.kv.n_seqs, p.a.kv.n_kv_heads);
-  return launch_overlapped(kv8_join_kernel<D, NT>, join, D, 0, st, p);
+  return launch_overlapped(kv8_join_kernel<D, NT>, join, D, 0, st, 1, p);
 }
 
 // The sequences [s0, s0 + n) of a call.
@@ -889,7 +950,7 @@ StreamWorkspace stream_workspace(int64_t rows, int D, int num_sms) {
   w.o = 2 * (kMaxSeqs + 8);  // the plan's int64
   w.ml = w.o + w.part_rows * D;
   w.first = w.ml + w.part_rows * 2;
-  w.total = w.first + (int64_t)num_sms * kWarps * tile * (D + 2);
+  w.total = w.first + (int64_t)num_sms * (narrow(rows) ? StreamCfg<128, 1, false>::kWarps : StreamCfg<128, 2, false>::kWarps) * tile * (D + 2);
   return w;
 }
 
@@ -900,7 +961,6 @@ cudaError_t attention(const KvAttention &a, cudaStream_t st) {
   StreamParams p;
   p.a = a;
   p.group = a.n_heads / a.kv.n_kv_heads;
-  p.warps = a.num_sms * kWarps;
   const int64_t rows = (int64_t)a.kv.max_rows * p.group;
   const StreamWorkspace w = stream_workspace(rows, D, a.num_sms);
   float *ws = static_cast<float *>(a.workspace);
@@ -924,12 +984,14 @@ cudaError_t weigh(const KvAttention &a, cudaStream_t st) {
   StreamParams p{};
   p.a = a;
   p.group = a.n_heads / a.kv.n_kv_heads;
-  p.warps = a.num_sms * kWarps;
-  const size_t smem = StreamCfg<D, true>::kSmem;
+  using Cfg = StreamCfg<D, 1, true>;
+  constexpr int kThreads = Cfg::kThreads;
+  p.warps = a.num_sms * Cfg::kWarps;
+  const size_t smem = Cfg::kSmem;
   for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kMaxSeqs) {
     p.a.kv = slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
-    const cudaError_t e = a.softcap > 0.f ? launch_overlapped(kv8_weigh_kernel<D, true>, a.num_sms, kThreads, smem, st, tk, p)
-                                          : launch_overlapped(kv8_weigh_kernel<D, false>, a.num_sms, kThreads, smem, st, tk, p);
+    const cudaError_t e = a.softcap > 0.f ? launch_overlapped(kv8_weigh_kernel<D, true>, a.num_sms, kThreads, smem, st, 1, tk, p)
+                                          : launch_overlapped(kv8_weigh_kernel<D, false>, a.num_sms, kThreads, smem, st, 1, tk, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -938,14 +1000,15 @@ cudaError_t weigh(const KvAttention &a, cudaStream_t st) {
 template <int D>
 cudaError_t init_dim() {
   cudaError_t e = cudaSuccess;
-  cudaFuncAttributes attr;
-  for (const void *f : {(const void *)kv8_stream_kernel<D, 1, false>, (const void *)kv8_stream_kernel<D, 1, true>,
-                        (const void *)kv8_stream_kernel<D, 2, false>, (const void *)kv8_stream_kernel<D, 2, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, false>::kSmem);
+  for (const void *f : {(const void *)kv8_stream_kernel<D, 1, false>, (const void *)kv8_stream_kernel<D, 1, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, 1, false>::kSmem);
+  for (const void *f : {(const void *)kv8_stream_kernel<D, 2, false>, (const void *)kv8_stream_kernel<D, 2, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, 2, false>::kSmem);
   for (const void *f : {(const void *)kv8_weigh_kernel<D, false>, (const void *)kv8_weigh_kernel<D, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, true>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, 1, true>::kSmem);
+  // the join takes the stream kernel's split of shared memory and L1: no SM waits to change it
   for (const void *f : {(const void *)kv8_join_kernel<D, 1>, (const void *)kv8_join_kernel<D, 2>})
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, f);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   return e;
 }
 

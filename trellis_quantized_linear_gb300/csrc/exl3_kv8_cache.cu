@@ -4,6 +4,7 @@
 
 #include "exl3_internal.h"
 #include "exl3_kv8.cuh"
+#include "exl3_tcgen05.cuh"
 
 namespace exl3 {
 
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(KvView kv, c
 
   const int c = threadIdx.x % kVecs, t0 = threadIdx.x / kVecs;
   uint4 raw[kPasses];
-  uint32_t amax = 0;                                 // fp16 magnitudes order like their bits
+  __half2 top = __half2half2(__ushort_as_half(0));   // a NaN never wins a maximum
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int pos = b * kKvBlock + i * kTokens + t0;
@@ -50,6 +51,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(KvView kv, c
       const int64_t off = (int64_t)(q.row0 + pos - first) * ld + h * D + c * 8;
       if (EXL3_SPAN(off, 8, (int64_t)(kv.rows - 1) * ld + (int64_t)kv.n_kv_heads * D))
         raw[i] = *reinterpret_cast<const uint4 *>(x + off);
+      const __half2 *w = reinterpret_cast<const __half2 *>(&raw[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = __hmax2(top, __habs2(w[j]));
+    }
+  }
+  // fp16 magnitudes order like their bits
+  uint32_t amax = __half_as_ushort(__hmax(__low2half(top), __high2half(top)));
+  if (amax == 0x7C00u) {  // an infinity: the largest finite value instead
+    amax = 0;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -104,55 +116,71 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// One CTA per (sequence, head). The keys of the tokens to choose among are read
-// once into shared memory (those past what fits are read again from memory); a
-// radix selection, 11 bits a pass from the top, finds the key of the last token
-// that is kept, and each warp then writes the kept positions of one contiguous
-// part, ties to the lower positions. The first pass's bins hold the sign, the
-// exponent and two bits: weights fill few of them, so each bin has eight copies,
-// one for every eighth lane.
+// One cluster of CTAs per (sequence, head), each with a contiguous part of the
+// tokens to choose among. Their keys are read once into shared memory (those past
+// what fits are read again from memory); a radix selection, 11 bits a pass from
+// the top over the sums of the CTAs' bins, finds the key of the last token that
+// is kept, and each warp then writes the kept positions of its part, ties to the
+// lower positions. The first pass's bins hold the sign, the exponent and two
+// bits: weights fill few of them, so each bin has four copies, one for every
+// fourth lane. 8 sequences of up to 32K tokens, 8 heads: 47 us with one CTA each
+// (bound by its instructions), less the more CTAs share them.
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectKeys = 38 * 1024;  // held in shared memory
-constexpr int kBins = 2048, kCopies = 8;
-constexpr int kSelectSmem = (kSelectKeys + kBins * kCopies) * 4;
+constexpr int kSelectKeys = 16 * 1024;  // held in shared memory
+constexpr int kBins = 2048, kCopies = 4;
+constexpr int kSelectMaxCluster = 8;
 
-__global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv, int budget, int recent, int32_t *kept,
-                                                                       int32_t *new_len) {
+__global__ void __launch_bounds__(kSelectThreads, 2) kv8_select_kernel(KvView kv, int budget, int recent, int held_max,
+                                                                       int32_t *kept, int32_t *new_len) {
   extern __shared__ __align__(16) uint32_t select_smem[];
-  uint32_t *keys = select_smem;
-  int *hist = reinterpret_cast<int *>(select_smem + kSelectKeys);
-  __shared__ int warp_count[kSelectWarps], warp_tie[kSelectWarps], s_bin, s_left;
-  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int *hist = reinterpret_cast<int *>(select_smem);            // kBins x kCopies, then the sums
+  uint32_t *keys = select_smem + kBins * kCopies;
+  __shared__ int sums[kBins];
+  __shared__ int warp_count[kSelectWarps], warp_tie[kSelectWarps], cta_count[2], s_bin, s_left;
+  const int h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x, ranks = gridDim.x;         // the cluster is one row of the grid
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int len = kv_length(kv, s);
   const int keep = min(len, budget);
-  if (h == 0 && tid == 0) new_len[s] = keep;
+  if (rank == 0 && h == 0 && tid == 0) new_len[s] = keep;
   int32_t *out = kept + ((int64_t)s * kv.n_kv_heads + h) * budget;
-  for (int i = keep + tid; i < budget; i += kSelectThreads) out[i] = -1;
+  const int every = (int)ranks * kSelectThreads, me = (int)rank * kSelectThreads + tid;
+  for (int i = keep + me; i < budget; i += every) out[i] = -1;
   const int early = len - min(recent, len);   // tokens that are kept by weight
   const int want = keep - (len - early);      // how many of them
-  for (int i = early + tid; i < len; i += kSelectThreads) out[want + i - early] = i;
-  if (want == 0) return;
+  for (int i = early + me; i < len; i += every) out[want + i - early] = i;
+  if (want == 0) return;                      // the same in every CTA of the cluster
   if (want == early) {
-    for (int i = tid; i < early; i += kSelectThreads) out[i] = i;
+    for (int i = me; i < early; i += every) out[i] = i;
     return;
   }
 
+  const int share = ((early + (int)ranks - 1) / (int)ranks + kKvBlock - 1) / kKvBlock * kKvBlock;
+  const int first = min((int)rank * share, early), n = min(share, early - first);  // this CTA's tokens
   auto read_key = [&](int i) {
     const int page = kv_page(kv, s, i / kKvBlock);
     return page < 0 ? 0u : weight_key(kv.weight[((int64_t)page * kv.n_kv_heads + h) * kKvBlock + i % kKvBlock]);
   };
-  auto key_at = [&](int i) { return i < kSelectKeys ? keys[i] : read_key(i); };
-  const int held = min(early, kSelectKeys);
-  for (int i = tid; i < held; i += kSelectThreads * 8) {
-    uint32_t k[8];
+  const int held = min(n, held_max);
+  auto key_at = [&](int i) { return i < held ? keys[i] : read_key(first + i); };
+  // a warp takes whole blocks, two tokens a lane; `first` is a multiple of a block
+  for (int b0 = warp; b0 * kKvBlock < held; b0 += kSelectWarps * 4) {
+    float2 w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j * kSelectThreads < held) k[j] = read_key(i + j * kSelectThreads);
+    for (int j = 0; j < 4; ++j) {
+      const int i = (b0 + j * kSelectWarps) * kKvBlock;
+      if (i >= held) continue;
+      const int page = kv_page(kv, s, (first + i) / kKvBlock);
+      w[j] = make_float2(NAN, NAN);
+      if (page >= 0) w[j] = reinterpret_cast<const float2 *>(kv.weight + ((int64_t)page * kv.n_kv_heads + h) * kKvBlock)[lane];
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j * kSelectThreads < held) keys[i + j * kSelectThreads] = k[j];
+    for (int j = 0; j < 4; ++j) {
+      const int i = (b0 + j * kSelectWarps) * kKvBlock + 2 * lane;
+      if (i < held) keys[i] = weight_key(w[j].x);
+      if (i + 1 < held) keys[i + 1] = weight_key(w[j].y);
+    }
   }
 
   uint32_t threshold = 0;  // the bits of the threshold's key found so far
@@ -163,18 +191,34 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv
     const uint32_t mask = pass == 2 ? 1023u : 2047u, above = pass == 0 ? 0u : ~0u << (shift + (pass == 2 ? 10 : 11));
     for (int i = tid; i < kBins * kCopies / 4; i += kSelectThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = tid; i < early; i += kSelectThreads) {
+    for (int i = tid; i < n; i += kSelectThreads) {
       const uint32_t key = key_at(i);
       if ((key & above) == threshold) atomicAdd(&hist[((key >> shift) & mask) * kCopies + lane % kCopies], 1);
     }
     __syncthreads();
-    // from the top: thread tid has bins 2047 - 2 tid and the one below
+    for (int i = tid; i < kBins; i += kSelectThreads) {
+      const int4 x = reinterpret_cast<const int4 *>(hist)[i];
+      sums[i] = x.x + x.y + x.z + x.w;
+    }
+    // from the top: thread tid has bins 2047 - 2 tid and the one below, of all CTAs
     const int hi = kBins - 1 - 2 * tid;
-    auto bin = [&](int b) {
-      const int4 x = reinterpret_cast<const int4 *>(hist)[2 * b], y = reinterpret_cast<const int4 *>(hist)[2 * b + 1];
-      return x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
-    };
-    const int c1 = bin(hi), c0 = bin(hi - 1);
+    int c1 = 0, c0 = 0;
+    if (ranks > 1) {
+      cluster_sync_all();
+      const uint32_t at = smem_u32(&sums[hi - 1]);
+#pragma unroll
+      for (uint32_t r = 0; r < kSelectMaxCluster; ++r)
+        if (r < ranks) {
+          int a, b;
+          asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(map_to_rank(at, r)) : "memory");
+          c0 += a;
+          c1 += b;
+        }
+    } else {
+      __syncthreads();
+      c0 = sums[hi - 1];
+      c1 = sums[hi];
+    }
     int sum = c1 + c0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -193,14 +237,15 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv
       s_bin = hi - 1;
       s_left = left - before - c1;
     }
-    __syncthreads();
+    if (ranks > 1) cluster_sync_all();  // no CTA reads this pass's sums any more
+    else __syncthreads();
     threshold |= (uint32_t)s_bin << shift;
     left = s_left;
   }
 
   // `left` tokens of the threshold's key are kept, the first ones.
-  const int part = ((early + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
-  const int i0 = min(warp * part, early), i1 = min(i0 + part, early);
+  const int part = ((n + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+  const int i0 = min(warp * part, n), i1 = min(i0 + part, n);
   int gt = 0, eq = 0;
   for (int i = i0 + lane; i < i1; i += 32) {
     const uint32_t key = key_at(i);
@@ -216,6 +261,25 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv
   __syncthreads();
   int g = __reduce_add_sync(0xffffffffu, lane < warp ? warp_count[lane] : 0);
   int e = __reduce_add_sync(0xffffffffu, lane < warp ? warp_tie[lane] : 0);
+  if (ranks > 1) {
+    if (tid == kSelectThreads - 1) {
+      cta_count[0] = g + gt;
+      cta_count[1] = e + eq;
+    }
+    __syncwarp();
+    cluster_sync_all();
+#pragma unroll
+    for (uint32_t r = 0; r < kSelectMaxCluster; ++r)
+      if (r < rank) {
+        int a, b;
+        const uint32_t at = map_to_rank(smem_u32(cta_count), r);
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(a) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(b) : "r"(at + 4) : "memory");
+        g += a;
+        e += b;
+      }
+    cluster_sync_all();  // a CTA stays until its counts have been read
+  }
   for (int i = i0 + lane; i - lane < i1; i += 32) {
     const uint32_t key = i < i1 ? key_at(i) : 0u;
     const bool is_gt = i < i1 && key > threshold, is_eq = i < i1 && key == threshold;
@@ -223,7 +287,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv
     const uint32_t below = (1u << lane) - 1;
     const int ties = e + __popc(me & below);
     const int at = g + __popc(mg & below) + min(ties, left);
-    if ((is_gt || (is_eq && ties < left)) && EXL3_RANGE(at, 0, want)) out[at] = i;
+    if ((is_gt || (is_eq && ties < left)) && EXL3_RANGE(at, 0, want)) out[at] = first + i;
     g += __popc(mg);
     e += __popc(me);
   }
@@ -232,7 +296,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv
 // One CTA per (new block, sequence, head): its keys and values. The block's scale
 // is the largest of its tokens' scales, so codes only ever shrink. Bound by the
 // bytes moved; all of a thread's loads are in flight before its first store.
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;
 
 __device__ __forceinline__ uint4 rescale_16(uint4 c, float factor) {
   const uint2 a = rescale_codes(make_uint2(c.x, c.y), factor), b = rescale_codes(make_uint2(c.z, c.w), factor);
@@ -310,19 +374,27 @@ cudaError_t launch_kv8_append(const KvView &kv, const void *k, int64_t ldk, cons
   // the most blocks that max_rows consecutive tokens touch
   const dim3 grid((unsigned)((kv.max_rows + (int64_t)2 * kKvBlock - 2) / kKvBlock), kv.n_seqs, 2 * kv.n_kv_heads);
   const __half *xk = static_cast<const __half *>(k), *xv = static_cast<const __half *>(v);
-  return launch_overlapped(kv.head_dim == 64 ? kv8_append_kernel<64> : kv8_append_kernel<128>, grid, kAppendThreads, 0, st, kv,
+  return launch_overlapped(kv.head_dim == 64 ? kv8_append_kernel<64> : kv8_append_kernel<128>, grid, kAppendThreads, 0, st, 1, kv,
                            xk, ldk, xv, ldv);
 }
 
 cudaError_t launch_kv8_evict(const KvView &kv, const int32_t *dst_pages, int budget, int recent, int32_t *kept,
-                             int32_t *new_len, cudaStream_t st) {
+                             int32_t *new_len, int num_sms, cudaStream_t st) {
   if (kv.n_seqs == 0) return cudaSuccess;
-  cudaError_t e = launch_overlapped(kv8_select_kernel, dim3(kv.n_kv_heads, kv.n_seqs), kSelectThreads, kSelectSmem, st, kv,
-                                    budget, recent, kept, new_len);
+  // As many CTAs to a (sequence, head) as the SMs hold at once, two an SM, but
+  // 4096 tokens to a CTA at least: more would wait for one another longer than
+  // they save (32K tokens, 64 clusters: 47 us with 1 CTA, 64 us with 8).
+  const int64_t most = (int64_t)kv.max_pages * kKvBlock, clusters = (int64_t)kv.n_kv_heads * kv.n_seqs;
+  int ranks = 1;
+  while (ranks < kSelectMaxCluster && most > (int64_t)ranks * 4096 && 2 * ranks * clusters <= 2 * num_sms) ranks *= 2;
+  const int64_t share = ceil_div(most, ranks * kKvBlock) * kKvBlock;
+  const int held = (int)(share < kSelectKeys ? share : kSelectKeys);
+  cudaError_t e = launch_overlapped(kv8_select_kernel, dim3(ranks, kv.n_kv_heads, kv.n_seqs), kSelectThreads,
+                                    (size_t)(kBins * kCopies + held) * 4, st, ranks, kv, budget, recent, held, kept, new_len);
   if (e != cudaSuccess) return e;
   const int blocks = (int)(((int64_t)budget + kKvBlock - 1) / kKvBlock);
   const dim3 grid(blocks, kv.n_seqs, kv.n_kv_heads);
-  return launch_overlapped(kv.head_dim == 64 ? kv8_move_kernel<64> : kv8_move_kernel<128>, grid, kMoveThreads, 0, st, kv,
+  return launch_overlapped(kv.head_dim == 64 ? kv8_move_kernel<64> : kv8_move_kernel<128>, grid, kMoveThreads, 0, st, 1, kv,
                            dst_pages, blocks, budget, kept);
 }
 
@@ -332,7 +404,8 @@ cudaError_t init_kv8_cache_kernels(int *status) {
   for (const void *f : {(const void *)kv8_append_kernel<64>, (const void *)kv8_append_kernel<128>,
                         (const void *)kv8_move_kernel<64>, (const void *)kv8_move_kernel<128>})
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, f);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (kBins * kCopies + kSelectKeys) * 4);
   return e;
 }
 

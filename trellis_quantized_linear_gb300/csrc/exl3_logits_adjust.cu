@@ -1,13 +1,16 @@
 // Penalties, biases and a grammar mask on logits, and the greedy choice from
 // what is left. Formula in include/exl3.h.
 //
-// A cluster of up to 16 CTAs per row, each with a contiguous range of the
-// vocabulary. A CTA counts the row's history into one 32-bit word for each of
-// its tokens in shared memory (integer adds: any order gives the same counts),
-// while its logits are already on their way into registers; each logit is read
-// and written once. The row's greedy choice is joined through the cluster's
-// shared memory. Biases are few: their tokens are marked, left out of the
-// stream and done one by one after it.
+// A cluster of CTAs per row; the row's tiles of 128 tokens go to them in turn (a
+// vocabulary has its common tokens together: contiguous ranges took half as long
+// again). Each CTA counts the row's history into a word for each of its tokens in
+// shared memory (integer adds: any order gives the same counts); a long history
+// is first dealt out, each CTA reading a share of it and handing every entry to
+// the CTA that has the token. Then one stream reads and writes each logit once.
+// The few tokens with a word (2 % at a history of 8192) are listed as they are
+// first counted and done after the stream, so that their divisions do not hold up
+// the rest, and so are the biases. The row's greedy choice is joined through the
+// cluster's shared memory.
 #include <limits.h>
 
 #include "exl3_internal.h"
@@ -18,7 +21,6 @@ namespace exl3 {
 
 namespace {
 
-constexpr int kAdjustVecs = 8;   // 4-token pieces that a thread holds at a time
 constexpr int kMaxCluster = 16;
 // A token's word: in the history at all, has a bias, times generated.
 constexpr uint32_t kSeen = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3FFFFFFFu;
@@ -29,7 +31,8 @@ struct AdjustParams {
   int32_t *argmax;
   int *status;
   int64_t ldl, ldo, M;
-  int n, range;  // tokens, tokens of a CTA (a multiple of 128)
+  int n, lg;  // tokens, log2 of a cluster's CTAs
+  int held;   // tokens of a CTA, rounded up (16-bit words in shared memory)
   exl3_logits_rules r;
 };
 
@@ -38,12 +41,10 @@ struct RowRules {
 };
 
 __device__ __forceinline__ float penalized(float x, uint32_t word, const RowRules &r) {
-  if (word & (kSeen | kCount)) {
-    x = x > 0.f ? __fdiv_rn(x, r.rep) : __fmul_rn(x, r.rep);
-    const uint32_t made = word & kCount;
-    if (made) x = __fsub_rn(x, __fadd_rn(__fmul_rn(r.freq, (float)made), r.pres));
-  }
-  return x;
+  if ((word & (kSeen | kCount)) == 0) return x;
+  x = x > 0.f ? __fdiv_rn(x, r.rep) : __fmul_rn(x, r.rep);
+  const uint32_t made = word & kCount;
+  return made ? __fsub_rn(x, __fadd_rn(__fmul_rn(r.freq, (float)made), r.pres)) : x;
 }
 
 // Start and end of row m in a list of `size` entries; an impossible range is
@@ -65,131 +66,271 @@ struct Best {
       t = i;
     }
   }
-  // Only the first maximum above -inf counts, so INT_MAX stays with -inf.
-  __device__ __forceinline__ void see(float y, int i) {
-    if (y > x) {
-      x = y;
-      t = i;
-    }
-  }
 };
 
-template <int kAdjustThreads>
-__global__ void __launch_bounds__(kAdjustThreads, 768 / kAdjustThreads) logits_adjust_kernel(const AdjustParams p) {
-  extern __shared__ __align__(16) uint32_t words[];  // one of each token of the range
-  __shared__ float sb[kAdjustThreads / 32], cb[kMaxCluster];
-  __shared__ int si[kAdjustThreads / 32], ci[kMaxCluster], duplicates;
+// The tokens' words: 16 bits each (seen, biased, 14 bits of count) where the
+// row's history is short enough to count in them, else 32 bits and half as many
+// tokens at a time.
+constexpr int kShortHistory = 1 << 14;
+struct Words {
+  uint32_t *at;
+  bool wide;
+  // Each of these returns the word as it was.
+  __device__ __forceinline__ uint32_t count(int i) const {
+    if (wide) return atomicAdd(&at[i], 1u);
+    return unpack(atomicAdd(&at[i >> 1], 1u << (16 * (i & 1))) >> (16 * (i & 1)));
+  }
+  __device__ __forceinline__ uint32_t set(int i, uint32_t flag) const {
+    if (wide) return atomicOr(&at[i], flag);
+    return unpack(atomicOr(&at[i >> 1], pack(flag) << (16 * (i & 1))) >> (16 * (i & 1)));
+  }
+  __device__ __forceinline__ uint32_t one(int i) const { return wide ? at[i] : unpack(at[i >> 1] >> (16 * (i & 1))); }
+  __device__ __forceinline__ uint4 four(int i) const {
+    if (wide) return *reinterpret_cast<const uint4 *>(at + i);
+    const uint2 w = *reinterpret_cast<const uint2 *>(at + (i >> 1));
+    if ((w.x | w.y) == 0) return make_uint4(0, 0, 0, 0);
+    return make_uint4(unpack(w.x), unpack(w.x >> 16), unpack(w.y), unpack(w.y >> 16));
+  }
+  __device__ static __forceinline__ uint32_t pack(uint32_t w) { return (w & kCount) | ((w & ~kCount) >> 16); }
+  __device__ static __forceinline__ uint32_t unpack(uint32_t w) { return (w & 0x3FFFu) | ((w & 0xC000u) << 16); }
+};
+
+constexpr int kList = 2048;               // history entries that are handed to a CTA
+constexpr uint32_t kMade = 0x80000000u;   // in a list: generated
+constexpr int kHeld = 16384;              // tokens that have words at a time, where there are many rows
+constexpr int kSpecial = 2048;            // tokens with a word that are listed
+struct AdjustSmem {
+  uint32_t list[kList];
+  uint32_t special[kSpecial];
+  uint32_t words[1];  // as many as the launch asks for
+};
+
+template <int T, int V, int CTAS>
+__global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustParams p) {
+  extern __shared__ __align__(16) uint8_t adjust_smem[];
+  AdjustSmem &sm = *reinterpret_cast<AdjustSmem *>(adjust_smem);
+  __shared__ int special_n, duplicates, list_n;
+  __shared__ float sb[T / 32], cb[kMaxCluster];
+  __shared__ int si[T / 32], ci[kMaxCluster];
   const int tid = threadIdx.x, lane = tid & 31;
   uint32_t rank, ranks;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
   const int64_t m = blockIdx.x / ranks;
-  const int t0 = (int)rank * p.range, t1 = min(t0 + p.range, p.n);  // this CTA's tokens
-  for (int i = tid * 4; i < p.range; i += kAdjustThreads * 4)
-    if (EXL3_SPAN(i, 4, p.range)) *reinterpret_cast<uint4 *>(words + i) = make_uint4(0, 0, 0, 0);
-  if (tid == 0) duplicates = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const float *logits = p.logits + m * p.ldl;
   float *out = p.out + m * p.ldo;
   const uint32_t *allowed = p.r.allowed ? p.r.allowed + m * ((p.n + 31) / 32) : nullptr;
-  float4 x[kAdjustVecs];
-  uint32_t bits[kAdjustVecs];
-  auto load = [&](int base) {
+  // This CTA's tokens in order, local index to token and back.
+  const int mine = ((p.n + 127) / 128 + (int)ranks - 1 - (int)rank) / (int)ranks * 128;
+  auto token = [&](int i) { return ((((i >> 7) << p.lg) | (int)rank) << 7) | (i & 127); };
+  auto owner = [&](uint32_t t) { return (t >> 7) & (ranks - 1); };
+  auto local = [&](uint32_t t) { return ((t >> 7 >> p.lg) << 7) | (t & 127); };
+  const int2 h = row_range(p.r.history_start, m, p.r.history_size, p.status);
+  const int2 b = row_range(p.r.bias_start, m, p.r.bias_size, p.status);
+  const int made_from = p.r.generated_from ? p.r.generated_from[m] : 0;
+  const RowRules r{p.r.repetition ? p.r.repetition[m] : 1.f, p.r.presence ? p.r.presence[m] : 0.f,
+                   p.r.frequency ? p.r.frequency[m] : 0.f};
+  const Words words{sm.words, h.y - h.x >= kShortHistory};
+  const int step = words.wide ? p.held / 2 : p.held;  // tokens that have words at a time
+  const bool rules = h.y > h.x || b.y > b.x;
+
+  float4 x[V];
+  uint32_t bits[V];
+  auto load = [&](int base, int end) {
 #pragma unroll
-    for (int k = 0; k < kAdjustVecs; ++k) {
-      const int t = base + (k * kAdjustThreads + tid) * 4;
-      if (t >= t1) continue;
+    for (int k = 0; k < V; ++k) {
+      const int i = base + (k * T + tid) * 4, t = token(i);
+      x[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      bits[k] = 0xFu;
+      if (i >= end || t >= p.n) continue;
       if (t + 4 <= p.n) {
         x[k] = *reinterpret_cast<const float4 *>(logits + t);
       } else {  // what lies past the last token is not read
         x[k].x = logits[t];
-        x[k].y = t + 1 < p.n ? logits[t + 1] : 0.f;
-        x[k].z = t + 2 < p.n ? logits[t + 2] : 0.f;
-        x[k].w = 0.f;
+        if (t + 1 < p.n) x[k].y = logits[t + 1];
+        if (t + 2 < p.n) x[k].z = logits[t + 2];
       }
-      bits[k] = allowed ? allowed[t >> 5] >> (t & 31) : 0xFu;
+      if (allowed) bits[k] = allowed[t >> 5] >> (t & 31);
     }
   };
-  load(t0);  // in flight while the history is counted
+  load(0, min(step, mine));  // in flight while the history is counted
 
-  const RowRules r{p.r.repetition ? p.r.repetition[m] : 1.f, p.r.presence ? p.r.presence[m] : 0.f,
-                   p.r.frequency ? p.r.frequency[m] : 0.f};
-  const int2 h = row_range(p.r.history_start, m, p.r.history_size, p.status);
-  const int2 b = row_range(p.r.bias_start, m, p.r.bias_size, p.status);
-  const int made_from = p.r.generated_from ? p.r.generated_from[m] : 0;
-  __syncthreads();
-  constexpr int kAhead = 8;
-  for (int i = h.x + tid; i < h.y; i += kAdjustThreads * kAhead) {
-    uint32_t t[kAhead];
+  bool listed = false;
+  if (h.y - h.x > 4 * T) {
+    if (tid == 0) list_n = 0;
+    cluster_sync_all();
+    const int every = T * (int)ranks;
+    constexpr int kAhead = 4;
+    for (int i0 = h.x + (int)rank * T; i0 < h.y; i0 += every * kAhead) {  // the same for every thread
+      uint32_t t[kAhead], at[kAhead], to_cta[kAhead], peers[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      t[k] = i + k * kAdjustThreads < h.y ? (uint32_t)p.r.history[i + k * kAdjustThreads] - (uint32_t)t0 : ~0u;
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (t[k] < (uint32_t)(t1 - t0) && t0 < t1) {
-        if (i + k * kAdjustThreads - h.x >= made_from) atomicAdd(&words[t[k]], 1u);
-        else atomicOr(&words[t[k]], kSeen);
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + tid + k * every;
+        t[k] = i < h.y ? (uint32_t)p.r.history[i] : ~0u;
       }
+      // one add for all of a warp's entries of the same owner: adds to one address wait for one another
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        to_cta[k] = t[k] < (uint32_t)p.n ? owner(t[k]) : ~0u;
+        peers[k] = __match_any_sync(0xffffffffu, to_cta[k]);
+        at[k] = 0;
+        if (to_cta[k] != ~0u && lane == __ffs(peers[k]) - 1)
+          asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;"
+                       : "=r"(at[k])
+                       : "r"(map_to_rank(smem_u32(&list_n), to_cta[k])), "r"(__popc(peers[k]))
+                       : "memory");
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t to = __shfl_sync(0xffffffffu, at[k], __ffs(peers[k]) - 1) + __popc(peers[k] & ((1u << lane) - 1));
+        if (to_cta[k] != ~0u && to < (uint32_t)kList)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32(&sm.list[to]), to_cta[k])),
+                       "r"(local(t[k]) | (i0 + tid + k * every - h.x >= made_from ? kMade : 0u))
+                       : "memory");
+      }
+    }
+    cluster_sync_all();
+    listed = list_n <= kList;  // else this CTA reads the history itself
   }
-  for (int i = b.x + tid; i < b.y; i += kAdjustThreads) {
-    const uint32_t t = (uint32_t)p.r.bias_id[i] - (uint32_t)t0;
-    if (t0 < t1 && t < (uint32_t)(t1 - t0) && (atomicOr(&words[t], kBiased) & kBiased)) duplicates = 1;
-  }
-  __syncthreads();
 
   Best best;
-  for (int base = t0; base < t1; base += kAdjustThreads * kAdjustVecs * 4) {
-    if (base != t0) load(base);
-#pragma unroll
-    for (int k = 0; k < kAdjustVecs; ++k) {
-      const int t = base + (k * kAdjustThreads + tid) * 4;
-      if (t >= t1 || !EXL3_SPAN(t - t0, 4, p.range)) continue;
-      const uint4 w = *reinterpret_cast<const uint4 *>(words + t - t0);
-      float v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-      if (w.x | w.y | w.z | w.w) {
-        v[0] = penalized(v[0], w.x, r);
-        v[1] = penalized(v[1], w.y, r);
-        v[2] = penalized(v[2], w.z, r);
-        v[3] = penalized(v[3], w.w, r);
-      }
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (!((bits[k] >> e) & 1u)) v[e] = -INFINITY;
-        if (!(ww[e] & kBiased) && t + e < p.n) best.see(v[e], t + e);
-      }
-      if (t + 4 <= p.n) {
-        *reinterpret_cast<float4 *>(out + t) = make_float4(v[0], v[1], v[2], v[3]);
+  for (int c0 = 0; c0 < mine; c0 += step) {
+    const int n = min(step, mine - c0);
+    if (rules) {
+      const int used = words.wide ? n : (n + 1) / 2;
+      for (int i = tid * 4; i < used; i += T * 4)
+        if (EXL3_SPAN(i, 4, p.held / 2)) *reinterpret_cast<uint4 *>(sm.words + i) = make_uint4(0, 0, 0, 0);
+      if (tid == 0) special_n = duplicates = 0;
+      __syncthreads();
+      // i: a token with a word, or anything else; every lane of the warp takes part
+      auto note = [&](uint32_t i, auto mark) {
+        const bool fresh = i < (uint32_t)n && mark((int)i) == 0;
+        const uint32_t all = __ballot_sync(0xffffffffu, fresh);
+        if (all == 0) return;
+        int at = 0;
+        if (lane == __ffs(all) - 1) at = atomicAdd(&special_n, __popc(all));
+        at = __shfl_sync(0xffffffffu, at, __ffs(all) - 1) + __popc(all & ((1u << lane) - 1));
+        if (fresh && at < kSpecial) sm.special[at] = i;
+      };
+      auto count = [&](uint32_t i, bool made) {
+        note(i, [&](int j) { return made ? words.count(j) : words.set(j, kSeen); });
+      };
+      auto word_of = [&](uint32_t t) { return t < (uint32_t)p.n && owner(t) == rank ? local(t) - (uint32_t)c0 : ~0u; };
+      if (listed) {
+        for (int i0 = 0; i0 < list_n; i0 += T) {
+          const uint32_t e = i0 + tid < list_n ? sm.list[i0 + tid] : ~0u;
+          count((e & ~kMade) - (uint32_t)c0, e & kMade);
+        }
       } else {
+        constexpr int kAhead = 8;
+        for (int i0 = h.x; i0 < h.y; i0 += T * kAhead) {
+          uint32_t t[kAhead];
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (t + e < p.n) out[t + e] = v[e];
+          for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + tid + k * T;
+            t[k] = i < h.y ? (uint32_t)p.r.history[i] : ~0u;
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) count(word_of(t[k]), i0 + tid + k * T - h.x >= made_from);
+        }
+      }
+      for (int i0 = b.x; i0 < b.y; i0 += T) {
+        const uint32_t t = i0 + tid < b.y ? (uint32_t)p.r.bias_id[i0 + tid] : ~0u;
+        note(word_of(t), [&](int j) {
+          const uint32_t was = words.set(j, kBiased);
+          if (was & kBiased) duplicates = 1;
+          return was;
+        });
+      }
+      __syncthreads();
+    }
+
+    int piece = INT_MAX;  // of the best token without a word
+    float top = best.x;
+    for (int base = 0; base < n; base += T * V * 4) {
+      if (c0 + base > 0) load(c0 + base, c0 + n);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int i = base + (k * T + tid) * 4, t = token(c0 + i);
+        const bool real = i < n && t < p.n;
+        float v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (bits[k] >> e) & 1u ? v[e] : -INFINITY;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (rules && real && EXL3_SPAN(i, 4, step)) w = words.four(i);
+        if (real) {
+          if (t + 4 <= p.n) {
+            *reinterpret_cast<float4 *>(out + t) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              if (t + e < p.n) out[t + e] = v[e];
+          }
+        }
+        if ((w.x | w.y | w.z | w.w) != 0) {  // those with a word: not by the stream
+          v[0] = w.x ? -INFINITY : v[0];
+          v[1] = w.y ? -INFINITY : v[1];
+          v[2] = w.z ? -INFINITY : v[2];
+          v[3] = w.w ? -INFINITY : v[3];
+        }
+        const float four = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        if (four > top) {
+          top = four;
+          piece = i;
+        }
       }
     }
-  }
-  if (b.y > b.x) {
-    // The stream has written l before the bias (or -inf) for the marked tokens;
-    // whoever clears a token's mark adds its bias: its entry, or all of them in
-    // their order where some token has several.
-    __syncthreads();
-    for (int i = b.x + tid; i < b.y; i += kAdjustThreads) {
+    if (piece != INT_MAX) {  // its first token of that value: the thread wrote it itself
+      const uint4 w = rules ? words.four(piece) : make_uint4(0, 0, 0, 0);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      const int t = token(c0 + piece);
+      for (int e = 0; e < 4; ++e)
+        if (t + e < p.n && ww[e] == 0 && out[t + e] == top) {
+          best.take(top, t + e);
+          break;
+        }
+    }
+    if (!rules) continue;
+    __syncthreads();  // the stream has written the tokens with a word as well: masked, not yet penalized
+    auto penalize = [&](int i) {
+      const uint32_t word = words.one(i);
+      if (word == 0 || (word & kBiased)) return;
+      const int t = token(c0 + i);
+      const float y = penalized(out[t], word, r);
+      out[t] = y;
+      if (y > -INFINITY) best.take(y, t);
+    };
+    if (special_n <= kSpecial)
+      for (int i = tid; i < special_n; i += T) penalize((int)sm.special[i]);
+    else  // too many to list: look at every word
+      for (int i = tid; i < n; i += T) penalize(i);
+    // A biased token is done by its entry, or by the first of several, which adds
+    // all of them up in their order.
+    for (int i = b.x + tid; i < b.y; i += T) {
       const int id = p.r.bias_id[i];
-      if (id < t0 || id >= t1 || !(atomicAnd(&words[id - t0], ~kBiased) & kBiased)) continue;
+      const uint32_t at = id >= 0 && id < p.n && owner((uint32_t)id) == rank ? local((uint32_t)id) - (uint32_t)c0 : ~0u;
+      if (at >= (uint32_t)n) continue;
+      const uint32_t word = words.one((int)at);
       float sum = p.r.bias_value[i];
       if (duplicates) {
+        bool first = true;
+        for (int j = b.x; j < i; ++j) first = first && p.r.bias_id[j] != id;
+        if (!first) continue;
         sum = 0.f;
-        for (int j = b.x; j < b.y; ++j)
+        for (int j = i; j < b.y; ++j)
           if (p.r.bias_id[j] == id) sum = __fadd_rn(sum, p.r.bias_value[j]);
       }
-      float v = out[id];
+      float y = out[id];
       if (!allowed || ((allowed[id >> 5] >> (id & 31)) & 1u)) {
-        v = __fadd_rn(v, sum);
-        out[id] = v;
+        y = __fadd_rn(penalized(y, word, r), sum);
+        out[id] = y;
       }
-      if (v > -INFINITY) best.take(v, id);
+      if (y > -INFINITY) best.take(y, id);
     }
+    __syncthreads();
   }
 
 #pragma unroll
@@ -201,7 +342,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 768 / kAdjustThreads) logits_a
   __syncthreads();
   if (tid < 32) {
     best = Best();
-    if (lane < kAdjustThreads / 32) best.take(sb[lane], si[lane]);
+    if (lane < T / 32) best.take(sb[lane], si[lane]);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) best.take(__shfl_xor_sync(0xffffffffu, best.x, k), __shfl_xor_sync(0xffffffffu, best.t, k));
     if (lane == 0) {  // to the first CTA of the cluster
@@ -223,18 +364,24 @@ __global__ void __launch_bounds__(kAdjustThreads, 768 / kAdjustThreads) logits_a
 cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules &r,
                                  float *out, int64_t ldo, int32_t *argmax, int *status, int num_sms, cudaStream_t st) {
   if (M == 0) return cudaSuccess;
-  // 2048 tokens (one piece a thread) to a CTA at least, up to 16 CTAs
-  int ranks = 1;
-  while (ranks < kMaxCluster && n > (int64_t)ranks * 2048) ranks *= 2;
-  AdjustParams p{logits, out, argmax, status, ldl, ldo, M, (int)n, (int)(ceil_div(n, 128 * ranks) * 128), r};
-  // Few rows: every CTA has an SM to itself and 512 threads hold its whole range;
-  // many rows: three CTAs of 256 threads an SM, so that one streams while another counts.
-  const bool few = M * ranks <= num_sms;
-  const auto kernel = few ? logits_adjust_kernel<512> : logits_adjust_kernel<256>;
+  // Few rows: clusters of up to 16 CTAs of 512 threads. Many rows: up to 8 of 256
+  // (clusters of 16 leave a quarter of the SMs without work), four an SM, so that
+  // one streams while another counts (64 rows of 248K tokens with all rules: 64 us;
+  // three an SM with twice the loads in flight 101 us, words for 8192 tokens at a
+  // time 81 us). At least 2048 tokens to a CTA.
+  const bool few = M * kMaxCluster <= num_sms;
+  const int most = few ? kMaxCluster : kMaxCluster / 2;
+  int lg = 0;
+  while ((1 << lg) < most && n > (int64_t)2048 << lg) ++lg;
+  const int ranks = 1 << lg;
+  const int64_t share = ceil_div(ceil_div(n, 128), ranks) * 128;
+  const int held = (int)(few || share < kHeld ? share : kHeld);
+  AdjustParams p{logits, out, argmax, status, ldl, ldo, M, (int)n, lg, held, r};
+  const auto kernel = few ? logits_adjust_kernel<512, 8, 1> : logits_adjust_kernel<256, 4, 4>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(M * ranks));
   cfg.blockDim = dim3(few ? 512 : 256);
-  cfg.dynamicSmemBytes = (size_t)p.range * 4;
+  cfg.dynamicSmemBytes = sizeof(AdjustSmem) + (size_t)held * 2;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -249,10 +396,10 @@ cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, in
 
 cudaError_t init_logits_adjust_kernels(int *status) {
   cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
-  for (const void *f : {(const void *)logits_adjust_kernel<256>, (const void *)logits_adjust_kernel<512>}) {
-    // the widest range: 2^19 tokens over 16 CTAs
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (1 << 19) / kMaxCluster * 4);
+  for (const void *f : {(const void *)logits_adjust_kernel<256, 4, 4>, (const void *)logits_adjust_kernel<512, 8, 1>}) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AdjustSmem) + (1 << 19) / 8 * 2);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   }
   return e;
 }
