@@ -95,6 +95,19 @@ __device__ __forceinline__ uint2 rescale_codes(uint2 c, float factor) {
   return make_uint2(o[0], o[1]);
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// log of a sum l of exponentials around m (log2 units).
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
+
+// First unit of worker w of W over T units, and the worker that owns unit z.
+__device__ __forceinline__ int64_t range_start(int64_t w, int64_t W, int64_t T) { return w * T / W; }
+__device__ __forceinline__ int64_t range_owner(int64_t z, int64_t W, int64_t T) { return ((z + 1) * W - 1) / T; }
+
 // softcap * tanh(s / softcap) through 1 - 2 / (exp(2 x) + 1): an absolute error
 // near softcap * 2^-23, which a direct tanh approximation (relative error 2^-11
 // of a score near the cap) would not give. exp overflows to inf: tanh is then 1.

@@ -117,10 +117,6 @@ __device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile
   __syncthreads();
 }
 
-// First unit of warp w of W over T units, and the warp that owns unit z.
-__device__ __forceinline__ int64_t range_start(int64_t w, int64_t W, int64_t T) { return w * T / W; }
-__device__ __forceinline__ int64_t range_owner(int64_t z, int64_t W, int64_t T) { return ((z + 1) * W - 1) / T; }
-
 // A place in the unit order; u < 0: entering the segment.
 struct Cursor {
   KvSeq q;
@@ -197,12 +193,6 @@ struct Blocks {
     }
   }
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -500,8 +490,6 @@ __device__ __forceinline__ void store_out(const KvAttention &a, int64_t row, int
     reinterpret_cast<uint4 *>(out)[k] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-
-__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
 
 // Parts of segments that a CTA's warps do not cover alone, two a warp: 2 w, the
 // end of a segment that began before the warp's range (in the workspace), and
@@ -903,6 +891,10 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
   }
 }
 
+// Rows of a (sequence, head) up to which the stream kernel takes a call: one tile.
+// More go to the tensor-core kernel of exl3_kv8_chunk.cu.
+constexpr int64_t kStreamRows = 16;
+
 // Up to 8 rows of a (sequence, head) in one tile: half the registers and
 // products of the 16-row tile.
 bool narrow(int64_t tile_rows) { return tile_rows <= 8; }
@@ -927,16 +919,6 @@ cudaError_t run_stream(const CUtensorMap &tk, const CUtensorMap &tv, const Strea
   if (e != cudaSuccess) return e;
   const dim3 join((unsigned)(p.a.kv.max_rows * (int64_t)p.group), p.a.kv.n_seqs, p.a.kv.n_kv_heads);
   return launch_overlapped(kv8_join_kernel<D, NT>, join, D, 0, st, 1, p);
-}
-
-// The sequences [s0, s0 + n) of a call.
-KvView slice(const KvView &kv, int s0, int n) {
-  KvView v = kv;
-  v.page_table += (int64_t)s0 * kv.max_pages;
-  v.kv_len += s0;
-  v.q_start += s0;
-  v.n_seqs = n;
-  return v;
 }
 
 // Floats of the workspace's parts, in the order of StreamParams; the plan first.
@@ -970,7 +952,7 @@ cudaError_t attention(const KvAttention &a, cudaStream_t st) {
   p.part_ml = ws + w.ml;
   p.first = ws + w.first;
   for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kMaxSeqs) {
-    p.a.kv = slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
+    p.a.kv = kv_slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
     const cudaError_t e = narrow(rows) ? run_stream<D, 1>(tk, tv, p, st) : run_stream<D, 2>(tk, tv, p, st);
     if (e != cudaSuccess) return e;
   }
@@ -989,7 +971,7 @@ cudaError_t weigh(const KvAttention &a, cudaStream_t st) {
   p.warps = a.num_sms * Cfg::kWarps;
   const size_t smem = Cfg::kSmem;
   for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kMaxSeqs) {
-    p.a.kv = slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
+    p.a.kv = kv_slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
     const cudaError_t e = a.softcap > 0.f ? launch_overlapped(kv8_weigh_kernel<D, true>, a.num_sms, kThreads, smem, st, 1, tk, p)
                                           : launch_overlapped(kv8_weigh_kernel<D, false>, a.num_sms, kThreads, smem, st, 1, tk, p);
     if (e != cudaSuccess) return e;
@@ -1016,11 +998,14 @@ cudaError_t init_dim() {
 
 size_t kv8_attention_workspace_bytes(const exl3_kv8_cache &c, const exl3_kv8_batch &b, int n_heads, int num_sms) {
   if (b.rows == 0 || b.n_seqs == 0 || b.max_rows == 0) return 16;
-  return (size_t)stream_workspace((int64_t)b.max_rows * (n_heads / c.n_kv_heads), c.head_dim, num_sms).total * sizeof(float);
+  const int64_t rows = (int64_t)b.max_rows * (n_heads / c.n_kv_heads);
+  if (rows > kStreamRows) return kv8_chunk_workspace_bytes(c.head_dim, num_sms);
+  return (size_t)stream_workspace(rows, c.head_dim, num_sms).total * sizeof(float);
 }
 
 cudaError_t launch_kv8_attention(const KvAttention &a, cudaStream_t st) {
   if (a.kv.rows == 0 || a.kv.n_seqs == 0 || a.kv.max_rows == 0) return cudaSuccess;
+  if ((int64_t)a.kv.max_rows * (a.n_heads / a.kv.n_kv_heads) > kStreamRows) return launch_kv8_chunk_attention(a, st);
   return a.kv.head_dim == 64 ? attention<64>(a, st) : attention<128>(a, st);
 }
 

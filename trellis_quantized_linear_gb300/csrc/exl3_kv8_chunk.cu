@@ -1,0 +1,695 @@
+// Attention over the 8-bit key/value cache for more than a few rows of a
+// sequence, on the 5th-gen tensor cores. Formulas in include/exl3.h.
+//
+// One CTA per SM. A segment is a (sequence, key/value head, 256 rows of its group
+// in token order: two tiles of 128); its units are 128 cached tokens. All units of
+// all segments lie one behind the other, and each CTA takes one equal, contiguous
+// range of them; segments that several CTAs share are joined by a second kernel.
+// Per unit:
+//   * warps 9..11 (converters): the unit's keys and values from global memory, one
+//     operand ahead in registers, to fp16 (exact) in the two-stage operand buffers
+//     (128-byte swizzle; the same layout serves keys as the K-major operand of
+//     Q K^T and values as the MN-major operand of P V). Each block's scale goes in
+//     as a power of two relative to the segment's largest, so one factor serves
+//     all scores and all outputs of a segment; only codes 2^15 and more below that
+//     largest block's lose bits, 2^-25 of it at most;
+//   * warp 8 (one lane): for each tile tcgen05.mma S = Q K^T into TMEM, then, when
+//     the tile's probabilities are there, O += P V with P read from TMEM, where it
+//     has taken the place of S;
+//   * warps 0..3 / 4..7 (tile 0 / 1; thread = row = TMEM lane): the row's 128
+//     scores in registers, mask, maximum, exp2, sum, probabilities as fp16 back to
+//     TMEM. While one tile's softmax runs, the tensor core works on the other's
+//     products. O is rescaled only when the maximum grows by more than 2^8 over
+//     the reference in use (the result is the same: the sum uses that reference),
+//     so rarely after the first units.
+// TMEM: S0 S1 O0 O1, 128 columns each.
+#include <cuda.h>
+
+#include "exl3_internal.h"
+#include "exl3_kv8.cuh"
+#include "exl3_tcgen05.cuh"
+
+namespace exl3 {
+
+namespace {
+
+constexpr int kTile = 128, kPair = 2 * kTile;  // rows
+constexpr int kTokens = 128;                   // of a unit
+constexpr int kChunkThreads = 384;
+constexpr int kConvWarps = 3;
+constexpr int kChunkSeqs = 1024;               // sequences of one launch
+// Entering a segment (queries, the blocks' largest scales, the output), in units.
+constexpr int kChunkEntry = 3;
+constexpr float kLazy = 8.0f;                  // log2 of how far a maximum may pass the reference
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kOperand = kHalves * 128 * 128;   // 128 rows (or tokens) x D fp16
+  static constexpr int kOffK = 2 * kOperand;             // two query tiles before it
+  static constexpr int kOffV = kOffK + 2 * kOperand;
+  static constexpr int kOffPlan = kOffV + 2 * kOperand;  // int64 prefix, scratch, int2 sequences
+  static constexpr int kOffBar = kOffPlan + (kChunkSeqs + 32) * 8 + (kChunkSeqs + 8) * 8;
+  static constexpr int kSmem = 1024 + kOffBar + 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+enum { kBarQ = 0, kBarKFull = 2, kBarKEmpty = 4, kBarVFull = 6, kBarVEmpty = 8, kBarS = 10, kBarP = 12, kBarO = 14,
+       kBarDone = 16, kNumBars = 17 };
+
+struct ChunkParams {
+  KvAttention a;
+  int group, ctas;
+  // Workspace: partial results of the CTAs (slot 0: a segment that began before
+  // the CTA's range, slot 1: one that began in it and goes on after it) and the plan.
+  float *part_o;      // CTAs x 2 x 256 x D
+  float *part_ml;     // CTAs x 2 x 256 x 2
+  int64_t *plan;
+  int64_t part_rows;  // 2 * CTAs * 256
+};
+
+// Units of the pair of tiles rt of a sequence: as far as its last row sees.
+__device__ __forceinline__ int pair_units(const KvSeq &q, int group, int causal, int rt) {
+  const int last = min((rt + 1) * kPair, q.rows * group) - 1;
+  const int seen = causal ? q.len - q.rows + last / group + 1 : q.len;
+  return seen > 0 ? (seen + kTokens - 1) / kTokens : 0;
+}
+__device__ __forceinline__ int pair_cost(const KvSeq &q, int group, int causal, int rt) {
+  const int u = pair_units(q, group, causal, rt);
+  return u > 0 ? u + kChunkEntry : 0;
+}
+__device__ __forceinline__ int pairs_of(const KvSeq &q, int group) { return (q.rows * group + kPair - 1) / kPair; }
+
+struct ChunkPlan {
+  int64_t *prefix;  // kChunkSeqs + 1, then scratch
+  int2 *seq;
+  __device__ __forceinline__ KvSeq at(int s) const {
+    const int2 a = seq[s];
+    return KvSeq{a.x, a.y < 0 ? 0 : seq[s + 1].x - a.x, a.y < 0 ? 0 : a.y};
+  }
+};
+
+// Ends with a barrier.
+__device__ __forceinline__ void build_chunk_plan(const KvView &kv, int group, int causal, const ChunkPlan &plan) {
+  int64_t *warp_sum = plan.prefix + kChunkSeqs + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  int64_t carry = 0;
+  if (threadIdx.x == 0) plan.prefix[0] = 0;
+  for (int c = 0; c < kv.n_seqs; c += blockDim.x) {
+    const int s = c + (int)threadIdx.x;
+    int64_t n = 0;
+    if (s < kv.n_seqs) {
+      const KvSeq q = kv_sequence(kv, s);
+      for (int rt = 0; rt < pairs_of(q, group); ++rt) n += pair_cost(q, group, causal, rt);
+      n *= kv.n_kv_heads;
+      plan.seq[s] = make_int2(kv.q_start[s], q.rows > 0 ? q.len : -1);
+      if (s + 1 == kv.n_seqs) plan.seq[s + 1] = make_int2(kv.q_start[s + 1], -1);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += o;
+    }
+    if (lane == 31) warp_sum[warp] = n;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < nwarps; ++w) {
+      const int64_t x = warp_sum[w];
+      if (w < warp) n += x;
+      total += x;
+    }
+    if (s < kv.n_seqs) plan.prefix[s + 1] = carry + n;
+    carry += total;
+    __syncthreads();
+  }
+  __syncthreads();
+}
+
+// A CTA's part of a segment: units u0 .. u1 - 1 of `units`.
+struct Segment {
+  KvSeq q;
+  int s, h, rt, rows;  // rows of the pair that exist
+  int units, u0, u1;
+};
+struct Walk {
+  int64_t z0, z1, zs;  // the CTA's range; where the segment (s, h, rt) begins
+  KvSeq q;
+  int s, h, rt;
+  __device__ __forceinline__ void begin(const KvView &kv, int group, int causal, const ChunkPlan &plan, int64_t a, int64_t b) {
+    z0 = a;
+    z1 = b;
+    int lo = 0, hi = kv.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (plan.prefix[mid + 1] > a) hi = mid;
+      else lo = mid + 1;
+    }
+    s = lo;
+    q = plan.at(s);
+    const int64_t head = (plan.prefix[s + 1] - plan.prefix[s]) / kv.n_kv_heads;
+    h = (int)((a - plan.prefix[s]) / head);
+    zs = plan.prefix[s] + h * head;
+    rt = 0;
+    for (int c; zs + (c = pair_cost(q, group, causal, rt)) <= a; ++rt) zs += c;
+  }
+  __device__ __forceinline__ bool next(const KvView &kv, int group, int causal, const ChunkPlan &plan, Segment &g) {
+    while (zs < z1) {
+      g.units = pair_units(q, group, causal, rt);
+      const int64_t first = zs + kChunkEntry;
+      g.u0 = (int)max(z0 - first, (int64_t)0);
+      g.u1 = (int)min((int64_t)g.units, z1 - first);
+      g.q = q;
+      g.s = s;
+      g.h = h;
+      g.rt = rt;
+      g.rows = min(kPair, q.rows * group - rt * kPair);
+      zs += g.units > 0 ? g.units + kChunkEntry : 0;
+      if (++rt == pairs_of(q, group)) {
+        rt = 0;
+        if (++h == kv.n_kv_heads) {
+          h = 0;
+          do ++s;
+          while (s < kv.n_seqs && plan.prefix[s + 1] == plan.prefix[s]);
+          if (s < kv.n_seqs) q = plan.at(s);
+          else zs = z1;
+        }
+      }
+      if (g.units > 0 && g.u1 > g.u0) return true;
+    }
+    return false;
+  }
+};
+
+// The largest exponents of the key and value scales of a segment's blocks. The
+// whole warp takes part.
+__device__ __forceinline__ int2 largest_scales(const KvView &kv, const Segment &g, int lane) {
+  const int blocks = min(g.units * (kTokens / kKvBlock), (g.q.len + kKvBlock - 1) / kKvBlock);
+  int ek = -127, ev = -127;
+#pragma unroll 4
+  for (int b = lane; b < blocks; b += 32) {
+    const int page = kv_page(kv, g.s, b);
+    if (page < 0) continue;
+    const int64_t slab = (int64_t)page * kv.n_kv_heads + g.h;
+    ek = max(ek, pow2_exponent(kv.k_scale[slab]));
+    ev = max(ev, pow2_exponent(kv.v_scale[slab]));
+  }
+  return make_int2(__reduce_max_sync(0xffffffffu, ek), __reduce_max_sync(0xffffffffu, ev));
+}
+
+// Byte offset of 16-byte piece c (of 8) of 128-byte row r in a swizzled operand half.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  if (EXL3_SMEM(addr, 16))
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 16 codes to two 16-byte pieces of fp16, times a power of two (one: none).
+__device__ __forceinline__ void convert_16(uint4 w, bool times, __half2 factor, uint32_t (&o)[8]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = e4m3x2_to_half2((uint16_t)(x[i] & 0xFFFFu));
+    o[2 * i + 1] = e4m3x2_to_half2((uint16_t)(x[i] >> 16));
+  }
+  if (times) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&o[i]), factor);
+      o[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+  }
+}
+
+// One lane's share of a unit's operand: pieces i = it * kConvWarps + cw of 32, each
+// 4 tokens (D = 128) or 8 (D = 64) of 16 codes a lane.
+template <int D>
+struct Operand {
+  static constexpr int kPieces = kTokens * D / 16 / 32;                 // warp-wide pieces
+  static constexpr int kMine = (kPieces + kConvWarps - 1) / kConvWarps;
+  static constexpr int kPerToken = D / 16;                              // lanes of a token
+  uint4 w[kMine];
+  __device__ __forceinline__ void load(const uint8_t *codes, const int64_t (&slab)[2], int tokens, int cw, int lane, int64_t size) {
+#pragma unroll
+    for (int it = 0; it < kMine; ++it) {
+      const int i = it * kConvWarps + cw;
+      const int tok = i * (32 / kPerToken) + lane / kPerToken, c = lane % kPerToken;
+      w[it] = make_uint4(0, 0, 0, 0);  // tokens past the sequence, and pages that the table does not name
+      if (i < kPieces && tok < tokens && slab[tok / kKvBlock] >= 0) {
+        const int64_t off = (slab[tok / kKvBlock] * kKvBlock + tok % kKvBlock) * D + c * 16;
+        if (EXL3_SPAN(off, 16, size)) w[it] = *reinterpret_cast<const uint4 *>(codes + off);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint32_t dst, const float (&factor)[2], int cw, int lane) const {
+#pragma unroll
+    for (int it = 0; it < kMine; ++it) {
+      const int i = it * kConvWarps + cw;
+      if (i >= kPieces) continue;
+      const int tok = i * (32 / kPerToken) + lane / kPerToken, c = lane % kPerToken;
+      const float f = factor[i * (32 / kPerToken) / kKvBlock];  // one block to a piece
+      uint32_t o[8];
+      convert_16(w[it], f != 1.0f, __float2half2_rn(f), o);
+      const uint32_t half = dst + (c >> 2) * (128 * 128);
+      // lanes of the second half of the dimension store their odd piece first: eight different bank groups
+      const int p = 2 * (c & 3), odd = c >> 2;
+      sts16(half + swizzled(tok, p + odd), odd ? o[4] : o[0], odd ? o[5] : o[1], odd ? o[6] : o[2], odd ? o[7] : o[3]);
+      sts16(half + swizzled(tok, p + (odd ^ 1)), odd ? o[0] : o[4], odd ? o[1] : o[5], odd ? o[2] : o[6], odd ? o[3] : o[7]);
+    }
+  }
+};
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const ChunkParams p) {
+  using Cfg = ChunkCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t base = smem_u32(smem);
+  const KvView &kv = p.a.kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const ChunkPlan plan{reinterpret_cast<int64_t *>(smem + Cfg::kOffPlan),
+                       reinterpret_cast<int2 *>(smem + Cfg::kOffPlan + (kChunkSeqs + 32) * 8)};
+  const uint32_t bars = base + Cfg::kOffBar;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kOffBar + 8 * kNumBars);
+  int *status = kv.status;
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(kBarQ + t), 4);
+      mbar_init(bar(kBarKFull + t), kConvWarps);
+      mbar_init(bar(kBarKEmpty + t), 1);
+      mbar_init(bar(kBarVFull + t), kConvWarps);
+      mbar_init(bar(kBarVEmpty + t), 1);
+      mbar_init(bar(kBarS + t), 1);
+      mbar_init(bar(kBarP + t), 4);
+      mbar_init(bar(kBarO + t), 1);
+    }
+    mbar_init(bar(kBarDone), 1);
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  tc_fence_before();
+  build_chunk_plan(kv, p.group, p.a.causal, plan);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t T = plan.prefix[kv.n_seqs], W = min((int64_t)p.ctas, T);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= kv.n_seqs; i += kChunkThreads) p.plan[i] = plan.prefix[i];
+
+  if (blockIdx.x < W) {
+    Walk walk;
+    walk.begin(kv, p.group, p.a.causal, plan, range_start(blockIdx.x, W, T), range_start(blockIdx.x + 1, W, T));
+    Segment g;
+    if (warp == 8) {
+      // ---------------- tensor core (one lane) ----------------
+      if (lane == 0) {
+        constexpr uint32_t kIdescS = f16_idesc(kTile, kTokens), kIdescO = f16_idesc(kTile, D) | kIdescBTransposed;
+        uint32_t unit = 0, seg_of[2] = {0, 0}, done_of[2] = {0, 0};  // units of the CTA; segments and units of a tile
+        bool ok = true;
+        auto scores = [&](int t, uint32_t n) {
+          const uint32_t q = base + t * Cfg::kOperand, k = base + Cfg::kOffK + (n & 1) * Cfg::kOperand;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const uint32_t off = (j >> 2) * (128 * 128) + (j & 3) * 32;
+            tc_mma(tmem + 128 * t, sw128_desc(q + off), sw128_desc(k + off), kIdescS, j > 0);
+          }
+          tc_commit(bar(kBarS + t));
+        };
+        while (ok && walk.next(kv, p.group, p.a.causal, plan, g)) {
+          const int tiles = g.rows > kTile ? 2 : 1, n = g.u1 - g.u0;
+          ok = mbar_wait(bar(kBarKFull + (unit & 1)), (unit >> 1) & 1, status);
+          for (int t = 0; ok && t < tiles; ++t) {
+            ok = mbar_wait(bar(kBarQ + t), seg_of[t]++ & 1, status);
+            if (!ok) break;
+            tc_fence_after();
+            scores(t, unit);
+          }
+          if (ok) tc_commit(bar(kBarKEmpty + (unit & 1)));
+          for (int j = 0; ok && j < n; ++j, ++unit) {
+            for (int t = 0; ok && t < tiles; ++t) {
+              if (t == 0) ok = mbar_wait(bar(kBarVFull + (unit & 1)), (unit >> 1) & 1, status);
+              ok = ok && mbar_wait(bar(kBarP + t), done_of[t]++ & 1, status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t v = base + Cfg::kOffV + (unit & 1) * Cfg::kOperand;
+#pragma unroll
+              for (int k = 0; k < kTokens / 16; ++k)
+                tc_mma_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, sw128_mn_desc(v + k * 2048, 128 * 128, 1024), kIdescO,
+                          (j | k) > 0);
+              tc_commit(bar(kBarO + t));
+              if (j + 1 < n) {
+                if (t == 0) ok = mbar_wait(bar(kBarKFull + ((unit + 1) & 1)), ((unit + 1) >> 1) & 1, status);
+                if (!ok) break;
+                tc_fence_after();
+                scores(t, unit + 1);
+              }
+            }
+            if (!ok) break;
+            tc_commit(bar(kBarVEmpty + (unit & 1)));
+            if (j + 1 < n) tc_commit(bar(kBarKEmpty + ((unit + 1) & 1)));
+          }
+        }
+        tc_commit(bar(kBarDone));  // every issued product ends before the TMEM is released
+        mbar_wait_short(bar(kBarDone), 0);
+      }
+    } else if (warp > 8) {
+      // ---------------- converters ----------------
+      const int cw = warp - 9;
+      const int64_t size = kv.n_pages * kv.n_kv_heads * kKvBlock * (int64_t)D;
+      const float sign = p.a.scale < 0.f ? -1.f : 1.f;
+      // powers of two below fp16's range are 0 (see above)
+      auto factor = [&](float scale, int top) {
+        const int d = pow2_exponent(scale) - top;
+        return d >= -24 ? pow2i(d) : 0.f;
+      };
+      uint32_t unit = 0;
+      bool more = walk.next(kv, p.group, p.a.causal, plan, g);
+      int u = g.u0;
+      int2 top = make_int2(0, 0);
+      int64_t slab[2] = {-1, -1}, slab_n[2] = {-1, -1};
+      float fk[2], fv[2];
+      auto find = [&](const Segment &s, int at, int64_t (&to)[2]) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int block = 2 * at + b;
+          const int page = block * kKvBlock < s.q.len ? kv_page(kv, s.s, block) : -1;
+          to[b] = page < 0 ? -1 : (int64_t)page * kv.n_kv_heads + s.h;
+        }
+      };
+      auto factors = [&]() {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          fk[b] = slab[b] < 0 ? 1.f : sign * factor(kv.k_scale[slab[b]], top.x);
+          fv[b] = slab[b] < 0 ? 1.f : factor(kv.v_scale[slab[b]], top.y);
+        }
+      };
+      Operand<D> keys, values;
+      if (more) {
+        top = largest_scales(kv, g, lane);
+        find(g, u, slab);
+        keys.load(kv.k, slab, g.q.len - u * kTokens, cw, lane, size);
+        factors();
+      }
+      while (more) {
+        // the unit after this one
+        Segment gn = g;
+        int un = u + 1;
+        bool more_n = true;
+        if (un == g.u1) {
+          more_n = walk.next(kv, p.group, p.a.causal, plan, gn);
+          un = gn.u0;
+        }
+        if (more_n) find(gn, un, slab_n);
+        values.load(kv.v, slab, g.q.len - u * kTokens, cw, lane, size);
+        const uint32_t st = unit & 1, ph = (unit >> 1) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarKEmpty + st), ph ^ 1, status))) break;
+        keys.store(base + Cfg::kOffK + st * Cfg::kOperand, fk, cw, lane);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarKFull + st));
+        if (more_n) keys.load(kv.k, slab_n, gn.q.len - un * kTokens, cw, lane, size);
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarVEmpty + st), ph ^ 1, status))) break;
+        values.store(base + Cfg::kOffV + st * Cfg::kOperand, fv, cw, lane);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarVFull + st));
+        ++unit;
+        if (more_n) {
+          if (un != u + 1 || gn.s != g.s || gn.h != g.h || gn.rt != g.rt) top = largest_scales(kv, gn, lane);
+          slab[0] = slab_n[0];
+          slab[1] = slab_n[1];
+          factors();
+        }
+        g = gn;
+        u = un;
+        more = more_n;
+      }
+    } else {
+      // ---------------- softmax: thread = row of tile t ----------------
+      const int t = warp >> 2, row = threadIdx.x & 127;
+      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t s_tmem = lane_base + 128 * t, o_tmem = lane_base + 256 + 128 * t;
+      const float cap = p.a.softcap, inv_cap = CAP ? 1.0f / cap : 0.f;
+      uint32_t count = 0;  // units of this tile so far
+      bool ok = true;
+      while (ok && walk.next(kv, p.group, p.a.causal, plan, g)) {
+        if (t * kTile >= g.rows) continue;  // the pair has no second tile
+        const int j = g.rt * kPair + t * kTile + row, i = j / p.group;
+        const bool real = i < g.q.rows;
+        const int head = g.h * p.group + j - i * p.group;
+        const int limit = !real ? 0 : p.a.causal ? g.q.len - g.q.rows + i + 1 : g.q.len;
+        const int least = __reduce_min_sync(0xffffffffu, limit);
+        {  // the query row; the products that read the last segment's are done (its scores have been read)
+          const int64_t off = (int64_t)(g.q.row0 + i) * p.a.ldq + (int64_t)head * D;
+          const __half *q = static_cast<const __half *>(p.a.q) + off;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (real && EXL3_SPAN(off + 8 * c, 8, (int64_t)(kv.rows - 1) * p.a.ldq + (int64_t)p.a.n_heads * D))
+              v = reinterpret_cast<const uint4 *>(q)[c];
+            sts16(base + t * Cfg::kOperand + (c >> 3) * (128 * 128) + swizzled(row, c & 7), v.x, v.y, v.z, v.w);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarQ + t));
+        }
+        const int2 top_scale = largest_scales(kv, g, lane);
+        // scores in log2 units are the products times c (without a cap)
+        const float c = fmaxf(fabsf(p.a.scale) * pow2i(top_scale.x) * (CAP ? 1.0f : kLog2e), 1e-37f);
+        float ref = -INFINITY, sum = 0.f;
+        for (int u = g.u0; u < g.u1; ++u, ++count) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarS + t), count & 1, status))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float s[128];
+          tmem_ld128(s_tmem, s);
+          if constexpr (CAP) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k) s[k] = soft_cap(s[k] * c, cap, inv_cap) * kLog2e;
+          }
+          if (u * kTokens + kTokens > least) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              if (u * kTokens + k >= limit) s[k] = -INFINITY;
+          }
+          float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int k = 4; k < 128; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
+          const float scale = CAP ? 1.0f : c;
+          const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
+          const float now = top > ref + kLazy || ref == -INFINITY ? top : ref;
+          const float keep = now == ref || ref == -INFINITY ? 1.0f : ex2(ref - now);
+          if (u > g.u0 && __any_sync(0xffffffffu, keep != 1.0f)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarO + t), (count - 1) & 1, status))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              float o[32];
+              tmem_ld32(o_tmem + 32 * k, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= keep;
+              tmem_st32(o_tmem + 32 * k, o);
+            }
+            sum *= keep;
+          }
+          ref = now;
+          const float shift = now == -INFINITY ? 0.f : -now;
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 128; ++k) {
+            s[k] = ex2(fmaf(s[k], scale, shift));
+            s4[k & 3] += s[k];
+          }
+          sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float packed[32];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const __half2 x = __floats2half2_rn(s[64 * hf + 2 * k], s[64 * hf + 2 * k + 1]);
+              packed[k] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&x));
+            }
+            tmem_st32(s_tmem + 32 * hf, packed);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarP + t));
+        }
+        if (!ok || !__all_sync(0xffffffffu, mbar_wait(bar(kBarO + t), (count - 1) & 1, status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool whole = g.u0 == 0 && g.u1 == g.units;
+        const float unit = pow2i(min(max(top_scale.y, -126), 127));
+        const float f = whole ? (sum == 0.f ? 0.f : unit / sum) : unit;
+        const int64_t slot = ((int64_t)blockIdx.x * 2 + (g.u0 == 0 ? 1 : 0)) * kPair + t * kTile + row;
+        const int64_t off = (int64_t)(g.q.row0 + i) * p.a.ldo + (int64_t)head * D;
+        const bool fits = whole ? EXL3_SPAN(real ? off : 0, D, (int64_t)(kv.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D)
+                                : EXL3_SPAN(slot, 1, p.part_rows);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          float o[32];
+          tmem_ld32(o_tmem + 32 * k, o);
+          if (!real || !fits) continue;
+          if (whole) {
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(p.a.out) + off + 32 * k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const __half2 h2 = __floats2half2_rn(o[8 * e + 2 * x] * f, o[8 * e + 2 * x + 1] * f);
+                w[x] = *reinterpret_cast<const uint32_t *>(&h2);
+              }
+              out[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float4 *out = reinterpret_cast<float4 *>(p.part_o + slot * D + 32 * k);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              out[e] = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+          }
+        }
+        if (real && fits) {
+          if (!whole) reinterpret_cast<float2 *>(p.part_ml)[slot] = make_float2(ref, sum);
+          else if (p.a.lse) p.a.lse[(int64_t)(g.q.row0 + i) * p.a.n_heads + head] = log_sum(ref, sum);
+        }
+        tc_fence_before();  // the output has been read: before the next segment's first products
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// Joins the partials of the segments that several CTAs worked on, in the order of
+// the CTAs, and writes the rows that see no token. A CTA has 64 rows of a
+// (sequence, key/value head), a warp one row at a time.
+constexpr int kJoinRows = 64, kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const ChunkParams p) {
+  const KvView &kv = p.a.kv;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int s = blockIdx.y, h = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const KvSeq q = kv_sequence(kv, s);
+  const int j0 = blockIdx.x * kJoinRows, rt = j0 / kPair;
+  if (j0 >= q.rows * p.group) return;
+  const int units = pair_units(q, p.group, p.a.causal, rt);
+  int64_t c0 = 0, c1 = -1;
+  if (units > 0) {
+    int before = 0;
+    for (int r = lane; r < rt; r += 32) before += pair_cost(q, p.group, p.a.causal, r);
+    before = __reduce_add_sync(0xffffffffu, before);
+    const int64_t T = p.plan[kv.n_seqs], W = min((int64_t)p.ctas, T);
+    const int64_t z = p.plan[s] + (p.plan[s + 1] - p.plan[s]) / kv.n_kv_heads * h + before + kChunkEntry;
+    c0 = range_owner(z, W, T);
+    c1 = range_owner(z + units - 1, W, T);
+    if (c0 == c1) return;  // the CTA wrote the result
+  }
+  constexpr int E = D / 32;
+  for (int j = j0 + warp; j < j0 + kJoinRows; j += kJoinThreads / 32) {
+    const int i = j / p.group;
+    if (i >= q.rows) return;
+    float m = -INFINITY, l = 0.f, o[E] = {};
+    for (int64_t c = c0; c <= c1; ++c) {
+      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * kPair + j % kPair;
+      if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
+      const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
+      const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+      const float a = ex2(m - ref), b = ex2(ml.x - ref);
+      l = l * a + ml.y * b;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * a + p.part_o[at * D + 32 * e + lane] * b;
+      m = top;
+    }
+    const int head = h * p.group + j - i * p.group;
+    const int64_t row = q.row0 + i, off = row * p.a.ldo + (int64_t)head * D;
+    if (EXL3_SPAN(off, D, (int64_t)(kv.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D))
+#pragma unroll
+      for (int e = 0; e < E; ++e) static_cast<__half *>(p.a.out)[off + 32 * e + lane] = __float2half_rn(l == 0.f ? 0.f : o[e] / l);
+    if (p.a.lse && lane == 0) p.a.lse[row * p.a.n_heads + head] = log_sum(m, l);
+  }
+}
+
+struct ChunkWorkspace {  // in floats; the plan first
+  int64_t part_rows, o, ml, total;
+};
+ChunkWorkspace chunk_workspace(int D, int num_sms) {
+  ChunkWorkspace w;
+  w.part_rows = (int64_t)num_sms * 2 * kPair;
+  w.o = 2 * (kChunkSeqs + 8);
+  w.ml = w.o + w.part_rows * D;
+  w.total = w.ml + w.part_rows * 2;
+  return w;
+}
+
+template <int D>
+cudaError_t chunk_attention(const KvAttention &a, cudaStream_t st) {
+  ChunkParams p;
+  p.a = a;
+  p.group = a.n_heads / a.kv.n_kv_heads;
+  p.ctas = a.num_sms;
+  const ChunkWorkspace w = chunk_workspace(D, a.num_sms);
+  float *ws = static_cast<float *>(a.workspace);
+  p.plan = reinterpret_cast<int64_t *>(ws);
+  p.part_o = ws + w.o;
+  p.part_ml = ws + w.ml;
+  p.part_rows = w.part_rows;
+  for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kChunkSeqs) {
+    p.a.kv = kv_slice(a.kv, s0, a.kv.n_seqs - s0 < kChunkSeqs ? a.kv.n_seqs - s0 : kChunkSeqs);
+    cudaError_t e = launch_overlapped(a.softcap > 0.f ? kv8_chunk_kernel<D, true> : kv8_chunk_kernel<D, false>, p.ctas,
+                                      kChunkThreads, ChunkCfg<D>::kSmem, st, 1, p);
+    if (e != cudaSuccess) return e;
+    const dim3 join((unsigned)ceil_div((int64_t)a.kv.max_rows * p.group, kJoinRows), p.a.kv.n_seqs, a.kv.n_kv_heads);
+    e = launch_overlapped(kv8_chunk_join_kernel<D>, join, kJoinThreads, 0, st, 1, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t kv8_chunk_workspace_bytes(int head_dim, int num_sms) {
+  return (size_t)chunk_workspace(head_dim, num_sms).total * sizeof(float);
+}
+
+cudaError_t launch_kv8_chunk_attention(const KvAttention &a, cudaStream_t st) {
+  return a.kv.head_dim == 64 ? chunk_attention<64>(a, st) : chunk_attention<128>(a, st);
+}
+
+cudaError_t init_kv8_chunk_kernels(int *status) {
+  cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
+  for (const void *f : {(const void *)kv8_chunk_kernel<64, false>, (const void *)kv8_chunk_kernel<64, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<64>::kSmem);
+  for (const void *f : {(const void *)kv8_chunk_kernel<128, false>, (const void *)kv8_chunk_kernel<128, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<128>::kSmem);
+  cudaFuncAttributes attr;
+  for (const void *f : {(const void *)kv8_chunk_join_kernel<64>, (const void *)kv8_chunk_join_kernel<128>})
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, f);
+  return e;
+}
+
+#if EXL3_DEBUG_BOUNDS
+cudaError_t bounds_probe_kv8_chunk(cudaStream_t st) { return launch_bounds_probe(st); }
+#endif
+
+}  // namespace exl3

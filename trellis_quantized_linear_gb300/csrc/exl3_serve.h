@@ -35,8 +35,19 @@ struct KvAttention {
   int num_sms;
 };
 
+// The sequences [s0, s0 + n) of a call.
+inline KvView kv_slice(const KvView &kv, int s0, int n) {
+  KvView v = kv;
+  v.page_table += (int64_t)s0 * kv.max_pages;
+  v.kv_len += s0;
+  v.q_start += s0;
+  v.n_seqs = n;
+  return v;
+}
+
 cudaError_t init_kv8_cache_kernels(int *status);
 cudaError_t init_kv8_attention_kernels(int *status);
+cudaError_t init_kv8_chunk_kernels(int *status);
 cudaError_t init_logits_adjust_kernels(int *status);
 
 cudaError_t launch_kv8_append(const KvView &kv, const void *k, int64_t ldk, const void *v, int64_t ldv, cudaStream_t st);
@@ -44,6 +55,9 @@ cudaError_t launch_kv8_evict(const KvView &kv, const int32_t *dst_pages, int bud
                              int32_t *new_len, int num_sms, cudaStream_t st);
 size_t kv8_attention_workspace_bytes(const exl3_kv8_cache &cache, const exl3_kv8_batch &batch, int n_heads, int num_sms);
 cudaError_t launch_kv8_attention(const KvAttention &p, cudaStream_t st);
+// More rows than the stream kernel takes (exl3_kv8_chunk.cu).
+size_t kv8_chunk_workspace_bytes(int head_dim, int num_sms);
+cudaError_t launch_kv8_chunk_attention(const KvAttention &p, cudaStream_t st);
 // lse of the call that p describes; adds to p.kv.weight.
 cudaError_t launch_kv8_weigh(const KvAttention &p, cudaStream_t st);
 cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules &r,
@@ -52,6 +66,7 @@ cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, in
 #if EXL3_DEBUG_BOUNDS
 cudaError_t bounds_probe_kv8_cache(cudaStream_t st);
 cudaError_t bounds_probe_kv8_attention(cudaStream_t st);
+cudaError_t bounds_probe_kv8_chunk(cudaStream_t st);
 cudaError_t bounds_probe_logits_adjust(cudaStream_t st);
 #endif
 
