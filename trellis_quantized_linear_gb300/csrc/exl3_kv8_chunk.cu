@@ -6,7 +6,7 @@
 // all segments lie one behind the other, and each CTA takes one equal, contiguous
 // range of them; segments that several CTAs share are joined by a second kernel.
 // Per unit:
-//   * warps 9..11 (converters): the unit's keys and values from global memory, one
+//   * warps 9..16 (converters): the unit's keys and values from global memory, one
 //     operand ahead in registers, to fp16 (exact) in the two-stage operand buffers
 //     (128-byte swizzle; the same layout serves keys as the K-major operand of
 //     Q K^T and values as the MN-major operand of P V). Each block's scale goes in
@@ -17,8 +17,8 @@
 //     the tile's probabilities are there, O += P V with P read from TMEM, where it
 //     has taken the place of S;
 //   * warps 0..3 / 4..7 (tile 0 / 1; thread = row = TMEM lane): the row's 128
-//     scores in registers, mask, maximum, exp2, sum, probabilities as fp16 back to
-//     TMEM. While one tile's softmax runs, the tensor core works on the other's
+//     scores, 64 at a time: maximum first, then mask, exp2, sum, probabilities as
+//     fp16 back to TMEM. While one tile's softmax runs, the tensor core works on the other's
 //     products. O is rescaled only when the maximum grows by more than 2^8 over
 //     the reference in use (the result is the same: the sum uses that reference),
 //     so rarely after the first units.
@@ -35,8 +35,8 @@ namespace {
 
 constexpr int kTile = 128, kPair = 2 * kTile;  // rows
 constexpr int kTokens = 128;                   // of a unit
-constexpr int kChunkThreads = 384;
-constexpr int kConvWarps = 3;
+constexpr int kConvWarps = 8;
+constexpr int kChunkThreads = (9 + kConvWarps) * 32;  // 96 registers a thread
 constexpr int kChunkSeqs = 1024;               // sequences of one launch
 // Entering a segment (queries, the blocks' largest scales, the output), in units.
 constexpr int kChunkEntry = 3;
@@ -220,40 +220,49 @@ __device__ __forceinline__ void convert_16(uint4 w, bool times, __half2 factor, 
   }
 }
 
-// One lane's share of a unit's operand: pieces i = it * kConvWarps + cw of 32, each
-// 4 tokens (D = 128) or 8 (D = 64) of 16 codes a lane.
+// One lane's share of a unit's operand: 16 codes of each of kMine tokens. A warp
+// has kPerToken lanes for each of 32 / kPerToken tokens; lanes of the dimension's
+// second half take the token next to it, so that eight lanes that store together
+// hit eight different bank groups (the swizzle differs between the two tokens).
 template <int D>
 struct Operand {
-  static constexpr int kPieces = kTokens * D / 16 / 32;                 // warp-wide pieces
-  static constexpr int kMine = (kPieces + kConvWarps - 1) / kConvWarps;
-  static constexpr int kPerToken = D / 16;                              // lanes of a token
+  static constexpr int kPerToken = D / 16;
+  static constexpr int kStep = kConvWarps * 32 / kPerToken;  // tokens between a lane's
+  static constexpr int kMine = kTokens / kStep;
+  static_assert(kKvBlock % kStep == 0 && kStep % 8 == 0, "one block and one swizzle row a piece");
   uint4 w[kMine];
+  __device__ static __forceinline__ int first(int cw, int lane) {
+    return cw * (32 / kPerToken) + (lane / kPerToken ^ (lane % kPerToken >> 2));
+  }
   __device__ __forceinline__ void load(const uint8_t *codes, const int64_t (&slab)[2], int tokens, int cw, int lane, int64_t size) {
+    const int tok0 = first(cw, lane), c = lane % kPerToken;
 #pragma unroll
     for (int it = 0; it < kMine; ++it) {
-      const int i = it * kConvWarps + cw;
-      const int tok = i * (32 / kPerToken) + lane / kPerToken, c = lane % kPerToken;
+      constexpr int kHalf = kMine / 2;  // pieces of a block
+      const int tok = tok0 + (it % kHalf) * kStep;
       w[it] = make_uint4(0, 0, 0, 0);  // tokens past the sequence, and pages that the table does not name
-      if (i < kPieces && tok < tokens && slab[tok / kKvBlock] >= 0) {
-        const int64_t off = (slab[tok / kKvBlock] * kKvBlock + tok % kKvBlock) * D + c * 16;
+      const int64_t at = slab[it / kHalf];
+      if (tok + (it / kHalf) * kKvBlock < tokens && at >= 0) {
+        const int64_t off = (at * kKvBlock + tok) * D + c * 16;
         if (EXL3_SPAN(off, 16, size)) w[it] = *reinterpret_cast<const uint4 *>(codes + off);
       }
     }
   }
   __device__ __forceinline__ void store(uint32_t dst, const float (&factor)[2], int cw, int lane) const {
+    const int tok0 = first(cw, lane), c = lane % kPerToken;
+    const uint32_t half = dst + (c >> 2) * (128 * 128);
+    const uint32_t lo = half + swizzled(tok0, 2 * (c & 3)), hi = half + swizzled(tok0, 2 * (c & 3) + 1);
 #pragma unroll
-    for (int it = 0; it < kMine; ++it) {
-      const int i = it * kConvWarps + cw;
-      if (i >= kPieces) continue;
-      const int tok = i * (32 / kPerToken) + lane / kPerToken, c = lane % kPerToken;
-      const float f = factor[i * (32 / kPerToken) / kKvBlock];  // one block to a piece
-      uint32_t o[8];
-      convert_16(w[it], f != 1.0f, __float2half2_rn(f), o);
-      const uint32_t half = dst + (c >> 2) * (128 * 128);
-      // lanes of the second half of the dimension store their odd piece first: eight different bank groups
-      const int p = 2 * (c & 3), odd = c >> 2;
-      sts16(half + swizzled(tok, p + odd), odd ? o[4] : o[0], odd ? o[5] : o[1], odd ? o[6] : o[2], odd ? o[7] : o[3]);
-      sts16(half + swizzled(tok, p + (odd ^ 1)), odd ? o[0] : o[4], odd ? o[1] : o[5], odd ? o[2] : o[6], odd ? o[3] : o[7]);
+    for (int b = 0; b < 2; ++b) {
+      const bool times = factor[b] != 1.0f;
+      const __half2 f = __float2half2_rn(factor[b]);
+#pragma unroll
+      for (int it = b * (kMine / 2); it < (b + 1) * (kMine / 2); ++it) {
+        uint32_t o[8];
+        convert_16(w[it], times, f, o);
+        sts16(lo + it * kStep * 128, o[0], o[1], o[2], o[3]);
+        sts16(hi + it * kStep * 128, o[4], o[5], o[6], o[7]);
+      }
     }
   }
 };
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
       int u = g.u0;
       int2 top = make_int2(0, 0);
       int64_t slab[2] = {-1, -1}, slab_n[2] = {-1, -1};
-      float fk[2], fv[2];
+      float fk[2], fv[2], ks[2], vs[2];
       auto find = [&](const Segment &s, int at, int64_t (&to)[2]) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -382,11 +391,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
           to[b] = page < 0 ? -1 : (int64_t)page * kv.n_kv_heads + s.h;
         }
       };
+      auto scales = [&](const int64_t (&at)[2]) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          ks[b] = at[b] < 0 ? 1.f : kv.k_scale[at[b]];
+          vs[b] = at[b] < 0 ? 1.f : kv.v_scale[at[b]];
+        }
+      };
       auto factors = [&]() {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          fk[b] = slab[b] < 0 ? 1.f : sign * factor(kv.k_scale[slab[b]], top.x);
-          fv[b] = slab[b] < 0 ? 1.f : factor(kv.v_scale[slab[b]], top.y);
+          fk[b] = sign * factor(ks[b], top.x);
+          fv[b] = factor(vs[b], top.y);
         }
       };
       Operand<D> keys, values;
@@ -394,6 +410,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
         top = largest_scales(kv, g, lane);
         find(g, u, slab);
         keys.load(kv.k, slab, g.q.len - u * kTokens, cw, lane, size);
+        scales(slab);
         factors();
       }
       while (more) {
@@ -413,7 +430,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarKFull + st));
-        if (more_n) keys.load(kv.k, slab_n, gn.q.len - un * kTokens, cw, lane, size);
+        if (more_n) {
+          keys.load(kv.k, slab_n, gn.q.len - un * kTokens, cw, lane, size);
+          scales(slab_n);
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarVEmpty + st), ph ^ 1, status))) break;
         values.store(base + Cfg::kOffV + st * Cfg::kOperand, fv, cw, lane);
         fence_proxy_async_shared();
@@ -469,22 +489,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
             break;
           }
           tc_fence_after();
-          float s[128];
-          tmem_ld128(s_tmem, s);
-          if constexpr (CAP) {
-#pragma unroll
-            for (int k = 0; k < 128; ++k) s[k] = soft_cap(s[k] * c, cap, inv_cap) * kLog2e;
-          }
-          if (u * kTokens + kTokens > least) {
-#pragma unroll
-            for (int k = 0; k < 128; ++k)
-              if (u * kTokens + k >= limit) s[k] = -INFINITY;
-          }
-          float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int k = 4; k < 128; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
+          const int pos0 = u * kTokens;
+          const bool masked = pos0 + kTokens > least;
           const float scale = CAP ? 1.0f : c;
-          const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
+          float top = -INFINITY;
+          // 64 scores of the row: capped (in log2 units) and masked
+          auto scores = [&](int hf, float (&s)[64]) {
+            tmem_ld64(s_tmem + 64 * hf, s);
+            if constexpr (CAP) {
+#pragma unroll
+              for (int k = 0; k < 64; ++k) s[k] = soft_cap(s[k] * c, cap, inv_cap) * kLog2e;
+            }
+            if (masked) {
+#pragma unroll
+              for (int k = 0; k < 64; ++k)
+                if (pos0 + 64 * hf + k >= limit) s[k] = -INFINITY;
+            }
+          };
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float s[64];
+            scores(hf, s);
+            float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int k = 4; k < 60; k += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[k + e], s[k + 4 + e]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[60 + e]);
+            top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+          }
+          top *= scale;
           const float now = top > ref + kLazy || ref == -INFINITY ? top : ref;
           const float keep = now == ref || ref == -INFINITY ? 1.0f : ex2(ref - now);
           if (u > g.u0 && __any_sync(0xffffffffu, keep != 1.0f)) {
@@ -505,23 +540,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
           }
           ref = now;
           const float shift = now == -INFINITY ? 0.f : -now;
-          float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < 128; ++k) {
-            s[k] = ex2(fmaf(s[k], scale, shift));
-            s4[k & 3] += s[k];
-          }
-          sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          const float2 scale2 = make_float2(scale, scale), shift2 = make_float2(shift, shift);
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            float packed[32];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
+            float s[64], packed[32];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
+            scores(hf, s);
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const __half2 x = __floats2half2_rn(s[64 * hf + 2 * k], s[64 * hf + 2 * k + 1]);
-              packed[k] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&x));
+              float2 x = fma2(make_float2(s[2 * k], s[2 * k + 1]), scale2, shift2);
+              x = make_float2(ex2(x.x), ex2(x.y));
+              part[k & 1] = add2(part[k & 1], x);
+              const __half2 h2 = __floats2half2_rn(x.x, x.y);
+              packed[k] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h2));
             }
             tmem_st32(s_tmem + 32 * hf, packed);
           }
+          part[0] = add2(part[0], part[1]);
+          sum += part[0].x + part[0].y;
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
