@@ -250,6 +250,7 @@ exl3_status exl3_init(int device) {
       init_decode_kernels(info.status) != cudaSuccess || init_prefill_kernels(info.status) != cudaSuccess ||
       init_fused_kernels(info.status) != cudaSuccess || init_fused_prefill_kernels(info.status) != cudaSuccess ||
       init_kv8_cache_kernels(info.status) != cudaSuccess || init_kv8_attention_kernels(info.status) != cudaSuccess || init_kv8_chunk_kernels(info.status) != cudaSuccess ||
+      init_kv8_weigh_chunk_kernels(info.status) != cudaSuccess ||
       init_logits_adjust_kernels(info.status) != cudaSuccess)
     return EXL3_ERR_CUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return EXL3_ERR_CUDA;

@@ -170,6 +170,9 @@ bool bits_supported(int bits);
 bool encode_tensor_map_2d(CUtensorMap *m, CUtensorMapDataType type, const void *ptr, uint64_t dim0, uint64_t dim1,
                           uint64_t stride_bytes, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle);
 
+bool encode_tensor_map_3d(CUtensorMap *m, CUtensorMapDataType type, const void *ptr, const uint64_t (&dims)[3],
+                          const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
+
 struct DeviceInfo;
 // The current device's cached set-up, or nullptr before exl3_init.
 const DeviceInfo *initialized_device();

@@ -95,6 +95,24 @@ __device__ __forceinline__ uint2 rescale_codes(uint2 c, float factor) {
   return make_uint2(o[0], o[1]);
 }
 
+// Byte offset of 16-byte piece c (of 8) of 128-byte row r in a swizzled operand half.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  if (EXL3_SMEM(addr, 16))
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 16 codes to 16 fp16 values, exact.
+__device__ __forceinline__ void codes_to_half(uint4 w, uint32_t (&o)[8]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = e4m3x2_to_half2((uint16_t)(x[i] & 0xFFFFu));
+    o[2 * i + 1] = e4m3x2_to_half2((uint16_t)(x[i] >> 16));
+  }
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -1011,6 +1011,7 @@ cudaError_t launch_kv8_attention(const KvAttention &a, cudaStream_t st) {
 
 cudaError_t launch_kv8_weigh(const KvAttention &a, cudaStream_t st) {
   if (a.kv.rows == 0 || a.kv.n_seqs == 0 || a.kv.max_rows == 0) return cudaSuccess;
+  if ((int64_t)a.kv.max_rows * (a.n_heads / a.kv.n_kv_heads) > kStreamRows) return launch_kv8_weigh_chunk(a, st);
   return a.kv.head_dim == 64 ? weigh<64>(a, st) : weigh<128>(a, st);
 }
 

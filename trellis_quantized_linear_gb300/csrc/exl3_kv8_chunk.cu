@@ -195,22 +195,9 @@ __device__ __forceinline__ int2 largest_scales(const KvView &kv, const Segment &
   return make_int2(__reduce_max_sync(0xffffffffu, ek), __reduce_max_sync(0xffffffffu, ev));
 }
 
-// Byte offset of 16-byte piece c (of 8) of 128-byte row r in a swizzled operand half.
-__device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  if (EXL3_SMEM(addr, 16))
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
 // 16 codes to two 16-byte pieces of fp16, times a power of two (one: none).
 __device__ __forceinline__ void convert_16(uint4 w, bool times, __half2 factor, uint32_t (&o)[8]) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = e4m3x2_to_half2((uint16_t)(x[i] & 0xFFFFu));
-    o[2 * i + 1] = e4m3x2_to_half2((uint16_t)(x[i] >> 16));
-  }
+  codes_to_half(w, o);
   if (times) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

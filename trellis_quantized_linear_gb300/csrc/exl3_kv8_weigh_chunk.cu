@@ -1,0 +1,397 @@
+// Accumulated attention weight of cached tokens under many query rows, on the
+// 5th-gen tensor cores. Formula in include/exl3.h.
+//
+// An item is 128 cached tokens of a (sequence, key/value head). Its keys come to
+// fp16 (exact) in shared memory once; the query rows that see it stream past, up
+// to 128 columns (rows x heads of the group) a step: S^T = K Q^T into one of two
+// TMEM buffers, thread = token = TMEM lane, and each thread adds up
+// exp2(s - lse) over the step's columns. No maximum, no second product: the
+// exponentials bound it, 128 x 128 of them a step against 512 cycles of tensor
+// work, so two CTAs share an SM and take turns.
+//   * warps 0..3: the item's keys, then per step the columns' lse (a step ahead,
+//     in registers, then shared memory), the exponentials and the sums;
+//   * warp 4 (one lane): tcgen05.mma;
+//   * warp 5 (one lane): TMA of the queries, a box of 64 dimensions x heads x rows,
+//     so a step is the group's heads of consecutive rows without a copy.
+// An item's sums are formed by one CTA in a fixed order. Items go to the CTAs in
+// turn, the ones that most rows see first.
+#include <cuda.h>
+
+#include "exl3_internal.h"
+#include "exl3_kv8.cuh"
+#include "exl3_tcgen05.cuh"
+
+namespace exl3 {
+
+namespace {
+
+constexpr int kItem = 128;         // tokens
+constexpr int kCols = 128;         // of a step
+constexpr int kWeighThreads = 192;
+constexpr int kWeighSeqs = 512;    // sequences of one launch
+
+template <int D>
+struct WeighCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kOperand = kHalves * 128 * 128;
+  static constexpr int kOffQ = kOperand;                    // two stages
+  static constexpr int kOffCol = kOffQ + 2 * kOperand;      // two buffers of (lse, limit) x 128
+  static constexpr int kOffPlan = kOffCol + 2 * kCols * 8;  // int prefix, then int2 sequences
+  static constexpr int kOffBar = kOffPlan + (kWeighSeqs + 8) * 4 + (kWeighSeqs + 8) * 8;
+  static constexpr int kSmem = 1024 + kOffBar + 256;
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+enum { kWQFull = 0, kWQEmpty = 2, kWSFull = 4, kWSEmpty = 6, kWKeys = 8, kWDone = 9, kWBars = 10 };
+
+struct WeighParams {
+  KvAttention a;
+  int group;
+  int heads, rows;  // of a step: heads * rows <= 128 columns
+};
+
+struct Item {
+  KvSeq q;
+  int s, h, tile;
+  int first;     // first row that sees the item
+  int chunks;    // steps of heads
+  int steps;     // in all
+};
+
+// Items (128-token tiles x heads) of all sequences before each; ends with a barrier.
+struct WeighPlan {
+  int *prefix;
+  int2 *seq;
+  __device__ __forceinline__ KvSeq at(int s) const {
+    const int2 a = seq[s];
+    return KvSeq{a.x, a.y < 0 ? 0 : seq[s + 1].x - a.x, a.y < 0 ? 0 : a.y};
+  }
+};
+__device__ __forceinline__ void build_weigh_plan(const KvView &kv, const WeighPlan &plan) {
+  for (int s = threadIdx.x; s < kv.n_seqs; s += blockDim.x) {
+    const KvSeq q = kv_sequence(kv, s);
+    plan.seq[s] = make_int2(kv.q_start[s], q.rows > 0 ? q.len : -1);
+    plan.prefix[s + 1] = q.rows > 0 ? (q.len + kItem - 1) / kItem * kv.n_kv_heads : 0;
+    if (s + 1 == kv.n_seqs) plan.seq[s + 1] = make_int2(kv.q_start[s + 1], -1);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {  // one warp: 32 at a time
+    const int lane = threadIdx.x;
+    int carry = 0;
+    if (lane == 0) plan.prefix[0] = 0;
+    for (int c = 0; c < kv.n_seqs; c += 32) {
+      int n = c + lane < kv.n_seqs ? plan.prefix[c + lane + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, n, d);
+        if (lane >= d) n += o;
+      }
+      if (c + lane < kv.n_seqs) plan.prefix[c + lane + 1] = carry + n;
+      carry += __shfl_sync(0xffffffffu, n, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// Item z, false past the last. Heads vary fastest: tiles of the sequence's front,
+// which most rows see, come first.
+__device__ __forceinline__ bool get_item(const WeighParams &p, const WeighPlan &plan, int z, Item &it) {
+  const KvView &kv = p.a.kv;
+  if (z >= plan.prefix[kv.n_seqs]) return false;
+  int lo = 0, hi = kv.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (plan.prefix[mid + 1] > z) hi = mid;
+    else lo = mid + 1;
+  }
+  it.s = lo;
+  it.q = plan.at(lo);
+  const int k = z - plan.prefix[lo];
+  it.h = k % kv.n_kv_heads;
+  it.tile = k / kv.n_kv_heads;
+  it.first = p.a.causal ? max(0, it.tile * kItem - (it.q.len - it.q.rows)) : 0;
+  it.chunks = (p.group + p.heads - 1) / p.heads;
+  it.steps = max(0, (it.q.rows - it.first + p.rows - 1) / p.rows) * it.chunks;
+  return true;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kWeighThreads, 2)
+    kv8_weigh_chunk_kernel(const __grid_constant__ CUtensorMap tq, const WeighParams p) {
+  using Cfg = WeighCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t base = smem_u32(smem);
+  const KvView &kv = p.a.kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WeighPlan plan{reinterpret_cast<int *>(smem + Cfg::kOffPlan),
+                       reinterpret_cast<int2 *>(smem + Cfg::kOffPlan + (kWeighSeqs + 8) * 4)};
+  const uint32_t bars = base + Cfg::kOffBar;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kOffBar + 8 * kWBars);
+  __shared__ uint32_t full[2][4];  // of a step's 32 columns: all see the whole item
+  int *status = kv.status;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(kWQFull + t), 1);
+      mbar_init(bar(kWQEmpty + t), 1);
+      mbar_init(bar(kWSFull + t), 1);
+      mbar_init(bar(kWSEmpty + t), 4);
+    }
+    mbar_init(bar(kWKeys), 4);
+    mbar_init(bar(kWDone), 1);
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(256)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  tc_fence_before();
+  build_weigh_plan(kv, plan);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int step_cols = p.heads * p.rows;
+  Item it;
+
+  if (warp == 5) {
+    // ---------------- queries (one lane) ----------------
+    if (lane == 0) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int z = blockIdx.x; ok && get_item(p, plan, z, it); z += gridDim.x)
+        for (int st = 0, chunk = 0, row = it.q.row0 + it.first; ok && st < it.steps; ++st, ++n) {
+          const uint32_t b = n & 1;
+          ok = mbar_wait(bar(kWQEmpty + b), ((n >> 1) & 1) ^ 1, status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(kWQFull + b), (uint32_t)(Cfg::kHalves * step_cols * 128));
+          const int head = it.h * p.group + chunk * p.heads;
+#pragma unroll
+          for (int hf = 0; hf < Cfg::kHalves; ++hf)
+            if (EXL3_RANGE(head, 0, p.a.n_heads) && EXL3_RANGE(row, 0, kv.rows))
+              tma_load_3d(base + Cfg::kOffQ + b * Cfg::kOperand + hf * (128 * 128), &tq, bar(kWQFull + b), 64 * hf, head, row);
+          if (++chunk == it.chunks) {
+            chunk = 0;
+            row += p.rows;
+          }
+        }
+      // the copies in flight land before the CTA leaves
+      for (uint32_t u = n > 2 ? n - 2 : 0; u < n; ++u) mbar_wait_short(bar(kWQFull + (u & 1)), (u >> 1) & 1);
+    }
+  } else if (warp == 4) {
+    // ---------------- tensor core (one lane) ----------------
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = f16_idesc(kItem, kCols);
+      uint32_t n = 0, items = 0;
+      bool ok = true;
+      for (int z = blockIdx.x; ok && get_item(p, plan, z, it); z += gridDim.x, ++items) {
+        ok = mbar_wait(bar(kWKeys), items & 1, status);
+        for (int st = 0; ok && st < it.steps; ++st, ++n) {
+          const uint32_t b = n & 1, ph = (n >> 1) & 1;
+          ok = mbar_wait(bar(kWQFull + b), ph, status) && mbar_wait(bar(kWSEmpty + b), ph ^ 1, status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t q = base + Cfg::kOffQ + b * Cfg::kOperand;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const uint32_t off = (j >> 2) * (128 * 128) + (j & 3) * 32;
+            tc_mma(tmem + 128 * b, sw128_desc(base + off), sw128_desc(q + off), kIdesc, j > 0);
+          }
+          tc_commit(bar(kWQEmpty + b));
+          tc_commit(bar(kWSFull + b));
+        }
+      }
+      tc_commit(bar(kWDone));
+      mbar_wait_short(bar(kWDone), 0);
+    }
+  } else {
+    // ---------------- exponentials: thread = token ----------------
+    const int tid = threadIdx.x;
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    const float cap = p.a.softcap, inv_cap = CAP ? 1.0f / cap : 0.f;
+    float *col_lse = reinterpret_cast<float *>(smem + Cfg::kOffCol);
+    int *col_limit = reinterpret_cast<int *>(smem + Cfg::kOffCol + 2 * kCols * 4);
+    [[maybe_unused]] const int64_t size = kv.n_pages * kv.n_kv_heads * kKvBlock * (int64_t)D;
+    // The tensor core cuts its partial sums off towards zero, D / 16 times: on average
+    // this share of a score. Without it heavy weights came out 2e-6 low.
+    const float untruncate = 1.0f + 0.6f * 0.5f * (D / 16 + 1) * 0.5f * 0x1p-23f;
+    const int my_row = tid / p.heads, my_head = tid % p.heads;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int z = blockIdx.x; ok && get_item(p, plan, z, it); z += gridDim.x) {
+      const int pos0 = it.tile * kItem, pos = pos0 + tid;
+      // the keys: a token has D / 16 lanes; lanes of the second half of the dimension take the token next to theirs
+      constexpr int kPerToken = D / 16, kStep = 128 / kPerToken;
+      const int c = tid % kPerToken, tok0 = tid / kPerToken ^ (c >> 2);
+      uint4 w[kItem / kStep];
+#pragma unroll
+      for (int i = 0; i < kItem / kStep; ++i) {
+        const int t = tok0 + i * kStep;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (pos0 + t >= it.q.len) continue;
+        const int page = kv_page(kv, it.s, (pos0 + t) / kKvBlock);
+        if (page < 0) continue;
+        const int64_t off = (((int64_t)page * kv.n_kv_heads + it.h) * kKvBlock + (pos0 + t) % kKvBlock) * D + c * 16;
+        if (EXL3_SPAN(off, 16, size)) w[i] = *reinterpret_cast<const uint4 *>(kv.k + off);
+      }
+      int page = -1;
+      float ks = 0.f;
+      if (pos < it.q.len) page = kv_page(kv, it.s, pos / kKvBlock);
+      const int64_t slab = (int64_t)max(page, 0) * kv.n_kv_heads + it.h;
+      if (page >= 0) ks = kv.k_scale[slab] * p.a.scale * untruncate;
+#pragma unroll
+      for (int i = 0; i < kItem / kStep; ++i) {
+        uint32_t o[8];
+        codes_to_half(w[i], o);
+        const uint32_t at = base + (c >> 2) * (128 * 128);
+        sts16(at + swizzled(tok0 + i * kStep, 2 * (c & 3)), o[0], o[1], o[2], o[3]);
+        sts16(at + swizzled(tok0 + i * kStep, 2 * (c & 3) + 1), o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kWKeys));
+
+      // column tid of the steps in order: its row's lse, and how many tokens the row sees
+      int col_row = it.first + my_row, col_chunk = 0;
+      auto column = [&](float &lse, int &limit) {
+        const int g = col_chunk * p.heads + my_head;
+        limit = 0;
+        lse = 0.f;
+        if (tid < step_cols && g < p.group && col_row < it.q.rows) {
+          const int64_t at = (int64_t)(it.q.row0 + col_row) * p.a.n_heads + it.h * p.group + g;
+          if (EXL3_SPAN(at, 1, (int64_t)kv.rows * p.a.n_heads)) lse = p.a.lse[at];
+          if (lse != -INFINITY) limit = p.a.causal ? it.q.len - it.q.rows + col_row + 1 : it.q.len;
+        }
+        if (++col_chunk == it.chunks) {
+          col_chunk = 0;
+          col_row += p.rows;
+        }
+      };
+      float lse = 0.f, total = 0.f;
+      int limit = 0;
+      if (it.steps > 0) column(lse, limit);
+      const int end = min(pos0 + kItem, it.q.len);
+      for (int st = 0; st < it.steps; ++st, ++n) {
+        const uint32_t b = n & 1;
+        col_lse[b * kCols + tid] = -lse;
+        col_limit[b * kCols + tid] = limit;
+        const uint32_t sees = __ballot_sync(0xffffffffu, limit >= end);
+        if (lane == 0) full[b][warp] = sees == 0xffffffffu;
+        if (st + 1 < it.steps) column(lse, limit);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kWSFull + b), (n >> 1) & 1, status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // exp(s - lse): the difference in natural units first, one rounding of a number
+        // that is small where the weight is not, so that the factor log2 e costs no bits
+        auto weight = [&](uint32_t a0, uint32_t a1, float2 minus) {
+          const float2 acc = make_float2(__uint_as_float(a0), __uint_as_float(a1));
+          float2 d;
+          if constexpr (CAP)
+            d = make_float2(soft_cap(acc.x * ks, cap, inv_cap) + minus.x, soft_cap(acc.y * ks, cap, inv_cap) + minus.y);
+          else
+            d = fma2(acc, make_float2(ks, ks), minus);
+          d = mul2(d, make_float2(kLog2e, kLog2e));
+          return make_float2(ex2(d.x), ex2(d.y));
+        };
+        uint32_t acc[2][32];  // 32 columns in use, the next 32 on their way
+        tmem_ld32_start(lane_base + 128 * b, acc[0]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t(&s)[32] = acc[q & 1];
+          tmem_wait_ld(s);
+          if (q < 3) {
+            tmem_ld32_start(lane_base + 128 * b + 32 * (q + 1), acc[(q + 1) & 1]);
+          } else {  // the buffer is free for the step after the next
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kWSEmpty + b));
+          }
+          const float *minus = col_lse + b * kCols + 32 * q;
+          if (full[b][q]) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 m = *reinterpret_cast<const float4 *>(minus + k);
+              part[0] = add2(part[0], weight(s[k], s[k + 1], make_float2(m.x, m.y)));
+              part[1] = add2(part[1], weight(s[k + 2], s[k + 3], make_float2(m.z, m.w)));
+            }
+          } else {
+            const int *seen = col_limit + b * kCols + 32 * q;
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 m = *reinterpret_cast<const float2 *>(minus + k);
+              const int2 l = *reinterpret_cast<const int2 *>(seen + k);
+              const float2 x = weight(s[k], s[k + 1], m);
+              part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], make_float2(pos < l.x ? x.x : 0.f, pos < l.y ? x.y : 0.f));
+            }
+          }
+        }
+        part[0] = add2(part[0], part[1]);
+        total += part[0].x + part[0].y;  // a sum of sums: 82 steps of 10240 rows lose no bits that matter
+      }
+      const int64_t at = slab * kKvBlock + pos % kKvBlock;
+      if (ok && page >= 0 && EXL3_SPAN(at, 1, kv.n_pages * kv.n_kv_heads * kKvBlock)) kv.weight[at] += total;
+      // all four warps are past the item's last step (its scores come from the last product that reads the keys)
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
+  }
+}
+
+template <int D>
+cudaError_t weigh_chunk(const KvAttention &a, cudaStream_t st) {
+  WeighParams p;
+  p.a = a;
+  p.group = a.n_heads / a.kv.n_kv_heads;
+  p.heads = p.group < kCols ? p.group : kCols;
+  p.rows = kCols / p.heads;
+  CUtensorMap tq;
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.n_heads, (uint64_t)a.kv.rows};
+  const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)a.ldq * 2};
+  const uint32_t box[3] = {64, (uint32_t)p.heads, (uint32_t)p.rows};
+  if (!encode_tensor_map_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kWeighSeqs) {
+    p.a.kv = kv_slice(a.kv, s0, a.kv.n_seqs - s0 < kWeighSeqs ? a.kv.n_seqs - s0 : kWeighSeqs);
+    const cudaError_t e = launch_overlapped(a.softcap > 0.f ? kv8_weigh_chunk_kernel<D, true> : kv8_weigh_chunk_kernel<D, false>,
+                                            2 * a.num_sms, kWeighThreads, WeighCfg<D>::kSmem, st, 1, tq, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_weigh_chunk(const KvAttention &a, cudaStream_t st) {
+  return a.kv.head_dim == 64 ? weigh_chunk<64>(a, st) : weigh_chunk<128>(a, st);
+}
+
+cudaError_t init_kv8_weigh_chunk_kernels(int *status) {
+  cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
+  for (const void *f : {(const void *)kv8_weigh_chunk_kernel<64, false>, (const void *)kv8_weigh_chunk_kernel<64, true>,
+                        (const void *)kv8_weigh_chunk_kernel<128, false>, (const void *)kv8_weigh_chunk_kernel<128, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, WeighCfg<128>::kSmem);
+  return e;
+}
+
+#if EXL3_DEBUG_BOUNDS
+cudaError_t bounds_probe_kv8_weigh_chunk(cudaStream_t st) { return launch_bounds_probe(st); }
+#endif
+
+}  // namespace exl3

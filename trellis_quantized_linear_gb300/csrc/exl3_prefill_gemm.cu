@@ -813,6 +813,15 @@ bool encode_tensor_map_2d(CUtensorMap *m, CUtensorMapDataType type, const void *
                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tensor_map_3d(CUtensorMap *m, CUtensorMapDataType type, const void *ptr, const uint64_t (&dims)[3],
+                          const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+  if (!g_encode) return false;
+  cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, s[2] = {strides[0], strides[1]};
+  cuuint32_t b[3] = {box[0], box[1], box[2]}, estr[3] = {1, 1, 1};
+  return g_encode(m, type, 3, const_cast<void *>(ptr), d, s, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t init_prefill_kernels(int *status) {
   const cudaError_t eb = EXL3_BIND_BOUNDS_WORD(status);
   if (eb != cudaSuccess) return eb;

@@ -48,6 +48,7 @@ inline KvView kv_slice(const KvView &kv, int s0, int n) {
 cudaError_t init_kv8_cache_kernels(int *status);
 cudaError_t init_kv8_attention_kernels(int *status);
 cudaError_t init_kv8_chunk_kernels(int *status);
+cudaError_t init_kv8_weigh_chunk_kernels(int *status);
 cudaError_t init_logits_adjust_kernels(int *status);
 
 cudaError_t launch_kv8_append(const KvView &kv, const void *k, int64_t ldk, const void *v, int64_t ldv, cudaStream_t st);
@@ -60,6 +61,8 @@ size_t kv8_chunk_workspace_bytes(int head_dim, int num_sms);
 cudaError_t launch_kv8_chunk_attention(const KvAttention &p, cudaStream_t st);
 // lse of the call that p describes; adds to p.kv.weight.
 cudaError_t launch_kv8_weigh(const KvAttention &p, cudaStream_t st);
+// The same for many rows (exl3_kv8_weigh_chunk.cu).
+cudaError_t launch_kv8_weigh_chunk(const KvAttention &p, cudaStream_t st);
 cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules &r,
                                  float *out, int64_t ldo, int32_t *argmax, int *status, int num_sms, cudaStream_t st);
 
@@ -67,6 +70,7 @@ cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, in
 cudaError_t bounds_probe_kv8_cache(cudaStream_t st);
 cudaError_t bounds_probe_kv8_attention(cudaStream_t st);
 cudaError_t bounds_probe_kv8_chunk(cudaStream_t st);
+cudaError_t bounds_probe_kv8_weigh_chunk(cudaStream_t st);
 cudaError_t bounds_probe_logits_adjust(cudaStream_t st);
 #endif
 

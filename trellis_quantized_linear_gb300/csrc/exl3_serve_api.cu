@@ -172,6 +172,7 @@ exl3_status exl3_selftest_bounds_serving(int *units_reported, int *units_total, 
   const exl3_status pending = exl3_get_device_status(stream);
   if (pending != EXL3_OK) return pending;
   cudaError_t (*const probes[])(cudaStream_t) = {bounds_probe_kv8_cache, bounds_probe_kv8_attention, bounds_probe_kv8_chunk,
+                                                 bounds_probe_kv8_weigh_chunk,
                                                  bounds_probe_logits_adjust};
   for (auto *probe : probes) {
     ++*units_total;
