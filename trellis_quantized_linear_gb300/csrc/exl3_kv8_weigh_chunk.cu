@@ -8,10 +8,12 @@
 // exp2(s - lse) over the step's columns. No maximum, no second product: the
 // exponentials bound it, 128 x 128 of them a step against 512 cycles of tensor
 // work, so two CTAs share an SM and take turns.
-//   * warps 0..3: the item's keys, then per step the columns' lse (a step ahead,
-//     in registers, then shared memory), the exponentials and the sums;
-//   * warp 4 (one lane): tcgen05.mma;
-//   * warp 5 (one lane): TMA of the queries, a box of 64 dimensions x heads x rows,
+//   * warps 0..7: the item's keys, then per step the columns' lse (a step ahead,
+//     in registers, then shared memory), the exponentials and the sums; warps 0..3
+//     have the first 64 columns and warps 4..7 the others (eight warps hide the
+//     latency of a dependent chain that four leave bare: 287 us with four);
+//   * warp 8 (one lane): tcgen05.mma;
+//   * warp 9 (one lane): TMA of the queries, a box of 64 dimensions x heads x rows,
 //     so a step is the group's heads of consecutive rows without a copy.
 // An item's sums are formed by one CTA in a fixed order. Items go to the CTAs in
 // turn, the ones that most rows see first.
@@ -27,7 +29,8 @@ namespace {
 
 constexpr int kItem = 128;         // tokens
 constexpr int kCols = 128;         // of a step
-constexpr int kWeighThreads = 192;
+constexpr int kExpWarps = 8;
+constexpr int kWeighThreads = (kExpWarps + 2) * 32;
 constexpr int kWeighSeqs = 512;    // sequences of one launch
 
 template <int D>
@@ -35,8 +38,8 @@ struct WeighCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kOperand = kHalves * 128 * 128;
   static constexpr int kOffQ = kOperand;                    // two stages
-  static constexpr int kOffCol = kOffQ + 2 * kOperand;      // two buffers of (lse, limit) x 128
-  static constexpr int kOffPlan = kOffCol + 2 * kCols * 8;  // int prefix, then int2 sequences
+  static constexpr int kOffCol = kOffQ + 2 * kOperand;      // two buffers of (lse, limit) x 128, then sums
+  static constexpr int kOffPlan = kOffCol + 2 * kCols * 8 + kItem * 4;  // int prefix, then int2 sequences
   static constexpr int kOffBar = kOffPlan + (kWeighSeqs + 8) * 4 + (kWeighSeqs + 8) * 8;
   static constexpr int kSmem = 1024 + kOffBar + 256;
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -121,6 +124,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// A barrier of the exponential warps that is true when every thread's `ok` is.
+__device__ __forceinline__ bool all_agree(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.red.and.pred p, 1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "n"(kExpWarps * 32)
+      : "memory");
+  return all != 0;
+}
+
 template <int D, bool CAP>
 __global__ void __launch_bounds__(kWeighThreads, 2)
     kv8_weigh_chunk_kernel(const __grid_constant__ CUtensorMap tq, const WeighParams p) {
@@ -142,13 +159,13 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       mbar_init(bar(kWQFull + t), 1);
       mbar_init(bar(kWQEmpty + t), 1);
       mbar_init(bar(kWSFull + t), 1);
-      mbar_init(bar(kWSEmpty + t), 4);
+      mbar_init(bar(kWSEmpty + t), kExpWarps);
     }
-    mbar_init(bar(kWKeys), 4);
+    mbar_init(bar(kWKeys), kExpWarps);
     mbar_init(bar(kWDone), 1);
     fence_barrier_init();
   }
-  if (warp == 4) {
+  if (warp == kExpWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(256)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -160,9 +177,14 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int step_cols = p.heads * p.rows;
+  // rows of the query stages that no copy fills
+  for (int i = threadIdx.x; i < (kCols - step_cols) * 8 * 2 * Cfg::kHalves; i += kWeighThreads)
+    sts16(base + Cfg::kOffQ + i / ((kCols - step_cols) * 8) * (128 * 128) + step_cols * 128 + i % ((kCols - step_cols) * 8) * 16, 0, 0, 0, 0);
+  fence_proxy_async_shared();
+  __syncthreads();
   Item it;
 
-  if (warp == 5) {
+  if (warp == kExpWarps + 1) {
     // ---------------- queries (one lane) ----------------
     if (lane == 0) {
       uint32_t n = 0;
@@ -186,7 +208,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       // the copies in flight land before the CTA leaves
       for (uint32_t u = n > 2 ? n - 2 : 0; u < n; ++u) mbar_wait_short(bar(kWQFull + (u & 1)), (u >> 1) & 1);
     }
-  } else if (warp == 4) {
+  } else if (warp == kExpWarps) {
     // ---------------- tensor core (one lane) ----------------
     if (lane == 0) {
       constexpr uint32_t kIdesc = f16_idesc(kItem, kCols);
@@ -214,11 +236,12 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     }
   } else {
     // ---------------- exponentials: thread = token ----------------
-    const int tid = threadIdx.x;
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    const int tid = threadIdx.x, row = tid & 127, half = tid >> 7;  // token of the item, half of the columns
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 64 * half;
     const float cap = p.a.softcap, inv_cap = CAP ? 1.0f / cap : 0.f;
     float *col_lse = reinterpret_cast<float *>(smem + Cfg::kOffCol);
     int *col_limit = reinterpret_cast<int *>(smem + Cfg::kOffCol + 2 * kCols * 4);
+    float *col_sum = reinterpret_cast<float *>(smem + Cfg::kOffCol + 4 * kCols * 4);
     [[maybe_unused]] const int64_t size = kv.n_pages * kv.n_kv_heads * kKvBlock * (int64_t)D;
     // The tensor core cuts its partial sums off towards zero, D / 16 times: on average
     // this share of a score. Without it heavy weights came out 2e-6 low.
@@ -227,9 +250,9 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     uint32_t n = 0;
     bool ok = true;
     for (int z = blockIdx.x; ok && get_item(p, plan, z, it); z += gridDim.x) {
-      const int pos0 = it.tile * kItem, pos = pos0 + tid;
+      const int pos0 = it.tile * kItem, pos = pos0 + row;
       // the keys: a token has D / 16 lanes; lanes of the second half of the dimension take the token next to theirs
-      constexpr int kPerToken = D / 16, kStep = 128 / kPerToken;
+      constexpr int kPerToken = D / 16, kStep = kExpWarps * 32 / kPerToken;
       const int c = tid % kPerToken, tok0 = tid / kPerToken ^ (c >> 2);
       uint4 w[kItem / kStep];
 #pragma unroll
@@ -281,13 +304,16 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       const int end = min(pos0 + kItem, it.q.len);
       for (int st = 0; st < it.steps; ++st, ++n) {
         const uint32_t b = n & 1;
-        col_lse[b * kCols + tid] = -lse;
-        col_limit[b * kCols + tid] = limit;
-        const uint32_t sees = __ballot_sync(0xffffffffu, limit >= end);
-        if (lane == 0) full[b][warp] = sees == 0xffffffffu;
-        if (st + 1 < it.steps) column(lse, limit);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(kWSFull + b), (n >> 1) & 1, status))) {
+        if (half == 0) {
+          col_lse[b * kCols + tid] = tid < step_cols ? -lse : -INFINITY;
+          col_limit[b * kCols + tid] = limit;
+          // (a column that no step has: its query row is zero and its lse infinite)
+          const uint32_t sees = __ballot_sync(0xffffffffu, limit >= end || tid >= step_cols);
+          if (lane == 0) full[b][warp] = sees == 0xffffffffu;
+          if (st + 1 < it.steps) column(lse, limit);
+        }
+        // the columns are there, and a wait that ran out ends the loop in all warps or in none
+        if (!all_agree(mbar_wait(bar(kWSFull + b), (n >> 1) & 1, status))) {
           ok = false;
           break;
         }
@@ -295,8 +321,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // exp(s - lse): the difference in natural units first, one rounding of a number
         // that is small where the weight is not, so that the factor log2 e costs no bits
-        auto weight = [&](uint32_t a0, uint32_t a1, float2 minus) {
-          const float2 acc = make_float2(__uint_as_float(a0), __uint_as_float(a1));
+        auto weight = [&](float a0, float a1, float2 minus) {
+          const float2 acc = make_float2(a0, a1);
           float2 d;
           if constexpr (CAP)
             d = make_float2(soft_cap(acc.x * ks, cap, inv_cap) + minus.x, soft_cap(acc.y * ks, cap, inv_cap) + minus.y);
@@ -305,15 +331,12 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
           d = mul2(d, make_float2(kLog2e, kLog2e));
           return make_float2(ex2(d.x), ex2(d.y));
         };
-        uint32_t acc[2][32];  // 32 columns in use, the next 32 on their way
-        tmem_ld32_start(lane_base + 128 * b, acc[0]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t(&s)[32] = acc[q & 1];
-          tmem_wait_ld(s);
-          if (q < 3) {
-            tmem_ld32_start(lane_base + 128 * b + 32 * (q + 1), acc[(q + 1) & 1]);
-          } else {  // the buffer is free for the step after the next
+        for (int i = 0; i < 2; ++i) {
+          const int q = 2 * half + i;
+          float s[32];
+          tmem_ld32(lane_base + 128 * b + 32 * i, s);
+          if (i == 1) {  // the buffer is free for the step after the next
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kWSEmpty + b));
@@ -340,15 +363,18 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         part[0] = add2(part[0], part[1]);
         total += part[0].x + part[0].y;  // a sum of sums: 82 steps of 10240 rows lose no bits that matter
       }
+      // the other half's sum; all warps are past the item's last step then (its scores
+      // come from the last product that reads the keys)
+      if (half == 1) col_sum[row] = total;
+      asm volatile("bar.sync 1, %0;" ::"n"(kExpWarps * 32) : "memory");
       const int64_t at = slab * kKvBlock + pos % kKvBlock;
-      if (ok && page >= 0 && EXL3_SPAN(at, 1, kv.n_pages * kv.n_kv_heads * kKvBlock)) kv.weight[at] += total;
-      // all four warps are past the item's last step (its scores come from the last product that reads the keys)
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (ok && half == 0 && page >= 0 && EXL3_SPAN(at, 1, kv.n_pages * kv.n_kv_heads * kKvBlock))
+        kv.weight[at] += total + col_sum[row];
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kExpWarps) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
   }
