@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         if (tid < step_cols && g < p.group && col_row < it.q.rows) {
           const int64_t at = (int64_t)(it.q.row0 + col_row) * p.a.n_heads + it.h * p.group + g;
           if (EXL3_SPAN(at, 1, (int64_t)kv.rows * p.a.n_heads)) lse = p.a.lse[at];
-          if (lse != -INFINITY) limit = p.a.causal ? it.q.len - it.q.rows + col_row + 1 : it.q.len;
+          limit = p.a.causal ? it.q.len - it.q.rows + col_row + 1 : it.q.len;
         }
         if (++col_chunk == it.chunks) {
           col_chunk = 0;
@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       for (int st = 0; st < it.steps; ++st, ++n) {
         const uint32_t b = n & 1;
         if (half == 0) {
+          if (lse == -INFINITY) limit = 0;  // a row that saw nothing (here, so that the load has had a step's time)
           col_lse[b * kCols + tid] = tid < step_cols ? -lse : -INFINITY;
           col_limit[b * kCols + tid] = limit;
           // (a column that no step has: its query row is zero and its lse infinite)
