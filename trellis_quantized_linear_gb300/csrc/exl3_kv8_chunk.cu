@@ -17,9 +17,9 @@
 //     the tile's probabilities are there, O += P V with P read from TMEM, where it
 //     has taken the place of S;
 //   * warps 0..3 / 4..7 (tile 0 / 1; thread = row = TMEM lane): the row's 128
-//     scores, 64 at a time: maximum first, then mask, exp2, sum, probabilities as
+//     scores, 32 at a time: maximum first, then mask, exp2, sum, probabilities as
 //     fp16 back to TMEM. While one tile's softmax runs, the tensor core works on the other's
-//     products. O is rescaled only when the maximum grows by more than 2^8 over
+//     products. O is rescaled only when the maximum grows by more than 2^14 over
 //     the reference in use (the result is the same: the sum uses that reference),
 //     so rarely after the first units.
 // TMEM: S0 S1 O0 O1, 128 columns each.
@@ -40,7 +40,9 @@ constexpr int kChunkThreads = (9 + kConvWarps) * 32;  // 96 registers a thread
 constexpr int kChunkSeqs = 1024;               // sequences of one launch
 // Entering a segment (queries, the blocks' largest scales, the output), in units.
 constexpr int kChunkEntry = 3;
-constexpr float kLazy = 8.0f;                  // log2 of how far a maximum may pass the reference
+// log2 of how far a maximum may pass the reference in use: probabilities up to 2^14
+// in fp16 (largest 2^16), so that a row is rescaled about once or not at all.
+constexpr float kLazy = 14.0f;
 
 template <int D>
 struct ChunkCfg {
@@ -480,30 +482,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
           const bool masked = pos0 + kTokens > least;
           const float scale = CAP ? 1.0f : c;
           float top = -INFINITY;
-          // 64 scores of the row: capped (in log2 units) and masked
-          auto scores = [&](int hf, float (&s)[64]) {
-            tmem_ld64(s_tmem + 64 * hf, s);
+          // 32 scores of the row: capped (in log2 units) and masked
+          auto prepare = [&](int q, float (&s)[32]) {
             if constexpr (CAP) {
 #pragma unroll
-              for (int k = 0; k < 64; ++k) s[k] = soft_cap(s[k] * c, cap, inv_cap) * kLog2e;
+              for (int k = 0; k < 32; ++k) s[k] = soft_cap(s[k] * c, cap, inv_cap) * kLog2e;
             }
             if (masked) {
 #pragma unroll
-              for (int k = 0; k < 64; ++k)
-                if (pos0 + 64 * hf + k >= limit) s[k] = -INFINITY;
+              for (int k = 0; k < 32; ++k)
+                if (pos0 + 32 * q + k >= limit) s[k] = -INFINITY;
             }
           };
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float s[64];
-            scores(hf, s);
+          // not unrolled, here and below: instruction fetch is part of the bound
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float s[32];
+            tmem_ld32(s_tmem + 32 * q, s);
+            prepare(q, s);
             float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int k = 4; k < 60; k += 8)
+            for (int k = 4; k < 28; k += 8)
 #pragma unroll
               for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[k + e], s[k + 4 + e]));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[60 + e]);
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[28 + e]);
             top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
           }
           top *= scale;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
               break;
             }
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
               float o[32];
               tmem_ld32(o_tmem + 32 * k, o);
@@ -529,19 +532,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
           const float shift = now == -INFINITY ? 0.f : -now;
           const float2 scale2 = make_float2(scale, scale), shift2 = make_float2(shift, shift);
           float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float s[32];
+            uint32_t packed[16];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
+            tmem_ld32(s_tmem + 32 * q, s);
+            prepare(q, s);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float s[64], packed[32];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
-            scores(hf, s);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
+            for (int k = 0; k < 16; ++k) {
               float2 x = fma2(make_float2(s[2 * k], s[2 * k + 1]), scale2, shift2);
               x = make_float2(ex2(x.x), ex2(x.y));
               part[k & 1] = add2(part[k & 1], x);
               const __half2 h2 = __floats2half2_rn(x.x, x.y);
-              packed[k] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h2));
+              packed[k] = *reinterpret_cast<const uint32_t *>(&h2);
             }
-            tmem_st32(s_tmem + 32 * hf, packed);
+            tmem_st16(s_tmem + 16 * q, packed);
           }
           part[0] = add2(part[0], part[1]);
           sum += part[0].x + part[0].y;
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
         const int64_t off = (int64_t)(g.q.row0 + i) * p.a.ldo + (int64_t)head * D;
         const bool fits = whole ? EXL3_SPAN(real ? off : 0, D, (int64_t)(kv.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D)
                                 : EXL3_SPAN(slot, 1, p.part_rows);
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           float o[32];
           tmem_ld32(o_tmem + 32 * k, o);
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
 
 // Joins the partials of the segments that several CTAs worked on, in the order of
 // the CTAs, and writes the rows that see no token. A CTA has 64 rows of a
-// (sequence, key/value head), a warp one row at a time.
+// (sequence, key/value head), a warp four at a time.
 constexpr int kJoinRows = 64, kJoinThreads = 256;
 
 template <int D>
@@ -628,28 +633,49 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
     c1 = range_owner(z + units - 1, W, T);
     if (c0 == c1) return;  // the CTA wrote the result
   }
-  constexpr int E = D / 32;
-  for (int j = j0 + warp; j < j0 + kJoinRows; j += kJoinThreads / 32) {
-    const int i = j / p.group;
-    if (i >= q.rows) return;
-    float m = -INFINITY, l = 0.f, o[E] = {};
-    for (int64_t c = c0; c <= c1; ++c) {
-      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * kPair + j % kPair;
-      if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
-      const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
-      const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
-      const float a = ex2(m - ref), b = ex2(ml.x - ref);
-      l = l * a + ml.y * b;
+  constexpr int E = D / 32, kAtOnce = 4;
+  for (int first = j0 + warp * kAtOnce; first < j0 + kJoinRows; first += kJoinThreads / 32 * kAtOnce) {
+    float m[kAtOnce], l[kAtOnce], o[kAtOnce][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * a + p.part_o[at * D + 32 * e + lane] * b;
-      m = top;
+    for (int r = 0; r < kAtOnce; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[r][e] = 0.f;
     }
-    const int head = h * p.group + j - i * p.group;
-    const int64_t row = q.row0 + i, off = row * p.a.ldo + (int64_t)head * D;
-    if (EXL3_SPAN(off, D, (int64_t)(kv.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D))
+    for (int64_t c = c0; c <= c1; ++c) {
+      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * kPair + first % kPair;
+      if (!EXL3_SPAN(at, kAtOnce, p.part_rows)) continue;
+      float2 ml[kAtOnce];
+      float x[kAtOnce][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) static_cast<__half *>(p.a.out)[off + 32 * e + lane] = __float2half_rn(l == 0.f ? 0.f : o[e] / l);
-    if (p.a.lse && lane == 0) p.a.lse[row * p.a.n_heads + head] = log_sum(m, l);
+      for (int r = 0; r < kAtOnce; ++r) {  // rows past the sequence's last hold nothing and are not written
+        ml[r] = reinterpret_cast<const float2 *>(p.part_ml)[at + r];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[r][e] = p.part_o[(at + r) * D + 32 * e + lane];
+      }
+#pragma unroll
+      for (int r = 0; r < kAtOnce; ++r) {
+        const float top = fmaxf(m[r], ml[r].x), ref = top == -INFINITY ? 0.f : top;
+        const float a = ex2(m[r] - ref), b = ex2(ml[r].x - ref);
+        l[r] = l[r] * a + ml[r].y * b;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[r][e] = o[r][e] * a + x[r][e] * b;
+        m[r] = top;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kAtOnce; ++r) {
+      const int j = first + r, i = j / p.group;
+      if (i >= q.rows) return;
+      const int head = h * p.group + j - i * p.group;
+      const int64_t row = q.row0 + i, off = row * p.a.ldo + (int64_t)head * D;
+      if (EXL3_SPAN(off, D, (int64_t)(kv.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D))
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          static_cast<__half *>(p.a.out)[off + 32 * e + lane] = __float2half_rn(l[r] == 0.f ? 0.f : o[r][e] / l[r]);
+      if (p.a.lse && lane == 0) p.a.lse[row * p.a.n_heads + head] = log_sum(m[r], l[r]);
+    }
   }
 }
 
