@@ -122,9 +122,15 @@ __device__ __forceinline__ float ex2(float x) {
 // log of a sum l of exponentials around m (log2 units).
 __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
 
-// First unit of worker w of W over T units, and the worker that owns unit z.
-__device__ __forceinline__ int64_t range_start(int64_t w, int64_t W, int64_t T) { return w * T / W; }
-__device__ __forceinline__ int64_t range_owner(int64_t z, int64_t W, int64_t T) { return ((z + 1) * W - 1) / T; }
+// First unit of worker w of W over T units, and the worker that owns unit z
+// (a 32-bit division where the numbers allow it: a 64-bit one takes about as long
+// as a load from memory).
+__device__ __forceinline__ int64_t range_start(int64_t w, int64_t W, int64_t T) {
+  return W * T < ((int64_t)1 << 31) ? (int64_t)((uint32_t)(w * T) / (uint32_t)W) : w * T / W;
+}
+__device__ __forceinline__ int64_t range_owner(int64_t z, int64_t W, int64_t T) {
+  return W * T < ((int64_t)1 << 31) ? (int64_t)(((uint32_t)((z + 1) * W) - 1) / (uint32_t)T) : ((z + 1) * W - 1) / T;
+}
 
 // softcap * tanh(s / softcap) through 1 - 2 / (exp(2 x) + 1): an absolute error
 // near softcap * 2^-23, which a direct tanh approximation (relative error 2^-11

@@ -139,9 +139,9 @@ __device__ __forceinline__ Cursor locate(const KvView &kv, int group, int tile, 
   c.s = lo;
   enter_sequence(plan, group, tile, c);
   const int64_t rem = z - plan.prefix[lo];
-  const int64_t seg = rem / (c.units + kEntry);
+  const int64_t seg = rem < ((int64_t)1 << 31) ? (int64_t)((uint32_t)rem / (uint32_t)(c.units + kEntry)) : rem / (c.units + kEntry);
   c.u = (int)(rem - seg * (c.units + kEntry)) - kEntry;
-  c.h = (int)(seg / c.tiles);
+  c.h = (int)((uint32_t)seg / (uint32_t)c.tiles);
   c.rt = (int)(seg - (int64_t)c.h * c.tiles);
   return c;
 }
@@ -644,6 +644,10 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
     for (int i = 0; i < Cfg::kStages; ++i) mbar_init(ring.bars + 8 * i, 1);
     fence_barrier_init();
   }
+  if (threadIdx.x == 0) {
+    prefetch_tensor_map(&tk);
+    prefetch_tensor_map(&tv);
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int tile = 8 * NT;
@@ -669,20 +673,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
     int limit[NT][2], min_limit = 0;  // tokens that this lane's rows see, and the tile's first row
     bool fresh = true, began = false;
     while (z < z1) {
-      while (zp < z1 && ring.in_flight < Cfg::kStages) {
-        if (!ahead.holds(cp)) ahead.load<false>(kv, cp, lane);
-        ring.issue(&tk, &tv, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
-        advance(kv, p.group, tile, plan, cp, zp);
-        skip_entry(cp, zp);
-      }
-      if (!now.holds(c)) {
-        if (ahead.holds(c)) now = ahead;
-        else now.load<false>(kv, c, lane);
-      }
-      const int at = (c.u >> 1) - now.base;
-      const int page = __shfl_sync(0xffffffffu, now.page, at);
-      const float ks = __shfl_sync(0xffffffffu, now.ks, at), vs = __shfl_sync(0xffffffffu, now.vs, at);
-      if (fresh) {
+      if (fresh) {  // first: on their way while the page numbers are
         fresh = false;
         began = c.u == 0;
         st.clear();
@@ -694,10 +685,23 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
         }
         min_limit = row_limit(p, c, c.rt * tile);  // rows come in order: the first sees the least
       }
+      while (zp < z1 && ring.in_flight < Cfg::kStages) {
+        if (!ahead.holds(cp)) ahead.load<false>(kv, cp, lane);
+        ring.issue(&tk, &tv, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
+        advance(kv, p.group, tile, plan, cp, zp);
+        skip_entry(cp, zp);
+      }
+      if (!now.holds(c)) {
+        if (ahead.holds(c)) now = ahead;
+        else now.load<false>(kv, c, lane);
+      }
       if (!ring.wait(kv.status)) {
         ring.drain();  // the call's outputs are undefined: the error word says so
         break;
       }
+      const int at = (c.u >> 1) - now.base;
+      const int page = __shfl_sync(0xffffffffu, now.page, at);
+      const float ks = __shfl_sync(0xffffffffu, now.ks, at), vs = __shfl_sync(0xffffffffu, now.vs, at);
       if (page >= 0)
         attend_unit<D, NT, CAP>(p, ring.stage(), c.u * kUnit, c.q.len, ks, vs, qf, limit, min_limit, inv_cap, lane, st);
       __syncwarp();  // every lane is done with the stage before it is filled again
@@ -791,6 +795,7 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
     for (int i = 0; i < Cfg::kStages; ++i) mbar_init(ring.bars + 8 * i, 1);
     fence_barrier_init();
   }
+  if (threadIdx.x == 0) prefetch_tensor_map(&tk);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   build_plan(kv, p.group, 0, plan);
@@ -809,8 +814,27 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
   int limit[2];
   float lse[2];  // in log2 units
   int held_s = -1, held_h = -1, held_j = -1;
+  // The queries, limits and lse of the 8 rows from j0 on, unless they are held.
+  auto hold = [&](int j0) {
+    if (held_s == c.s && held_h == c.h && held_j == j0) return;
+    held_s = c.s;
+    held_h = c.h;
+    held_j = j0;
+    load_query<D>(p, c, j0 + g, lane, qf[0]);
+#pragma unroll
+    for (int col = 0; col < 2; ++col) {
+      const int j = j0 + 2 * t + col, i = j / p.group;
+      limit[col] = row_limit(p, c, j);
+      lse[col] = limit[col] > 0 ? p.a.lse[(int64_t)(c.q.row0 + i) * p.a.n_heads + c.h * p.group + j - i * p.group] : 0.f;
+      if (lse[col] == -INFINITY) limit[col] = 0;
+      lse[col] *= kLog2e;
+    }
+  };
+  // The first row that sees a token of the cursor's unit.
+  auto first_row = [&]() { return p.a.causal ? max(0, c.u * kUnit - (c.q.len - c.q.rows)) * p.group : 0; };
 
   while (z < z1) {
+    if (held_s != c.s || held_h != c.h) hold(first_row() & ~7);  // on their way while the page numbers are
     while (zp < z1 && ring.in_flight < Cfg::kStages) {
       if (!ahead.holds(cp)) ahead.load<true>(kv, cp, lane);
       ring.issue(&tk, nullptr, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
@@ -821,36 +845,22 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
       if (ahead.holds(c)) now = ahead;
       else now.load<true>(kv, c, lane);
     }
-    const int at = (c.u >> 1) - now.base;
-    const int page = __shfl_sync(0xffffffffu, now.page, at);
-    const float ks = __shfl_sync(0xffffffffu, now.ks, at) * p.a.scale * (CAP ? 1.0f : kLog2e);
     if (!ring.wait(kv.status)) {
       ring.drain();
       return;
     }
+    const int at = (c.u >> 1) - now.base;
+    const int page = __shfl_sync(0xffffffffu, now.page, at);
+    const float ks = __shfl_sync(0xffffffffu, now.ks, at) * p.a.scale * (CAP ? 1.0f : kLog2e);
     if (page >= 0) {
       uint32_t words[2][2][D / 16];
       load_keys<D>(ring.stage(), lane, words);
       const int pos0 = c.u * kUnit, J = c.q.rows * p.group;
-      // the first row that sees a token of the unit
-      const int first = p.a.causal ? max(0, pos0 - (c.q.len - c.q.rows)) * p.group : 0;
+      const int first = first_row();
       float sum[2][2] = {}, part[2][2] = {};
       int n = 0;
       for (int j0 = first & ~7; j0 < J; j0 += 8) {
-        if (held_s != c.s || held_h != c.h || held_j != j0) {
-          held_s = c.s;
-          held_h = c.h;
-          held_j = j0;
-          load_query<D>(p, c, j0 + g, lane, qf[0]);
-#pragma unroll
-          for (int col = 0; col < 2; ++col) {
-            const int j = j0 + 2 * t + col, i = j / p.group;
-            limit[col] = row_limit(p, c, j);
-            lse[col] = limit[col] > 0 ? p.a.lse[(int64_t)(c.q.row0 + i) * p.a.n_heads + c.h * p.group + j - i * p.group] : 0.f;
-            if (lse[col] == -INFINITY) limit[col] = 0;
-            lse[col] *= kLog2e;
-          }
-        }
+        hold(j0);
         float s[1][2][4];
         score_products<D, 1>(words, qf, s);
 #pragma unroll
