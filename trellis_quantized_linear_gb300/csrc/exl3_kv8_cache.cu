@@ -116,21 +116,20 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// One cluster of CTAs per (sequence, head), each with a contiguous part of the
-// tokens to choose among. Their keys are read once into shared memory (those past
-// what fits are read again from memory); a radix selection, 11 bits a pass from
-// the top over the sums of the CTAs' bins, finds the key of the last token that
-// is kept, and each warp then writes the kept positions of its part, ties to the
-// lower positions. The first pass's bins hold the sign, the exponent and two
-// bits: weights fill few of them, so each bin has four copies, one for every
-// fourth lane. 8 sequences of up to 32K tokens, 8 heads: 47 us with one CTA each
-// (bound by its instructions), less the more CTAs share them.
+// One CTA per (sequence, head), or a cluster of them, each with a contiguous part
+// of the tokens, where the keys of the tokens to choose among do not fit one's
+// shared memory. The keys are read once (those past what a cluster of eight holds
+// are read again from memory); a radix selection, 11 bits a pass from the top over
+// the sums of the CTAs' bins, finds the key of the last token that is kept, and
+// each warp then writes the kept positions of its part, ties to the lower
+// positions. The first pass's bins hold the sign, the exponent and two bits:
+// weights fill few of them, so each bin has four copies, one for every fourth lane.
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectKeys = 16 * 1024;  // held in shared memory
+constexpr int kSelectKeys = 44 * 1024;  // held in shared memory
 constexpr int kBins = 2048, kCopies = 4;
 constexpr int kSelectMaxCluster = 8;
 
-__global__ void __launch_bounds__(kSelectThreads, 2) kv8_select_kernel(KvView kv, int budget, int recent, int held_max,
+__global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv, int budget, int recent, int held_max,
                                                                        int32_t *kept, int32_t *new_len) {
   extern __shared__ __align__(16) uint32_t select_smem[];
   int *hist = reinterpret_cast<int *>(select_smem);            // kBins x kCopies, then the sums
@@ -163,23 +162,35 @@ __global__ void __launch_bounds__(kSelectThreads, 2) kv8_select_kernel(KvView kv
     return page < 0 ? 0u : weight_key(kv.weight[((int64_t)page * kv.n_kv_heads + h) * kKvBlock + i % kKvBlock]);
   };
   const int held = min(n, held_max);
-  auto key_at = [&](int i) { return i < held ? keys[i] : read_key(first + i); };
+  // Keys i .. i + 3 (i a multiple of 4), 0 past the last: no weight has that key, so
+  // it is never counted on (the tokens wanted have higher ones) nor chosen.
+  auto four = [&](int i) {
+    if (i < held) return *reinterpret_cast<const uint4 *>(keys + i);
+    uint32_t k[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k[e] = i + e < n ? read_key(first + i + e) : 0u;
+    return make_uint4(k[0], k[1], k[2], k[3]);
+  };
   // a warp takes whole blocks, two tokens a lane; `first` is a multiple of a block
-  for (int b0 = warp; b0 * kKvBlock < held; b0 += kSelectWarps * 4) {
-    float2 w[4];
+  for (int b0 = warp; b0 * kKvBlock < held; b0 += kSelectWarps * 32) {
+    // page numbers of the warp's next 32 blocks, one a lane
+    const int mine = (b0 + lane * kSelectWarps) * kKvBlock;
+    const int page = mine < held ? kv_page(kv, s, (first + mine) / kKvBlock) : -1;
+    constexpr int kAhead = 8;
+    for (int j0 = 0; j0 < 32 && (b0 + j0 * kSelectWarps) * kKvBlock < held; j0 += kAhead) {
+      float2 w[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = (b0 + j * kSelectWarps) * kKvBlock;
-      if (i >= held) continue;
-      const int page = kv_page(kv, s, (first + i) / kKvBlock);
-      w[j] = make_float2(NAN, NAN);
-      if (page >= 0) w[j] = reinterpret_cast<const float2 *>(kv.weight + ((int64_t)page * kv.n_kv_heads + h) * kKvBlock)[lane];
-    }
+      for (int j = 0; j < kAhead; ++j) {
+        const int p = __shfl_sync(0xffffffffu, page, j0 + j);
+        w[j] = make_float2(NAN, NAN);
+        if (p >= 0) w[j] = reinterpret_cast<const float2 *>(kv.weight + ((int64_t)p * kv.n_kv_heads + h) * kKvBlock)[lane];
+      }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = (b0 + j * kSelectWarps) * kKvBlock + 2 * lane;
-      if (i < held) keys[i] = weight_key(w[j].x);
-      if (i + 1 < held) keys[i + 1] = weight_key(w[j].y);
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = (b0 + (j0 + j) * kSelectWarps) * kKvBlock + 2 * lane;
+        if (i < ((held + 3) & ~3))
+          *reinterpret_cast<uint2 *>(keys + i) = make_uint2(i < held ? weight_key(w[j].x) : 0u, i + 1 < held ? weight_key(w[j].y) : 0u);
+      }
     }
   }
 
@@ -191,9 +202,12 @@ __global__ void __launch_bounds__(kSelectThreads, 2) kv8_select_kernel(KvView kv
     const uint32_t mask = pass == 2 ? 1023u : 2047u, above = pass == 0 ? 0u : ~0u << (shift + (pass == 2 ? 10 : 11));
     for (int i = tid; i < kBins * kCopies / 4; i += kSelectThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = tid; i < n; i += kSelectThreads) {
-      const uint32_t key = key_at(i);
-      if ((key & above) == threshold) atomicAdd(&hist[((key >> shift) & mask) * kCopies + lane % kCopies], 1);
+    for (int i = tid * 4; i < n; i += kSelectThreads * 4) {
+      const uint4 k = four(i);
+      const uint32_t key[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((key[e] & above) == threshold) atomicAdd(&hist[((key[e] >> shift) & mask) * kCopies + lane % kCopies], 1);
     }
     __syncthreads();
     for (int i = tid; i < kBins; i += kSelectThreads) {
@@ -244,13 +258,13 @@ __global__ void __launch_bounds__(kSelectThreads, 2) kv8_select_kernel(KvView kv
   }
 
   // `left` tokens of the threshold's key are kept, the first ones.
-  const int part = ((n + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+  const int part = ((n + kSelectWarps - 1) / kSelectWarps + 127) & ~127;
   const int i0 = min(warp * part, n), i1 = min(i0 + part, n);
   int gt = 0, eq = 0;
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const uint32_t key = key_at(i);
-    gt += key > threshold;
-    eq += key == threshold;
+  for (int i = i0 + 4 * lane; i < i1; i += 128) {
+    const uint4 k = four(i);
+    gt += (k.x > threshold) + (k.y > threshold) + (k.z > threshold) + (k.w > threshold);
+    eq += (k.x == threshold) + (k.y == threshold) + (k.z == threshold) + (k.w == threshold);
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
@@ -280,16 +294,32 @@ __global__ void __launch_bounds__(kSelectThreads, 2) kv8_select_kernel(KvView kv
       }
     cluster_sync_all();  // a CTA stays until its counts have been read
   }
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t key = i < i1 ? key_at(i) : 0u;
-    const bool is_gt = i < i1 && key > threshold, is_eq = i < i1 && key == threshold;
-    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
-    const uint32_t below = (1u << lane) - 1;
-    const int ties = e + __popc(me & below);
-    const int at = g + __popc(mg & below) + min(ties, left);
-    if ((is_gt || (is_eq && ties < left)) && EXL3_RANGE(at, 0, want)) out[at] = first + i;
-    g += __popc(mg);
-    e += __popc(me);
+  for (int b = i0; b < i1; b += 128) {
+    const int i = b + 4 * lane;
+    const uint4 k = i < i1 ? four(i) : make_uint4(0, 0, 0, 0);
+    const uint32_t key[4] = {k.x, k.y, k.z, k.w};
+    // above the threshold in the low half, at it in the high half: one sum over the lanes before
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mine += key[e] > threshold ? 1 : key[e] == threshold ? 0x10000 : 0;
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    const int all = __shfl_sync(0xffffffffu, sum, 31);
+    int above = g + ((sum - mine) & 0xFFFF), ties = e + ((sum - mine) >> 16);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const bool is_gt = key[x] > threshold, is_eq = key[x] == threshold;
+      const int at = above + min(ties, left);
+      if ((is_gt || (is_eq && ties < left)) && EXL3_RANGE(at, 0, want)) out[at] = first + i + x;
+      above += is_gt;
+      ties += is_eq;
+    }
+    g += all & 0xFFFF;
+    e += all >> 16;
   }
 }
 
@@ -379,14 +409,14 @@ cudaError_t launch_kv8_append(const KvView &kv, const void *k, int64_t ldk, cons
 }
 
 cudaError_t launch_kv8_evict(const KvView &kv, const int32_t *dst_pages, int budget, int recent, int32_t *kept,
-                             int32_t *new_len, int num_sms, cudaStream_t st) {
+                             int32_t *new_len, cudaStream_t st) {
   if (kv.n_seqs == 0) return cudaSuccess;
-  // As many CTAs to a (sequence, head) as the SMs hold at once, two an SM, but
-  // 4096 tokens to a CTA at least: more would wait for one another longer than
-  // they save (32K tokens, 64 clusters: 47 us with 1 CTA, 64 us with 8).
-  const int64_t most = (int64_t)kv.max_pages * kKvBlock, clusters = (int64_t)kv.n_kv_heads * kv.n_seqs;
+  // As many CTAs to a (sequence, head) as hold its keys. A pass over a cluster's
+  // bins costs 5 us in barriers and remote reads, whatever the length: 8 sequences
+  // of up to 32K tokens, 8 heads, take 23 us with one CTA each and 26 us with four.
+  const int64_t most = (int64_t)kv.max_pages * kKvBlock;
   int ranks = 1;
-  while (ranks < kSelectMaxCluster && most > (int64_t)ranks * 4096 && 2 * ranks * clusters <= 2 * num_sms) ranks *= 2;
+  while (ranks < kSelectMaxCluster && most > (int64_t)ranks * kSelectKeys) ranks *= 2;
   const int64_t share = ceil_div(most, ranks * kKvBlock) * kKvBlock;
   const int held = (int)(share < kSelectKeys ? share : kSelectKeys);
   cudaError_t e = launch_overlapped(kv8_select_kernel, dim3(ranks, kv.n_kv_heads, kv.n_seqs), kSelectThreads,

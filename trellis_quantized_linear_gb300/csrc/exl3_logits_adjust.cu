@@ -156,7 +156,6 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
       if (allowed) bits[k] = allowed[t >> 5] >> (t & 31);
     }
   };
-  load(0, min(step, mine));  // in flight while the history is counted
 
   bool listed = false;
   if (h.y - h.x > 4 * T) {
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
     int piece = INT_MAX;  // of the best token without a word
     float top = best.x;
     for (int base = 0; base < n; base += T * V * 4) {
-      if (c0 + base > 0) load(c0 + base, c0 + n);
+      load(c0 + base, c0 + n);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int i = base + (k * T + tid) * 4, t = token(c0 + i);

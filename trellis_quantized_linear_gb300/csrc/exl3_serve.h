@@ -53,7 +53,7 @@ cudaError_t init_logits_adjust_kernels(int *status);
 
 cudaError_t launch_kv8_append(const KvView &kv, const void *k, int64_t ldk, const void *v, int64_t ldv, cudaStream_t st);
 cudaError_t launch_kv8_evict(const KvView &kv, const int32_t *dst_pages, int budget, int recent, int32_t *kept,
-                             int32_t *new_len, int num_sms, cudaStream_t st);
+                             int32_t *new_len, cudaStream_t st);
 size_t kv8_attention_workspace_bytes(const exl3_kv8_cache &cache, const exl3_kv8_batch &batch, int n_heads, int num_sms);
 cudaError_t launch_kv8_attention(const KvAttention &p, cudaStream_t st);
 // More rows than the stream kernel takes (exl3_kv8_chunk.cu).

@@ -138,7 +138,7 @@ exl3_status exl3_kv8_evict(const exl3_kv8_cache *cache, const exl3_kv8_batch *ba
   KvView kv;
   const exl3_status s = validate_kv(cache, batch, false, &dev, &kv);
   if (s != EXL3_OK) return s;
-  return from_cuda(launch_kv8_evict(kv, dst_pages, budget, recent, kept, new_len, dev->num_sms, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_kv8_evict(kv, dst_pages, budget, recent, kept, new_len, static_cast<cudaStream_t>(stream)));
 }
 
 exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules *rules,
