@@ -274,8 +274,8 @@ exl3_status exl3_logits_masked(const void *x, int64_t M, int64_t K, const uint16
  * EXL3_ERR_DEVICE_TIMEOUT if a kernel gave up one of its bounded waits,
  * EXL3_ERR_OUT_OF_BOUNDS if a check of the bounds-checked build failed,
  * EXL3_ERR_DEVICE_INDEX if a serving call met a page number, length or row
- * range on the device that its buffers do not hold (what it names was
- * skipped); EXL3_OK otherwise.
+ * range on the device that its buffers do not hold (it was not followed; the
+ * call's outputs for that sequence are undefined); EXL3_OK otherwise.
  * The word is one per device, shared by every stream and workspace on it
  * (some entry points that wait on the device have no workspace): with
  * several streams, a timeout is reported to whichever caller reads first.
@@ -428,7 +428,9 @@ typedef struct {
  *         one fused projection's output will do.
  * Each block that receives tokens gets the scale above. Where it grows, the
  * older tokens' codes are rescaled, E4M3(code * 2^(e_old - e)); new codes are
- * E4M3(x * 2^-e), both rounded to nearest even. Infinities saturate at
+ * E4M3(x * 2^-e), both rounded to nearest even. New tokens before position 0
+ * (kv_len below the sequence's rows) are dropped and recorded as
+ * EXL3_ERR_DEVICE_INDEX. Infinities saturate at
  * +-448 * 2^e; NaN is stored as NaN (E4M3 has one) and takes no part in the
  * scale. Slots past a sequence's length keep what they held. The cache's
  * `weight` of the new tokens is set to 0 where the cache has one.
@@ -455,9 +457,15 @@ exl3_status exl3_kv8_append(const exl3_kv8_cache *cache, const exl3_kv8_batch *b
  * the sequence in this call, also rows before its position.
  * Sums, maxima and the softmax are fp32; the probabilities enter the product
  * with the values as fp16.
- *   scale: finite; softcap: finite, 0 (off) or more.
+ *   scale: finite; softcap: 0 (off) or finite and at least 1e-30.
  *   workspace: exl3_kv8_attention_workspace_bytes bytes (0 for invalid
- *         arguments), contents undefined before and after.
+ *         arguments; it goes by rows, max_rows, the heads and head_dim),
+ *         contents undefined before and after. Calls that share one must be
+ *         ordered.
+ * Up to 16 rows of a sequence and key/value head (max_rows x heads of a group)
+ * go through a kernel bound by reading the cache once, more through one on the
+ * tensor cores; both split long sequences over all SMs by the lengths that they
+ * find on the device, and the result does not depend on scheduling.
  */
 size_t exl3_kv8_attention_workspace_bytes(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, int32_t n_heads);
 exl3_status exl3_kv8_attention(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, const void *q, int64_t ldq,

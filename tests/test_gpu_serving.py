@@ -530,6 +530,56 @@ def test_bad_indexes_on_the_device_are_reported_and_skipped():
         assert torch.equal(t[same], b[same])
 
 
+@pytest.mark.parametrize("table,kv_len,start", [([[-1] * 3, [1 << 30] * 3], [100, 100], [0, 20, 40]),
+                                                (None, [1000, -5], [0, 20, 40]), (None, [100, 100], [0, 41, 40]),
+                                                (None, [100, 100], [-3, 0, 40])])
+def test_bad_indexes_on_the_device_with_many_rows(table, kv_len, start):
+    torch = torch_mod()
+    pool = Pool([100, 100], 1, 128, seed=1)
+    cache = pool.on_device()
+    q = rows_on_device(np.ones((40, 128), dtype=np.float16), 0)
+    batch = tql.Exl3Kv8Batch(dev(np.array(pool.table if table is None else table, dtype=np.int32)), dev(np.array(kv_len, dtype=np.int32)),
+                             dev(np.array(start, dtype=np.int32)), 40, 20)
+    out = torch.zeros((40, 128), dtype=torch.float16, device="cuda")
+    ws = torch.empty(tql.exl3_kv8_attention_workspace_bytes(cache, batch, 1), dtype=torch.uint8, device="cuda")
+    for call in (lambda: tql.exl3_kv8_attention(cache, batch, q, 1, 1.0, out, ws), lambda: tql.exl3_kv8_append(cache, batch, q, q),
+                 lambda: tql.exl3_kv8_weigh(cache, batch, q, 1, 1.0, torch.zeros((40, 1), device="cuda"))):
+        call()
+        assert tql.exl3_get_device_status() == 10
+        assert tql.exl3_get_device_status() == 0
+
+
+def test_chunk_lengths_change_under_one_graph():
+    """As above for the kernels of many rows: a captured chunk serves other lengths and rows."""
+    torch = torch_mod()
+    pool = Pool([500, 300], 2, 64, seed=22)
+    cache = pool.on_device()
+    batch = pool.batch([60, 40])
+    q = pool.rng.standard_normal((100, 4, 64)).astype(np.float16)
+    qd = rows_on_device(q.reshape(100, -1), 0)
+    out = torch.zeros((100, 256), dtype=torch.float16, device="cuda")
+    lse = torch.zeros((100, 4), device="cuda")
+    ws = torch.empty(tql.exl3_kv8_attention_workspace_bytes(cache, batch, 4), dtype=torch.uint8, device="cuda")
+
+    def call():
+        tql.exl3_kv8_attention(cache, batch, qd, 4, 0.2, out, ws, lse=lse)
+        tql.exl3_kv8_weigh(cache, batch, qd, 4, 0.2, lse)
+
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for kv_len, counts in (([500, 300], [60, 40]), ([130, 60], [45, 55]), ([33, 7], [60, 40])):
+        batch._keep[1].copy_(dev(np.array(kv_len, dtype=np.int32)))
+        batch._keep[2].copy_(dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)))
+        g.replay()
+        torch.cuda.synchronize()
+        want = ref.attention(pool.codes[0], pool.scales[0], pool.codes[1], pool.scales[1], pool.table, kv_len, counts,
+                             q, 0.2, 0.0, True)
+        check_attention(out.float().cpu().numpy().reshape(100, 4, 64), lse.cpu().numpy(), want, 64, 0.0, 500)
+
+
 def test_empty_calls_are_no_ops():
     torch = torch_mod()
     pool = Pool([10], 1, 64, seed=1)

@@ -91,7 +91,7 @@ def test_append_refusals(lib):
 def test_attention_refusals(lib):
     for call in (attend, weigh):
         for kw in (dict(heads=0), dict(heads=-8), dict(heads=12), dict(ldq=4088), dict(ldq=4100), dict(scale=float("nan")),
-                   dict(scale=float("inf")), dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf"))):
+                   dict(scale=float("inf")), dict(cap=-1.0), dict(cap=1e-35), dict(cap=float("nan")), dict(cap=float("inf"))):
             assert call(lib, **kw) == INVALID, kw
     for kw in (dict(q=None), dict(q=GOOD + 8), dict(lse=GOOD + 2)):
         assert attend(lib, **kw) == ALIGNMENT and weigh(lib, **kw) == ALIGNMENT, kw

@@ -46,6 +46,9 @@ bool attention_shape_ok(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch
          n_heads % cache->n_kv_heads == 0 && (int64_t)batch->rows * n_heads <= INT32_MAX;
 }
 
+// 0 is off; below 1e-30 the scores' quotient by it would leave fp32.
+bool softcap_ok(float c) { return c == 0.f || (isfinite(c) && c >= 1e-30f); }
+
 bool ld_ok(int64_t ld, int64_t width) { return ld >= width && ld % 8 == 0 && ld <= INT32_MAX; }
 
 }  // namespace
@@ -83,7 +86,7 @@ exl3_status exl3_kv8_attention(const exl3_kv8_cache *cache, const exl3_kv8_batch
                                float *lse, void *workspace, size_t workspace_bytes, void *stream) {
   if (!attention_shape_ok(cache, batch, n_heads)) return EXL3_ERR_INVALID_ARG;
   const int64_t width = (int64_t)n_heads * cache->head_dim;
-  if (!ld_ok(ldq, width) || !ld_ok(ldo, width) || !isfinite(scale) || !isfinite(softcap) || softcap < 0.f)
+  if (!ld_ok(ldq, width) || !ld_ok(ldo, width) || !isfinite(scale) || !softcap_ok(softcap))
     return EXL3_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)) || !aligned(workspace, 16))
     return EXL3_ERR_ALIGNMENT;
@@ -110,7 +113,7 @@ exl3_status exl3_kv8_attention(const exl3_kv8_cache *cache, const exl3_kv8_batch
 exl3_status exl3_kv8_weigh(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, const void *q, int64_t ldq,
                            int32_t n_heads, float scale, float softcap, int causal, const float *lse, void *stream) {
   if (!attention_shape_ok(cache, batch, n_heads)) return EXL3_ERR_INVALID_ARG;
-  if (!ld_ok(ldq, (int64_t)n_heads * cache->head_dim) || !isfinite(scale) || !isfinite(softcap) || softcap < 0.f)
+  if (!ld_ok(ldq, (int64_t)n_heads * cache->head_dim) || !isfinite(scale) || !softcap_ok(softcap))
     return EXL3_ERR_INVALID_ARG;
   if (!cache->weight || !aligned(q, 16) || !aligned(lse, 4)) return EXL3_ERR_ALIGNMENT;
   KvAttention p{};
