@@ -8,10 +8,11 @@
 // exp2(s - lse) over the step's columns. No maximum, no second product: the
 // exponentials bound it, 128 x 128 of them a step against 512 cycles of tensor
 // work, so two CTAs share an SM and take turns.
-//   * warps 0..7: the item's keys, then per step the columns' lse (a step ahead,
-//     in registers, then shared memory), the exponentials and the sums; warps 0..3
-//     have the first 64 columns and warps 4..7 the others (eight warps hide the
-//     latency of a dependent chain that four leave bare: 287 us with four);
+//   * warps 0..7: the item's keys, then per step the columns' lse, the exponentials
+//     and the sums; warps 0..3 have the first 64 columns and warps 4..7 the others
+//     (eight warps hide the latency of a dependent chain that four leave bare: 287 us
+//     with four). Each warp brings its own 64 lse, a step ahead in registers, then in
+//     shared memory of its own: with one copy for all, a barrier a step, 224 us;
 //   * warp 8 (one lane): tcgen05.mma;
 //   * warp 9 (one lane): TMA of the queries, a box of 64 dimensions x heads x rows,
 //     so a step is the group's heads of consecutive rows without a copy.
@@ -38,8 +39,8 @@ struct WeighCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kOperand = kHalves * 128 * 128;
   static constexpr int kOffQ = kOperand;                    // two stages
-  static constexpr int kOffCol = kOffQ + 2 * kOperand;      // two buffers of (lse, limit) x 128, then sums
-  static constexpr int kOffPlan = kOffCol + 2 * kCols * 8 + kItem * 4;  // int prefix, then int2 sequences
+  static constexpr int kOffCol = kOffQ + 2 * kOperand;      // (lse, limit) x 64 a warp, then sums
+  static constexpr int kOffPlan = kOffCol + kExpWarps * (kCols / 2) * 8 + kItem * 4;  // int prefix, then int2 sequences
   static constexpr int kOffBar = kOffPlan + (kWeighSeqs + 8) * 4 + (kWeighSeqs + 8) * 8;
   static constexpr int kSmem = 1024 + kOffBar + 256;
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -152,7 +153,6 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
   const uint32_t bars = base + Cfg::kOffBar;
   auto bar = [&](int i) { return bars + 8 * i; };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kOffBar + 8 * kWBars);
-  __shared__ uint32_t full[2][4];  // of a step's 32 columns: all see the whole item
   int *status = kv.status;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -239,14 +239,17 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     const int tid = threadIdx.x, row = tid & 127, half = tid >> 7;  // token of the item, half of the columns
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 64 * half;
     const float cap = p.a.softcap, inv_cap = CAP ? 1.0f / cap : 0.f;
-    float *col_lse = reinterpret_cast<float *>(smem + Cfg::kOffCol);
-    int *col_limit = reinterpret_cast<int *>(smem + Cfg::kOffCol + 2 * kCols * 4);
-    float *col_sum = reinterpret_cast<float *>(smem + Cfg::kOffCol + 4 * kCols * 4);
+    constexpr int kHalf = kCols / 2;
+    float *col_lse = reinterpret_cast<float *>(smem + Cfg::kOffCol) + warp * 2 * kHalf;  // the warp's own
+    int *col_limit = reinterpret_cast<int *>(col_lse + kHalf);
+    float *col_sum = reinterpret_cast<float *>(smem + Cfg::kOffCol) + kExpWarps * 2 * kHalf;
     [[maybe_unused]] const int64_t size = kv.n_pages * kv.n_kv_heads * kKvBlock * (int64_t)D;
     // The tensor core cuts its partial sums off towards zero, D / 16 times: on average
     // this share of a score. Without it heavy weights came out 2e-6 low.
     const float untruncate = 1.0f + 0.6f * 0.5f * (D / 16 + 1) * 0.5f * 0x1p-23f;
-    const int my_row = tid / p.heads, my_head = tid % p.heads;
+    // a lane brings two of its warp's columns
+    const int col0 = half * kHalf + lane, col1 = col0 + 32;
+    const int row_0 = col0 / p.heads, head_0 = col0 % p.heads, row_1 = col1 / p.heads, head_1 = col1 % p.heads;
     uint32_t n = 0;
     bool ok = true;
     for (int z = blockIdx.x; ok && get_item(p, plan, z, it); z += gridDim.x) {
@@ -282,39 +285,47 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kWKeys));
 
-      // column tid of the steps in order: its row's lse, and how many tokens the row sees
-      int col_row = it.first + my_row, col_chunk = 0;
-      auto column = [&](float &lse, int &limit) {
-        const int g = col_chunk * p.heads + my_head;
+      // a column of the steps in order: its row's lse, and how many tokens the row sees
+      int step_row = it.first, chunk = 0;
+      auto column = [&](int col, int r, int hd, float &lse, int &limit) {
+        const int g = chunk * p.heads + hd;
+        r += step_row;
         limit = 0;
         lse = 0.f;
-        if (tid < step_cols && g < p.group && col_row < it.q.rows) {
-          const int64_t at = (int64_t)(it.q.row0 + col_row) * p.a.n_heads + it.h * p.group + g;
+        if (col < step_cols && g < p.group && r < it.q.rows) {
+          const int64_t at = (int64_t)(it.q.row0 + r) * p.a.n_heads + it.h * p.group + g;
           if (EXL3_SPAN(at, 1, (int64_t)kv.rows * p.a.n_heads)) lse = p.a.lse[at];
-          limit = p.a.causal ? it.q.len - it.q.rows + col_row + 1 : it.q.len;
-        }
-        if (++col_chunk == it.chunks) {
-          col_chunk = 0;
-          col_row += p.rows;
+          limit = p.a.causal ? it.q.len - it.q.rows + r + 1 : it.q.len;
         }
       };
-      float lse = 0.f, total = 0.f;
-      int limit = 0;
-      if (it.steps > 0) column(lse, limit);
+      float lse0 = 0.f, lse1 = 0.f, total = 0.f;
+      int limit0 = 0, limit1 = 0;
+      auto columns = [&]() {
+        column(col0, row_0, head_0, lse0, limit0);
+        column(col1, row_1, head_1, lse1, limit1);
+        if (++chunk == it.chunks) {
+          chunk = 0;
+          step_row += p.rows;
+        }
+      };
+      if (it.steps > 0) columns();
       const int end = min(pos0 + kItem, it.q.len);
       for (int st = 0; st < it.steps; ++st, ++n) {
         const uint32_t b = n & 1;
-        if (half == 0) {
-          if (lse == -INFINITY) limit = 0;  // a row that saw nothing (here, so that the load has had a step's time)
-          col_lse[b * kCols + tid] = tid < step_cols ? -lse : -INFINITY;
-          col_limit[b * kCols + tid] = limit;
-          // (a column that no step has: its query row is zero and its lse infinite)
-          const uint32_t sees = __ballot_sync(0xffffffffu, limit >= end || tid >= step_cols);
-          if (lane == 0) full[b][warp] = sees == 0xffffffffu;
-          if (st + 1 < it.steps) column(lse, limit);
+        if (lse0 == -INFINITY) limit0 = 0;  // a row that saw nothing (here, so that the load has had a step's time)
+        if (lse1 == -INFINITY) limit1 = 0;
+        // (a column that no step has: its query row is zero and its lse infinite)
+        const bool full = __all_sync(0xffffffffu, (limit0 >= end || col0 >= step_cols) && (limit1 >= end || col1 >= step_cols));
+        col_lse[lane] = col0 < step_cols ? -lse0 : -INFINITY;
+        col_lse[lane + 32] = col1 < step_cols ? -lse1 : -INFINITY;
+        if (!full) {
+          col_limit[lane] = limit0;
+          col_limit[lane + 32] = limit1;
         }
-        // the columns are there, and a wait that ran out ends the loop in all warps or in none
-        if (!all_agree(mbar_wait(bar(kWSFull + b), (n >> 1) & 1, status))) {
+        if (st + 1 < it.steps) columns();
+        __syncwarp();
+        ok = mbar_wait(bar(kWSFull + b), (n >> 1) & 1, status);
+        if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
@@ -332,42 +343,48 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
           d = mul2(d, make_float2(kLog2e, kLog2e));
           return make_float2(ex2(d.x), ex2(d.y));
         };
+        auto release = [&]() {  // the buffer is free for the step after the next
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kWSEmpty + b));
+        };
+        if (full) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int q = 2 * half + i;
-          float s[32];
-          tmem_ld32(lane_base + 128 * b + 32 * i, s);
-          if (i == 1) {  // the buffer is free for the step after the next
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kWSEmpty + b));
-          }
-          const float *minus = col_lse + b * kCols + 32 * q;
-          if (full[b][q]) {
+          for (int i = 0; i < 2; ++i) {
+            float s[32];
+            tmem_ld32(lane_base + 128 * b + 32 * i, s);
+            if (i == 1) release();
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
-              const float4 m = *reinterpret_cast<const float4 *>(minus + k);
+              const float4 m = *reinterpret_cast<const float4 *>(col_lse + 32 * i + k);
               part[0] = add2(part[0], weight(s[k], s[k + 1], make_float2(m.x, m.y)));
               part[1] = add2(part[1], weight(s[k + 2], s[k + 3], make_float2(m.z, m.w)));
             }
-          } else {
-            const int *seen = col_limit + b * kCols + 32 * q;
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            float s[32];
+            tmem_ld32(lane_base + 128 * b + 32 * i, s);
+            if (i == 1) release();
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
-              const float2 m = *reinterpret_cast<const float2 *>(minus + k);
-              const int2 l = *reinterpret_cast<const int2 *>(seen + k);
+              const float2 m = *reinterpret_cast<const float2 *>(col_lse + 32 * i + k);
+              const int2 l = *reinterpret_cast<const int2 *>(col_limit + 32 * i + k);
               const float2 x = weight(s[k], s[k + 1], m);
               part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], make_float2(pos < l.x ? x.x : 0.f, pos < l.y ? x.y : 0.f));
             }
           }
         }
+        __syncwarp();  // all lanes are past the columns
         part[0] = add2(part[0], part[1]);
         total += part[0].x + part[0].y;  // a sum of sums: 82 steps of 10240 rows lose no bits that matter
       }
       // the other half's sum; all warps are past the item's last step then (its scores
-      // come from the last product that reads the keys)
+      // come from the last product that reads the keys), and a wait that ran out in one
+      // ends the loop in all
       if (half == 1) col_sum[row] = total;
-      asm volatile("bar.sync 1, %0;" ::"n"(kExpWarps * 32) : "memory");
+      ok = all_agree(ok);
       const int64_t at = slab * kKvBlock + pos % kKvBlock;
       if (ok && half == 0 && page >= 0 && EXL3_SPAN(at, 1, kv.n_pages * kv.n_kv_heads * kKvBlock))
         kv.weight[at] += total + col_sum[row];
