@@ -477,8 +477,9 @@ exl3_status exl3_kv8_attention(const exl3_kv8_cache *cache, const exl3_kv8_batch
  * this call sees the attention that it gets,
  *     weight[t] += sum over rows and query heads of the group: exp(s[t] - lse),
  * with s as in exl3_kv8_attention and lse as that call returned it (rows whose
- * lse is -inf add nothing). Each token's sum is formed in a fixed order: the
- * result does not depend on scheduling.
+ * lse is -inf add nothing). Each sequence's sum for a token is formed in a fixed
+ * order: the result does not depend on scheduling, except where sequences of the
+ * call share a block, whose sums are added to its weights in any order.
  */
 exl3_status exl3_kv8_weigh(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, const void *q, int64_t ldq,
                            int32_t n_heads, float scale, float softcap, int causal, const float *lse, void *stream);

@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
           const int tok = 16 * mi + g + 8 * r;
           const int64_t off = slab * kKvBlock + (c.u & 1) * kUnit + tok;
           if (t == 0 && pos0 + tok < c.q.len && EXL3_SPAN(off, 1, kv.n_pages * kv.n_kv_heads * kKvBlock))
-            atomicAdd(&kv.weight[off], x);  // the only add to this token in the call: without a wait for the old value
+            atomicAdd(&kv.weight[off], x);  // alone but for sequences that share the block; no wait for the old value
         }
     }
     __syncwarp();

@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       ok = all_agree(ok);
       const int64_t at = slab * kKvBlock + pos % kKvBlock;
       if (ok && half == 0 && page >= 0 && EXL3_SPAN(at, 1, kv.n_pages * kv.n_kv_heads * kKvBlock))
-        kv.weight[at] += total + col_sum[row];
+        atomicAdd(&kv.weight[at], total + col_sum[row]);  // alone but for sequences that share the block
     }
   }
   tc_fence_before();
