@@ -1,15 +1,16 @@
 // Attention over the 8-bit key/value cache, and the accumulated attention weight
 // of its tokens. Formulas in include/exl3.h.
 //
-// Stream kernel. All work is cut into units of 32 cached tokens; the units of
-// every (sequence, key/value head, row tile) lie one behind the other, and each
-// warp of a persistent grid takes one equal, contiguous range of them, whatever
-// the sequences' lengths are (they are read on the device). A warp keeps its own
-// ring of TMA copies in flight and its own running maximum, sum and output, so
-// warps do not wait for one another. Where ranges end inside a segment, the
-// partial results are joined in the order of the ranges: those of a CTA's warps
-// through shared memory when the CTA is done, those of several CTAs through the
-// workspace by a second kernel.
+// Stream kernel, for up to 16 rows (row of the sequence x head of the group) of a
+// segment, a (sequence, key/value head). All work is cut into units of 32 cached
+// tokens; the units of all segments lie one behind the other, and each warp of a
+// persistent grid takes one equal, contiguous range of them, whatever the
+// sequences' lengths are (they are read on the device). A warp keeps its own ring
+// of TMA copies in flight and its own running maximum, sum and output, so warps do
+// not wait for one another. Where ranges end inside a segment, the partial results
+// are joined in the order of the ranges: those of a CTA's warps through shared
+// memory when the CTA is done, those of several CTAs through the workspace by a
+// second kernel.
 //
 // The bound is the cache stream: D + D bytes a token and head. The tensor core's
 // narrow side takes the rows (S^T = K Q^T and O^T = V^T P^T, m16n8k16): 8 rows
@@ -37,7 +38,7 @@ constexpr int kMaxSeqs = 1024;    // sequences of one launch
 // average without it.
 constexpr int kEntry = 3;
 
-// NT tiles of 8 rows. 8 rows leave room for 12 warps an SM (168 registers a
+// NT x 8 rows. 8 rows leave room for 12 warps an SM (168 registers a
 // thread), 16 rows for 8; the kernel is bound by the latency of dependent
 // instructions until there are about 12.
 template <int D, int NT, bool WEIGH>
@@ -59,12 +60,12 @@ struct StreamParams {
   // Workspace: partial results of the CTAs (slot 0: a segment that began before
   // the CTA's range, slot 1: one that began in it and goes on after it), and the
   // plan for the join.
-  float *part_o;      // CTAs x 2 x tile rows x D
-  float *part_ml;     // CTAs x 2 x tile rows x 2 (maximum in log2 units, sum)
-  float *first;       // warps x tile rows x (D + 2): see Parts
+  float *part_o;      // CTAs x 2 x rows x D
+  float *part_ml;     // CTAs x 2 x rows x 2 (maximum in log2 units, sum)
+  float *first;       // warps x rows x (D + 2): see Parts
   int64_t *plan;      // prefix of build_plan
   int warps;          // of the stream grid
-  int64_t part_rows;  // 2 * CTAs * tile rows
+  int64_t part_rows;  // 2 * CTAs * rows
 };
 
 __device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
@@ -81,9 +82,8 @@ struct Plan {
 
 __device__ __forceinline__ int64_t segment_units(int len) { return len > 0 ? units_of(len) + kEntry : 0; }
 
-// Row tiles of `tile` rows (0: the rows are not tiled). Every thread of the CTA
-// takes part; ends with a barrier.
-__device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile, const Plan &plan) {
+// Every thread of the CTA takes part; ends with a barrier.
+__device__ __forceinline__ void build_plan(const KvView &kv, const Plan &plan) {
   int64_t *warp_sum = plan.prefix + kMaxSeqs + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
   int64_t carry = 0;
@@ -93,7 +93,7 @@ __device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile
     int64_t n = 0;
     if (s < kv.n_seqs) {
       const KvSeq q = kv_sequence(kv, s);
-      if (q.rows > 0) n = segment_units(q.len) * kv.n_kv_heads * (tile ? ((int64_t)q.rows * group + tile - 1) / tile : 1);
+      if (q.rows > 0) n = segment_units(q.len) * kv.n_kv_heads;
       plan.seq[s] = make_int2(kv.q_start[s], q.rows > 0 ? q.len : -1);
       if (s + 1 == kv.n_seqs) plan.seq[s + 1] = make_int2(kv.q_start[s + 1], -1);
     }
@@ -120,15 +120,14 @@ __device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile
 // A place in the unit order; u < 0: entering the segment.
 struct Cursor {
   KvSeq q;
-  int s, h, rt, u;    // sequence, key/value head, row tile, unit of the segment
-  int units, tiles;   // of this sequence's segments
+  int s, h, u;        // sequence, key/value head, unit of the segment
+  int units;          // of this sequence's segments
 };
-__device__ __forceinline__ void enter_sequence(const Plan &plan, int group, int tile, Cursor &c) {
+__device__ __forceinline__ void enter_sequence(const Plan &plan, Cursor &c) {
   c.q = plan.at(c.s);
   c.units = units_of(c.q.len);
-  c.tiles = tile ? (c.q.rows * group + tile - 1) / tile : 1;
 }
-__device__ __forceinline__ Cursor locate(const KvView &kv, int group, int tile, const Plan &plan, int64_t z) {
+__device__ __forceinline__ Cursor locate(const KvView &kv, const Plan &plan, int64_t z) {
   Cursor c;
   int lo = 0, hi = kv.n_seqs - 1;  // the s with prefix[s] <= z < prefix[s + 1]
   while (lo < hi) {
@@ -137,26 +136,22 @@ __device__ __forceinline__ Cursor locate(const KvView &kv, int group, int tile, 
     else lo = mid + 1;
   }
   c.s = lo;
-  enter_sequence(plan, group, tile, c);
+  enter_sequence(plan, c);
   const int64_t rem = z - plan.prefix[lo];
-  const int64_t seg = rem < ((int64_t)1 << 31) ? (int64_t)((uint32_t)rem / (uint32_t)(c.units + kEntry)) : rem / (c.units + kEntry);
-  c.u = (int)(rem - seg * (c.units + kEntry)) - kEntry;
-  c.h = (int)((uint32_t)seg / (uint32_t)c.tiles);
-  c.rt = (int)(seg - (int64_t)c.h * c.tiles);
+  c.h = rem < ((int64_t)1 << 31) ? (int)((uint32_t)rem / (uint32_t)(c.units + kEntry)) : (int)(rem / (c.units + kEntry));
+  c.u = (int)(rem - (int64_t)c.h * (c.units + kEntry)) - kEntry;
   return c;
 }
 // The next place; z moves with it.
-__device__ __forceinline__ void advance(const KvView &kv, int group, int tile, const Plan &plan, Cursor &c, int64_t &z) {
+__device__ __forceinline__ void advance(const KvView &kv, const Plan &plan, Cursor &c, int64_t &z) {
   ++z;
   if (++c.u < c.units) return;
   c.u = -kEntry;
-  if (++c.rt < c.tiles) return;
-  c.rt = 0;
   if (++c.h < kv.n_kv_heads) return;
   c.h = 0;
   do ++c.s;
   while (c.s < kv.n_seqs && plan.prefix[c.s + 1] == plan.prefix[c.s]);
-  if (c.s < kv.n_seqs) enter_sequence(plan, group, tile, c);
+  if (c.s < kv.n_seqs) enter_sequence(plan, c);
 }
 // Past the places of entering.
 __device__ __forceinline__ void skip_entry(Cursor &c, int64_t &z) {
@@ -230,7 +225,7 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t *w) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
 }
 
-// The B operand of S^T: this lane's D / 4 elements of row j (lane / 4) of the tile.
+// The B operand of S^T: this lane's D / 4 elements of row j (from lane / 4).
 template <int D>
 __device__ __forceinline__ void load_query(const StreamParams &p, const Cursor &c, int j, int lane, uint32_t (&qf)[D / 8]) {
   const int t = lane & 3;
@@ -271,7 +266,7 @@ __device__ __forceinline__ void load_keys(uint32_t base, int lane, uint32_t (&w)
       for (int x = 0; x < D / 64; ++x) lds<4>(piece<D>(base, 16 * mi + 8 * r + g, (D / 64) * t + x), &w[mi][r][4 * x]);
 }
 
-// S^T of a unit for NT tiles of 8 rows; the chains of the two 16-token halves and
+// S^T of a unit for NT x 8 rows; the chains of the two 16-token halves and
 // of even and odd k-steps are independent.
 template <int D, int NT>
 __device__ __forceinline__ void score_products(const uint32_t (&w)[2][2][D / 16], const uint32_t (&qf)[NT][D / 8],
@@ -495,7 +490,7 @@ __device__ __forceinline__ void store_out(const KvAttention &a, int64_t row, int
 // end of a segment that began before the warp's range (in the workspace), and
 // 2 w + 1, its last segment (in shared memory, the ring's).
 struct Part {
-  int s, h, rt;  // the segment; s < 0: no part
+  int s, h;  // the segment; s < 0: no part
   int begins, ends;
 };
 template <int D, int NT>
@@ -540,7 +535,7 @@ __device__ __forceinline__ void write_rows(const StreamParams &p, const Cursor &
 #pragma unroll
     for (int col = 0; col < 2; ++col) {
       const float l = st.l[n][col], f = l == 0.f ? 0.f : pow2i(st.ev) / l;
-      const int j = c.rt * 8 * NT + 8 * n + 2 * t + col, i = j / p.group;
+      const int j = 8 * n + 2 * t + col, i = j / p.group;
       if (i >= c.q.rows) continue;
       float v[D / 8];
 #pragma unroll
@@ -600,10 +595,10 @@ __device__ __forceinline__ void join_cta(const StreamParams &p, const Parts<D, N
       const bool last = part.ends || (left & (left - 1)) == 0;
       if (!last) continue;
       const KvSeq q = kv_sequence(p.a.kv, part.s);
-      const int j = part.rt * P::kRows + r, row = j / p.group;
+      const int row = r / p.group;
       if (row < q.rows) {
         if (begins && part.ends) {
-          const int head = part.h * p.group + j - row * p.group;
+          const int head = part.h * p.group + r - row * p.group;
           const int64_t off = (int64_t)(q.row0 + row) * p.a.ldo + (int64_t)head * D + d0;
           const float f = l == 0.f ? 0.f : 1.0f / l;
           const __half2 lo = __floats2half2_rn(o.x * f, o.y * f), hi = __floats2half2_rn(o.z * f, o.w * f);
@@ -650,8 +645,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int tile = 8 * NT;
-  build_plan(kv, p.group, tile, plan);
+  build_plan(kv, plan);
   const int64_t T = plan.prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   if (blockIdx.x == 0)
@@ -663,14 +657,14 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
   if (w < W) {
     int64_t z = range_start(w, W, T);
     const int64_t z1 = range_start(w + 1, W, T);
-    Cursor c = locate(kv, p.group, tile, plan, z);
+    Cursor c = locate(kv, plan, z);
     skip_entry(c, z);
     int64_t zp = z;
     Cursor cp = c;
     Blocks ahead, now;
     const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
     uint32_t qf[NT][D / 8];
-    int limit[NT][2], min_limit = 0;  // tokens that this lane's rows see, and the tile's first row
+    int limit[NT][2], min_limit = 0;  // tokens that this lane's rows see, and the first row
     bool fresh = true, began = false;
     while (z < z1) {
       if (fresh) {  // first: on their way while the page numbers are
@@ -679,16 +673,16 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
         st.clear();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          load_query<D>(p, c, c.rt * tile + 8 * n + (lane >> 2), lane, qf[n]);
-          limit[n][0] = row_limit(p, c, c.rt * tile + 8 * n + 2 * (lane & 3));
-          limit[n][1] = row_limit(p, c, c.rt * tile + 8 * n + 2 * (lane & 3) + 1);
+          load_query<D>(p, c, 8 * n + (lane >> 2), lane, qf[n]);
+          limit[n][0] = row_limit(p, c, 8 * n + 2 * (lane & 3));
+          limit[n][1] = row_limit(p, c, 8 * n + 2 * (lane & 3) + 1);
         }
-        min_limit = row_limit(p, c, c.rt * tile);  // rows come in order: the first sees the least
+        min_limit = row_limit(p, c, 0);  // rows come in order: the first sees the least
       }
       while (zp < z1 && ring.in_flight < Cfg::kStages) {
         if (!ahead.holds(cp)) ahead.load<false>(kv, cp, lane);
         ring.issue(&tk, &tv, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
-        advance(kv, p.group, tile, plan, cp, zp);
+        advance(kv, plan, cp, zp);
         skip_entry(cp, zp);
       }
       if (!now.holds(c)) {
@@ -713,17 +707,17 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
         if (end && began) {
           write_rows<D, NT>(p, c, lane, st);
         } else if (done) {
-          last = Part{c.s, c.h, c.rt, began, end};
+          last = Part{c.s, c.h, began, end};
           break;  // kept in registers
         } else {
           // the end of a segment that began before this range: the first part of
           // a range only, and the ring is in use, so it goes to the workspace
-          first = Part{c.s, c.h, c.rt, false, true};
+          first = Part{c.s, c.h, false, true};
           keep_part<D, NT>(parts.o(2 * warp), parts.ml(2 * warp), lane, st);
         }
         fresh = true;
       }
-      advance(kv, p.group, tile, plan, c, z);
+      advance(kv, plan, c, z);
       skip_entry(c, z);
     }
   }
@@ -743,7 +737,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
 template <int D, int NT>
 __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
   const KvView &kv = p.a.kv;
-  constexpr int tile = 8 * NT, kWarps = StreamCfg<D, NT, false>::kWarps;
+  constexpr int kRows = 8 * NT, kWarps = StreamCfg<D, NT, false>::kWarps;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.y, h = blockIdx.z, j = blockIdx.x, i = j / p.group;
@@ -753,13 +747,13 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
   const int head = h * p.group + j - i * p.group;
   float m = -INFINITY, l = 0.f, o = 0.f;
   if (units_s > 0) {
-    const int tiles = (q.rows * p.group + tile - 1) / tile, units = units_of(q.len);
-    const int64_t z = z0 + ((int64_t)h * tiles + j / tile) * (units + kEntry) + kEntry;
+    const int units = units_of(q.len);
+    const int64_t z = z0 + (int64_t)h * (units + kEntry) + kEntry;
     const int64_t c0 = range_owner(z, W, T) / kWarps, c1 = range_owner(z + units - 1, W, T) / kWarps;
     if (c0 == c1) return;  // the CTA wrote the result
 #pragma unroll 4
     for (int64_t c = c0; c <= c1; ++c) {
-      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * tile + j % tile;
+      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * kRows + j;
       if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
       const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
       const float x = p.part_o[at * D + threadIdx.x];
@@ -798,13 +792,13 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
   if (threadIdx.x == 0) prefetch_tensor_map(&tk);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  build_plan(kv, p.group, 0, plan);
+  build_plan(kv, plan);
   const int64_t T = plan.prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   if (w >= W) return;
   int64_t z = range_start(w, W, T);
   const int64_t z1 = range_start(w + 1, W, T);
-  Cursor c = locate(kv, p.group, 0, plan, z);
+  Cursor c = locate(kv, plan, z);
   skip_entry(c, z);
   int64_t zp = z;
   Cursor cp = c;
@@ -838,7 +832,7 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
     while (zp < z1 && ring.in_flight < Cfg::kStages) {
       if (!ahead.holds(cp)) ahead.load<true>(kv, cp, lane);
       ring.issue(&tk, nullptr, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
-      advance(kv, p.group, 0, plan, cp, zp);
+      advance(kv, plan, cp, zp);
       skip_entry(cp, zp);
     }
     if (!now.holds(c)) {
@@ -857,8 +851,7 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
       load_keys<D>(ring.stage(), lane, words);
       const int pos0 = c.u * kUnit, J = c.q.rows * p.group;
       const int first = first_row();
-      float sum[2][2] = {}, part[2][2] = {};
-      int n = 0;
+      float sum[2][2] = {};
       for (int j0 = first & ~7; j0 < J; j0 += 8) {
         hold(j0);
         float s[1][2][4];
@@ -868,17 +861,7 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (pos0 + 16 * mi + g + 8 * (k >> 1) < limit[k & 1])
-              part[mi][k >> 1] += ex2(score<CAP>(s[0][mi][k], ks, p.a.softcap, inv_cap) - lse[k & 1]);
-        // sums of sums: 16 tiles to a part, so that long chunks do not lose bits
-        if ((++n & 15) == 0 || j0 + 8 >= J) {
-#pragma unroll
-          for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              sum[mi][r] += part[mi][r];
-              part[mi][r] = 0.f;
-            }
-        }
+              sum[mi][k >> 1] += ex2(score<CAP>(s[0][mi][k], ks, p.a.softcap, inv_cap) - lse[k & 1]);
       }
       const int64_t slab = (int64_t)page * kv.n_kv_heads + c.h;
 #pragma unroll
@@ -896,18 +879,16 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
     }
     __syncwarp();
     ring.next();
-    advance(kv, p.group, 0, plan, c, z);
+    advance(kv, plan, c, z);
     skip_entry(c, z);
   }
 }
 
-// Rows of a (sequence, head) up to which the stream kernel takes a call: one tile.
-// More go to the tensor-core kernel of exl3_kv8_chunk.cu.
+// Rows of a (sequence, head) up to which the stream kernel takes a call. More go to the tensor-core kernel of exl3_kv8_chunk.cu.
 constexpr int64_t kStreamRows = 16;
 
-// Up to 8 rows of a (sequence, head) in one tile: half the registers and
-// products of the 16-row tile.
-bool narrow(int64_t tile_rows) { return tile_rows <= 8; }
+// Up to 8 rows of a (sequence, head): half the registers and products of 16.
+bool narrow(int64_t rows) { return rows <= 8; }
 
 template <int D>
 bool cache_map(CUtensorMap *m, const KvView &kv, const uint8_t *codes) {
@@ -937,12 +918,12 @@ struct StreamWorkspace {
 };
 StreamWorkspace stream_workspace(int64_t rows, int D, int num_sms) {
   StreamWorkspace w;
-  const int64_t tile = narrow(rows) ? 8 : 16;
-  w.part_rows = num_sms * 2 * tile;
+  const int64_t kept = narrow(rows) ? 8 : 16;
+  w.part_rows = num_sms * 2 * kept;
   w.o = 2 * (kMaxSeqs + 8);  // the plan's int64
   w.ml = w.o + w.part_rows * D;
   w.first = w.ml + w.part_rows * 2;
-  w.total = w.first + (int64_t)num_sms * (narrow(rows) ? StreamCfg<128, 1, false>::kWarps : StreamCfg<128, 2, false>::kWarps) * tile * (D + 2);
+  w.total = w.first + (int64_t)num_sms * (narrow(rows) ? StreamCfg<128, 1, false>::kWarps : StreamCfg<128, 2, false>::kWarps) * kept * (D + 2);
   return w;
 }
 
