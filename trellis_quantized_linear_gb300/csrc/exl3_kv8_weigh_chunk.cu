@@ -16,8 +16,11 @@
 //   * warp 8 (one lane): tcgen05.mma;
 //   * warp 9 (one lane): TMA of the queries, a box of 64 dimensions x heads x rows,
 //     so a step is the group's heads of consecutive rows without a copy.
-// An item's sums are formed by one CTA in a fixed order. Items go to the CTAs in
-// turn, the ones that most rows see first.
+// The items go to pairs of CTAs (clusters) in turn, the ones that most rows see
+// first, and a pair shares an item's steps: the first half of them and the second,
+// whose sums the other CTA's shared memory receives. So sums are formed in a fixed
+// order, and there are twice the pieces to deal out (2048 rows of 40 heads over 8192
+// tokens are 512 items of up to 82 steps for 304 CTAs: 206 us with an item a CTA).
 #include <cuda.h>
 
 #include "exl3_internal.h"
@@ -39,13 +42,13 @@ struct WeighCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kOperand = kHalves * 128 * 128;
   static constexpr int kOffQ = kOperand;                    // two stages
-  static constexpr int kOffCol = kOffQ + 2 * kOperand;      // (lse, limit) x 64 a warp, then sums
-  static constexpr int kOffPlan = kOffCol + kExpWarps * (kCols / 2) * 8 + kItem * 4;  // int prefix, then int2 sequences
+  static constexpr int kOffCol = kOffQ + 2 * kOperand;      // (lse, limit) x 64 a warp, then sums: two of the other half, two of the other CTA
+  static constexpr int kOffPlan = kOffCol + kExpWarps * (kCols / 2) * 8 + 4 * kItem * 4;  // int prefix, then int2 sequences
   static constexpr int kOffBar = kOffPlan + (kWeighSeqs + 8) * 4 + (kWeighSeqs + 8) * 8;
   static constexpr int kSmem = 1024 + kOffBar + 256;
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
-enum { kWQFull = 0, kWQEmpty = 2, kWSFull = 4, kWSEmpty = 6, kWKeys = 8, kWDone = 9, kWBars = 10 };
+enum { kWQFull = 0, kWQEmpty = 2, kWSFull = 4, kWSEmpty = 6, kWKeys = 8, kWDone = 9, kWPeer = 10, kWTaken = 12, kWBars = 14 };
 
 struct WeighParams {
   KvAttention a;
@@ -58,7 +61,7 @@ struct Item {
   int s, h, tile;
   int first;     // first row that sees the item
   int chunks;    // steps of heads
-  int steps;     // in all
+  int step0, steps;  // of this CTA: the first, how many
 };
 
 // Items (128-token tiles x heads) of all sequences before each; ends with a barrier.
@@ -96,10 +99,14 @@ __device__ __forceinline__ void build_weigh_plan(const KvView &kv, const WeighPl
   __syncthreads();
 }
 
-// Item z, false past the last. Heads vary fastest: tiles of the sequence's front,
-// which most rows see, come first.
-__device__ __forceinline__ bool get_item(const WeighParams &p, const WeighPlan &plan, int z, Item &it) {
+// Item k of this CTA pair, false past the last. Heads vary fastest: tiles of the
+// sequence's front, which most rows see, come first. Every other round goes the
+// other way, so that the pairs with the shorter items of a round get the longer of
+// the next. The first CTA of the pair has the first half of an item's steps.
+__device__ __forceinline__ bool get_item(const WeighParams &p, const WeighPlan &plan, int k, Item &it) {
   const KvView &kv = p.a.kv;
+  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1, rank = blockIdx.x & 1;
+  const int z = k * pairs + (k & 1 ? pairs - 1 - pair : pair);
   if (z >= plan.prefix[kv.n_seqs]) return false;
   int lo = 0, hi = kv.n_seqs - 1;
   while (lo < hi) {
@@ -109,12 +116,14 @@ __device__ __forceinline__ bool get_item(const WeighParams &p, const WeighPlan &
   }
   it.s = lo;
   it.q = plan.at(lo);
-  const int k = z - plan.prefix[lo];
-  it.h = k % kv.n_kv_heads;
-  it.tile = k / kv.n_kv_heads;
+  const int i = z - plan.prefix[lo];
+  it.h = i % kv.n_kv_heads;
+  it.tile = i / kv.n_kv_heads;
   it.first = p.a.causal ? max(0, it.tile * kItem - (it.q.len - it.q.rows)) : 0;
   it.chunks = (p.group + p.heads - 1) / p.heads;
-  it.steps = max(0, (it.q.rows - it.first + p.rows - 1) / p.rows) * it.chunks;
+  const int steps = max(0, (it.q.rows - it.first + p.rows - 1) / p.rows) * it.chunks;
+  it.step0 = rank ? (steps + 1) / 2 : 0;
+  it.steps = rank ? steps / 2 : (steps + 1) / 2;
   return true;
 }
 
@@ -163,6 +172,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     }
     mbar_init(bar(kWKeys), kExpWarps);
     mbar_init(bar(kWDone), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(kWPeer + t), 4);
+      mbar_init(bar(kWTaken + t), 4);
+    }
     fence_barrier_init();
   }
   if (warp == kExpWarps) {
@@ -170,6 +183,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  cluster_sync_all();  // the other CTA's barriers are there
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
@@ -189,8 +203,9 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     if (lane == 0) {
       uint32_t n = 0;
       bool ok = true;
-      for (int z = blockIdx.x; ok && get_item(p, plan, z, it); z += gridDim.x)
-        for (int st = 0, chunk = 0, row = it.q.row0 + it.first; ok && st < it.steps; ++st, ++n) {
+      for (int k = 0; ok && get_item(p, plan, k, it); ++k)
+        for (int st = 0, chunk = it.step0 % it.chunks, row = it.q.row0 + it.first + it.step0 / it.chunks * p.rows;
+             ok && st < it.steps; ++st, ++n) {
           const uint32_t b = n & 1;
           ok = mbar_wait(bar(kWQEmpty + b), ((n >> 1) & 1) ^ 1, status);
           if (!ok) break;
@@ -212,10 +227,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     // ---------------- tensor core (one lane) ----------------
     if (lane == 0) {
       constexpr uint32_t kIdesc = f16_idesc(kItem, kCols);
-      uint32_t n = 0, items = 0;
+      uint32_t n = 0;
       bool ok = true;
-      for (int z = blockIdx.x; ok && get_item(p, plan, z, it); z += gridDim.x, ++items) {
-        ok = mbar_wait(bar(kWKeys), items & 1, status);
+      for (int k = 0; ok && get_item(p, plan, k, it); ++k) {
+        ok = mbar_wait(bar(kWKeys), k & 1, status);
         for (int st = 0; ok && st < it.steps; ++st, ++n) {
           const uint32_t b = n & 1, ph = (n >> 1) & 1;
           ok = mbar_wait(bar(kWQFull + b), ph, status) && mbar_wait(bar(kWSEmpty + b), ph ^ 1, status);
@@ -242,7 +257,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     constexpr int kHalf = kCols / 2;
     float *col_lse = reinterpret_cast<float *>(smem + Cfg::kOffCol) + warp * 2 * kHalf;  // the warp's own
     int *col_limit = reinterpret_cast<int *>(col_lse + kHalf);
-    float *col_sum = reinterpret_cast<float *>(smem + Cfg::kOffCol) + kExpWarps * 2 * kHalf;
+    float *half_sum = reinterpret_cast<float *>(smem + Cfg::kOffCol) + kExpWarps * 2 * kHalf;
+    float *peer_sum = half_sum + 2 * kItem;
+    const int rank = blockIdx.x & 1;
+    const uint32_t peer_smem = map_to_rank(base, 1 - rank);
     [[maybe_unused]] const int64_t size = kv.n_pages * kv.n_kv_heads * kKvBlock * (int64_t)D;
     // The tensor core cuts its partial sums off towards zero, D / 16 times: on average
     // this share of a score. Without it heavy weights came out 2e-6 low.
@@ -252,7 +270,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     const int row_0 = col0 / p.heads, head_0 = col0 % p.heads, row_1 = col1 / p.heads, head_1 = col1 % p.heads;
     uint32_t n = 0;
     bool ok = true;
-    for (int z = blockIdx.x; ok && get_item(p, plan, z, it); z += gridDim.x) {
+    for (int k = 0; get_item(p, plan, k, it); ++k) {
       const int pos0 = it.tile * kItem, pos = pos0 + row;
       // the keys: a token has D / 16 lanes; lanes of the second half of the dimension take the token next to theirs
       constexpr int kPerToken = D / 16, kStep = kExpWarps * 32 / kPerToken;
@@ -286,7 +304,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       if (lane == 0) mbar_arrive(bar(kWKeys));
 
       // a column of the steps in order: its row's lse, and how many tokens the row sees
-      int step_row = it.first, chunk = 0;
+      int step_row = it.first + it.step0 / it.chunks * p.rows, chunk = it.step0 % it.chunks;
       auto column = [&](int col, int r, int hd, float &lse, int &limit) {
         const int g = chunk * p.heads + hd;
         r += step_row;
@@ -310,7 +328,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       };
       if (it.steps > 0) columns();
       const int end = min(pos0 + kItem, it.q.len);
-      for (int st = 0; st < it.steps; ++st, ++n) {
+      for (int st = 0; ok && st < it.steps; ++st, ++n) {
         const uint32_t b = n & 1;
         if (lse0 == -INFINITY) limit0 = 0;  // a row that saw nothing (here, so that the load has had a step's time)
         if (lse1 == -INFINITY) limit1 = 0;
@@ -381,17 +399,37 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         total += part[0].x + part[0].y;  // a sum of sums: 82 steps of 10240 rows lose no bits that matter
       }
       // the other half's sum; all warps are past the item's last step then (its scores
-      // come from the last product that reads the keys), and a wait that ran out in one
-      // ends the loop in all
-      if (half == 1) col_sum[row] = total;
+      // come from the last product that reads the keys), and a wait that ran out in one,
+      // here or in the join of the item before, ends the loop in all
+      const int slot = (k & 1) * kItem + row;
+      if (half == 1) half_sum[slot] = total;
       ok = all_agree(ok);
-      const int64_t at = slab * kKvBlock + pos % kKvBlock;
-      if (ok && half == 0 && page >= 0 && EXL3_SPAN(at, 1, kv.n_pages * kv.n_kv_heads * kKvBlock))
-        atomicAdd(&kv.weight[at], total + col_sum[row]);  // alone but for sequences that share the block
+      if (!ok) break;
+      if (half == 1) continue;
+      total += half_sum[slot];
+      // the other CTA's sum, through two slots
+      const uint32_t full = bar(kWPeer + (k & 1)), taken = bar(kWTaken + (k & 1)), ph = (k >> 1) & 1;
+      if (rank == 1) {
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(taken, ph ^ 1, status, kWaitLimitNs));
+        if (!ok) continue;
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_smem + (smem_u32(peer_sum + slot) - base)), "f"(total) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(peer_smem + (full - base));
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(full, ph, status, kWaitLimitNs));
+        if (!ok) continue;
+        total += peer_sum[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(peer_smem + (taken - base));
+        const int64_t at = slab * kKvBlock + pos % kKvBlock;
+        if (page >= 0 && EXL3_SPAN(at, 1, kv.n_pages * kv.n_kv_heads * kKvBlock))
+          atomicAdd(&kv.weight[at], total);  // alone but for sequences that share the block
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // nothing of the other CTA is on its way here
   if (warp == kExpWarps) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
@@ -414,7 +452,7 @@ cudaError_t weigh_chunk(const KvAttention &a, cudaStream_t st) {
   for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kWeighSeqs) {
     p.a.kv = kv_slice(a.kv, s0, a.kv.n_seqs - s0 < kWeighSeqs ? a.kv.n_seqs - s0 : kWeighSeqs);
     const cudaError_t e = launch_overlapped(a.softcap > 0.f ? kv8_weigh_chunk_kernel<D, true> : kv8_weigh_chunk_kernel<D, false>,
-                                            2 * a.num_sms, kWeighThreads, WeighCfg<D>::kSmem, st, 1, tq, p);
+                                            2 * a.num_sms, kWeighThreads, WeighCfg<D>::kSmem, st, 2, tq, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
