@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
   Best best;
   for (int c0 = 0; c0 < mine; c0 += step) {
     const int n = min(step, mine - c0);
+    // where token t has its word in this chunk, or something past the last
+    auto word_of = [&](uint32_t t) { return t < (uint32_t)p.n && owner(t) == rank ? local(t) - (uint32_t)c0 : ~0u; };
     if (rules) {
       const int used = words.wide ? n : (n + 1) / 2;
       for (int i = tid * 4; i < used; i += T * 4)
@@ -217,7 +219,6 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
       auto count = [&](uint32_t i, bool made) {
         note(i, [&](int j) { return made ? words.count(j) : words.set(j, kSeen); });
       };
-      auto word_of = [&](uint32_t t) { return t < (uint32_t)p.n && owner(t) == rank ? local(t) - (uint32_t)c0 : ~0u; };
       if (listed) {
         for (int i0 = 0; i0 < list_n; i0 += T) {
           const uint32_t e = i0 + tid < list_n ? sm.list[i0 + tid] : ~0u;
@@ -294,40 +295,69 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
     }
     if (!rules) continue;
     __syncthreads();  // the stream has written the tokens with a word as well: masked, not yet penalized
-    auto penalize = [&](int i) {
-      const uint32_t word = words.one(i);
-      if (word == 0 || (word & kBiased)) return;
-      const int t = token(c0 + i);
-      const float y = penalized(out[t], word, r);
-      out[t] = y;
-      if (y > -INFINITY) best.take(y, t);
+    // four at a time: their logits come from L2
+    constexpr int kAhead = 4;
+    auto penalize = [&](int count, auto entry) {
+      for (int i0 = tid; i0 < count; i0 += T * kAhead) {
+        uint32_t word[kAhead];
+        int t[kAhead];
+        float y[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int at = i0 + k * T < count ? entry(i0 + k * T) : -1;
+          word[k] = at < 0 ? 0u : words.one(at);
+          if (word[k] & kBiased) word[k] = 0u;
+          t[k] = token(c0 + at);
+          y[k] = word[k] ? out[t[k]] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (word[k] == 0) continue;
+          y[k] = penalized(y[k], word[k], r);
+          out[t[k]] = y[k];
+          if (y[k] > -INFINITY) best.take(y[k], t[k]);
+        }
+      }
     };
-    if (special_n <= kSpecial)
-      for (int i = tid; i < special_n; i += T) penalize((int)sm.special[i]);
-    else  // too many to list: look at every word
-      for (int i = tid; i < n; i += T) penalize(i);
+    if (special_n <= kSpecial) penalize(special_n, [&](int i) { return (int)sm.special[i]; });
+    else penalize(n, [](int i) { return i; });  // too many to list: look at every word
     // A biased token is done by its entry, or by the first of several, which adds
     // all of them up in their order.
-    for (int i = b.x + tid; i < b.y; i += T) {
-      const int id = p.r.bias_id[i];
-      const uint32_t at = id >= 0 && id < p.n && owner((uint32_t)id) == rank ? local((uint32_t)id) - (uint32_t)c0 : ~0u;
-      if (at >= (uint32_t)n) continue;
-      const uint32_t word = words.one((int)at);
-      float sum = p.r.bias_value[i];
-      if (duplicates) {
-        bool first = true;
-        for (int j = b.x; j < i; ++j) first = first && p.r.bias_id[j] != id;
-        if (!first) continue;
-        sum = 0.f;
-        for (int j = i; j < b.y; ++j)
-          if (p.r.bias_id[j] == id) sum = __fadd_rn(sum, p.r.bias_value[j]);
+    for (int i0 = b.x + tid; i0 < b.y; i0 += T * 2) {
+      int id[2];
+      float sum[2], y[2];
+      uint32_t at[2];
+      bool may[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        id[k] = i0 + k * T < b.y ? p.r.bias_id[i0 + k * T] : -1;
+        sum[k] = i0 + k * T < b.y ? p.r.bias_value[i0 + k * T] : 0.f;
       }
-      float y = out[id];
-      if (!allowed || ((allowed[id >> 5] >> (id & 31)) & 1u)) {
-        y = __fadd_rn(penalized(y, word, r), sum);
-        out[id] = y;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        at[k] = word_of((uint32_t)id[k]);
+        const bool here = at[k] < (uint32_t)n;
+        y[k] = here ? out[id[k]] : 0.f;
+        may[k] = !here || !allowed || ((allowed[id[k] >> 5] >> (id[k] & 31)) & 1u);
       }
-      if (y > -INFINITY) best.take(y, id);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (at[k] >= (uint32_t)n) continue;
+        if (duplicates) {
+          const int i = i0 + k * T;
+          bool first = true;
+          for (int j = b.x; j < i; ++j) first = first && p.r.bias_id[j] != id[k];
+          if (!first) continue;
+          sum[k] = 0.f;
+          for (int j = i; j < b.y; ++j)
+            if (p.r.bias_id[j] == id[k]) sum[k] = __fadd_rn(sum[k], p.r.bias_value[j]);
+        }
+        if (may[k]) {
+          y[k] = __fadd_rn(penalized(y[k], words.one((int)at[k]), r), sum[k]);
+          out[id[k]] = y[k];
+        }
+        if (y[k] > -INFINITY) best.take(y[k], id[k]);
+      }
     }
     __syncthreads();
   }
