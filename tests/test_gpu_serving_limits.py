@@ -47,14 +47,26 @@ def check_both(pool, counts, heads, cap=0.0, causal=True):
     check_weigh(pool, counts, heads, q, want[1].astype(np.float32), scale, cap, causal)
 
 
-@pytest.mark.parametrize("most", [1, 19])
+@pytest.mark.parametrize("most", [1, 19, 40, 60])
 def test_more_sequences_than_a_launch_holds(most):
     rng = np.random.default_rng(most)
     kv_len = rng.integers(0, 100, 1100)
-    counts = np.minimum(rng.integers(0, most + 1, 1100), kv_len)
+    counts = np.minimum(rng.integers(0, min(most, 19) + 1, 1100), kv_len)
     counts[0] = min(most, kv_len[0])
     kv_len[1030], counts[1030] = 77, most  # in every launch
     check_both(Pool(kv_len, 1, 64, seed=most), counts.tolist(), 2)
+
+
+@pytest.mark.parametrize("kv_len,counts,heads,dim,cap,causal", [
+    ([130, 700, 9], [5, 13, 9], 8, 64, 0.0, True),        # 20, 52 and 36 rows of a group of four
+    ([3000, 64], [12, 1], 10, 128, 20.0, True),           # 60 rows, segments over several CTAs
+    ([500, 501], [32, 31], 4, 64, 0.0, False),            # 64: the most that the tiles of 16 take
+    ([500, 501], [1, 1], 130, 128, 0.0, True),            # 65
+    ([900], [56], 4, 128, 0.0, True), ([900], [57], 4, 64, 0.0, True),  # 112 and 114, where weights change over
+    ([40, 200], [0, 20], 2, 128, 0.0, True),
+])
+def test_rows_around_the_tiles_of_sixteen(kv_len, counts, heads, dim, cap, causal):
+    check_both(Pool(kv_len, 2, dim, seed=sum(kv_len) + heads), counts, heads, cap, causal)
 
 
 def test_append_to_more_sequences_than_a_launch_holds():

@@ -1,10 +1,10 @@
 // Attention over the 8-bit key/value cache, and the accumulated attention weight
 // of its tokens. Formulas in include/exl3.h.
 //
-// Stream kernel, for up to 16 rows (row of the sequence x head of the group) of a
-// segment, a (sequence, key/value head). All work is cut into units of 32 cached
-// tokens; the units of all segments lie one behind the other, and each warp of a
-// persistent grid takes one equal, contiguous range of them, whatever the
+// Stream kernel, for few rows (row of the sequence x head of the group). A segment is
+// a (sequence, key/value head, tile of up to 16 rows). All work is cut into units of
+// 32 cached tokens; the units of all segments lie one behind the other, and each
+// warp of a persistent grid takes one equal, contiguous range of them, whatever the
 // sequences' lengths are (they are read on the device). A warp keeps its own ring
 // of TMA copies in flight and its own running maximum, sum and output, so warps do
 // not wait for one another. Where ranges end inside a segment, the partial results
@@ -19,6 +19,11 @@
 // exactly. The dimension is permuted so that a lane's 16 bytes of a key serve
 // four k-steps and its 16 bytes of a value four rows of the output, without a
 // shuffle.
+//
+// Measured, 40 heads on 8, D = 128: two sequences of 98K to 131K tokens 87 us (471
+// MB, 5.4 TB/s); 16 sequences of 61 to 8192 tokens 36 us (136 MB; while the units
+// run they come at the copy rate, the rest is launch, plan, page numbers and the two
+// joins, 5 us before and 8 after); one of 777 tokens 11 us, all latency.
 #include <cuda.h>
 
 #include "exl3_internal.h"
@@ -82,8 +87,15 @@ struct Plan {
 
 __device__ __forceinline__ int64_t segment_units(int len) { return len > 0 ? units_of(len) + kEntry : 0; }
 
+// Tiles of `tile` rows that a sequence's rows make.
+template <bool TILED>
+__device__ __forceinline__ int row_tiles(int rows, int group, int tile) {
+  return TILED ? (rows * group + tile - 1) / tile : 1;
+}
+
 // Every thread of the CTA takes part; ends with a barrier.
-__device__ __forceinline__ void build_plan(const KvView &kv, const Plan &plan) {
+template <bool TILED>
+__device__ __forceinline__ void build_plan(const KvView &kv, int group, int tile, const Plan &plan) {
   int64_t *warp_sum = plan.prefix + kMaxSeqs + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
   int64_t carry = 0;
@@ -93,7 +105,7 @@ __device__ __forceinline__ void build_plan(const KvView &kv, const Plan &plan) {
     int64_t n = 0;
     if (s < kv.n_seqs) {
       const KvSeq q = kv_sequence(kv, s);
-      if (q.rows > 0) n = segment_units(q.len) * kv.n_kv_heads;
+      if (q.rows > 0) n = segment_units(q.len) * kv.n_kv_heads * row_tiles<TILED>(q.rows, group, tile);
       plan.seq[s] = make_int2(kv.q_start[s], q.rows > 0 ? q.len : -1);
       if (s + 1 == kv.n_seqs) plan.seq[s + 1] = make_int2(kv.q_start[s + 1], -1);
     }
@@ -120,14 +132,17 @@ __device__ __forceinline__ void build_plan(const KvView &kv, const Plan &plan) {
 // A place in the unit order; u < 0: entering the segment.
 struct Cursor {
   KvSeq q;
-  int s, h, u;        // sequence, key/value head, unit of the segment
-  int units;          // of this sequence's segments
+  int s, h, rt, u;    // sequence, key/value head, row tile, unit of the segment
+  int units, tiles;   // of this sequence's segments
 };
-__device__ __forceinline__ void enter_sequence(const Plan &plan, Cursor &c) {
+template <bool TILED>
+__device__ __forceinline__ void enter_sequence(const Plan &plan, int group, int tile, Cursor &c) {
   c.q = plan.at(c.s);
   c.units = units_of(c.q.len);
+  c.tiles = row_tiles<TILED>(c.q.rows, group, tile);
 }
-__device__ __forceinline__ Cursor locate(const KvView &kv, const Plan &plan, int64_t z) {
+template <bool TILED>
+__device__ __forceinline__ Cursor locate(const KvView &kv, int group, int tile, const Plan &plan, int64_t z) {
   Cursor c;
   int lo = 0, hi = kv.n_seqs - 1;  // the s with prefix[s] <= z < prefix[s + 1]
   while (lo < hi) {
@@ -136,22 +151,29 @@ __device__ __forceinline__ Cursor locate(const KvView &kv, const Plan &plan, int
     else lo = mid + 1;
   }
   c.s = lo;
-  enter_sequence(plan, c);
+  enter_sequence<TILED>(plan, group, tile, c);
   const int64_t rem = z - plan.prefix[lo];
-  c.h = rem < ((int64_t)1 << 31) ? (int)((uint32_t)rem / (uint32_t)(c.units + kEntry)) : (int)(rem / (c.units + kEntry));
-  c.u = (int)(rem - (int64_t)c.h * (c.units + kEntry)) - kEntry;
+  const int seg = rem < ((int64_t)1 << 31) ? (int)((uint32_t)rem / (uint32_t)(c.units + kEntry)) : (int)(rem / (c.units + kEntry));
+  c.u = (int)(rem - (int64_t)seg * (c.units + kEntry)) - kEntry;
+  c.h = TILED ? seg / c.tiles : seg;
+  c.rt = TILED ? seg - c.h * c.tiles : 0;
   return c;
 }
 // The next place; z moves with it.
-__device__ __forceinline__ void advance(const KvView &kv, const Plan &plan, Cursor &c, int64_t &z) {
+template <bool TILED>
+__device__ __forceinline__ void advance(const KvView &kv, int group, int tile, const Plan &plan, Cursor &c, int64_t &z) {
   ++z;
   if (++c.u < c.units) return;
   c.u = -kEntry;
+  if (TILED) {
+    if (++c.rt < c.tiles) return;
+    c.rt = 0;
+  }
   if (++c.h < kv.n_kv_heads) return;
   c.h = 0;
   do ++c.s;
   while (c.s < kv.n_seqs && plan.prefix[c.s + 1] == plan.prefix[c.s]);
-  if (c.s < kv.n_seqs) enter_sequence(plan, c);
+  if (c.s < kv.n_seqs) enter_sequence<TILED>(plan, group, tile, c);
 }
 // Past the places of entering.
 __device__ __forceinline__ void skip_entry(Cursor &c, int64_t &z) {
@@ -490,7 +512,7 @@ __device__ __forceinline__ void store_out(const KvAttention &a, int64_t row, int
 // end of a segment that began before the warp's range (in the workspace), and
 // 2 w + 1, its last segment (in shared memory, the ring's).
 struct Part {
-  int s, h;  // the segment; s < 0: no part
+  int s, h, rt;  // the segment; s < 0: no part
   int begins, ends;
 };
 template <int D, int NT>
@@ -535,7 +557,7 @@ __device__ __forceinline__ void write_rows(const StreamParams &p, const Cursor &
 #pragma unroll
     for (int col = 0; col < 2; ++col) {
       const float l = st.l[n][col], f = l == 0.f ? 0.f : pow2i(st.ev) / l;
-      const int j = 8 * n + 2 * t + col, i = j / p.group;
+      const int j = c.rt * 8 * NT + 8 * n + 2 * t + col, i = j / p.group;
       if (i >= c.q.rows) continue;
       float v[D / 8];
 #pragma unroll
@@ -595,10 +617,10 @@ __device__ __forceinline__ void join_cta(const StreamParams &p, const Parts<D, N
       const bool last = part.ends || (left & (left - 1)) == 0;
       if (!last) continue;
       const KvSeq q = kv_sequence(p.a.kv, part.s);
-      const int row = r / p.group;
+      const int j = part.rt * P::kRows + r, row = j / p.group;
       if (row < q.rows) {
         if (begins && part.ends) {
-          const int head = part.h * p.group + r - row * p.group;
+          const int head = part.h * p.group + j - row * p.group;
           const int64_t off = (int64_t)(q.row0 + row) * p.a.ldo + (int64_t)head * D + d0;
           const float f = l == 0.f ? 0.f : 1.0f / l;
           const __half2 lo = __floats2half2_rn(o.x * f, o.y * f), hi = __floats2half2_rn(o.z * f, o.w * f);
@@ -622,7 +644,7 @@ __device__ __forceinline__ void join_cta(const StreamParams &p, const Parts<D, N
   }
 }
 
-template <int D, int NT, bool CAP>
+template <int D, int NT, bool CAP, bool TILED>
 __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
     kv8_stream_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const StreamParams p) {
   using Cfg = StreamCfg<D, NT, false>;
@@ -645,7 +667,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  build_plan(kv, plan);
+  constexpr int tile = 8 * NT;
+  build_plan<TILED>(kv, p.group, tile, plan);
   const int64_t T = plan.prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   if (blockIdx.x == 0)
@@ -657,7 +680,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
   if (w < W) {
     int64_t z = range_start(w, W, T);
     const int64_t z1 = range_start(w + 1, W, T);
-    Cursor c = locate(kv, plan, z);
+    Cursor c = locate<TILED>(kv, p.group, tile, plan, z);
     skip_entry(c, z);
     int64_t zp = z;
     Cursor cp = c;
@@ -670,19 +693,20 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
       if (fresh) {  // first: on their way while the page numbers are
         fresh = false;
         began = c.u == 0;
+        const int j0 = TILED ? c.rt * tile : 0;
         st.clear();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          load_query<D>(p, c, 8 * n + (lane >> 2), lane, qf[n]);
-          limit[n][0] = row_limit(p, c, 8 * n + 2 * (lane & 3));
-          limit[n][1] = row_limit(p, c, 8 * n + 2 * (lane & 3) + 1);
+          load_query<D>(p, c, j0 + 8 * n + (lane >> 2), lane, qf[n]);
+          limit[n][0] = row_limit(p, c, j0 + 8 * n + 2 * (lane & 3));
+          limit[n][1] = row_limit(p, c, j0 + 8 * n + 2 * (lane & 3) + 1);
         }
-        min_limit = row_limit(p, c, 0);  // rows come in order: the first sees the least
+        min_limit = row_limit(p, c, j0);  // rows come in order: the first sees the least
       }
       while (zp < z1 && ring.in_flight < Cfg::kStages) {
         if (!ahead.holds(cp)) ahead.load<false>(kv, cp, lane);
         ring.issue(&tk, &tv, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
-        advance(kv, plan, cp, zp);
+        advance<TILED>(kv, p.group, tile, plan, cp, zp);
         skip_entry(cp, zp);
       }
       if (!now.holds(c)) {
@@ -707,17 +731,17 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
         if (end && began) {
           write_rows<D, NT>(p, c, lane, st);
         } else if (done) {
-          last = Part{c.s, c.h, began, end};
+          last = Part{c.s, c.h, c.rt, began, end};
           break;  // kept in registers
         } else {
           // the end of a segment that began before this range: the first part of
           // a range only, and the ring is in use, so it goes to the workspace
-          first = Part{c.s, c.h, false, true};
+          first = Part{c.s, c.h, c.rt, false, true};
           keep_part<D, NT>(parts.o(2 * warp), parts.ml(2 * warp), lane, st);
         }
         fresh = true;
       }
-      advance(kv, plan, c, z);
+      advance<TILED>(kv, p.group, tile, plan, c, z);
       skip_entry(c, z);
     }
   }
@@ -734,7 +758,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
 // Joins the partials of the segments that several CTAs worked on, in the order of
 // the CTAs, and writes the rows of segments without tokens. One CTA of D threads
 // per (row of a group, sequence, key/value head).
-template <int D, int NT>
+template <int D, int NT, bool TILED>
 __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
   const KvView &kv = p.a.kv;
   constexpr int kRows = 8 * NT, kWarps = StreamCfg<D, NT, false>::kWarps;
@@ -748,12 +772,13 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
   float m = -INFINITY, l = 0.f, o = 0.f;
   if (units_s > 0) {
     const int units = units_of(q.len);
-    const int64_t z = z0 + (int64_t)h * (units + kEntry) + kEntry;
+    const int tiles = row_tiles<TILED>(q.rows, p.group, kRows);
+    const int64_t z = z0 + ((int64_t)h * tiles + (TILED ? j / kRows : 0)) * (units + kEntry) + kEntry;
     const int64_t c0 = range_owner(z, W, T) / kWarps, c1 = range_owner(z + units - 1, W, T) / kWarps;
     if (c0 == c1) return;  // the CTA wrote the result
 #pragma unroll 4
     for (int64_t c = c0; c <= c1; ++c) {
-      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * kRows + j;
+      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * kRows + (TILED ? j % kRows : j);
       if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
       const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
       const float x = p.part_o[at * D + threadIdx.x];
@@ -772,6 +797,9 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
 
 // Accumulated weight: the same stream over the keys alone; a unit's weights are
 // the sums over all rows of the sequence, formed by the warp that owns the unit.
+// 16 sequences of 61 to 8192 tokens, 40 heads on 8, D = 128: 20 us (72 MB, 3.6 TB/s;
+// bound as the attention is, and the shorter the stream the larger the share of its
+// beginning and end).
 template <int D, bool CAP>
 __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
     kv8_weigh_kernel(const __grid_constant__ CUtensorMap tk, const StreamParams p) {
@@ -792,13 +820,13 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
   if (threadIdx.x == 0) prefetch_tensor_map(&tk);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  build_plan(kv, plan);
+  build_plan<false>(kv, p.group, 0, plan);
   const int64_t T = plan.prefix[kv.n_seqs], W = min((int64_t)p.warps, T);
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   if (w >= W) return;
   int64_t z = range_start(w, W, T);
   const int64_t z1 = range_start(w + 1, W, T);
-  Cursor c = locate(kv, plan, z);
+  Cursor c = locate<false>(kv, p.group, 0, plan, z);
   skip_entry(c, z);
   int64_t zp = z;
   Cursor cp = c;
@@ -832,7 +860,7 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
     while (zp < z1 && ring.in_flight < Cfg::kStages) {
       if (!ahead.holds(cp)) ahead.load<true>(kv, cp, lane);
       ring.issue(&tk, nullptr, kv, cp, __shfl_sync(0xffffffffu, ahead.page, (cp.u >> 1) - ahead.base), lane);
-      advance(kv, plan, cp, zp);
+      advance<false>(kv, p.group, 0, plan, cp, zp);
       skip_entry(cp, zp);
     }
     if (!now.holds(c)) {
@@ -879,15 +907,23 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
     }
     __syncwarp();
     ring.next();
-    advance(kv, plan, c, z);
+    advance<false>(kv, p.group, 0, plan, c, z);
     skip_entry(c, z);
   }
 }
 
-// Rows of a (sequence, head) up to which the stream kernel takes a call. More go to the tensor-core kernel of exl3_kv8_chunk.cu.
-constexpr int64_t kStreamRows = 16;
+// Rows of a (sequence, head) up to which the stream kernels take a call; more go to
+// the tensor-core kernels of exl3_kv8_chunk.cu and exl3_kv8_weigh_chunk.cu, whose time
+// hardly depends on the rows below 128. Attention, one tile of 16 rows after another,
+// 5 heads a group: 16 sequences of up to 8192 tokens 69 / 109 / 123 / 174 us at 20 / 50 /
+// 65 / 100 rows (there 117), one of 60000 tokens 60 / 99 / 121 / 162 (there 147 to 163),
+// one of 777 tokens 16 (there 29 to 38). Weights, the rows 8 at a time over a unit's
+// keys in registers: 34 / 63 / 102 / 148 us at 20 / 50 / 100 / 160 rows for the 16 (there
+// 127 to 131), 31 / 53 / 91 / 135 for the one (there 108 to 121).
+constexpr int64_t kStreamRows = 64, kWeighRows = 112;
 
-// Up to 8 rows of a (sequence, head): half the registers and products of 16.
+// Up to 8 rows of a (sequence, head): half the registers and products of 16 (5 rows
+// over 16 sequences 35.6 us, 41.8 in the form of 16; one of 777 tokens 12.1 and 13.6).
 bool narrow(int64_t rows) { return rows <= 8; }
 
 template <int D>
@@ -897,7 +933,7 @@ bool cache_map(CUtensorMap *m, const KvView &kv, const uint8_t *codes) {
                               D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TILED>
 cudaError_t run_stream(const CUtensorMap &tk, const CUtensorMap &tv, const StreamParams &params, cudaStream_t st) {
   using Cfg = StreamCfg<D, NT, false>;
   StreamParams p = params;
@@ -905,11 +941,11 @@ cudaError_t run_stream(const CUtensorMap &tk, const CUtensorMap &tv, const Strea
   p.warps = grid * Cfg::kWarps;
   const size_t smem = Cfg::kSmem;
   const cudaError_t e =
-      p.a.softcap > 0.f ? launch_overlapped(kv8_stream_kernel<D, NT, true>, grid, kThreads, smem, st, 1, tk, tv, p)
-                        : launch_overlapped(kv8_stream_kernel<D, NT, false>, grid, kThreads, smem, st, 1, tk, tv, p);
+      p.a.softcap > 0.f ? launch_overlapped(kv8_stream_kernel<D, NT, true, TILED>, grid, kThreads, smem, st, 1, tk, tv, p)
+                        : launch_overlapped(kv8_stream_kernel<D, NT, false, TILED>, grid, kThreads, smem, st, 1, tk, tv, p);
   if (e != cudaSuccess) return e;
   const dim3 join((unsigned)(p.a.kv.max_rows * (int64_t)p.group), p.a.kv.n_seqs, p.a.kv.n_kv_heads);
-  return launch_overlapped(kv8_join_kernel<D, NT>, join, D, 0, st, 1, p);
+  return launch_overlapped(kv8_join_kernel<D, NT, TILED>, join, D, 0, st, 1, p);
 }
 
 // Floats of the workspace's parts, in the order of StreamParams; the plan first.
@@ -944,7 +980,9 @@ cudaError_t attention(const KvAttention &a, cudaStream_t st) {
   p.first = ws + w.first;
   for (int s0 = 0; s0 < a.kv.n_seqs; s0 += kMaxSeqs) {
     p.a.kv = kv_slice(a.kv, s0, a.kv.n_seqs - s0 < kMaxSeqs ? a.kv.n_seqs - s0 : kMaxSeqs);
-    const cudaError_t e = narrow(rows) ? run_stream<D, 1>(tk, tv, p, st) : run_stream<D, 2>(tk, tv, p, st);
+    const cudaError_t e = narrow(rows) ? run_stream<D, 1, false>(tk, tv, p, st)
+                          : rows <= 16 ? run_stream<D, 2, false>(tk, tv, p, st)
+                                       : run_stream<D, 2, true>(tk, tv, p, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -973,14 +1011,15 @@ cudaError_t weigh(const KvAttention &a, cudaStream_t st) {
 template <int D>
 cudaError_t init_dim() {
   cudaError_t e = cudaSuccess;
-  for (const void *f : {(const void *)kv8_stream_kernel<D, 1, false>, (const void *)kv8_stream_kernel<D, 1, true>})
+  for (const void *f : {(const void *)kv8_stream_kernel<D, 1, false, false>, (const void *)kv8_stream_kernel<D, 1, true, false>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, 1, false>::kSmem);
-  for (const void *f : {(const void *)kv8_stream_kernel<D, 2, false>, (const void *)kv8_stream_kernel<D, 2, true>})
+  for (const void *f : {(const void *)kv8_stream_kernel<D, 2, false, false>, (const void *)kv8_stream_kernel<D, 2, true, false>,
+                        (const void *)kv8_stream_kernel<D, 2, false, true>, (const void *)kv8_stream_kernel<D, 2, true, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, 2, false>::kSmem);
   for (const void *f : {(const void *)kv8_weigh_kernel<D, false>, (const void *)kv8_weigh_kernel<D, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, 1, true>::kSmem);
   // the join takes the stream kernel's split of shared memory and L1: no SM waits to change it
-  for (const void *f : {(const void *)kv8_join_kernel<D, 1>, (const void *)kv8_join_kernel<D, 2>})
+  for (const void *f : {(const void *)kv8_join_kernel<D, 1, false>, (const void *)kv8_join_kernel<D, 2, false>, (const void *)kv8_join_kernel<D, 2, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   return e;
 }
@@ -1002,7 +1041,7 @@ cudaError_t launch_kv8_attention(const KvAttention &a, cudaStream_t st) {
 
 cudaError_t launch_kv8_weigh(const KvAttention &a, cudaStream_t st) {
   if (a.kv.rows == 0 || a.kv.n_seqs == 0 || a.kv.max_rows == 0) return cudaSuccess;
-  if ((int64_t)a.kv.max_rows * (a.n_heads / a.kv.n_kv_heads) > kStreamRows) return launch_kv8_weigh_chunk(a, st);
+  if ((int64_t)a.kv.max_rows * (a.n_heads / a.kv.n_kv_heads) > kWeighRows) return launch_kv8_weigh_chunk(a, st);
   return a.kv.head_dim == 64 ? weigh<64>(a, st) : weigh<128>(a, st);
 }
 

@@ -13,7 +13,9 @@ namespace {
 // One CTA per (block that receives tokens, sequence, head, keys or values). The
 // block's new values stay in registers between the maximum and the conversion:
 // 2 bytes read and 1 written per value, the older codes touched only when the
-// scale grows.
+// scale grows. Bound by those bytes and, until they fill the chip, by the chain
+// length - page - values - store: 6.8K tokens of 8 heads, D = 128, keys and values (42
+// MB) 10.3 us, 4.1 TB/s; 16 tokens 2.6 us, less than the launch takes the host.
 constexpr int kAppendThreads = 256;
 
 template <int D>
@@ -124,6 +126,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // each warp then writes the kept positions of its part, ties to the lower
 // positions. The first pass's bins hold the sign, the exponent and two bits:
 // weights fill few of them, so each bin has four copies, one for every fourth lane.
+// Eight sequences of 9K to 32K tokens, 8 heads: 22.5 us on 64 CTAs, bound by their
+// instructions (2.5 a cycle); the 5 MB of weights are a microsecond of it.
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectKeys = 44 * 1024;  // held in shared memory
 constexpr int kBins = 2048, kCopies = 4;
@@ -325,7 +329,9 @@ __global__ void __launch_bounds__(kSelectThreads, 1) kv8_select_kernel(KvView kv
 
 // One CTA per (new block, sequence, head): its keys and values. The block's scale
 // is the largest of its tokens' scales, so codes only ever shrink. Bound by the
-// bytes moved; all of a thread's loads are in flight before its first store.
+// bytes moved; all of a thread's loads are in flight before its first store. Eight
+// sequences, 8 heads, 4096 tokens of D = 128 each: 22 us for 137 MB, 6.2 TB/s (with the
+// codes' loads before the scales are compared no faster: it is not the chain that binds).
 constexpr int kMoveThreads = 128;
 
 __device__ __forceinline__ uint4 rescale_16(uint4 c, float factor) {

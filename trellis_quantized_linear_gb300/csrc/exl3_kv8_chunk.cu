@@ -10,8 +10,8 @@
 //     operand ahead in registers, to fp16 (exact) in the two-stage operand buffers
 //     (128-byte swizzle; the same layout serves keys as the K-major operand of
 //     Q K^T and values as the MN-major operand of P V). Each block's scale goes in
-//     as a power of two relative to the segment's largest, so one factor serves
-//     all scores and all outputs of a segment; only codes 2^15 and more below that
+//     as a power of two relative to the largest of the CTA's part of the segment, so
+//     one factor serves all its scores and outputs; only codes 2^15 and more below that
 //     largest block's lose bits, 2^-25 of it at most;
 //   * warp 8 (one lane): for each tile tcgen05.mma S = Q K^T into TMEM, then, when
 //     the tile's probabilities are there, O += P V with P read from TMEM, where it
@@ -23,6 +23,14 @@
 //     the reference in use (the result is the same: the sum uses that reference),
 //     so rarely after the first units.
 // TMEM: S0 S1 O0 O1, 128 columns each.
+//
+// Measured: 2048 rows of 40 heads on 8 over 8192 cached tokens, D = 128: 321 us (301
+// GFLOP, 937 TFLOP/s, the join 15 to 20 us of it). The softmax binds it: a chain of
+// TMEM reads, maximum, exponentials and TMEM writes per tile and unit, 2 row warps a
+// scheduler; the tensor pipe is busy 42 % of the time. Not bound by the operands: Q
+// from TMEM (half the shared-memory reads of Q K^T) took 321 us of then 326. Slower
+// were two threads a row (72 registers, 452 us), a register split by role (419 us and
+// more), one pass over the scores with a guessed maximum (345 us).
 #include <cuda.h>
 
 #include "exl3_internal.h"
@@ -181,13 +189,15 @@ struct Walk {
   }
 };
 
-// The largest exponents of the key and value scales of a segment's blocks. The
-// whole warp takes part.
+// The largest exponents of the key and value scales of the CTA's blocks of a
+// segment (partial results carry them, so the CTAs need not agree: with the whole
+// segment's, 20 rows over 60000 tokens took 183 us). The whole warp takes part.
 __device__ __forceinline__ int2 largest_scales(const KvView &kv, const Segment &g, int lane) {
-  const int blocks = min(g.units * (kTokens / kKvBlock), (g.q.len + kKvBlock - 1) / kKvBlock);
+  constexpr int kBlocks = kTokens / kKvBlock;
+  const int end = min(g.u1 * kBlocks, (g.q.len + kKvBlock - 1) / kKvBlock);
   int ek = -127, ev = -127;
 #pragma unroll 4
-  for (int b = lane; b < blocks; b += 32) {
+  for (int b = g.u0 * kBlocks + lane; b < end; b += 32) {
     const int page = kv_page(kv, g.s, b);
     if (page < 0) continue;
     const int64_t slab = (int64_t)page * kv.n_kv_heads + g.h;

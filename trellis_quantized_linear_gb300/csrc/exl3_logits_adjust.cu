@@ -11,6 +11,12 @@
 // first counted and done after the stream, so that their divisions do not hold up
 // the rest, and so are the biases. The row's greedy choice is joined through the
 // cluster's shared memory.
+//
+// Measured, 248077 tokens: 64 rows with histories of 8192, 300 biases and a mask 55 us
+// (131 MB, 2.4 TB/s). Without rules the stream takes 29 us; the mask adds 4, the biases
+// 6, handing out, counting and penalizing the history 15: latencies that all CTAs meet
+// at the same time, as they are all resident. One row with a history of 700 and 20
+// biases 10.4 us, 5.2 without rules.
 #include <limits.h>
 
 #include "exl3_internal.h"
@@ -157,6 +163,9 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
     }
   };
 
+  // Long histories are handed out: 64 rows of 1500 / 3000 / 8192 entries 43 / 45 / 53 us,
+  // 44 / 49 / 64 with every CTA reading all; below 4 entries a thread the two cluster
+  // barriers cost a single row 1 us.
   bool listed = false;
   if (h.y - h.x > 4 * T) {
     if (tid == 0) list_n = 0;
@@ -395,9 +404,10 @@ cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, in
   if (M == 0) return cudaSuccess;
   // Few rows: clusters of up to 16 CTAs of 512 threads. Many rows: up to 8 of 256
   // (clusters of 16 leave a quarter of the SMs without work), four an SM, so that
-  // one streams while another counts (64 rows of 248K tokens with all rules: 64 us;
-  // three an SM with twice the loads in flight 101 us, words for 8192 tokens at a
-  // time 81 us). At least 2048 tokens to a CTA.
+  // one streams while another counts. 248K tokens, histories of 700, 9 / 16 / 32 / 64
+  // rows: 20 / 35 / 62 / 121 us in the first form, 23 / 33 / 38 / 43 in the second.
+  // (Three CTAs an SM with twice the loads in flight 101 us where four took 64, words
+  // for 8192 tokens at a time 81.) At least 2048 tokens to a CTA.
   const bool few = M * kMaxCluster <= num_sms;
   const int most = few ? kMaxCluster : kMaxCluster / 2;
   int lg = 0;
