@@ -31,10 +31,11 @@ def test_bounds_checked_selftest_every_serving_unit_reports():
     assert "bounds selftest ok" in r.stdout
 
 
-def test_serving_suite_under_bounds_checks():
-    r = _child(["-m", "pytest", "tests/test_gpu_serving.py", "-m", "gpu", "-x", "-q", "-p", "no:cacheprovider"], timeout=1800)
+@pytest.mark.parametrize("suite,least", [("test_gpu_serving.py", 140), ("test_gpu_serving_limits.py", 30)])
+def test_serving_suite_under_bounds_checks(suite, least):
+    r = _child(["-m", "pytest", f"tests/{suite}", "-m", "gpu", "-x", "-q", "-p", "no:cacheprovider"], timeout=1800)
     assert r.returncode == 0, r.stdout[-6000:] + r.stderr[-4000:]
     assert "exl3 bounds check failed" not in r.stdout + r.stderr
     summary = r.stdout.strip().splitlines()[-1]
     m = re.search(r"(\d+) passed", summary)
-    assert m and int(m.group(1)) >= 140 and "skipped" not in summary and "failed" not in summary, summary
+    assert m and int(m.group(1)) >= least and "skipped" not in summary and "failed" not in summary, summary
