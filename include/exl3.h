@@ -462,7 +462,7 @@ exl3_status exl3_kv8_append(const exl3_kv8_cache *cache, const exl3_kv8_batch *b
  *         arguments; it goes by rows, max_rows, the heads and head_dim),
  *         contents undefined before and after. Calls that share one must be
  *         ordered.
- * Up to 64 rows of a sequence and key/value head (max_rows x heads of a group)
+ * Up to 48 rows of a sequence and key/value head (max_rows x heads of a group)
  * go through a kernel bound by reading the cache once, more through one on the
  * tensor cores; both split long sequences over all SMs by the lengths that they
  * find on the device, and the result does not depend on scheduling.

@@ -60,7 +60,9 @@ def test_more_sequences_than_a_launch_holds(most):
 @pytest.mark.parametrize("kv_len,counts,heads,dim,cap,causal", [
     ([130, 700, 9], [5, 13, 9], 8, 64, 0.0, True),        # 20, 52 and 36 rows of a group of four
     ([3000, 64], [12, 1], 10, 128, 20.0, True),           # 60 rows, segments over several CTAs
-    ([500, 501], [32, 31], 4, 64, 0.0, False),            # 64: the most that the tiles of 16 take
+    ([500, 501], [24, 23], 4, 64, 0.0, False),            # 48: the most that the tiles of 16 take
+    ([500, 501], [25, 1], 4, 128, 0.0, True),             # 50
+    ([500, 501], [32, 31], 4, 64, 0.0, False),            # 64
     ([500, 501], [1, 1], 130, 128, 0.0, True),            # 65
     ([900], [56], 4, 128, 0.0, True), ([900], [57], 4, 64, 0.0, True),  # 112 and 114, where weights change over
     ([40, 200], [0, 20], 2, 128, 0.0, True),

@@ -915,12 +915,12 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
 // Rows of a (sequence, head) up to which the stream kernels take a call; more go to
 // the tensor-core kernels of exl3_kv8_chunk.cu and exl3_kv8_weigh_chunk.cu, whose time
 // hardly depends on the rows below 128. Attention, one tile of 16 rows after another,
-// 5 heads a group: 16 sequences of up to 8192 tokens 69 / 109 / 123 / 174 us at 20 / 50 /
-// 65 / 100 rows (there 117), one of 60000 tokens 60 / 99 / 121 / 162 (there 147 to 163),
-// one of 777 tokens 16 (there 29 to 38). Weights, the rows 8 at a time over a unit's
+// 5 heads a group: 16 sequences of up to 8192 tokens 69 / 85 / 109 / 123 us at 20 / 45 /
+// 50 / 65 rows (there 103), one of 60000 tokens 60 / 81 / 99 / 121 (there 95), one of
+// 777 tokens 15.5 (there 16.3). Weights, the rows 8 at a time over a unit's
 // keys in registers: 34 / 63 / 102 / 148 us at 20 / 50 / 100 / 160 rows for the 16 (there
 // 127 to 131), 31 / 53 / 91 / 135 for the one (there 108 to 121).
-constexpr int64_t kStreamRows = 64, kWeighRows = 112;
+constexpr int64_t kStreamRows = 48, kWeighRows = 112;
 
 // Up to 8 rows of a (sequence, head): half the registers and products of 16 (5 rows
 // over 16 sequences 35.6 us, 41.8 in the form of 16; one of 777 tokens 12.1 and 13.6).

@@ -24,8 +24,8 @@
 //     so rarely after the first units.
 // TMEM: S0 S1 O0 O1, 128 columns each.
 //
-// Measured: 2048 rows of 40 heads on 8 over 8192 cached tokens, D = 128: 321 us (301
-// GFLOP, 937 TFLOP/s, the join 15 to 20 us of it). The softmax binds it: a chain of
+// Measured: 2048 rows of 40 heads on 8 over 8192 cached tokens, D = 128: 323 us (301
+// GFLOP, 930 TFLOP/s, the join 15 to 20 us of it). The softmax binds it: a chain of
 // TMEM reads, maximum, exponentials and TMEM writes per tile and unit, 2 row warps a
 // scheduler; the tensor pipe is busy 42 % of the time. Not bound by the operands: Q
 // from TMEM (half the shared-memory reads of Q K^T) took 321 us of then 326. Slower
@@ -69,6 +69,7 @@ enum { kBarQ = 0, kBarKFull = 2, kBarKEmpty = 4, kBarVFull = 6, kBarVEmpty = 8, 
 struct ChunkParams {
   KvAttention a;
   int group, ctas;
+  int join_rows;  // of a CTA of the join: kJoinRows or a multiple that divides 256
   // Workspace: partial results of the CTAs (slot 0: a segment that began before
   // the CTA's range, slot 1: one that began in it and goes on after it) and the plan.
   float *part_o;      // CTAs x 2 x 256 x D
@@ -618,9 +619,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
 }
 
 // Joins the partials of the segments that several CTAs worked on, in the order of
-// the CTAs, and writes the rows that see no token. A CTA has 64 rows of a
-// (sequence, key/value head), a warp four at a time.
-constexpr int kJoinRows = 64, kJoinThreads = 256;
+// the CTAs, and writes the rows that see no token. All latency, so a warp has two
+// rows and the loads of four partials in flight: 65 rows over 777 tokens, 10 partials
+// each, took 38 us in ncu with 64 rows a CTA and one partial after the other.
+constexpr int kJoinRows = 16, kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const ChunkParams p) {
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.y, h = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const KvSeq q = kv_sequence(kv, s);
-  const int j0 = blockIdx.x * kJoinRows, rt = j0 / kPair;
+  const int j0 = blockIdx.x * p.join_rows, rt = j0 / kPair;
   if (j0 >= q.rows * p.group) return;
   const int units = pair_units(q, p.group, p.a.causal, rt);
   int64_t c0 = 0, c1 = -1;
@@ -643,8 +645,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
     c1 = range_owner(z + units - 1, W, T);
     if (c0 == c1) return;  // the CTA wrote the result
   }
-  constexpr int E = D / 32, kAtOnce = 4;
-  for (int first = j0 + warp * kAtOnce; first < j0 + kJoinRows; first += kJoinThreads / 32 * kAtOnce) {
+  constexpr int E = D / 32, kAtOnce = kJoinRows / (kJoinThreads / 32), kAhead = 4;
+  for (int first = j0 + warp * kAtOnce; first < j0 + p.join_rows; first += kJoinRows) {
     float m[kAtOnce], l[kAtOnce], o[kAtOnce][E];
 #pragma unroll
     for (int r = 0; r < kAtOnce; ++r) {
@@ -653,25 +655,32 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
 #pragma unroll
       for (int e = 0; e < E; ++e) o[r][e] = 0.f;
     }
-    for (int64_t c = c0; c <= c1; ++c) {
-      const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * kPair + first % kPair;
-      if (!EXL3_SPAN(at, kAtOnce, p.part_rows)) continue;
-      float2 ml[kAtOnce];
-      float x[kAtOnce][E];
+    for (int64_t c = c0; c <= c1; c += kAhead) {
+      float2 ml[kAhead][kAtOnce];
+      float x[kAhead][kAtOnce][E];
 #pragma unroll
-      for (int r = 0; r < kAtOnce; ++r) {  // rows past the sequence's last hold nothing and are not written
-        ml[r] = reinterpret_cast<const float2 *>(p.part_ml)[at + r];
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t at = (2 * (c + i) + (c + i == c0 ? 1 : 0)) * kPair + first % kPair;
+        const bool there = c + i <= c1 && EXL3_SPAN(at, kAtOnce, p.part_rows);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[r][e] = p.part_o[(at + r) * D + 32 * e + lane];
+        for (int r = 0; r < kAtOnce; ++r) {  // rows past the sequence's last hold nothing and are not written
+          ml[i][r] = there ? reinterpret_cast<const float2 *>(p.part_ml)[at + r] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[i][r][e] = there ? p.part_o[(at + r) * D + 32 * e + lane] : 0.f;
+        }
       }
 #pragma unroll
-      for (int r = 0; r < kAtOnce; ++r) {
-        const float top = fmaxf(m[r], ml[r].x), ref = top == -INFINITY ? 0.f : top;
-        const float a = ex2(m[r] - ref), b = ex2(ml[r].x - ref);
-        l[r] = l[r] * a + ml[r].y * b;
+      for (int i = 0; i < kAhead; ++i) {
+        if (c + i > c1) continue;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[r][e] = o[r][e] * a + x[r][e] * b;
-        m[r] = top;
+        for (int r = 0; r < kAtOnce; ++r) {
+          const float top = fmaxf(m[r], ml[i][r].x), ref = top == -INFINITY ? 0.f : top;
+          const float a = ex2(m[r] - ref), b = ex2(ml[i][r].x - ref);
+          l[r] = l[r] * a + ml[i][r].y * b;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[r][e] = o[r][e] * a + x[i][r][e] * b;
+          m[r] = top;
+        }
       }
     }
 #pragma unroll
@@ -718,7 +727,12 @@ cudaError_t chunk_attention(const KvAttention &a, cudaStream_t st) {
     cudaError_t e = launch_overlapped(a.softcap > 0.f ? kv8_chunk_kernel<D, true> : kv8_chunk_kernel<D, false>, p.ctas,
                                       kChunkThreads, ChunkCfg<D>::kSmem, st, 1, p);
     if (e != cudaSuccess) return e;
-    const dim3 join((unsigned)ceil_div((int64_t)a.kv.max_rows * p.group, kJoinRows), p.a.kv.n_seqs, a.kv.n_kv_heads);
+    // With many rows what a CTA does before its first load counts, so it has more of
+    // them: 10240 rows of 8 heads over 8192 tokens 323 us with 64, 330 with 16; 255 rows
+    // over 777 tokens 34 with 64, 23.4 with 16, over 60000 tokens 130 and 105.
+    const int64_t joins = ceil_div((int64_t)a.kv.max_rows * p.group, kJoinRows) * p.a.kv.n_seqs * a.kv.n_kv_heads;
+    p.join_rows = joins > 16 * a.num_sms ? 4 * kJoinRows : kJoinRows;
+    const dim3 join((unsigned)ceil_div((int64_t)a.kv.max_rows * p.group, p.join_rows), p.a.kv.n_seqs, a.kv.n_kv_heads);
     e = launch_overlapped(kv8_chunk_join_kernel<D>, join, kJoinThreads, 0, st, 1, p);
     if (e != cudaSuccess) return e;
   }
