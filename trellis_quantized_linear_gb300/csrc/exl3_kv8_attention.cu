@@ -756,15 +756,16 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
 }
 
 // Joins the partials of the segments that several CTAs worked on, in the order of
-// the CTAs, and writes the rows of segments without tokens. One CTA of D threads
+// the CTAs, and writes the rows of segments without tokens. One CTA of G x D threads
 // per (row of a group, sequence, key/value head).
-template <int D, int NT, bool TILED>
-__global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
+template <int D, int NT, bool TILED, int G>
+__global__ void __launch_bounds__(D * G) kv8_join_kernel(const StreamParams p) {
   const KvView &kv = p.a.kv;
   constexpr int kRows = 8 * NT, kWarps = StreamCfg<D, NT, false>::kWarps;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.y, h = blockIdx.z, j = blockIdx.x, i = j / p.group;
+  const int d = threadIdx.x % D, g = threadIdx.x / D;
   const int64_t z0 = p.plan[s], units_s = p.plan[s + 1] - z0, T = p.plan[kv.n_seqs], W = min((int64_t)p.warps, T);
   const KvSeq q = kv_sequence(kv, s);
   if (i >= q.rows) return;
@@ -776,12 +777,13 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
     const int64_t z = z0 + ((int64_t)h * tiles + (TILED ? j / kRows : 0)) * (units + kEntry) + kEntry;
     const int64_t c0 = range_owner(z, W, T) / kWarps, c1 = range_owner(z + units - 1, W, T) / kWarps;
     if (c0 == c1) return;  // the CTA wrote the result
+    const int64_t share = (c1 - c0 + G) / G, first = c0 + g * share, last = min(c1, first + share - 1);
 #pragma unroll 4
-    for (int64_t c = c0; c <= c1; ++c) {
+    for (int64_t c = first; c <= last; ++c) {
       const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * kRows + (TILED ? j % kRows : j);
       if (!EXL3_SPAN(at, 1, p.part_rows)) continue;
       const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
-      const float x = p.part_o[at * D + threadIdx.x];
+      const float x = p.part_o[at * D + d];
       const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
       const float a = ex2(m - ref), b = ex2(ml.x - ref);
       l = l * a + ml.y * b;
@@ -789,7 +791,25 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const StreamParams p) {
       m = top;
     }
   }
-  const int64_t row = q.row0 + i, off = row * p.a.ldo + (int64_t)head * D + threadIdx.x;
+  if constexpr (G > 1) {  // the groups' results, in their order
+    __shared__ float so[G][D], sm[G], sl[G];
+    so[g][d] = o;
+    if (d == 0) {
+      sm[g] = m;
+      sl[g] = l;
+    }
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int k = 1; k < G; ++k) {
+      const float top = fmaxf(m, sm[k]), ref = top == -INFINITY ? 0.f : top;
+      const float a = ex2(m - ref), b = ex2(sm[k] - ref);
+      l = l * a + sl[k] * b;
+      o = o * a + so[k][d] * b;
+      m = top;
+    }
+  }
+  const int64_t row = q.row0 + i, off = row * p.a.ldo + (int64_t)head * D + d;
   if (EXL3_SPAN(off, 1, (int64_t)(kv.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D))
     static_cast<__half *>(p.a.out)[off] = __float2half_rn(l == 0.f ? 0.f : o / l);
   if (p.a.lse && threadIdx.x == 0) p.a.lse[row * p.a.n_heads + head] = log_sum(m, l);
@@ -945,7 +965,14 @@ cudaError_t run_stream(const CUtensorMap &tk, const CUtensorMap &tv, const Strea
                         : launch_overlapped(kv8_stream_kernel<D, NT, false, TILED>, grid, kThreads, smem, st, 1, tk, tv, p);
   if (e != cudaSuccess) return e;
   const dim3 join((unsigned)(p.a.kv.max_rows * (int64_t)p.group), p.a.kv.n_seqs, p.a.kv.n_kv_heads);
-  return launch_overlapped(kv8_join_kernel<D, NT, TILED>, join, D, 0, st, 1, p);
+  // A long sequence's segments are spread over all CTAs: with few heads, groups of
+  // threads share a row's many partials. One token over 72000, 1 head, D = 64: 17.7 us
+  // with 8 groups, 39.6 with one; 16 tokens over 500 to 4000, 2 heads: 14.7 and 16.7.
+  // With 8 heads a row has 19 at most, and larger CTAs would only cost.
+  constexpr int G = 512 / D;
+  if (p.a.kv.n_kv_heads * 24 < p.a.num_sms)
+    return launch_overlapped(kv8_join_kernel<D, NT, TILED, G>, join, D * G, 0, st, 1, p);
+  return launch_overlapped(kv8_join_kernel<D, NT, TILED, 1>, join, D, 0, st, 1, p);
 }
 
 // Floats of the workspace's parts, in the order of StreamParams; the plan first.
@@ -1019,7 +1046,9 @@ cudaError_t init_dim() {
   for (const void *f : {(const void *)kv8_weigh_kernel<D, false>, (const void *)kv8_weigh_kernel<D, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<D, 1, true>::kSmem);
   // the join takes the stream kernel's split of shared memory and L1: no SM waits to change it
-  for (const void *f : {(const void *)kv8_join_kernel<D, 1, false>, (const void *)kv8_join_kernel<D, 2, false>, (const void *)kv8_join_kernel<D, 2, true>})
+  for (const void *f : {(const void *)kv8_join_kernel<D, 1, false, 1>, (const void *)kv8_join_kernel<D, 2, false, 1>,
+                        (const void *)kv8_join_kernel<D, 2, true, 1>, (const void *)kv8_join_kernel<D, 1, false, 512 / D>,
+                        (const void *)kv8_join_kernel<D, 2, false, 512 / D>, (const void *)kv8_join_kernel<D, 2, true, 512 / D>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   return e;
 }

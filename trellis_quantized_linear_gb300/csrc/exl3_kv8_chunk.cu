@@ -493,12 +493,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
           const bool masked = pos0 + kTokens > least;
           const float scale = CAP ? 1.0f : c;
           float top = -INFINITY;
-          // 32 scores of the row: capped (in log2 units) and masked
-          auto prepare = [&](int q, float (&s)[32]) {
-            if constexpr (CAP) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) s[k] = soft_cap(s[k] * c, cap, inv_cap) * kLog2e;
-            }
+          auto mask = [&](int q, float (&s)[32]) {
             if (masked) {
 #pragma unroll
               for (int k = 0; k < 32; ++k)
@@ -510,7 +505,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
           for (int q = 0; q < 4; ++q) {
             float s[32];
             tmem_ld32(s_tmem + 32 * q, s);
-            prepare(q, s);
+            mask(q, s);
             float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
             for (int k = 4; k < 28; k += 8)
@@ -520,7 +515,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
             for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[28 + e]);
             top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
           }
-          top *= scale;
+          if constexpr (CAP) top = top == -INFINITY ? top : soft_cap(top * c, cap, inv_cap) * kLog2e;  // as the cap is monotonic
+          else top *= scale;
           const float now = top > ref + kLazy || ref == -INFINITY ? top : ref;
           const float keep = now == ref || ref == -INFINITY ? 1.0f : ex2(ref - now);
           if (u > g.u0 && __any_sync(0xffffffffu, keep != 1.0f)) {
@@ -548,7 +544,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
             float s[32];
             uint32_t packed[16];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
             tmem_ld32(s_tmem + 32 * q, s);
-            prepare(q, s);
+            if constexpr (CAP) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[k] = soft_cap(s[k] * c, cap, inv_cap) * kLog2e;
+            }
+            mask(q, s);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float2 x = fma2(make_float2(s[2 * k], s[2 * k + 1]), scale2, shift2);
@@ -624,7 +624,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
 // each, took 38 us in ncu with 64 rows a CTA and one partial after the other.
 constexpr int kJoinRows = 16, kJoinThreads = 256;
 
-template <int D>
+// SPLIT warps share two rows' partials.
+template <int D, int SPLIT>
 __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const ChunkParams p) {
   const KvView &kv = p.a.kv;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -646,7 +647,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
     if (c0 == c1) return;  // the CTA wrote the result
   }
   constexpr int E = D / 32, kAtOnce = kJoinRows / (kJoinThreads / 32), kAhead = 4;
-  for (int first = j0 + warp * kAtOnce; first < j0 + p.join_rows; first += kJoinRows) {
+  const int64_t share = (c1 - c0 + SPLIT) / SPLIT, a0 = c0 + warp % SPLIT * share, a1 = min(c1, a0 + share - 1);
+  for (int first = j0 + warp / SPLIT * kAtOnce; first < j0 + p.join_rows; first += kJoinRows / SPLIT) {
     float m[kAtOnce], l[kAtOnce], o[kAtOnce][E];
 #pragma unroll
     for (int r = 0; r < kAtOnce; ++r) {
@@ -655,13 +657,13 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
 #pragma unroll
       for (int e = 0; e < E; ++e) o[r][e] = 0.f;
     }
-    for (int64_t c = c0; c <= c1; c += kAhead) {
+    for (int64_t c = a0; c <= a1; c += kAhead) {
       float2 ml[kAhead][kAtOnce];
       float x[kAhead][kAtOnce][E];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int64_t at = (2 * (c + i) + (c + i == c0 ? 1 : 0)) * kPair + first % kPair;
-        const bool there = c + i <= c1 && EXL3_SPAN(at, kAtOnce, p.part_rows);
+        const bool there = c + i <= a1 && EXL3_SPAN(at, kAtOnce, p.part_rows);
 #pragma unroll
         for (int r = 0; r < kAtOnce; ++r) {  // rows past the sequence's last hold nothing and are not written
           ml[i][r] = there ? reinterpret_cast<const float2 *>(p.part_ml)[at + r] : make_float2(-INFINITY, 0.f);
@@ -671,7 +673,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (c + i > c1) continue;
+        if (c + i > a1) continue;
 #pragma unroll
         for (int r = 0; r < kAtOnce; ++r) {
           const float top = fmaxf(m[r], ml[i][r].x), ref = top == -INFINITY ? 0.f : top;
@@ -682,6 +684,30 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
           m[r] = top;
         }
       }
+    }
+    if constexpr (SPLIT > 1) {  // the warps' results, in their order; a CTA has one pass then
+      __shared__ float so[SPLIT][kAtOnce][D];
+      __shared__ float2 sml[SPLIT][kAtOnce];
+#pragma unroll
+      for (int r = 0; r < kAtOnce; ++r) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[warp][r][32 * e + lane] = o[r][e];
+        if (lane == 0) sml[warp][r] = make_float2(m[r], l[r]);
+      }
+      __syncthreads();
+      if (warp > 0) return;
+#pragma unroll
+      for (int w = 1; w < SPLIT; ++w)
+#pragma unroll
+        for (int r = 0; r < kAtOnce; ++r) {
+          const float2 ml = sml[w][r];
+          const float top = fmaxf(m[r], ml.x), ref = top == -INFINITY ? 0.f : top;
+          const float a = ex2(m[r] - ref), b = ex2(ml.x - ref);
+          l[r] = l[r] * a + ml.y * b;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[r][e] = o[r][e] * a + so[w][r][32 * e + lane] * b;
+          m[r] = top;
+        }
     }
 #pragma unroll
     for (int r = 0; r < kAtOnce; ++r) {
@@ -732,8 +758,15 @@ cudaError_t chunk_attention(const KvAttention &a, cudaStream_t st) {
     // over 777 tokens 34 with 64, 23.4 with 16, over 60000 tokens 130 and 105.
     const int64_t joins = ceil_div((int64_t)a.kv.max_rows * p.group, kJoinRows) * p.a.kv.n_seqs * a.kv.n_kv_heads;
     p.join_rows = joins > 16 * a.num_sms ? 4 * kJoinRows : kJoinRows;
+    // A long sequence's segments are spread over all CTAs: where it has few, and there are
+    // few rows, the warps of a CTA share two rows' many partials. 1 head, 800 rows over
+    // 6000 tokens: 29 us so, 38 without; 8 such sequences of 600 tokens: 46 and 26.
+    constexpr int kSplit = kJoinThreads / 32;
+    const int64_t segments = ceil_div((int64_t)a.kv.max_rows * p.group, kPair) * a.kv.n_kv_heads;
+    const bool split = segments * 24 < a.num_sms && joins * kSplit <= 4 * a.num_sms;
+    if (split) p.join_rows = kJoinRows / kSplit;
     const dim3 join((unsigned)ceil_div((int64_t)a.kv.max_rows * p.group, p.join_rows), p.a.kv.n_seqs, a.kv.n_kv_heads);
-    e = launch_overlapped(kv8_chunk_join_kernel<D>, join, kJoinThreads, 0, st, 1, p);
+    e = launch_overlapped(split ? kv8_chunk_join_kernel<D, kSplit> : kv8_chunk_join_kernel<D, 1>, join, kJoinThreads, 0, st, 1, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -756,7 +789,8 @@ cudaError_t init_kv8_chunk_kernels(int *status) {
   for (const void *f : {(const void *)kv8_chunk_kernel<128, false>, (const void *)kv8_chunk_kernel<128, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<128>::kSmem);
   cudaFuncAttributes attr;
-  for (const void *f : {(const void *)kv8_chunk_join_kernel<64>, (const void *)kv8_chunk_join_kernel<128>})
+  for (const void *f : {(const void *)kv8_chunk_join_kernel<64, 1>, (const void *)kv8_chunk_join_kernel<128, 1>,
+                        (const void *)kv8_chunk_join_kernel<64, 8>, (const void *)kv8_chunk_join_kernel<128, 8>})
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, f);
   return e;
 }
