@@ -372,9 +372,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
       const int cw = warp - 9;
       const int64_t size = kv.n_pages * kv.n_kv_heads * kKvBlock * (int64_t)D;
       const float sign = p.a.scale < 0.f ? -1.f : 1.f;
-      // powers of two below fp16's range are 0 (see above)
+      // Powers of two below fp16's range are 0 (see above). A block that is not there
+      // (past the sequence, or a page that the table does not name) has zero codes and
+      // the scale 1, which may be far above `top`: a factor past fp16's range would make
+      // NaN of the zeros, and no block that is there has a factor above 1.
       auto factor = [&](float scale, int top) {
-        const int d = pow2_exponent(scale) - top;
+        const int d = min(pow2_exponent(scale) - top, 0);
         return d >= -24 ? pow2i(d) : 0.f;
       };
       uint32_t unit = 0;
