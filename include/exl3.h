@@ -457,7 +457,8 @@ exl3_status exl3_kv8_append(const exl3_kv8_cache *cache, const exl3_kv8_batch *b
  * the sequence in this call, also rows before its position.
  * Sums, maxima and the softmax are fp32; the probabilities enter the product
  * with the values as fp16.
- *   scale: finite; softcap: 0 (off) or finite and at least 1e-30.
+ *   scale: finite; softcap: 0 (off) or finite and at least 1e-30. A capped score
+ *         has an error of 2^-19 of itself at most, besides that of the products.
  *   workspace: exl3_kv8_attention_workspace_bytes bytes (0 for invalid
  *         arguments; it goes by rows, max_rows, the heads and head_dim),
  *         contents undefined before and after. Calls that share one must be

@@ -9,7 +9,7 @@ import pytest
 import serving_ref as ref
 import trellis_quantized_linear_gb300 as tql
 from gpu_util import torch_mod
-from test_gpu_serving import Pool, attend, check_attention, dev, gpu, rows_on_device  # noqa: F401 (gpu: fixture)
+from test_gpu_serving import U, Pool, attend, check_attention, dev, gpu, rows_on_device  # noqa: F401 (gpu: fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,29 @@ def test_small_values_in_blocks(kv_len, counts, blocks, exponent):
     got = check_pool(pool, counts, 1)
     if exponent is None and blocks == "all":
         assert np.all(got == 0)
+
+
+@pytest.mark.parametrize("cap", [30.0, 1e3, 1e6, 1e8, 1e30, 3e38])
+@pytest.mark.parametrize("counts", [[1, 3], [70, 49]])
+def test_caps_far_above_the_scores(cap, counts):
+    """cap * tanh(s / cap) to an error relative to s: 2^-19, which is less than the products' (D + 8) ulp that the
+    tolerance without a cap has. Caps of 1e8 and more are no caps: the weights too."""
+    kv_len, heads, dim = [300, 999], 4, 128
+    pool = Pool(kv_len, 2, dim, seed=31)
+    pool.on_device()
+    R, scale = sum(counts), 0.25
+    q = (2 * pool.rng.standard_normal((R, heads, dim))).astype(np.float16)
+    got, lse = attend(pool, counts, q, heads, scale, cap, True)
+    args = (pool.table, kv_len, counts, q)
+    want = ref.attention(pool.codes[0], pool.scales[0], pool.codes[1], pool.scales[1], *args, scale, cap, True)
+    check_attention(got, lse, want, dim, 0.0, max(kv_len))
+    lse = want[1].astype(np.float32)
+    tql.exl3_kv8_weigh(pool.cache, pool.batch(counts), rows_on_device(q.reshape(R, -1), 8), heads, scale, dev(lse), softcap=cap)
+    got = pool.t[4].cpu().numpy()
+    add, bound = ref.weigh(pool.codes[0], pool.scales[0], *args, lse, scale, cap, True, 64 * pool.max_pages)
+    for s, length in enumerate(kv_len):
+        for b in range(-(-length // 64)):
+            page, a, e = pool.table[s][b], add[s, :, 64 * b:64 * b + 64], bound[s, :, 64 * b:64 * b + 64]
+            w = pool.weight[page].astype(np.float64) + a
+            tol = ((dim + 8) * U + 2.0 ** -20) * e + (max(counts) * heads + 2) * U * (a + w)
+            assert np.all(np.abs(got[page] - w) <= tol)

@@ -318,11 +318,12 @@ __device__ __forceinline__ void score_products(const uint32_t (&w)[2][2][D / 16]
       for (int k = 0; k < 4; ++k) s[n][mi][k] += odd[n][mi][k];
 }
 
-// Scores in log2 units. ks: key scale * softmax scale (* log2 e without a cap).
+// Scores of two products in log2 units. c: key scale * softmax scale * log2 e.
 template <bool CAP>
-__device__ __forceinline__ float score(float acc, float ks, float cap, float inv_cap) {
-  if constexpr (CAP) return soft_cap(acc * ks, cap, inv_cap) * kLog2e;
-  return acc * ks;
+__device__ __forceinline__ float2 score(float acc0, float acc1, float c, const SoftCap &cap) {
+  const float2 s = mul2(make_float2(acc0, acc1), make_float2(c, c));
+  if constexpr (CAP) return cap(s);
+  return s;
 }
 
 // A warp's ring of copies: issues the keys (and values) of units in order.
@@ -394,7 +395,7 @@ struct RowState {
 template <int D, int NT, bool CAP>
 __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stage, int pos0, int len, float ks, float vs,
                                             const uint32_t (&qf)[NT][D / 8], const int (&limit)[NT][2], int min_limit,
-                                            float inv_cap, int lane, RowState<D, NT> &st) {
+                                            const SoftCap &cap, int lane, RowState<D, NT> &st) {
   const int g = lane >> 2, t = lane & 3;
   float s[NT][2][4];
   {
@@ -402,16 +403,18 @@ __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stag
     load_keys<D>(stage, lane, w);
     score_products<D, NT>(w, qf, s);
   }
-  const float c = ks * p.a.scale * (CAP ? 1.0f : kLog2e);
+  const float c = ks * p.a.scale * kLog2e;
   const bool masked = pos0 + kUnit > min_limit;  // some row does not see the whole unit
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s[n][mi][k] = score<CAP>(s[n][mi][k], c, p.a.softcap, inv_cap);
-        if (masked && pos0 + 16 * mi + g + 8 * (k >> 1) >= limit[n][k & 1]) s[n][mi][k] = -INFINITY;
+      for (int k = 0; k < 4; k += 2) {
+        const float2 x = score<CAP>(s[n][mi][k], s[n][mi][k + 1], c, cap);
+        const int pos = pos0 + 16 * mi + g + 4 * k;
+        s[n][mi][k] = masked && pos >= limit[n][0] ? -INFINITY : x.x;
+        s[n][mi][k + 1] = masked && pos >= limit[n][1] ? -INFINITY : x.y;
       }
   const int ev = pow2_exponent(vs);
   const float unit = pow2i(max(min(st.ev - ev, 127), -126));  // exact: O in the new unit
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
     int64_t zp = z;
     Cursor cp = c;
     Blocks ahead, now;
-    const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
+    const SoftCap cap(p.a.softcap, kLog2e);
     uint32_t qf[NT][D / 8];
     int limit[NT][2], min_limit = 0;  // tokens that this lane's rows see, and the first row
     bool fresh = true, began = false;
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT, false>::kThreads, 1)
       const int page = __shfl_sync(0xffffffffu, now.page, at);
       const float ks = __shfl_sync(0xffffffffu, now.ks, at), vs = __shfl_sync(0xffffffffu, now.vs, at);
       if (page >= 0)
-        attend_unit<D, NT, CAP>(p, ring.stage(), c.u * kUnit, c.q.len, ks, vs, qf, limit, min_limit, inv_cap, lane, st);
+        attend_unit<D, NT, CAP>(p, ring.stage(), c.u * kUnit, c.q.len, ks, vs, qf, limit, min_limit, cap, lane, st);
       __syncwarp();  // every lane is done with the stage before it is filled again
       ring.next();
       const bool end = c.u + 1 == c.units;
@@ -852,7 +855,7 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
   int64_t zp = z;
   Cursor cp = c;
   Blocks ahead, now;
-  const float inv_cap = CAP ? 1.0f / p.a.softcap : 0.f;
+  const SoftCap cap(p.a.softcap, kLog2e);
   uint32_t qf[1][D / 8];
   int limit[2];
   float lse[2];  // in log2 units
@@ -894,7 +897,7 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
     }
     const int at = (c.u >> 1) - now.base;
     const int page = __shfl_sync(0xffffffffu, now.page, at);
-    const float ks = __shfl_sync(0xffffffffu, now.ks, at) * p.a.scale * (CAP ? 1.0f : kLog2e);
+    const float ks = __shfl_sync(0xffffffffu, now.ks, at) * p.a.scale * kLog2e;
     if (page >= 0) {
       uint32_t words[2][2][D / 16];
       load_keys<D>(ring.stage(), lane, words);
@@ -908,9 +911,12 @@ __global__ void __launch_bounds__(StreamCfg<D, 1, true>::kThreads, 1)
 #pragma unroll
         for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (pos0 + 16 * mi + g + 8 * (k >> 1) < limit[k & 1])
-              sum[mi][k >> 1] += ex2(score<CAP>(s[0][mi][k], ks, p.a.softcap, inv_cap) - lse[k & 1]);
+          for (int k = 0; k < 4; k += 2) {
+            const float2 x = score<CAP>(s[0][mi][k], s[0][mi][k + 1], ks, cap);
+            const int pos = pos0 + 16 * mi + g + 4 * k;
+            if (pos < limit[0]) sum[mi][k >> 1] += ex2(x.x - lse[0]);
+            if (pos < limit[1]) sum[mi][k >> 1] += ex2(x.y - lse[1]);
+          }
       }
       const int64_t slab = (int64_t)page * kv.n_kv_heads + c.h;
 #pragma unroll

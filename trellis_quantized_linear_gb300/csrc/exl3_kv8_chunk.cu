@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
       const int t = warp >> 2, row = threadIdx.x & 127;
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_tmem = lane_base + 128 * t, o_tmem = lane_base + 256 + 128 * t;
-      const float cap = p.a.softcap, inv_cap = CAP ? 1.0f / cap : 0.f;
+      const SoftCap cap(p.a.softcap, kLog2e);
       uint32_t count = 0;  // units of this tile so far
       bool ok = true;
       while (ok && walk.next(kv, p.group, p.a.causal, plan, g)) {
@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
           if (lane == 0) mbar_arrive(bar(kBarQ + t));
         }
         const int2 top_scale = largest_scales(kv, g, lane);
-        // scores in log2 units are the products times c (without a cap)
-        const float c = fmaxf(fabsf(p.a.scale) * pow2i(top_scale.x) * (CAP ? 1.0f : kLog2e), 1e-37f);
+        // scores in log2 units are the products times c, then capped
+        const float c = fmaxf(fabsf(p.a.scale) * pow2i(top_scale.x) * kLog2e, 1e-37f);
         float ref = -INFINITY, sum = 0.f;
         for (int u = g.u0; u < g.u1; ++u, ++count) {
           if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarS + t), count & 1, status))) {
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
             for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[28 + e]);
             top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
           }
-          if constexpr (CAP) top = top == -INFINITY ? top : soft_cap(top * c, cap, inv_cap) * kLog2e;  // as the cap is monotonic
+          if constexpr (CAP) top = top == -INFINITY ? top : cap(make_float2(top * c, 0.f)).x;  // as the cap is monotonic
           else top *= scale;
           const float now = top > ref + kLazy || ref == -INFINITY ? top : ref;
           const float keep = now == ref || ref == -INFINITY ? 1.0f : ex2(ref - now);
@@ -549,7 +549,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
             tmem_ld32(s_tmem + 32 * q, s);
             if constexpr (CAP) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) s[k] = soft_cap(s[k] * c, cap, inv_cap) * kLog2e;
+              for (int k = 0; k < 32; k += 2) {
+                const float2 x = cap(mul2(make_float2(s[k], s[k + 1]), make_float2(c, c)));
+                s[k] = x.x;
+                s[k + 1] = x.y;
+              }
             }
             mask(q, s);
 #pragma unroll

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     // ---------------- exponentials: thread = token ----------------
     const int tid = threadIdx.x, row = tid & 127, half = tid >> 7;  // token of the item, half of the columns
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 64 * half;
-    const float cap = p.a.softcap, inv_cap = CAP ? 1.0f / cap : 0.f;
+    const SoftCap cap(p.a.softcap, 1.0f);
     constexpr int kHalf = kCols / 2;
     float *col_lse = reinterpret_cast<float *>(smem + Cfg::kOffCol) + warp * 2 * kHalf;  // the warp's own
     int *col_limit = reinterpret_cast<int *>(col_lse + kHalf);
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
           const float2 acc = make_float2(a0, a1);
           float2 d;
           if constexpr (CAP)
-            d = make_float2(soft_cap(acc.x * ks, cap, inv_cap) + minus.x, soft_cap(acc.y * ks, cap, inv_cap) + minus.y);
+            d = add2(cap(mul2(acc, make_float2(ks, ks))), minus);
           else
             d = fma2(acc, make_float2(ks, ks), minus);
           d = mul2(d, make_float2(kLog2e, kLog2e));
