@@ -456,7 +456,8 @@ exl3_status exl3_kv8_append(const exl3_kv8_cache *cache, const exl3_kv8_batch *b
  * A NaN among the values of a sequence may reach every row that attends to
  * the sequence in this call, also rows before its position.
  * Sums, maxima and the softmax are fp32; the probabilities enter the product
- * with the values as fp16.
+ * with the values as fp16, scaled so that one of 2^-26 of a row's largest has all
+ * its 11 bits and one of 2^-37 still counts.
  *   scale: finite; softcap: 0 (off) or finite and at least 1e-30. A capped score
  *         has an error of 2^-19 of itself at most, besides that of the products.
  *   workspace: exl3_kv8_attention_workspace_bytes bytes (0 for invalid

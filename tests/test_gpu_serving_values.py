@@ -75,3 +75,56 @@ def test_caps_far_above_the_scores(cap, counts):
             w = pool.weight[page].astype(np.float64) + a
             tol = ((dim + 8) * U + 2.0 ** -20) * e + (max(counts) * heads + 2) * U * (a + w)
             assert np.all(np.abs(got[page] - w) <= tol)
+
+
+@pytest.mark.parametrize("cap", [1e-3, 1.0, 30.0, 5e4])
+@pytest.mark.parametrize("rows", [1, 50])
+def test_capped_score_to_its_stated_error(cap, rows):
+    """A sequence of one token: lse is its capped score, to 2^-19 of it and two more roundings."""
+    torch = torch_mod()
+    seqs, heads, dim = 500, 2, 64
+    codes = [torch.zeros((1, 1, 64, dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    codes[0][0, 0, 0, 0] = 7 << 3  # 1.0
+    cache = tql.Exl3Kv8Cache(*codes, *[torch.ones((1, 1), device="cuda") for _ in range(2)])
+    batch = tql.Exl3Kv8Batch(torch.zeros((seqs, 1), dtype=torch.int32, device="cuda"), torch.ones(seqs, dtype=torch.int32, device="cuda"),
+                             torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * rows, seqs * rows, rows)
+    rng = np.random.default_rng(int(cap * 1000) + rows)
+    x = (rng.choice([-1.0, 1.0], (seqs * rows, heads)) * 2.0 ** rng.uniform(-12, 4, (seqs * rows, heads))).astype(np.float16)
+    q = np.zeros((seqs * rows, heads, dim), dtype=np.float16)
+    q[:, :, 0] = x
+    qd = dev(q.reshape(seqs * rows, -1))
+    out, lse = torch.empty_like(qd), torch.empty((seqs * rows, heads), device="cuda")
+    ws = torch.empty(tql.exl3_kv8_attention_workspace_bytes(cache, batch, heads), dtype=torch.uint8, device="cuda")
+    tql.exl3_kv8_attention(cache, batch, qd, heads, cap, out, ws, softcap=cap, causal=False, lse=lse)
+    c = float(np.float32(cap))
+    want = c * np.tanh(x.astype(np.float64))
+    assert np.all(np.abs(lse.double().cpu().numpy() - want) <= (2.0 ** -19 + 4 * U) * np.abs(want) + 16 * U)
+
+
+@pytest.mark.parametrize("rows,length,seqs,heads", [(1, 131072, 20, 8), (2, 65536, 40, 8), (60, 65536, 20, 8), (256, 40000, 20, 8)])
+def test_weight_spread_over_many_tokens(rows, length, seqs, heads):
+    """One token takes nearly all the weight and has no value; the others have 2^-25.25 of its weight each, and all the
+    value. Each of their probabilities is rounded to 11 bits, the sums (an output is one of at most `length` / 16 steps in
+    fp32, which the tensor cores cut off) and the fp16 result: 2^-10 + length / 16 * 2^-23 in all."""
+    torch = torch_mod()
+    dim, blocks = 64, length // 64
+    small = 2.0 ** -25.25
+    codes = [torch.zeros((2, heads, 64, dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    one = 7 << 3  # 1.0 in E4M3
+    codes[0][0, :, 0, 0] = one
+    codes[1][:] = one
+    codes[1][0, :, 0] = 0
+    cache = tql.Exl3Kv8Cache(*codes, *[torch.ones((2, heads), device="cuda") for _ in range(2)])
+    table = torch.ones((seqs, blocks), dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    batch = tql.Exl3Kv8Batch(table, torch.full((seqs,), length, dtype=torch.int32, device="cuda"),
+                             torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * rows, seqs * rows, rows)
+    q = torch.zeros((seqs * rows, heads * dim), dtype=torch.float16, device="cuda")
+    q[:, ::dim] = 1.0
+    out, lse = torch.empty_like(q), torch.empty((seqs * rows, heads), device="cuda")
+    ws = torch.empty(tql.exl3_kv8_attention_workspace_bytes(cache, batch, heads), dtype=torch.uint8, device="cuda")
+    tql.exl3_kv8_attention(cache, batch, q, heads, float(-np.log(small)), out, ws, causal=False, lse=lse)
+    rest = (length - 1) * small
+    want = rest / (1 + rest)
+    assert np.abs(out.double().cpu().numpy() / want - 1).max() <= 2.0 ** -10 + length / 16 * 2.0 ** -23
+    assert np.abs(lse.double().cpu().numpy() - (np.log1p(rest) - np.log(small))).max() <= 2.0 ** -16

@@ -67,7 +67,7 @@ struct StreamParams {
   // the CTA's range, slot 1: one that began in it and goes on after it), and the
   // plan for the join.
   float *part_o;      // CTAs x 2 x rows x D
-  float *part_ml;     // CTAs x 2 x rows x 2 (maximum in log2 units, sum)
+  float *part_ml;     // CTAs x 2 x rows x 2 (reference in log2 units, sum)
   float *first;       // warps x rows x (D + 2): see Parts
   int64_t *plan;      // prefix of build_plan
   int warps;          // of the stream grid
@@ -372,10 +372,15 @@ struct Ring {
   }
 };
 
+// log2 of the probabilities' scale: the reference m of a row is its maximum less this, so
+// that a row's many small probabilities keep their bits in fp16 (one of 2^-28 of the
+// largest still has all 11; fp16 ends 2^-39 below it).
+constexpr float kHeadroom = 14.0f;
+
 template <int D, int NT>
 struct RowState {
   float o[NT][D / 16][4];  // O^T in units of 2^e_v: d by lane / 4, rows 2 t, 2 t + 1
-  float m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2];  // reference in log2 units, sum of exp2(score - m)
   int ev;                  // exponent of the value scale that o is in units of
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -391,7 +396,7 @@ struct RowState {
   }
 };
 
-// One unit: scores, running maximum and sum, O^T += V^T P^T.
+// One unit: scores, running reference and sum, O^T += V^T P^T.
 template <int D, int NT, bool CAP>
 __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stage, int pos0, int len, float ks, float vs,
                                             const uint32_t (&qf)[NT][D / 8], const int (&limit)[NT][2], int min_limit,
@@ -429,7 +434,7 @@ __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stag
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      const float now = fmaxf(st.m[n][col], top);
+      const float now = fmaxf(st.m[n][col], top - kHeadroom);
       const float ref = now == -INFINITY ? 0.f : now;
       const float keep = ex2(st.m[n][col] - ref);
       still = still && (keep == 1.0f || st.m[n][col] == -INFINITY);
@@ -446,7 +451,7 @@ __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stag
       st.l[n][col] = st.l[n][col] * keep + sum;
       alpha[n][col] = keep * unit;
     }
-    // fp16 probabilities: relative error 2^-12 on average, the size of the result's own rounding
+    // fp16 probabilities, 1 to 2^14 for the largest: relative error 2^-12 on average, the size of the result's own rounding
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
@@ -524,7 +529,7 @@ struct Parts {
   using Cfg = StreamCfg<D, NT, false>;
   static constexpr int kWarps = Cfg::kWarps;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kFloats = kRows * (D + 2);  // output, then (maximum, sum) of each row
+  static constexpr int kFloats = kRows * (D + 2);  // output, then (reference, sum) of each row
   static constexpr int kHeads = kWarps * kFloats * 4;
   static_assert(kHeads + 2 * kWarps * (int)sizeof(Part) <= Cfg::kRing, "parts fit the ring");
   uint8_t *smem;

@@ -19,9 +19,9 @@
 //   * warps 0..3 / 4..7 (tile 0 / 1; thread = row = TMEM lane): the row's 128
 //     scores, 32 at a time: maximum first, then mask, exp2, sum, probabilities as
 //     fp16 back to TMEM. While one tile's softmax runs, the tensor core works on the other's
-//     products. O is rescaled only when the maximum grows by more than 2^14 over
-//     the reference in use (the result is the same: the sum uses that reference),
-//     so rarely after the first units.
+//     products. O is rescaled only when the maximum grows by more than 2^3.75 over the
+//     one that the reference in use was set by (the result is the same: the sum uses
+//     that reference), so rarely after the first units.
 // TMEM: S0 S1 O0 O1, 128 columns each.
 //
 // Measured: 2048 rows of 40 heads on 8 over 8192 cached tokens, D = 128: 323 us (301
@@ -48,9 +48,13 @@ constexpr int kChunkThreads = (9 + kConvWarps) * 32;  // 96 registers a thread
 constexpr int kChunkSeqs = 1024;               // sequences of one launch
 // Entering a segment (queries, the blocks' largest scales, the output), in units.
 constexpr int kChunkEntry = 3;
-// log2 of how far a maximum may pass the reference in use: probabilities up to 2^14
-// in fp16 (largest 2^16), so that a row is rescaled about once or not at all.
-constexpr float kLazy = 14.0f;
+// A row's reference is set 2^12 below its maximum (kHeadroom), and set anew when a maximum
+// passes it by more than 2^15.75 (kLazy; fp16 ends at 2^16): a row is rescaled a few times
+// at most, and the many small probabilities of a long sequence keep their bits (one of
+// 2^-26 of the largest has all 11; fp16 ends 2^-37 below it). 2048 rows over 8192 tokens:
+// 329 us, 327 with 2^7 and 2^15, 324 with 1 and 2^14, where what is below 2^-25 of the
+// largest is lost (65536 tokens there have up to 2^-9 of the weight).
+constexpr float kHeadroom = 12.0f, kLazy = 15.75f;
 
 template <int D>
 struct ChunkCfg {
@@ -520,7 +524,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
           }
           if constexpr (CAP) top = top == -INFINITY ? top : cap(make_float2(top * c, 0.f)).x;  // as the cap is monotonic
           else top *= scale;
-          const float now = top > ref + kLazy || ref == -INFINITY ? top : ref;
+          const float now = top > ref + kLazy || ref == -INFINITY ? top - kHeadroom : ref;
           const float keep = now == ref || ref == -INFINITY ? 1.0f : ex2(ref - now);
           if (u > g.u0 && __any_sync(0xffffffffu, keep != 1.0f)) {
             if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarO + t), (count - 1) & 1, status))) {
@@ -545,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             float s[32];
-            uint32_t packed[16];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
+            uint32_t packed[16];  // fp16 probabilities: 2^-12 on average (see kHeadroom), the size of the result's own rounding
             tmem_ld32(s_tmem + 32 * q, s);
             if constexpr (CAP) {
 #pragma unroll
