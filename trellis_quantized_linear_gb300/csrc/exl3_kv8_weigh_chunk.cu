@@ -231,10 +231,11 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     // ---------------- tensor core (one lane) ----------------
     if (lane == 0) {
       constexpr uint32_t kIdesc = f16_idesc(kItem, kCols);
-      uint32_t n = 0;
+      uint32_t n = 0, held = 0;  // steps; items with steps, whose keys are brought
       bool ok = true;
       for (int k = 0; ok && get_item(p, plan, k, it); ++k) {
-        ok = mbar_wait(bar(kWKeys), k & 1, status);
+        if (it.steps == 0) continue;
+        ok = mbar_wait(bar(kWKeys), held++ & 1, status);
         for (int st = 0; ok && st < it.steps; ++st, ++n) {
           const uint32_t b = n & 1, ph = (n >> 1) & 1;
           ok = mbar_wait(bar(kWQFull + b), ph, status) && mbar_wait(bar(kWSEmpty + b), ph ^ 1, status);
@@ -276,36 +277,41 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     bool ok = true;
     for (int k = 0; get_item(p, plan, k, it); ++k) {
       const int pos0 = it.tile * kItem, pos = pos0 + row;
-      // the keys: a token has D / 16 lanes; lanes of the second half of the dimension take the token next to theirs
-      constexpr int kPerToken = D / 16, kStep = kExpWarps * 32 / kPerToken;
-      const int c = tid % kPerToken, tok0 = tid / kPerToken ^ (c >> 2);
-      uint4 w[kItem / kStep];
-#pragma unroll
-      for (int i = 0; i < kItem / kStep; ++i) {
-        const int t = tok0 + i * kStep;
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (pos0 + t >= it.q.len) continue;
-        const int page = kv_page(kv, it.s, (pos0 + t) / kKvBlock);
-        if (page < 0) continue;
-        const int64_t off = (((int64_t)page * kv.n_kv_heads + it.h) * kKvBlock + (pos0 + t) % kKvBlock) * D + c * 16;
-        if (EXL3_SPAN(off, 16, size)) w[i] = *reinterpret_cast<const uint4 *>(kv.k + off);
-      }
       int page = -1;
       float ks = 0.f;
       if (pos < it.q.len) page = kv_page(kv, it.s, pos / kKvBlock);
       const int64_t slab = (int64_t)max(page, 0) * kv.n_kv_heads + it.h;
       if (page >= 0) ks = kv.k_scale[slab] * p.a.scale * untruncate;
+      // The keys, where this CTA has a step of the item: a product that reads them, and the wait for
+      // its scores, are what keeps these warps within one item of the tensor core's lane (without
+      // them the barrier could pass two phases between its looks). A token has D / 16 lanes; lanes
+      // of the second half of the dimension take the token next to theirs.
+      if (it.steps > 0) {
+        constexpr int kPerToken = D / 16, kStep = kExpWarps * 32 / kPerToken;
+        const int c = tid % kPerToken, tok0 = tid / kPerToken ^ (c >> 2);
+        uint4 w[kItem / kStep];
 #pragma unroll
-      for (int i = 0; i < kItem / kStep; ++i) {
-        uint32_t o[8];
-        codes_to_half(w[i], o);
-        const uint32_t at = base + (c >> 2) * (128 * 128);
-        sts16(at + swizzled(tok0 + i * kStep, 2 * (c & 3)), o[0], o[1], o[2], o[3]);
-        sts16(at + swizzled(tok0 + i * kStep, 2 * (c & 3) + 1), o[4], o[5], o[6], o[7]);
+        for (int i = 0; i < kItem / kStep; ++i) {
+          const int t = tok0 + i * kStep;
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (pos0 + t >= it.q.len) continue;
+          const int page = kv_page(kv, it.s, (pos0 + t) / kKvBlock);
+          if (page < 0) continue;
+          const int64_t off = (((int64_t)page * kv.n_kv_heads + it.h) * kKvBlock + (pos0 + t) % kKvBlock) * D + c * 16;
+          if (EXL3_SPAN(off, 16, size)) w[i] = *reinterpret_cast<const uint4 *>(kv.k + off);
+        }
+#pragma unroll
+        for (int i = 0; i < kItem / kStep; ++i) {
+          uint32_t o[8];
+          codes_to_half(w[i], o);
+          const uint32_t at = base + (c >> 2) * (128 * 128);
+          sts16(at + swizzled(tok0 + i * kStep, 2 * (c & 3)), o[0], o[1], o[2], o[3]);
+          sts16(at + swizzled(tok0 + i * kStep, 2 * (c & 3) + 1), o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kWKeys));
       }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kWKeys));
 
       // a column of the steps in order: its row's lse, and how many tokens the row sees
       int step_row = it.first + it.step0 / it.chunks * p.rows, chunk = it.step0 % it.chunks;
