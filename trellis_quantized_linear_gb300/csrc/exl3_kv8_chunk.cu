@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
         }
         const int2 top_scale = largest_scales(kv, g, lane);
         // scores in log2 units are the products times c, then capped
-        const float c = fmaxf(fabsf(p.a.scale) * pow2i(top_scale.x) * kLog2e, 1e-37f);
+        const float c = fmaxf(fabsf(p.a.scale) * pow2i(top_scale.x) * Raised<D>::kLog2e, 1e-37f);
         float ref = -INFINITY, sum = 0.f;
         for (int u = g.u0; u < g.u1; ++u, ++count) {
           if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarS + t), count & 1, status))) {

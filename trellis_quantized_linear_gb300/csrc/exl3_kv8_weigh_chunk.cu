@@ -267,9 +267,6 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     const int rank = blockIdx.x & 1;
     const uint32_t peer_smem = map_to_rank(base, 1 - rank);
     [[maybe_unused]] const int64_t size = kv.n_pages * kv.n_kv_heads * kKvBlock * (int64_t)D;
-    // The tensor core cuts its partial sums off towards zero, D / 16 times: on average
-    // this share of a score. Without it heavy weights came out 2e-6 low.
-    const float untruncate = 1.0f + 0.6f * 0.5f * (D / 16 + 1) * 0.5f * 0x1p-23f;
     // a lane brings two of its warp's columns
     const int col0 = half * kHalf + lane, col1 = col0 + 32;
     const int row_0 = col0 / p.heads, head_0 = col0 % p.heads, row_1 = col1 / p.heads, head_1 = col1 % p.heads;
@@ -281,7 +278,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       float ks = 0.f;
       if (pos < it.q.len) page = kv_page(kv, it.s, pos / kKvBlock);
       const int64_t slab = (int64_t)max(page, 0) * kv.n_kv_heads + it.h;
-      if (page >= 0) ks = kv.k_scale[slab] * p.a.scale * untruncate;
+      if (page >= 0) ks = kv.k_scale[slab] * p.a.scale * Raised<D>::kOne;
       // The keys, where this CTA has a step of the item: a product that reads them, and the wait for
       // its scores, are what keeps these warps within one item of the tensor core's lane (without
       // them the barrier could pass two phases between its looks). A token has D / 16 lanes; lanes
