@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
   auto token = [&](int i) { return ((((i >> 7) << p.lg) | (int)rank) << 7) | (i & 127); };
   auto owner = [&](uint32_t t) { return (t >> 7) & (ranks - 1); };
   auto local = [&](uint32_t t) { return ((t >> 7 >> p.lg) << 7) | (t & 127); };
+  auto permits = [&](int t) { return !allowed || ((allowed[t >> 5] >> (t & 31)) & 1u); };
   const int2 h = row_range(p.r.history_start, m, p.r.history_size, p.status);
   const int2 b = row_range(p.r.bias_start, m, p.r.bias_size, p.status);
   const int made_from = p.r.generated_from ? p.r.generated_from[m] : 0;
@@ -322,7 +323,10 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           if (word[k] == 0) continue;
-          y[k] = penalized(y[k], word[k], r);
+          const float was = y[k];
+          y[k] = penalized(was, word[k], r);
+          // a penalty that is not finite would bring back what the mask forbids
+          if (was == -INFINITY && y[k] != -INFINITY && !permits(t[k])) continue;
           out[t[k]] = y[k];
           if (y[k] > -INFINITY) best.take(y[k], t[k]);
         }
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
         at[k] = word_of((uint32_t)id[k]);
         const bool here = at[k] < (uint32_t)n;
         y[k] = here ? out[id[k]] : 0.f;
-        may[k] = !here || !allowed || ((allowed[id[k] >> 5] >> (id[k] & 31)) & 1u);
+        may[k] = !here || permits(id[k]);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
