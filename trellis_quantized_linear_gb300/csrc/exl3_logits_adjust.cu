@@ -123,6 +123,9 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
   const int64_t m = blockIdx.x / ranks;
+  if (tid == 0) list_n = 0;
+  __syncwarp();
+  cluster_arrive_all();  // awaited before the first access to another CTA's shared memory: that CTA has started then
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -168,9 +171,9 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
   // 44 / 49 / 64 with every CTA reading all; below 4 entries a thread the two cluster
   // barriers cost a single row 1 us.
   bool listed = false;
-  if (h.y - h.x > 4 * T) {
-    if (tid == 0) list_n = 0;
-    cluster_sync_all();
+  const bool handed_out = h.y - h.x > 4 * T;  // the same in every CTA of the cluster
+  if (handed_out) {
+    cluster_wait_all();
     const int every = T * (int)ranks;
     constexpr int kAhead = 4;
     for (int i0 = h.x + (int)rank * T; i0 < h.y; i0 += every * kAhead) {  // the same for every thread
@@ -381,6 +384,8 @@ __global__ void __launch_bounds__(T, CTAS) logits_adjust_kernel(const AdjustPara
     sb[tid >> 5] = best.x;
     si[tid >> 5] = best.t;
   }
+  __syncwarp();
+  if (!handed_out) cluster_wait_all();
   __syncthreads();
   if (tid < 32) {
     best = Best();
