@@ -537,7 +537,7 @@ typedef struct {
 /*
  *   logits, out: M x n fp32, leading dimensions ldl, ldo (multiples of 4, at
  *          least n): exl3_logits_masked's logits with n = n_decodable. They may
- *          be the same buffer. Columns from n on are neither read nor written.
+ *          be the same buffer, with ldl = ldo. Columns from n on are neither read nor written.
  *   argmax: M int32: the first index of the row's maximum (a NaN is never
  *          the maximum); -1 where no token is left (all -inf or NaN).
  *   1 <= n <= 2^19, 0 <= M <= 65535; at most 2^29 history and 2^29 bias entries.

@@ -149,6 +149,8 @@ exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int6
   if (!rules || M < 0 || M > 65535 || n < 1 || n > (1 << 19) || ldl < n || ldl % 4 || ldo < n || ldo % 4 ||
       rules->history_size < 0 || rules->history_size > (1 << 29) || rules->bias_size < 0 || rules->bias_size > (1 << 29))
     return EXL3_ERR_INVALID_ARG;
+  // rows of one buffer at two distances would run into one another
+  if (logits == out && ldl != ldo && M > 1) return EXL3_ERR_INVALID_ARG;
   const exl3_logits_rules &r = *rules;
   // parts of a rule go together
   if ((r.history == nullptr) != (r.history_start == nullptr) || (r.generated_from && !r.history) ||
