@@ -26,3 +26,117 @@ def test_one_logits_buffer_has_one_row_distance(lib):
 
     assert call(2, GOOD, 256, GOOD, 260) == 1
     assert call(1, GOOD, 256, GOOD, 260) == 5 and call(2, GOOD, 256, GOOD, 256) == 5 and call(2, GOOD, 256, 2 * GOOD, 260) == 5
+
+
+def goes(f):
+    """The call gets past every check of its arguments."""
+    with pytest.raises(tql.Exl3Error) as e:
+        f()
+    assert e.value.status == 5
+
+
+def objects():
+    import torch
+    codes, s, w = torch.zeros((3, 2, 64, 64), dtype=torch.uint8), torch.ones((3, 2)), torch.zeros((3, 2, 64))
+    cache = tql.Exl3Kv8Cache(codes, codes, s, s, w)
+    start = torch.tensor([0, 2, 5], dtype=torch.int32)
+    batch = tql.Exl3Kv8Batch(torch.zeros((2, 1), dtype=torch.int32), torch.ones(2, dtype=torch.int32), start, 5, 3)
+    return torch, cache, batch
+
+
+def test_append_looks_at_its_tensors(lib):
+    torch, cache, batch = objects()
+    x = torch.zeros((5, 2 * 128), dtype=torch.float16)
+
+    def call(k, v):
+        tql.exl3_kv8_append(cache, batch, k, v, stream=0)
+
+    for good in (x[:, :128], x[:, 128:], torch.zeros((7, 128)).half(), x[:, :128].reshape(5, 2, 64), x):
+        goes(lambda: call(good, x[:, :128]))
+        goes(lambda: call(x[:, :128], good))
+    for bad in (x.float()[:, :128], x.bfloat16()[:, :128], x[:4, :128], x[:, :120], torch.zeros((128, 5)).half().t(), x[:, ::2], x.view(-1),
+                x[:, :128].reshape(5, 2, 64).transpose(1, 2), torch.zeros((5, 3, 64)).half()[:, ::2]):
+        for args in ((bad, x[:, :128]), (x[:, :128], bad)):
+            with pytest.raises(ValueError):
+                call(*args)
+
+
+def test_one_row_needs_no_row_stride(lib):
+    torch, cache, _ = objects()
+    one = tql.Exl3Kv8Batch(torch.zeros((1, 1), dtype=torch.int32), torch.ones(1, dtype=torch.int32), torch.tensor([0, 1], dtype=torch.int32), 1, 1)
+    x = torch.zeros((128, 1), dtype=torch.float16).t()  # strides (1, 1)
+    goes(lambda: tql.exl3_kv8_append(cache, one, x, x.contiguous(), stream=0))
+    logits = torch.zeros((1, 1001))  # a row stride that is no multiple of 4
+    goes(lambda: tql.exl3_logits_adjust(logits, 1001, logits, torch.zeros(1, dtype=torch.int32), stream=0))
+
+
+def test_attention_and_weigh_look_at_their_tensors(lib):
+    torch, cache, batch = objects()
+    q, out, lse = torch.zeros((5, 300)).half()[:, :256], torch.zeros((5, 256)).half(), torch.zeros((5, 4))
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    q = torch.zeros((5, 304)).half()[:, :256]
+
+    def attend(**kw):
+        a = dict(q=q, out=out, lse=lse) | kw
+        tql.exl3_kv8_attention(cache, batch, a["q"], 4, 0.1, a["out"], ws, lse=a["lse"], workspace_bytes=1 << 40, stream=0)
+
+    def weigh(**kw):
+        a = dict(q=q, lse=lse) | kw
+        tql.exl3_kv8_weigh(cache, batch, a["q"], 4, 0.1, a["lse"], stream=0)
+
+    goes(attend)
+    goes(weigh)
+    goes(lambda: attend(lse=None))
+    goes(lambda: attend(lse=lse.view(-1)))
+    for bad in (q.float(), q[:4], q[:, :248], torch.zeros((256, 5)).half().t()):
+        for call in (lambda: attend(q=bad), lambda: attend(out=bad), lambda: weigh(q=bad)):
+            with pytest.raises(ValueError):
+                call()
+    for bad in (lse.double(), lse.half(), lse[:4], torch.zeros((4, 5)).t(), lse[:, :3]):
+        for call in (lambda: attend(lse=bad), lambda: weigh(lse=bad)):
+            with pytest.raises(ValueError):
+                call()
+
+
+def test_evict_looks_at_its_tensors(lib):
+    torch, cache, batch = objects()
+    a = dict(dst=torch.zeros((2, 2), dtype=torch.int32), kept=torch.zeros((2, 2, 100), dtype=torch.int32), new_len=torch.zeros(2, dtype=torch.int32))
+
+    def call(**kw):
+        b = a | kw
+        tql.exl3_kv8_evict(cache, batch, b["dst"], 100, 10, b["kept"], b["new_len"], stream=0)
+
+    goes(call)
+    for name, t in a.items():
+        for bad in (t.long(), t.float(), t.view(-1)[:-1], torch.zeros(2 * t.numel(), dtype=torch.int32)[::2]):
+            with pytest.raises(ValueError):
+                call(**{name: bad})
+
+
+def test_logits_look_at_their_tensors(lib):
+    torch, _, _ = objects()
+    M, n = 3, 250
+    i32 = dict(dtype=torch.int32)
+    x = torch.zeros((M, 256))
+    a = dict(logits=x, out=x, argmax=torch.zeros(M, **i32), history=torch.zeros(9, **i32), history_start=torch.zeros(M + 1, **i32),
+             generated_from=torch.zeros(M, **i32), repetition=torch.ones(M), presence=torch.ones(M), frequency=torch.ones(M),
+             bias_id=torch.zeros(7, **i32), bias_value=torch.zeros(7), bias_start=torch.zeros(M + 1, **i32), allowed=torch.zeros((M, 8), **i32))
+
+    def call(**kw):
+        b = a | kw
+        tql.exl3_logits_adjust(b.pop("logits"), n, b.pop("out"), b.pop("argmax"), stream=0, **b)
+
+    goes(call)
+    goes(lambda: call(allowed=a["allowed"].view(torch.uint32), out=torch.zeros((M, 252))))
+    goes(lambda: call(bias_id=None, bias_value=None, bias_start=None, allowed=None))
+    for name, t in a.items():
+        bad = [t.double() if t.is_floating_point() else t.long(), t.int() if t.is_floating_point() else t.float()]
+        if name in ("logits", "out"):
+            bad += [t[:, :249], torch.zeros((256, M)).t()] + ([t[:2]] if name == "out" else [])
+        else:
+            bad += [torch.zeros(2 * t.numel(), dtype=t.dtype)[::2]]
+            if name not in ("history", "bias_id"):
+                bad += [t.reshape(-1)[:-1]]
+        for b in bad:
+            with pytest.raises(ValueError, match=name):
+                call(**{name: b})

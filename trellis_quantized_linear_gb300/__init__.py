@@ -378,11 +378,49 @@ def exl3_silu_mul(gate, up, out, n: int | None = None, stream=None) -> None:
     _check(load().exl3_silu_mul(_ptr(gate), _ptr(up), _ptr(out), int(n), _stream(stream)), "exl3_silu_mul")
 
 
+# The tensors of the serving operators' calls, checked in as few steps as a call of a few
+# microseconds allows: types, sizes and strides, as the kernels will read them.
+_F16 = _F32 = _I32 = None
+
+
+def _need_dtypes():
+    global _F16, _F32, _I32
+    import torch
+    _F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
+    return _F16
+
+
+def _rows(what, t, dtype, rows, cols):
+    """Row stride of t, `rows` rows of at least `cols` elements (any row stride, each row contiguous)."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or len(shape) < 2 or shape[0] < rows or stride[-1] != 1 or shape[1] < cols and (
+            len(shape) == 2 or rows > 0 and (not t[0].is_contiguous() or t[0].numel() < cols)):
+        raise ValueError(f"{what}: expected {dtype}, {rows} x {cols} with contiguous rows, got {t.dtype} {tuple(shape)} with strides {stride}")
+    return stride[0] if shape[0] > 1 else -(-cols // 8) * 8  # a single row's stride says nothing
+
+
+def _array(what, t, dtype, n):
+    """Pointer of t, contiguous and of at least n elements (an int address as it is; 0 for None)."""
+    if t is None:
+        return 0
+    if isinstance(t, int):
+        return t
+    if t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    if dtype is _I32 and t.element_size() == 4 and not t.is_floating_point() and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()  # other 32-bit integers
+    raise ValueError(f"{what}: expected at least {n} contiguous {dtype}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
 def exl3_kv8_append(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, k, v, stream=None) -> None:
     """Quantizes rows of keys and values (fp16, rows x n_kv_heads * head_dim,
     any row stride) into the 8-bit cache."""
-    _check(load().exl3_kv8_append(cache._ref, batch._ref, _ptr(k), k.stride(0), _ptr(v), v.stride(0),
-                                  _stream(stream)), "exl3_kv8_append")
+    lib = _lib or load()
+    rows, cols, f16 = batch.rows, cache.n_kv_heads * cache.head_dim, _F16 or _need_dtypes()
+    ldk, ldv = _rows("exl3_kv8_append: k", k, f16, rows, cols), _rows("exl3_kv8_append: v", v, f16, rows, cols)
+    status = lib.exl3_kv8_append(cache._ref, batch._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_kv8_append")
 
 
 def exl3_kv8_attention_workspace_bytes(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, n_heads: int) -> int:
@@ -394,18 +432,29 @@ def exl3_kv8_attention(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, q, n_heads: int
                        stream=None) -> None:
     """Attention of q (fp16, rows x n_heads * head_dim, any row stride) over the
     8-bit cache into out (fp16, same shape); lse: rows x n_heads fp32 or None."""
+    lib = _lib or load()
+    rows, cols, f16 = batch.rows, n_heads * cache.head_dim, _F16 or _need_dtypes()
+    ldq, ldo = _rows("exl3_kv8_attention: q", q, f16, rows, cols), _rows("exl3_kv8_attention: out", out, f16, rows, cols)
+    lse = _array("exl3_kv8_attention: lse", lse, _F32, rows * n_heads)
     nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
-    _check(load().exl3_kv8_attention(cache._ref, batch._ref, _ptr(q), q.stride(0), n_heads, scale, softcap, causal,
-                                     _ptr(out), out.stride(0), _ptr(lse), _ptr(workspace), nbytes, _stream(stream)),
-           "exl3_kv8_attention")
+    status = lib.exl3_kv8_attention(cache._ref, batch._ref, q.data_ptr(), ldq, n_heads, scale, softcap, causal,
+                                    out.data_ptr(), ldo, lse, _ptr(workspace), nbytes, _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_kv8_attention")
 
 
 def exl3_kv8_weigh(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, q, n_heads: int, scale: float, lse, softcap: float = 0.0,
                    causal: bool = True, stream=None) -> None:
     """Adds the attention that q's rows give each cached token to cache.weight;
     lse as exl3_kv8_attention returned it."""
-    _check(load().exl3_kv8_weigh(cache._ref, batch._ref, _ptr(q), q.stride(0), n_heads, scale, softcap, causal,
-                                 _ptr(lse), _stream(stream)), "exl3_kv8_weigh")
+    lib = _lib or load()
+    rows, f16 = batch.rows, _F16 or _need_dtypes()
+    ldq = _rows("exl3_kv8_weigh: q", q, f16, rows, n_heads * cache.head_dim)
+    lse = _array("exl3_kv8_weigh: lse", lse, _F32, rows * n_heads)
+    status = lib.exl3_kv8_weigh(cache._ref, batch._ref, q.data_ptr(), ldq, n_heads, scale, softcap, causal, lse,
+                                _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_kv8_weigh")
 
 
 def exl3_kv8_evict(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, dst_pages, budget: int, recent: int, kept, new_len,
@@ -413,20 +462,46 @@ def exl3_kv8_evict(cache: Exl3Kv8Cache, batch: Exl3Kv8Batch, dst_pages, budget: 
     """Moves each sequence's last `recent` and heaviest other tokens, `budget` in
     all, to dst_pages (int32, n_seqs x ceil(budget / 64)); kept (int32, n_seqs x
     n_kv_heads x budget) and new_len (int32, n_seqs) receive what was kept."""
-    _check(load().exl3_kv8_evict(cache._ref, batch._ref, _ptr(dst_pages), budget, recent, _ptr(kept), _ptr(new_len),
-                                 _stream(stream)), "exl3_kv8_evict")
+    lib = _lib or load()
+    if _F16 is None:
+        _need_dtypes()
+    n = batch.n_seqs
+    dst_pages = _array("exl3_kv8_evict: dst_pages", dst_pages, _I32, n * -(-budget // EXL3_KV8_BLOCK))
+    kept = _array("exl3_kv8_evict: kept", kept, _I32, n * cache.n_kv_heads * budget)
+    new_len = _array("exl3_kv8_evict: new_len", new_len, _I32, n)
+    status = lib.exl3_kv8_evict(cache._ref, batch._ref, dst_pages, budget, recent, kept, new_len, _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_kv8_evict")
 
 
 def exl3_logits_adjust(logits, n: int, out, argmax, history=None, history_start=None, generated_from=None,
                        repetition=None, presence=None, frequency=None, bias_id=None, bias_value=None, bias_start=None,
                        allowed=None, stream=None) -> None:
     """Penalties, biases and a grammar mask on the first n columns of logits
-    (fp32, M x ld) into out (may be logits), and the greedy choice."""
-    rules = _PACK_RULES(*[0 if t is None else t.data_ptr() for t in (
-        history, history_start, generated_from, repetition, presence, frequency, bias_id, bias_value, bias_start, allowed)],
-        0 if history is None else history.numel(), 0 if bias_id is None else bias_id.numel())
-    _check(load().exl3_logits_adjust(logits.data_ptr(), logits.stride(0), logits.size(0), n, rules, out.data_ptr(),
-                                     out.stride(0), argmax.data_ptr(), _stream(stream)), "exl3_logits_adjust")
+    (fp32, M x ld) into out (may be logits), and the greedy choice (int32, M).
+    Token ids, starts and generated_from are int32, the penalties and
+    bias_value fp32, allowed M x ceil(n / 32) words of 32 bits."""
+    lib = _lib or load()
+    if _F16 is None:
+        _need_dtypes()
+    i32, f32, M = _I32, _F32, logits.shape[0]
+    ldl, ldo = _rows("exl3_logits_adjust: logits", logits, f32, M, n), _rows("exl3_logits_adjust: out", out, f32, M, n)
+    n_history, n_bias = 0 if history is None else history.numel(), 0 if bias_id is None else bias_id.numel()
+    rules = _PACK_RULES(
+        _array("exl3_logits_adjust: history", history, i32, 0),
+        _array("exl3_logits_adjust: history_start", history_start, i32, M + 1),
+        _array("exl3_logits_adjust: generated_from", generated_from, i32, M),
+        _array("exl3_logits_adjust: repetition", repetition, f32, M),
+        _array("exl3_logits_adjust: presence", presence, f32, M),
+        _array("exl3_logits_adjust: frequency", frequency, f32, M),
+        _array("exl3_logits_adjust: bias_id", bias_id, i32, 0),
+        _array("exl3_logits_adjust: bias_value", bias_value, f32, n_bias),
+        _array("exl3_logits_adjust: bias_start", bias_start, i32, M + 1),
+        _array("exl3_logits_adjust: allowed", allowed, i32, M * -(-n // 32)), n_history, n_bias)
+    argmax = _array("exl3_logits_adjust: argmax", argmax, i32, M)
+    status = lib.exl3_logits_adjust(logits.data_ptr(), ldl, M, n, rules, out.data_ptr(), ldo, argmax, _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_logits_adjust")
 
 
 def exl3_selftest_bounds_serving(stream=None) -> tuple[int, int]:
