@@ -6,10 +6,11 @@ Tolerances as in test_gpu_serving.py.
 import numpy as np
 import pytest
 
+import serving_ref as ref
 import trellis_quantized_linear_gb300 as tql
 from gpu_util import torch_mod
-from test_gpu_serving import Pool, attend, dev, gpu, rows_on_device  # noqa: F401 (gpu: fixture)
-from test_gpu_serving_limits import check_weigh
+from test_gpu_serving import U, Pool, attend, check_attention, dev, gpu, rows_on_device  # noqa: F401 (gpu: fixture)
+from test_gpu_serving_limits import check_both, check_weigh
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +89,65 @@ def test_scores_of_heavy_tokens_have_no_common_error(dim, rows):
     got = cache._keep[4][:, 0, 0].double().view(n, 1) / rows
     want = torch.exp(s - exact.double()).view(n, rows).mean(1, keepdim=True)
     assert abs(float(((got - want) * rows).sum())) <= 0.75 * step
+
+
+@pytest.mark.parametrize("kv_len,counts,heads,causal", [([400, 290, 333], [120, 130, 1], 4, True), ([700, 290, 500], [60, 57, 60], 4, False)])
+def test_sequences_that_share_pages(kv_len, counts, heads, causal):
+    """A common beginning is read by all of them, and gets the weight of all: many rows add to it at once."""
+    pool = Pool(kv_len, 2, 64, seed=13)
+    for s in (1, 2):
+        pool.table[s][:2] = pool.table[0][:2]
+    check_both(pool, counts, heads, causal=causal)
+
+
+@pytest.mark.parametrize("rows", [49, 113, 150])
+def test_pages_past_32_bit_offsets(rows):
+    """Pages more than 4 GiB into the pool."""
+    torch = torch_mod()
+    n, heads, dim, length = 70000, 8, 128, 200
+    codes = [torch.zeros((n, heads, 64, dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones((n, heads), device="cuda") for _ in range(2)]
+    cache = tql.Exl3Kv8Cache(*codes, *scales, torch.zeros((n, heads, 64), device="cuda"))
+    at = np.array([n - 1, n - 7, 3, n - 20])
+    small = Pool([length], heads, dim, seed=rows)
+    order = small.table[0][:4]
+    for i in range(2):
+        codes[i][at] = dev(small.codes[i][order])
+        scales[i][at] = dev(small.scales[i][order])
+    batch = tql.Exl3Kv8Batch(dev(at[None].astype(np.int32)), dev(np.array([length], dtype=np.int32)), dev(np.array([0, rows], dtype=np.int32)),
+                             rows, rows)
+    q = small.rng.standard_normal((rows, heads, dim)).astype(np.float16)
+    got, lse = attend(type("P", (), {"cache": cache, "dim": dim}), [rows], q, heads, 0.1, 0.0, True, batch=batch)
+    want = ref.attention(small.codes[0], small.scales[0], small.codes[1], small.scales[1], small.table, [length], [rows], q, 0.1, 0.0, True)
+    check_attention(got, lse, want, dim, 0.0, length)
+    lse = want[1].astype(np.float32)
+    tql.exl3_kv8_weigh(cache, batch, rows_on_device(q.reshape(rows, -1), 0), heads, 0.1, dev(lse))
+    w = cache._keep[4][at].cpu().numpy().transpose(1, 0, 2).reshape(heads, -1)
+    add, bound = ref.weigh(small.codes[0], small.scales[0], small.table, [length], [rows], q, lse, 0.1, 0.0, True, 256)
+    assert np.all(np.abs(w - add[0]) <= ((dim + 8) * U + 2.0 ** -20) * bound[0] + (rows + 2) * U * add[0])
+
+
+@pytest.mark.parametrize("table,kv_len,start", [([[-1] * 3, [1 << 30] * 3], [100, 100], [0, 130, 260]),
+                                                (None, [1000, -5], [0, 130, 260]), (None, [100, 100], [0, 261, 260]),
+                                                (None, [100, 100], [-3, 0, 260])])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_bad_indexes_on_the_device(table, kv_len, start, cap):
+    """Reported and not followed, by the kernels of 130 rows of a group; pages that no sequence has are untouched."""
+    torch = torch_mod()
+    pool = Pool([100, 100], 1, 128, seed=1)
+    cache = pool.on_device()
+    before = [t.clone() for t in pool.t]
+    q = rows_on_device(np.ones((260, 128), dtype=np.float16), 0)
+    batch = tql.Exl3Kv8Batch(dev(np.array(pool.table if table is None else table, dtype=np.int32)), dev(np.array(kv_len, dtype=np.int32)),
+                             dev(np.array(start, dtype=np.int32)), 260, 130)
+    out = torch.zeros((260, 128), dtype=torch.float16, device="cuda")
+    ws = torch.empty(tql.exl3_kv8_attention_workspace_bytes(cache, batch, 1), dtype=torch.uint8, device="cuda")
+    for call in (lambda: tql.exl3_kv8_attention(cache, batch, q, 1, 1.0, out, ws, softcap=cap),
+                 lambda: tql.exl3_kv8_weigh(cache, batch, q, 1, 1.0, torch.zeros((260, 1), device="cuda"), softcap=cap),
+                 lambda: tql.exl3_kv8_append(cache, batch, q, q)):
+        call()
+        assert tql.exl3_get_device_status() == 10
+        assert tql.exl3_get_device_status() == 0
+    same = np.setdiff1d(np.arange(pool.n), pool.table.ravel())
+    for t, b in zip(pool.t, before):
+        assert torch.equal(t[same], b[same])

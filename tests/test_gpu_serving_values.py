@@ -10,6 +10,7 @@ import serving_ref as ref
 import trellis_quantized_linear_gb300 as tql
 from gpu_util import torch_mod
 from test_gpu_serving import U, Pool, attend, check_attention, dev, gpu, rows_on_device  # noqa: F401 (gpu: fixture)
+from test_gpu_serving_limits import check_weigh
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,38 @@ def test_weight_spread_over_many_tokens(rows, length, seqs, heads):
     want = rest / (1 + rest)
     assert np.abs(out.double().cpu().numpy() / want - 1).max() <= 2.0 ** -10 + length / 16 * 2.0 ** -23
     assert np.abs(lse.double().cpu().numpy() - (np.log1p(rest) - np.log(small))).max() <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0])
+@pytest.mark.parametrize("counts,cap", [([1, 2], 0.0), ([20, 9], 20.0), ([60, 130], 0.0), ([60, 130], 20.0)])
+def test_scales_of_either_sign(scale, counts, cap):
+    pool = Pool([300, 257], 2, 64, seed=41)
+    pool.on_device()
+    q = (2 * pool.rng.standard_normal((sum(counts), 4, 64))).astype(np.float16)
+    got, lse = attend(pool, counts, q, 4, scale, cap, True)
+    want = ref.attention(pool.codes[0], pool.scales[0], pool.codes[1], pool.scales[1], pool.table, pool.kv_len, counts, q, scale, cap, True)
+    check_attention(got, lse, want, 64, cap, 300)
+    check_weigh(pool, counts, 4, q, want[1].astype(np.float32), scale, cap, True)
+
+
+@pytest.mark.parametrize("which", ["keys", "values"])
+@pytest.mark.parametrize("counts", [[1], [60]])
+def test_blocks_of_very_different_size(which, counts):
+    """Scales from 2^-29 to 2^8. Single tokens have every block exactly. Many rows lose what is below 2^-25 of the largest
+    block's largest value (448 scales), seen or not: that much of a key element or value, on top of the other tolerances."""
+    pool = Pool([900], 1, 64, seed=43, spread=0)
+    i = 0 if which == "keys" else 1
+    for b in range(15):
+        pool.scales[i][pool.table[0][b]] = 2.0 ** [8, -29, -16, -10, -18, 0, -25, -17, -7, -29, -24, -20, 4, -27, -12][(b + 4) % 15]
+    pool.on_device()
+    scale = 2.0 ** -14 if which == "keys" else 0.125
+    q = pool.rng.standard_normal((sum(counts), 1, 64)).astype(np.float16)
+    got, lse = attend(pool, counts, q, 1, scale, 0.0, True)
+    out, wlse, mag, sabs = ref.attention(pool.codes[0], pool.scales[0], pool.codes[1], pool.scales[1], pool.table, [900], counts, q, scale,
+                                         0.0, True)
+    lost = 0.0 if counts == [1] else 2.0 ** -25 * 448 * 2.0 ** 8
+    s_lost = lost * scale * np.abs(q.astype(np.float64)).sum(2) if which == "keys" else 0 * wlse
+    s_err = (64 + 8) * U * sabs + 2.0 ** -20 * (1 + np.abs(wlse) + sabs) + s_lost
+    assert np.all(np.abs(lse - wlse) <= s_err)
+    tol = 2.0 ** -11 * np.abs(out) + (2.0 ** -11 + 2 * s_err[:, :, None]) * mag + 2.0 ** -25 + (lost if which == "values" else 0.0)
+    assert np.all(np.abs(got - out) <= tol)
