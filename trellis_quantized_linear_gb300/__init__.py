@@ -222,22 +222,21 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_current_stream = None
+_raw_stream = _raw_device = None  # (device) -> handle of torch's current stream, and () -> device
 
 
 def _stream(stream):
     if stream is None:
-        global _current_stream
-        if _current_stream is None:
+        global _raw_stream, _raw_device
+        if _raw_device is None:
             import torch
             # the raw handle of torch's current stream: torch.cuda.current_stream() builds an object
             # for it at every call, which takes longer than a launch
             get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
             if get is None or device is None:
-                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-            else:
-                _current_stream = lambda: get(device())  # noqa: E731
-        return _current_stream()
+                get, device = (lambda _: torch.cuda.current_stream().cuda_stream), (lambda: None)
+            _raw_stream, _raw_device = get, device  # the device last: another thread may be here
+        return _raw_stream(_raw_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -386,7 +385,7 @@ _F16 = _F32 = _I32 = None
 def _need_dtypes():
     global _F16, _F32, _I32
     import torch
-    _F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
+    _F32, _I32, _F16 = torch.float32, torch.int32, torch.float16  # the one that is asked for last
     return _F16
 
 
@@ -401,12 +400,13 @@ def _rows(what, t, dtype, rows, cols):
 
 def _array(what, t, dtype, n):
     """Pointer of t, contiguous and of at least n elements (an int address as it is; 0 for None)."""
-    if t is None:
-        return 0
-    if isinstance(t, int):
-        return t
-    if t.dtype is dtype and t.numel() >= n and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.numel() >= n and (n == 1 or t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t or 0
+        raise
     if dtype is _I32 and t.element_size() == 4 and not t.is_floating_point() and t.numel() >= n and t.is_contiguous():
         return t.data_ptr()  # other 32-bit integers
     raise ValueError(f"{what}: expected at least {n} contiguous {dtype}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
