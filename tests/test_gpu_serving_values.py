@@ -164,3 +164,18 @@ def test_blocks_of_very_different_size(which, counts):
     assert np.all(np.abs(lse - wlse) <= s_err)
     tol = 2.0 ** -11 * np.abs(out) + (2.0 ** -11 + 2 * s_err[:, :, None]) * mag + 2.0 ** -25 + (lost if which == "values" else 0.0)
     assert np.all(np.abs(got - out) <= tol)
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -22, 2.0 ** -6])
+@pytest.mark.parametrize("rows", [1, 60])
+def test_lse_of_few_tokens_with_small_scores(gain, rows):
+    """As test_gpu_serving.py has it: 2^-21 of 1 + |lse|, besides the products' error."""
+    rng = np.random.default_rng(rows)
+    kv_len = rng.integers(1, 40, 300).tolist()
+    counts = [rows] + rng.integers(0, rows + 1, 299).tolist()
+    pool = Pool(kv_len, 1, 64, seed=51, spread=0, gain=gain)
+    pool.on_device()
+    q = rng.standard_normal((sum(counts), 1, 64)).astype(np.float16)
+    got, lse = attend(pool, counts, q, 1, 0.125, 0.0, False)
+    want = ref.attention(pool.codes[0], pool.scales[0], pool.codes[1], pool.scales[1], pool.table, kv_len, counts, q, 0.125, 0.0, False)
+    assert np.all(np.abs(lse - want[1]) <= 2.0 ** -21 * (1 + np.abs(want[1]) + want[3]) + (64 + 8) * U * want[3])

@@ -67,7 +67,7 @@ struct StreamParams {
   // the CTA's range, slot 1: one that began in it and goes on after it), and the
   // plan for the join.
   float *part_o;      // CTAs x 2 x rows x D
-  float *part_ml;     // CTAs x 2 x rows x 2 (reference in log2 units, sum)
+  float *part_ml;     // CTAs x 2 x rows x 2 (maximum in log2 units, sum)
   float *first;       // warps x rows x (D + 2): see Parts
   int64_t *plan;      // prefix of build_plan
   int warps;          // of the stream grid
@@ -372,15 +372,14 @@ struct Ring {
   }
 };
 
-// log2 of the probabilities' scale: the reference m of a row is its maximum less this, so
-// that a row's many small probabilities keep their bits in fp16 (one of 2^-28 of the
-// largest still has all 11; fp16 ends 2^-39 below it).
-constexpr float kHeadroom = 14.0f;
+// The probabilities' scale in fp16: a row's many small ones keep their bits (one of
+// 2^-28 of the largest still has all 11; fp16 ends 2^-39 below it).
+constexpr float kHeadroom = 0x1p14f;
 
 template <int D, int NT>
 struct RowState {
-  float o[NT][D / 16][4];  // O^T in units of 2^e_v: d by lane / 4, rows 2 t, 2 t + 1
-  float m[NT][2], l[NT][2];  // reference in log2 units, sum of exp2(score - m)
+  float o[NT][D / 16][4];  // O^T in units of 2^e_v / kHeadroom: d by lane / 4, rows 2 t, 2 t + 1
+  float m[NT][2], l[NT][2];
   int ev;                  // exponent of the value scale that o is in units of
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -396,7 +395,7 @@ struct RowState {
   }
 };
 
-// One unit: scores, running reference and sum, O^T += V^T P^T.
+// One unit: scores, running maximum and sum, O^T += V^T P^T.
 template <int D, int NT, bool CAP>
 __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stage, int pos0, int len, float ks, float vs,
                                             const uint32_t (&qf)[NT][D / 8], const int (&limit)[NT][2], int min_limit,
@@ -434,7 +433,7 @@ __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stag
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      const float now = fmaxf(st.m[n][col], top - kHeadroom);
+      const float now = fmaxf(st.m[n][col], top);
       const float ref = now == -INFINITY ? 0.f : now;
       const float keep = ex2(st.m[n][col] - ref);
       still = still && (keep == 1.0f || st.m[n][col] == -INFINITY);
@@ -451,12 +450,13 @@ __device__ __forceinline__ void attend_unit(const StreamParams &p, uint32_t stag
       st.l[n][col] = st.l[n][col] * keep + sum;
       alpha[n][col] = keep * unit;
     }
-    // fp16 probabilities, 1 to 2^14 for the largest: relative error 2^-12 on average, the size of the result's own rounding
+    // fp16 probabilities times kHeadroom: relative error 2^-12 on average, the size of the result's own rounding
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const __half2 h = __floats2half2_rn(s[n][mi][2 * r], s[n][mi][2 * r + 1]);
+        const float2 scaled = mul2(make_float2(s[n][mi][2 * r], s[n][mi][2 * r + 1]), make_float2(kHeadroom, kHeadroom));
+        const __half2 h = __floats2half2_rn(scaled.x, scaled.y);
         b[n][mi][r] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&h));
       }
   }
@@ -529,7 +529,7 @@ struct Parts {
   using Cfg = StreamCfg<D, NT, false>;
   static constexpr int kWarps = Cfg::kWarps;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kFloats = kRows * (D + 2);  // output, then (reference, sum) of each row
+  static constexpr int kFloats = kRows * (D + 2);  // output, then (maximum, sum) of each row
   static constexpr int kHeads = kWarps * kFloats * 4;
   static_assert(kHeads + 2 * kWarps * (int)sizeof(Part) <= Cfg::kRing, "parts fit the ring");
   uint8_t *smem;
@@ -565,7 +565,7 @@ __device__ __forceinline__ void write_rows(const StreamParams &p, const Cursor &
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int col = 0; col < 2; ++col) {
-      const float l = st.l[n][col], f = l == 0.f ? 0.f : pow2i(st.ev) / l;
+      const float l = st.l[n][col], f = l == 0.f ? 0.f : pow2i(st.ev) / kHeadroom / l;
       const int j = c.rt * 8 * NT + 8 * n + 2 * t + col, i = j / p.group;
       if (i >= c.q.rows) continue;
       float v[D / 8];
@@ -583,7 +583,7 @@ __device__ __forceinline__ void write_rows(const StreamParams &p, const Cursor &
 template <int D, int NT>
 __device__ __forceinline__ void keep_part(float *part_o, float2 *part_ml, int lane, const RowState<D, NT> &st) {
   const int g = lane >> 2, t = lane & 3;
-  const float unit = pow2i(st.ev);
+  const float unit = pow2i(st.ev) / kHeadroom;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -53,8 +53,11 @@ constexpr int kChunkEntry = 3;
 // at most, and the many small probabilities of a long sequence keep their bits (one of
 // 2^-26 of the largest has all 11; fp16 ends 2^-37 below it). 2048 rows over 8192 tokens:
 // 329 us, 327 with 2^7 and 2^15, 324 with 1 and 2^14, where what is below 2^-25 of the
-// largest is lost (65536 tokens there have up to 2^-9 of the weight).
+// largest is lost (65536 tokens there have up to 2^-9 of the weight); 337 with the exact
+// product by 2^12 in place of the sum, which rounds exponents to 2^-21.
 constexpr float kHeadroom = 12.0f, kLazy = 15.75f;
+// With the reference back at the maximum first: a logarithm near 12 would be 2^-20 off.
+__device__ __forceinline__ float row_lse(float ref, float sum) { return log_sum(ref + kHeadroom, sum * 0x1p-12f); }
 
 template <int D>
 struct ChunkCfg {
@@ -615,7 +618,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const Chunk
         }
         if (real && fits) {
           if (!whole) reinterpret_cast<float2 *>(p.part_ml)[slot] = make_float2(ref, sum);
-          else if (p.a.lse) p.a.lse[(int64_t)(g.q.row0 + i) * p.a.n_heads + head] = log_sum(ref, sum);
+          else if (p.a.lse) p.a.lse[(int64_t)(g.q.row0 + i) * p.a.n_heads + head] = row_lse(ref, sum);
         }
         tc_fence_before();  // the output has been read: before the next segment's first products
       }
@@ -730,7 +733,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_chunk_join_kernel(const Chun
 #pragma unroll
         for (int e = 0; e < E; ++e)
           static_cast<__half *>(p.a.out)[off + 32 * e + lane] = __float2half_rn(l[r] == 0.f ? 0.f : o[r][e] / l[r]);
-      if (p.a.lse && lane == 0) p.a.lse[row * p.a.n_heads + head] = log_sum(m[r], l[r]);
+      if (p.a.lse && lane == 0) p.a.lse[row * p.a.n_heads + head] = row_lse(m[r], l[r]);
     }
   }
 }
