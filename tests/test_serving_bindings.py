@@ -140,3 +140,16 @@ def test_logits_look_at_their_tensors(lib):
         for b in bad:
             with pytest.raises(ValueError, match=name):
                 call(**{name: b})
+
+
+def test_empty_lists_are_lists(lib):
+    """No token said yet, no bias on any row: not a rule with parts missing."""
+    torch, _, _ = objects()
+    x, am = torch.zeros((2, 256)), torch.zeros(2, dtype=torch.int32)
+    none, starts = torch.zeros(0, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    goes(lambda: tql.exl3_logits_adjust(x, 250, x, am, history=none, history_start=starts, generated_from=am, presence=torch.ones(2), stream=0))
+    goes(lambda: tql.exl3_logits_adjust(x, 250, x, am, bias_id=none, bias_value=torch.zeros(0), bias_start=starts, stream=0))
+    for kw in (dict(history_start=starts), dict(bias_start=starts), dict(generated_from=am), dict(bias_id=none.new_zeros(1), bias_value=torch.zeros(1))):
+        with pytest.raises(tql.Exl3Error) as e:
+            tql.exl3_logits_adjust(x, 250, x, am, stream=0, **kw)
+        assert e.value.status == 1

@@ -487,6 +487,11 @@ def exl3_logits_adjust(logits, n: int, out, argmax, history=None, history_start=
     i32, f32, M = _I32, _F32, logits.shape[0]
     ldl, ldo = _rows("exl3_logits_adjust: logits", logits, f32, M, n), _rows("exl3_logits_adjust: out", out, f32, M, n)
     n_history, n_bias = 0 if history is None else history.numel(), 0 if bias_id is None else bias_id.numel()
+    # an empty tensor has no address: what belongs to an empty list is left out with it
+    if n_history == 0 and history is not None:
+        history_start = generated_from = None
+    if n_bias == 0 and bias_id is not None:
+        bias_value = bias_start = None
     rules = _PACK_RULES(
         _array("exl3_logits_adjust: history", history, i32, 0),
         _array("exl3_logits_adjust: history_start", history_start, i32, M + 1),
