@@ -381,7 +381,8 @@ exl3_status exl3_linear_decode_noalloc(const void *x, int64_t M, int64_t K, cons
  *
  * Matrices (codes, q, k, v, out, logits) and `weight` are 16-byte aligned;
  * scales, lse and integer arrays by their elements (4 bytes). A NULL or
- * misaligned pointer returns EXL3_ERR_ALIGNMENT.
+ * misaligned pointer returns EXL3_ERR_ALIGNMENT, except in a call without rows
+ * (or, to evict, without sequences), which does nothing and looks at none.
  *
  * The cache holds E4M3 codes in blocks (pages) of 64 tokens. A block holds,
  * for each key/value head, 64 x head_dim codes and ONE scale, a power of two;

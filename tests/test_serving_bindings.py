@@ -153,3 +153,20 @@ def test_empty_lists_are_lists(lib):
         with pytest.raises(tql.Exl3Error) as e:
             tql.exl3_logits_adjust(x, 250, x, am, stream=0, **kw)
         assert e.value.status == 1
+
+
+def test_calls_without_rows_do_nothing(lib):
+    """Also with the tensors of an empty batch, which have no addresses."""
+    torch, cache, _ = objects()
+    i32 = dict(dtype=torch.int32)
+    none = tql.Exl3Kv8Batch(torch.zeros((0, 4), **i32), torch.zeros(0, **i32), torch.zeros(1, **i32), 0, 0)
+    idle = tql.Exl3Kv8Batch(torch.zeros((2, 4), **i32), torch.ones(2, **i32), torch.zeros(3, **i32), 0, 0)
+    x, q, lse = torch.zeros((0, 128)).half(), torch.zeros((0, 256)).half(), torch.zeros((0, 4))
+    for batch in (none, idle):
+        tql.exl3_kv8_append(cache, batch, x, x, stream=0)
+        tql.exl3_kv8_attention(cache, batch, q, 4, 0.1, torch.empty_like(q), torch.zeros(16, dtype=torch.uint8), lse=lse, stream=0)
+        tql.exl3_kv8_weigh(cache, batch, q, 4, 0.1, lse, stream=0)
+        with pytest.raises(tql.Exl3Error):  # shapes are looked at all the same
+            tql.exl3_kv8_weigh(cache, batch, torch.zeros((0, 192)).half(), 3, 0.1, lse, stream=0)
+    tql.exl3_kv8_evict(cache, none, torch.zeros((0, 1), **i32), 64, 0, torch.zeros((0, 2, 64), **i32), torch.zeros(0, **i32), stream=0)
+    tql.exl3_logits_adjust(torch.zeros((0, 256)), 250, torch.zeros((0, 256)), torch.zeros(0, **i32), stream=0)

@@ -25,6 +25,10 @@ bool batch_shape_ok(const exl3_kv8_batch &b) {
          b.rows >= 0 && b.max_rows >= 0 && b.max_rows <= b.rows;
 }
 
+// Nothing to do: a call without rows or sequences is over after its shape checks, and may
+// come with the null pointers that empty tensors have.
+bool no_rows(const exl3_kv8_batch &b) { return b.rows == 0 || b.n_seqs == 0 || b.max_rows == 0; }
+
 // Shape checks come first (they need no pointers), then alignment, then the
 // device, as in every entry point of the library.
 exl3_status validate_kv(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, bool rows, const DeviceInfo **dev,
@@ -64,6 +68,7 @@ exl3_status exl3_kv8_append(const exl3_kv8_cache *cache, const exl3_kv8_batch *b
   if (!cache || !batch || !cache_shape_ok(*cache) || !batch_shape_ok(*batch)) return EXL3_ERR_INVALID_ARG;
   const int64_t width = (int64_t)cache->n_kv_heads * cache->head_dim;
   if (!ld_ok(ldk, width) || !ld_ok(ldv, width)) return EXL3_ERR_INVALID_ARG;
+  if (no_rows(*batch)) return EXL3_OK;
   if (!aligned(k, 16) || !aligned(v, 16)) return EXL3_ERR_ALIGNMENT;
   const DeviceInfo *dev;
   KvView kv;
@@ -88,6 +93,7 @@ exl3_status exl3_kv8_attention(const exl3_kv8_cache *cache, const exl3_kv8_batch
   const int64_t width = (int64_t)n_heads * cache->head_dim;
   if (!ld_ok(ldq, width) || !ld_ok(ldo, width) || !isfinite(scale) || !softcap_ok(softcap))
     return EXL3_ERR_INVALID_ARG;
+  if (no_rows(*batch)) return EXL3_OK;
   if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)) || !aligned(workspace, 16))
     return EXL3_ERR_ALIGNMENT;
   KvAttention p{};
@@ -115,6 +121,7 @@ exl3_status exl3_kv8_weigh(const exl3_kv8_cache *cache, const exl3_kv8_batch *ba
   if (!attention_shape_ok(cache, batch, n_heads)) return EXL3_ERR_INVALID_ARG;
   if (!ld_ok(ldq, (int64_t)n_heads * cache->head_dim) || !isfinite(scale) || !softcap_ok(softcap))
     return EXL3_ERR_INVALID_ARG;
+  if (no_rows(*batch)) return EXL3_OK;
   if (!cache->weight || !aligned(q, 16) || !aligned(lse, 4)) return EXL3_ERR_ALIGNMENT;
   KvAttention p{};
   const DeviceInfo *dev;
@@ -136,6 +143,7 @@ exl3_status exl3_kv8_evict(const exl3_kv8_cache *cache, const exl3_kv8_batch *ba
   if (!cache || !batch || !cache_shape_ok(*cache) || batch->n_seqs < 0 || batch->n_seqs > 65535 || batch->max_pages < 0 ||
       batch->max_pages > INT32_MAX / EXL3_KV8_BLOCK || budget < 1 || budget > (1 << 30) || recent < 0 || recent > budget)
     return EXL3_ERR_INVALID_ARG;
+  if (batch->n_seqs == 0) return EXL3_OK;
   if (!cache->weight || !aligned(dst_pages, 4) || !aligned(kept, 4) || !aligned(new_len, 4)) return EXL3_ERR_ALIGNMENT;
   const DeviceInfo *dev;
   KvView kv;
@@ -156,6 +164,7 @@ exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int6
   if ((r.history == nullptr) != (r.history_start == nullptr) || (r.generated_from && !r.history) ||
       (r.bias_id == nullptr) != (r.bias_value == nullptr) || (r.bias_id == nullptr) != (r.bias_start == nullptr))
     return EXL3_ERR_INVALID_ARG;
+  if (M == 0) return EXL3_OK;
   if (!aligned(logits, 16) || !aligned(out, 16) || !aligned(argmax, 4)) return EXL3_ERR_ALIGNMENT;
   for (const void *p : {(const void *)r.history, (const void *)r.history_start, (const void *)r.generated_from,
                         (const void *)r.repetition, (const void *)r.presence, (const void *)r.frequency,
