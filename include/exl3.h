@@ -466,9 +466,14 @@ exl3_status exl3_kv8_append(const exl3_kv8_cache *cache, const exl3_kv8_batch *b
  *         contents undefined before and after. Calls that share one must be
  *         ordered.
  * Up to 48 rows of a sequence and key/value head (max_rows x heads of a group)
- * go through a kernel bound by reading the cache once, more through one on the
- * tensor cores; both split long sequences over all SMs by the lengths that they
- * find on the device, and the result does not depend on scheduling.
+ * go through a kernel bound by reading the cache, once for each 16 rows; more go
+ * through one for 256 rows at a time. Both split long sequences over all SMs by the
+ * lengths that they find on the device, and the result does not depend on
+ * scheduling. max_rows decides for the whole call: single tokens beside a long
+ * chunk are better served by a call of their own.
+ * With more than 48 rows, keys and values are held relative to the largest scale of
+ * the blocks that are worked on together, in fp16: what is below 2^-25 of that
+ * block's largest value (448 scales) is lost, whether a row sees that block or not.
  */
 size_t exl3_kv8_attention_workspace_bytes(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, int32_t n_heads);
 exl3_status exl3_kv8_attention(const exl3_kv8_cache *cache, const exl3_kv8_batch *batch, const void *q, int64_t ldq,

@@ -164,7 +164,7 @@ struct SoftCap {
   // 1 - 2 / (exp(2 x) + 1), an absolute error near cap * 2^-22, which a direct tanh
   // approximation (relative error 2^-11 of a score near the cap) would not give. exp
   // overflows to inf: tanh is then 1. 2048 rows of 40 heads over 8192 tokens, cap 30:
-  // attention 610 us and weights 410 with the series, 588 and 394 by the exponential alone.
+  // weights 409 us, 394 by the exponential alone; attention 617, and 22 less.
   __device__ __forceinline__ float2 operator()(float2 s) const {
     auto both = [](float v) { return make_float2(v, v); };
     const float2 x = mul2(s, both(inv)), y = mul2(x, x), e = mul2(x, both(2.0f * kLog2e));

@@ -7,12 +7,12 @@
 // range of them; segments that several CTAs share are joined by a second kernel.
 // Per unit:
 //   * warps 9..16 (converters): the unit's keys and values from global memory, one
-//     operand ahead in registers, to fp16 (exact) in the two-stage operand buffers
+//     operand ahead in registers, to fp16 in the two-stage operand buffers
 //     (128-byte swizzle; the same layout serves keys as the K-major operand of
 //     Q K^T and values as the MN-major operand of P V). Each block's scale goes in
 //     as a power of two relative to the largest of the CTA's part of the segment, so
-//     one factor serves all its scores and outputs; only codes 2^15 and more below that
-//     largest block's lose bits, 2^-25 of it at most;
+//     one factor serves all its scores and outputs: exact, but for codes of blocks 2^15
+//     and more below the largest, which lose 2^-25 of its largest code at most;
 //   * warp 8 (one lane): for each tile tcgen05.mma S = Q K^T into TMEM, then, when
 //     the tile's probabilities are there, O += P V with P read from TMEM, where it
 //     has taken the place of S;
@@ -24,8 +24,8 @@
 //     that reference), so rarely after the first units.
 // TMEM: S0 S1 O0 O1, 128 columns each.
 //
-// Measured: 2048 rows of 40 heads on 8 over 8192 cached tokens, D = 128: 323 us (301
-// GFLOP, 930 TFLOP/s, the join 15 to 20 us of it). The softmax binds it: a chain of
+// Measured: 2048 rows of 40 heads on 8 over 8192 cached tokens, D = 128: 329 us (301
+// GFLOP, 915 TFLOP/s, the join 15 to 20 us of it). The softmax binds it: a chain of
 // TMEM reads, maximum, exponentials and TMEM writes per tile and unit, 2 row warps a
 // scheduler; the tensor pipe is busy 42 % of the time. Not bound by the operands: Q
 // from TMEM (half the shared-memory reads of Q K^T) took 321 us of then 326. Slower
@@ -768,8 +768,8 @@ cudaError_t chunk_attention(const KvAttention &a, cudaStream_t st) {
                                       kChunkThreads, ChunkCfg<D>::kSmem, st, 1, p);
     if (e != cudaSuccess) return e;
     // With many rows what a CTA does before its first load counts, so it has more of
-    // them: 10240 rows of 8 heads over 8192 tokens 323 us with 64, 330 with 16; 255 rows
-    // over 777 tokens 34 with 64, 23.4 with 16, over 60000 tokens 130 and 105.
+    // them: 10240 rows of 8 heads over 8192 tokens take 7 us less with 64 than with 16;
+    // 255 rows over 777 tokens 34 with 64, 23.4 with 16, over 60000 tokens 130 and 105.
     const int64_t joins = ceil_div((int64_t)a.kv.max_rows * p.group, kJoinRows) * p.a.kv.n_seqs * a.kv.n_kv_heads;
     p.join_rows = joins > 16 * a.num_sms ? 4 * kJoinRows : kJoinRows;
     // A long sequence's segments are spread over all CTAs: where it has few, and there are

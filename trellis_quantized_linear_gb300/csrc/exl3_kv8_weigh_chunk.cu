@@ -21,7 +21,7 @@
 // whose sums the other CTA's shared memory receives. So sums are formed in a fixed
 // order, and there are twice the pieces to deal out (2048 rows of 40 heads over 8192
 // tokens are 512 items of up to 82 steps for 304 CTAs: 206 us with an item a CTA,
-// 167 us so: 150 GFLOP, 900 TFLOP/s, and 0.6 G exponentials). Bound by a step's chain
+// 170 us so: 150 GFLOP, 885 TFLOP/s, and 0.6 G exponentials). Bound by a step's chain
 // of TMEM read, difference, exponential and sum, which two CTAs of eight warps an SM
 // hide in part: of an earlier 225 us the exponentials themselves were 19 us and the
 // broadcast reads of the lse 42.

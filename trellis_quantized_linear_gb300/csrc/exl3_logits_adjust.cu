@@ -16,7 +16,7 @@
 // (131 MB, 2.4 TB/s). Without rules the stream takes 29 us; the mask adds 4, the biases
 // 6, handing out, counting and penalizing the history 15: latencies that all CTAs meet
 // at the same time, as they are all resident. One row with a history of 700 and 20
-// biases 10.4 us, 5.2 without rules.
+// biases 10.2 us in a graph, 5.2 without rules.
 #include <limits.h>
 
 #include "exl3_internal.h"
