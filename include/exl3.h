@@ -552,7 +552,138 @@ exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int6
                                float *out, int64_t ldo, int32_t *argmax, void *stream);
 
 /*
- * exl3_selftest_bounds, for the translation units of the serving operators.
+ * ---------------------------------------------------------------------------
+ * Step operators: what a serving step does around its projections before the
+ * cache is read. exl3_kv8_plan makes a step's lengths, row ranges, block tables,
+ * positions and slots; exl3_rms_norm stands before a projection; exl3_qk_rotary
+ * between the projection of queries, keys and values and exl3_kv8_append;
+ * exl3_prompt_attention attends over prompts that begin in this step, which have
+ * all their keys and values at hand in fp16.
+ * ---------------------------------------------------------------------------
+ *
+ * exl3_kv8_plan: the step's batch from its requests, on the device.
+ *   batch:      page_table (n_seqs x max_pages), kv_len and q_start are WRITTEN; n_seqs,
+ *               max_pages, rows and max_rows bound the step.
+ *   tokens:     n_seqs int32: the new tokens of each sequence in this step; 0: none;
+ *               negative: the sequence has ended.
+ *   cached:     n_seqs int32: its tokens in the cache before this step, 0 .. 64 * max_pages;
+ *               may be the batch's kv_len. The first ceil(cached / 64) entries of its row of
+ *               page_table are its pages; what lies behind them is not read.
+ *   free_pages: a stack of free_capacity entries, of which the first *free_count are the
+ *               numbers of free pages; the last of them is taken first. free_left receives
+ *               how many are left (one int32; may be free_count).
+ *   First the pages of ended sequences go onto the stack, in the order of the sequences
+ *   and of their blocks; their kv_len becomes 0. Then the sequences are served in their
+ *   order: kv_len = cached + tokens, and the blocks that this needs beyond those that it
+ *   has get pages from the stack, in order of sequence and block. A sequence does not
+ *   fit where pages run out, where the rows of this and the earlier sequences exceed
+ *   batch->rows, or its own batch->max_rows, or cached + tokens exceeds 64 * max_pages.
+ *   From the first one that does not fit on, sequences get no rows and keep kv_len = cached
+ *   (ended ones have ended all the same); *served is the number of sequences before it
+ *   (n_seqs: all).
+ *   q_start:    the rows' ranges, n_seqs + 1.
+ *   position, slot: batch->rows int32. Row r of sequence s stands at position
+ *               kv_len[s] - (q_start[s + 1] - r) and in slot
+ *               64 * page_table[s][position / 64] + position % 64. Rows from
+ *               q_start[n_seqs] on have -1 in both.
+ * A `cached` out of its range is recorded as EXL3_ERR_DEVICE_INDEX: the sequence does not
+ * fit, and its kv_len becomes 0. So is a page number outside 0 .. n_pages - 1 that a row
+ * needs (its slot is -1, and a page so taken from the stack is entered as -1), a
+ * *free_count outside 0 .. free_capacity (it is brought into it), and pages given back
+ * beyond free_capacity (they are dropped).
+ * The other arrays must not overlap. n_pages: 1 .. 2^25 - 1; rows, free_capacity below 2^30.
+ */
+exl3_status exl3_kv8_plan(const exl3_kv8_batch *batch, const int32_t *tokens, const int32_t *cached, int32_t *free_pages,
+                          int32_t free_capacity, const int32_t *free_count, int32_t *free_left, int64_t n_pages,
+                          int32_t *position, int32_t *slot, int32_t *served, void *stream);
+
+/*
+ * exl3_rms_norm: the residual's addition and the root-mean-square norm of each row,
+ *     h = x + residual
+ *     y = h / sqrt(sum h^2 / cols + eps) * (weight + weight_offset)
+ * in fp32 from inputs to outputs, each rounded once: residual_out = h, y in fp16, and
+ * 8-bit codes with a scale for each `group` columns,
+ *     scale = max(max |y| / 448, 2^-40) over the group's finite values, code = E4M3(y / scale),
+ * nearest even, infinities saturating, NaN to NaN.
+ */
+typedef struct {
+    const void *x;         /* rows x cols, x_dtype */
+    const void *residual;  /* rows x cols, residual_dtype; NULL: none */
+    void *residual_out;    /* rows x cols, residual_dtype; NULL: not written (and always without a residual) */
+    const void *weight;    /* cols fp16; NULL: the factor is 1, without the offset */
+    void *y;               /* rows x cols fp16; NULL: not written */
+    void *codes;           /* rows x cols E4M3; NULL, with scales: not written */
+    float *scales;         /* rows x (cols / group) fp32 */
+    int64_t rows, cols;    /* rows >= 0 (below 2^31); cols a multiple of 8, 8 .. 32768 */
+    int64_t ldx, ldr, ldro, ldy, ldc; /* leading dimensions in elements: multiples of 8, at least cols, below 2^31 */
+    int32_t x_dtype, residual_dtype;  /* exl3_dtype */
+    int32_t group;         /* with codes: 32, 64 or 128, which divides cols, or cols itself */
+    float eps, weight_offset;         /* finite, eps >= 0 */
+} exl3_norm;
+/*
+ * At least one of residual_out, y and codes is written. An output may be an input's own
+ * buffer where type and leading dimension are the same; otherwise they must not overlap.
+ * The squares' sum must stay in fp32.
+ */
+exl3_status exl3_rms_norm(const exl3_norm *norm, void *stream);
+
+/*
+ * exl3_qk_rotary: rotates the query and key heads of each row by its position, after a
+ * root-mean-square norm of each head where weights are given. With x a head, after
+ *     x = x / sqrt(sum x^2 / head_dim + eps) * (weight + weight_offset)      (if normed)
+ * its first rot_dim elements turn in pairs i = 0 .. rot_dim / 2 - 1:
+ *     a' = a cos - b sin,  b' = b cos + a sin
+ *     (a, b) = (x[i], x[i + rot_dim / 2]), or (x[2 i], x[2 i + 1]) if interleaved,
+ * and the others stay. fp32, rounded once.
+ *   x, out:   rows x ((q_heads + k_heads) * head_dim) fp16: the query heads, then the key
+ *             heads, as a fused projection gives them; leading dimensions ldx, ldo
+ *             (multiples of 8). out may be x, with ldo = ldx; otherwise they must not overlap.
+ *   position: rows int32, as exl3_kv8_plan gives them: a row with a negative one is neither
+ *             read nor written; one of n_positions or more is recorded as
+ *             EXL3_ERR_DEVICE_INDEX and treated so.
+ *   cos_sin:  n_positions x rot_dim fp32, 16-byte aligned: for each position the cosines
+ *             of the pairs' angles, then their sines. rot_dim: a multiple of 16, 16 .. head_dim.
+ *   q_weight, k_weight: head_dim fp16 each, or both NULL (no norm; with no key heads,
+ *             k_weight may be NULL too).
+ *   head_dim: 64 or 128. q_heads, k_heads: at least 0, together 1 .. 65535.
+ */
+exl3_status exl3_qk_rotary(const void *x, int64_t ldx, void *out, int64_t ldo, int64_t rows, int32_t q_heads,
+                           int32_t k_heads, int32_t head_dim, const int32_t *position, const float *cos_sin,
+                           int64_t n_positions, int32_t rot_dim, int interleaved, const void *q_weight,
+                           const void *k_weight, float eps, float weight_offset, void *stream);
+
+/*
+ * exl3_prompt_attention: attention of each row over the rows of its own sequence,
+ *     s[t] = scale * sum_d q[d] k[t][d];  s = softcap * tanh(s / softcap) if softcap > 0
+ *     out  = sum_t softmax(s)[t] v[t]
+ * over the rows t of the sequence up to its own (causal != 0) or all of them. Sequences
+ * lie one behind the other: rows q_start[s] .. q_start[s + 1] - 1 (n_seqs + 1 int32 on the
+ * device, 0 <= q_start, not decreasing, at most rows).
+ *   q, out:  rows x (n_heads * head_dim) fp16, leading dimensions ldq, ldo.
+ *   k, v:    rows x (n_kv_heads * head_dim) fp16, leading dimensions ldk, ldv. All
+ *            leading dimensions are multiples of 8: column ranges of one fused
+ *            projection's output will do. Query head h reads key/value head
+ *            h / (n_heads / n_kv_heads), at most 128 query heads one of them.
+ *   lse:     rows x n_heads fp32, log sum_t exp(s[t]); or NULL.
+ * Rows of no sequence are left as they are in out and lse, and whatever they hold in q, k
+ * and v reaches no other row; so it is with the rows that a row does not see, infinities and
+ * NaN among them. A row that sees an infinity or NaN in v gets it in that column (or NaN).
+ * A sequence whose range is not in the rows is recorded as EXL3_ERR_DEVICE_INDEX and
+ * left out.
+ * Sums, maxima and the softmax are fp32; the probabilities enter the product with the
+ * values as fp16, scaled so that one of 2^-26 of a row's largest has all its 11 bits and
+ * one of 2^-37 still counts. The result does not depend on scheduling.
+ *   head_dim: 64 or 128; scale: finite; softcap: 0 (off) or finite and at least 1e-30 (a
+ *   capped score has an error of 2^-19 of itself at most, besides that of the products);
+ *   n_seqs: 0 .. 65535; rows * n_heads below 2^31. out must not overlap q, k or v.
+ */
+exl3_status exl3_prompt_attention(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                  int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, const int32_t *q_start,
+                                  int32_t n_seqs, int64_t rows, float scale, float softcap, int causal, void *out,
+                                  int64_t ldo, float *lse, void *stream);
+
+/*
+ * exl3_selftest_bounds, for the translation units of the serving and step operators.
  */
 exl3_status exl3_selftest_bounds_serving(int *units_reported, int *units_total, void *stream);
 

@@ -28,7 +28,8 @@ __all__ = [
     "exl3_weight_rotated_workspace_bytes", "exl3_linear_weight_rotated", "exl3_bounds_checked",
     "exl3_selftest_bounds", "EXL3_KV8_BLOCK", "Exl3Kv8Cache", "Exl3Kv8Batch", "exl3_kv8_append",
     "exl3_kv8_attention_workspace_bytes", "exl3_kv8_attention", "exl3_kv8_weigh", "exl3_kv8_evict",
-    "exl3_logits_adjust", "exl3_selftest_bounds_serving", "HEADER_SYMBOLS", "BOUNDS_CHECKED",
+    "exl3_logits_adjust", "exl3_kv8_plan", "exl3_rms_norm", "exl3_qk_rotary", "exl3_prompt_attention",
+    "exl3_selftest_bounds_serving", "HEADER_SYMBOLS", "BOUNDS_CHECKED",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -59,7 +60,8 @@ HEADER_SYMBOLS = (
     "exl3_linear_decode_noalloc", "exl3_silu_mul", "exl3_reconstruct_rotated",
     "exl3_weight_rotated_workspace_bytes", "exl3_linear_weight_rotated", "exl3_bounds_checked",
     "exl3_selftest_bounds", "exl3_kv8_append", "exl3_kv8_attention_workspace_bytes", "exl3_kv8_attention",
-    "exl3_kv8_weigh", "exl3_kv8_evict", "exl3_logits_adjust", "exl3_selftest_bounds_serving",
+    "exl3_kv8_weigh", "exl3_kv8_evict", "exl3_logits_adjust", "exl3_kv8_plan", "exl3_rms_norm", "exl3_qk_rotary",
+    "exl3_prompt_attention", "exl3_selftest_bounds_serving",
 )
 
 
@@ -127,6 +129,15 @@ class _LogitsRules(ctypes.Structure):
 _PACK_RULES = struct.Struct("@10P2i").pack  # a _LogitsRules' bytes, in a quarter of the time
 
 
+class _Norm(ctypes.Structure):
+    _fields_ = [("x", _vp), ("residual", _vp), ("residual_out", _vp), ("weight", _vp), ("y", _vp), ("codes", _vp), ("scales", _vp),
+                ("rows", _i64), ("cols", _i64), ("ldx", _i64), ("ldr", _i64), ("ldro", _i64), ("ldy", _i64), ("ldc", _i64),
+                ("x_dtype", _i32), ("residual_dtype", _i32), ("group", _i32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+_PACK_NORM = struct.Struct("@7P7q3i2f4x").pack  # the same of a _Norm
+
+
 def _require_f32_contiguous(where, *tensors):
     for t in tensors:
         if t is not None and (t.element_size() != 4 or not t.is_floating_point() or not t.is_contiguous()):
@@ -190,6 +201,12 @@ def load():
                                               _vp, _vp]),
             "exl3_kv8_evict": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp]),
             "exl3_logits_adjust": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp]),
+            "exl3_kv8_plan": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+            "exl3_rms_norm": (ctypes.c_int, [_vp, _vp]),
+            "exl3_qk_rotary": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _i32, ctypes.c_int, _vp, _vp,
+                                              ctypes.c_float, ctypes.c_float, _vp]),
+            "exl3_prompt_attention": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _i32, _i64, ctypes.c_float,
+                                                     ctypes.c_float, ctypes.c_int, _vp, _i64, _vp, _vp]),
             "exl3_selftest_bounds_serving": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int),
                                                             ctypes.POINTER(ctypes.c_int), _vp]),
         }
@@ -509,8 +526,119 @@ def exl3_logits_adjust(logits, n: int, out, argmax, history=None, history_start=
         raise Exl3Error(status, "exl3_logits_adjust")
 
 
+def exl3_kv8_plan(batch: Exl3Kv8Batch, tokens, cached, free_pages, free_count, free_left, n_pages: int, position, slot, served,
+                  stream=None) -> None:
+    """A step's lengths, row ranges and block table (batch.kv_len, q_start and
+    page_table are written), positions and slots (int32, batch.rows each) from the
+    new tokens (int32, n_seqs; negative: ended) and cached tokens (int32, n_seqs;
+    may be kv_len) of each sequence, with pages from the stack free_pages (int32),
+    of which the first free_count (int32, 1) are free; free_left (int32, 1; may be
+    free_count) and served (int32, 1) say how many are left and how many sequences
+    fit."""
+    lib = _lib or load()
+    if _F16 is None:
+        _need_dtypes()
+    i32, n, rows = _I32, batch.n_seqs, batch.rows
+    if not batch.q_start:
+        raise ValueError("exl3_kv8_plan: the batch has no q_start")
+    status = lib.exl3_kv8_plan(
+        batch._ref, _array("exl3_kv8_plan: tokens", tokens, i32, n), _array("exl3_kv8_plan: cached", cached, i32, n),
+        _array("exl3_kv8_plan: free_pages", free_pages, i32, 0), free_pages.numel(), _array("exl3_kv8_plan: free_count", free_count, i32, 1),
+        _array("exl3_kv8_plan: free_left", free_left, i32, 1), n_pages, _array("exl3_kv8_plan: position", position, i32, rows),
+        _array("exl3_kv8_plan: slot", slot, i32, rows), _array("exl3_kv8_plan: served", served, i32, 1), _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_kv8_plan")
+
+
+def _norm_rows(what, t, rows, cols):
+    """Type and row stride of t, rows x cols of fp16 or fp32."""
+    dtype = t.dtype
+    if dtype is not _F32:
+        dtype = _F16
+    return EXL3_F32 if dtype is _F32 else EXL3_F16, _rows(what, t, dtype, rows, cols)
+
+
+def exl3_rms_norm(x, y=None, weight=None, residual=None, residual_out=None, eps: float = 1e-6, weight_offset: float = 0.0, codes=None,
+                  scales=None, stream=None) -> None:
+    """Root-mean-square norm of x + residual (rows x cols, fp16 or fp32 each, any row
+    stride) times weight (fp16, cols) + weight_offset: the sum into residual_out
+    (residual's type), the norm into y (fp16) and, as E4M3 with one scale for each
+    cols / scales.shape[1] columns, into codes (torch.float8_e4m3fn or uint8) and
+    scales (fp32, rows x groups)."""
+    lib = _lib or load()
+    f16 = _F16 or _need_dtypes()
+    rows, cols = x.shape
+    x_type, ldx = _norm_rows("exl3_rms_norm: x", x, rows, cols)
+    r = ro = py = pc = ps = 0
+    r_type = ldr = ldro = ldy = ldc = group = 0
+    if residual is not None:
+        r_type, ldr = _norm_rows("exl3_rms_norm: residual", residual, rows, cols)
+        r = residual.data_ptr()
+        if residual_out is not None:
+            ro, ldro = residual_out.data_ptr(), _rows("exl3_rms_norm: residual_out", residual_out, residual.dtype, rows, cols)
+    elif residual_out is not None:
+        raise ValueError("exl3_rms_norm: residual_out without a residual")
+    if y is not None:
+        py, ldy = y.data_ptr(), _rows("exl3_rms_norm: y", y, f16, rows, cols)
+    if (codes is None) != (scales is None):
+        raise ValueError("exl3_rms_norm: codes and scales go together")
+    if codes is not None:
+        if codes.element_size() != 1 or scales.dim() != 2 or scales.shape[1] < 1 or cols % scales.shape[1]:
+            raise ValueError("exl3_rms_norm: codes are one byte an element, scales rows x groups with cols a multiple of the groups")
+        group = cols // scales.shape[1]
+        pc, ldc = codes.data_ptr(), _rows("exl3_rms_norm: codes", codes, codes.dtype, rows, cols)
+        ps = _array("exl3_rms_norm: scales", scales, _F32, rows * scales.shape[1])
+    status = lib.exl3_rms_norm(_PACK_NORM(x.data_ptr(), r, ro, _array("exl3_rms_norm: weight", weight, f16, cols), py, pc, ps, rows, cols,
+                                          ldx, ldr, ldro, ldy, ldc, x_type, r_type, group, eps, weight_offset), _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_rms_norm")
+
+
+def exl3_qk_rotary(x, out, q_heads: int, k_heads: int, head_dim: int, position, cos_sin, interleaved: bool = False, q_weight=None,
+                   k_weight=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None) -> None:
+    """Rotates the query and key heads in the first columns of x (fp16, any row
+    stride) by their rows' positions (int32) into out (may be x), after a norm of each
+    head where q_weight and k_weight (fp16, head_dim) are given; cos_sin (fp32,
+    positions x rot_dim) holds the cosines, then the sines of each position's angles."""
+    lib = _lib or load()
+    f16 = _F16 or _need_dtypes()
+    rows, cols = x.shape[0], (q_heads + k_heads) * head_dim
+    ldx, ldo = _rows("exl3_qk_rotary: x", x, f16, rows, cols), _rows("exl3_qk_rotary: out", out, f16, rows, cols)
+    if cos_sin.dim() != 2:
+        raise ValueError("exl3_qk_rotary: cos_sin is positions x rot_dim")
+    n_positions, rot_dim = cos_sin.shape
+    status = lib.exl3_qk_rotary(
+        x.data_ptr(), ldx, out.data_ptr(), ldo, rows, q_heads, k_heads, head_dim, _array("exl3_qk_rotary: position", position, _I32, rows),
+        _array("exl3_qk_rotary: cos_sin", cos_sin, _F32, n_positions * rot_dim), n_positions, rot_dim, interleaved,
+        _array("exl3_qk_rotary: q_weight", q_weight, f16, head_dim), _array("exl3_qk_rotary: k_weight", k_weight, f16, head_dim), eps,
+        weight_offset, _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_qk_rotary")
+
+
+def exl3_prompt_attention(q, k, v, n_heads: int, n_kv_heads: int, head_dim: int, q_start, scale: float, out, softcap: float = 0.0,
+                          causal: bool = True, lse=None, stream=None) -> None:
+    """Attention of each row of q over its own sequence's rows of k and v (fp16, rows x
+    heads * head_dim, any row stride) into out; sequence s has the rows q_start[s] ..
+    q_start[s + 1] - 1 (int32, on the device); lse: rows x n_heads fp32 or None."""
+    lib = _lib or load()
+    f16 = _F16 or _need_dtypes()
+    rows, width, kv_width = q.shape[0], n_heads * head_dim, n_kv_heads * head_dim
+    n_seqs = q_start.numel() - 1
+    if n_seqs < 0:
+        raise ValueError("exl3_prompt_attention: q_start has n_seqs + 1 entries")
+    status = lib.exl3_prompt_attention(
+        q.data_ptr(), _rows("exl3_prompt_attention: q", q, f16, rows, width), k.data_ptr(),
+        _rows("exl3_prompt_attention: k", k, f16, rows, kv_width), v.data_ptr(), _rows("exl3_prompt_attention: v", v, f16, rows, kv_width),
+        n_heads, n_kv_heads, head_dim, _array("exl3_prompt_attention: q_start", q_start, _I32, n_seqs + 1), n_seqs, rows, scale, softcap,
+        causal, out.data_ptr(), _rows("exl3_prompt_attention: out", out, f16, rows, width),
+        _array("exl3_prompt_attention: lse", lse, _F32, rows * n_heads), _stream(stream))
+    if status:
+        raise Exl3Error(status, "exl3_prompt_attention")
+
+
 def exl3_selftest_bounds_serving(stream=None) -> tuple[int, int]:
-    """exl3_selftest_bounds for the serving operators' translation units."""
+    """exl3_selftest_bounds for the serving and step operators' translation units."""
     rep, tot = ctypes.c_int(0), ctypes.c_int(0)
     _check(load().exl3_selftest_bounds_serving(ctypes.byref(rep), ctypes.byref(tot), _stream(stream)),
            "exl3_selftest_bounds_serving")

@@ -1,0 +1,164 @@
+// Norm and rotation of query and key heads. Formulas in include/exl3.h.
+//
+// A thread has 16 elements of a head, in two pieces of 8 that hold both partners of its
+// 8 pairs, and the angles of those pairs in registers for all heads that it works on: a
+// row's table entry is read once a CTA. Bound by the bytes.
+#include "exl3_internal.h"
+#include "exl3_kv8.cuh"
+
+namespace exl3 {
+
+namespace {
+
+constexpr int kRotaryThreads = 128;
+
+struct Piece {
+  float v[8];
+  __device__ __forceinline__ void load(const __half *p) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  __device__ __forceinline__ void store(__half *p) const {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      x[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+};
+
+// D / 16 lanes a head; blockIdx.y takes its share of the heads. `each`: heads of a CTA.
+template <int D, bool INTERLEAVED, bool NORM>
+__global__ void __launch_bounds__(kRotaryThreads) qk_rotary_kernel(const QkRotary p, int each) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kLanes = D / 16, kAtOnce = kRotaryThreads / kLanes;
+  const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
+  const int heads = p.q_heads + p.k_heads, h0 = blockIdx.y * each, h1 = min(h0 + each, heads);
+  const bool turns = 16 * l < p.rot_dim;
+  // first elements of the two pieces
+  const int a0 = INTERLEAVED || !turns ? 16 * l : 8 * l;
+  const int b0 = INTERLEAVED || !turns ? 16 * l + 8 : p.rot_dim / 2 + 8 * l;
+  [[maybe_unused]] const int64_t size_x = (int64_t)(p.rows - 1) * p.ldx + (int64_t)heads * D, size_o = (int64_t)(p.rows - 1) * p.ldo + (int64_t)heads * D;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int pos = p.position[row];
+    if (pos < 0) continue;
+    if (pos >= p.n_positions) {
+      if (threadIdx.x == 0) report_index(p.status);
+      continue;
+    }
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
+    if (turns) {
+      const int64_t at = (int64_t)pos * p.rot_dim + 8 * l;
+      if (EXL3_SPAN(at, p.rot_dim / 2 + 8, (int64_t)p.n_positions * p.rot_dim)) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 c = *reinterpret_cast<const float4 *>(p.cos_sin + at + e);
+          const float4 s = *reinterpret_cast<const float4 *>(p.cos_sin + at + p.rot_dim / 2 + e);
+          cs[e] = c.x, cs[e + 1] = c.y, cs[e + 2] = c.z, cs[e + 3] = c.w;
+          sn[e] = s.x, sn[e + 1] = s.y, sn[e + 2] = s.z, sn[e + 3] = s.w;
+        }
+      }
+    }
+    // all lanes of a warp go round as often as each other: the norm's shuffles
+    for (int first = h0; first < h1; first += kAtOnce) {
+      const int h = first + slot;
+      const int64_t from = row * p.ldx + (int64_t)h * D, to = row * p.ldo + (int64_t)h * D;
+      const bool there = h < h1 && EXL3_SPAN(from, D, size_x) && EXL3_SPAN(to, D, size_o);
+      Piece a, b;
+      if (there) {
+        a.load(static_cast<const __half *>(p.x) + from + a0);
+        b.load(static_cast<const __half *>(p.x) + from + b0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a.v[e] = b.v[e] = 0.f;
+      }
+      if constexpr (NORM) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(a.v[e], a.v[e], fmaf(b.v[e], b.v[e], sum));
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float r = rsqrtf(sum / (float)D + p.eps);
+        if (there) {
+          const __half *w = static_cast<const __half *>(h < p.q_heads ? p.q_weight : p.k_weight);
+          Piece wa, wb;
+          wa.load(w + a0);
+          wb.load(w + b0);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            a.v[e] *= r * (wa.v[e] + p.weight_offset);
+            b.v[e] *= r * (wb.v[e] + p.weight_offset);
+          }
+        }
+      }
+      if (!there) continue;
+      Piece oa, ob;
+      if constexpr (INTERLEAVED) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          oa.v[2 * e] = a.v[2 * e] * cs[e] - a.v[2 * e + 1] * sn[e];
+          oa.v[2 * e + 1] = a.v[2 * e + 1] * cs[e] + a.v[2 * e] * sn[e];
+          ob.v[2 * e] = b.v[2 * e] * cs[4 + e] - b.v[2 * e + 1] * sn[4 + e];
+          ob.v[2 * e + 1] = b.v[2 * e + 1] * cs[4 + e] + b.v[2 * e] * sn[4 + e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          oa.v[e] = a.v[e] * cs[e] - b.v[e] * sn[e];
+          ob.v[e] = b.v[e] * cs[e] + a.v[e] * sn[e];
+        }
+      }
+      // not rotated: as they are, also infinities and NaN, which 0 times would spread
+      (turns ? oa : a).store(static_cast<__half *>(p.out) + to + a0);
+      (turns ? ob : b).store(static_cast<__half *>(p.out) + to + b0);
+    }
+  }
+}
+
+template <int D, bool INTERLEAVED>
+cudaError_t rotary(const QkRotary &p, int num_sms, cudaStream_t st) {
+  constexpr int kAtOnce = kRotaryThreads * 16 / D;
+  const int heads = p.q_heads + p.k_heads;
+  // few rows: the heads of a row are shared by CTAs, which finish at once
+  const bool few = p.rows < 4 * num_sms;
+  const int each = few ? kAtOnce : heads;
+  const int64_t most = (int64_t)num_sms * (2048 / kRotaryThreads);
+  const dim3 grid((unsigned)(p.rows < most ? p.rows : most), (unsigned)ceil_div(heads, each));
+  return launch_overlapped(p.q_weight || p.k_weight ? qk_rotary_kernel<D, INTERLEAVED, true> : qk_rotary_kernel<D, INTERLEAVED, false>, grid,
+                           kRotaryThreads, 0, st, 1, p, each);
+}
+
+}  // namespace
+
+cudaError_t launch_qk_rotary(const QkRotary &p, int num_sms, cudaStream_t st) {
+  if (p.interleaved) return p.head_dim == 64 ? rotary<64, true>(p, num_sms, st) : rotary<128, true>(p, num_sms, st);
+  return p.head_dim == 64 ? rotary<64, false>(p, num_sms, st) : rotary<128, false>(p, num_sms, st);
+}
+
+cudaError_t init_qk_rotary_kernels(int *status) {
+  cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
+  cudaFuncAttributes attr;
+  for (const void *f : {(const void *)qk_rotary_kernel<64, false, false>, (const void *)qk_rotary_kernel<64, false, true>,
+                        (const void *)qk_rotary_kernel<64, true, false>, (const void *)qk_rotary_kernel<64, true, true>,
+                        (const void *)qk_rotary_kernel<128, false, false>, (const void *)qk_rotary_kernel<128, false, true>,
+                        (const void *)qk_rotary_kernel<128, true, false>, (const void *)qk_rotary_kernel<128, true, true>})
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, f);
+  return e;
+}
+
+#if EXL3_DEBUG_BOUNDS
+cudaError_t bounds_probe_qk_rotary(cudaStream_t st) { return launch_bounds_probe(st); }
+#endif
+
+}  // namespace exl3

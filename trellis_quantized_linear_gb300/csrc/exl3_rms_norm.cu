@@ -1,0 +1,262 @@
+// Root-mean-square norm with the residual's addition, fp16 or 8-bit output. Formulas in
+// include/exl3.h.
+//
+// A row stays in registers from its one load to its stores: 8 elements a thread and
+// piece, the sum of squares by shuffles and, where a row has more than a warp, one
+// exchange through shared memory. Bound by the bytes.
+#include <math.h>
+
+#include <type_traits>
+
+#include "exl3_internal.h"
+#include "exl3_kv8.cuh"
+
+namespace exl3 {
+
+namespace {
+
+constexpr float kCodeMax = 448.0f, kLeastScale = 0x1p-40f;
+
+struct Eight {
+  float v[8];
+  __device__ __forceinline__ void load(const __half *p) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  __device__ __forceinline__ void load(const float *p) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void store(__half *p) const {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      x[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  __device__ __forceinline__ void store(float *p) const {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+
+// Sum (or maximum) over the row's threads: `lanes` of a warp, or the whole CTA.
+template <bool CTA_ROW, bool MAX>
+__device__ __forceinline__ float over_row(float x, int lanes, float *scratch) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+  if constexpr (!CTA_ROW) {
+    for (int d = lanes >> 1; d > 0; d >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+  } else {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, d));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) scratch[warp] = x;
+    __syncthreads();
+    x = lane < warps ? scratch[lane] : 0.f;  // 0: of sums of squares and of magnitudes
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+  }
+}
+
+// X, R: types of x and of the residual (void: none). V: pieces of 8 elements a thread.
+template <typename X, typename R, int V, bool CTA_ROW>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const exl3_norm p, int lanes) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float scratch[3][32];
+  constexpr bool kResidual = !std::is_void<R>::value;
+  using Rt = typename std::conditional<kResidual, R, float>::type;
+  const int per_row = CTA_ROW ? (int)blockDim.x : lanes, at = threadIdx.x % per_row;
+  const int rows_at_once = CTA_ROW ? 1 : (int)blockDim.x / lanes;
+  const int pieces = (int)(p.cols >> 3);
+  Eight w[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * per_row + at;
+    if (p.weight && c < pieces && EXL3_SPAN(c * 8, 8, p.cols)) {
+      w[i].load(static_cast<const __half *>(p.weight) + c * 8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[i].v[e] += p.weight_offset;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[i].v[e] = 1.f;
+    }
+  }
+  int turn = 0;  // sums alternate between two buffers, so that one barrier a row is enough
+  // every lane of a warp stays to the end: rows past the last are nobody's, but their lanes take part in the shuffles
+  for (int64_t first = (int64_t)blockIdx.x * rows_at_once; first < p.rows; first += (int64_t)gridDim.x * rows_at_once, turn ^= 1) {
+    const int64_t row = first + (CTA_ROW ? 0 : threadIdx.x / per_row);
+    Eight h[V];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = i * per_row + at;
+      const bool there = row < p.rows && c < pieces;
+      if (there && EXL3_SPAN(row * p.ldx + c * 8, 8, (p.rows - 1) * p.ldx + p.cols)) {
+        h[i].load(static_cast<const X *>(p.x) + row * p.ldx + c * 8);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i].v[e] = 0.f;
+      }
+      if constexpr (kResidual) {
+        if (there && EXL3_SPAN(row * p.ldr + c * 8, 8, (p.rows - 1) * p.ldr + p.cols)) {
+          Eight r;
+          r.load(static_cast<const Rt *>(p.residual) + row * p.ldr + c * 8);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[i].v[e] += r.v[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = fmaf(h[i].v[e], h[i].v[e], s);
+      sum += s;
+    }
+    if constexpr (kResidual) {
+      if (p.residual_out) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int c = i * per_row + at;
+          if (row < p.rows && c < pieces && EXL3_SPAN(row * p.ldro + c * 8, 8, (p.rows - 1) * p.ldro + p.cols))
+            h[i].store(static_cast<Rt *>(p.residual_out) + row * p.ldro + c * 8);
+        }
+      }
+    }
+    sum = over_row<CTA_ROW, false>(sum, lanes, scratch[turn]);
+    const float r = rsqrtf(sum / (float)p.cols + p.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i].v[e] *= w[i].v[e];
+    if (p.codes) {
+      // the row's factor cancels in y / (max |y| / 448): codes are of h * w times 448 / max |h * w|
+      float most[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        most[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = fabsf(h[i].v[e]);
+          most[i] = fmaxf(most[i], a <= 3.402823466e38f ? a : 0.f);
+        }
+      }
+      const bool whole = p.group == p.cols;
+      if (whole) {
+        float m = most[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) m = fmaxf(m, most[i]);
+        m = over_row<CTA_ROW, true>(m, lanes, scratch[2]);
+        if constexpr (CTA_ROW) __syncthreads();  // its buffer is used by every row
+#pragma unroll
+        for (int i = 0; i < V; ++i) most[i] = m;
+      } else {
+        for (int d = p.group >> 4; d > 0; d >>= 1)
+#pragma unroll
+          for (int i = 0; i < V; ++i) most[i] = fmaxf(most[i], __shfl_xor_sync(0xffffffffu, most[i], d));
+      }
+      const int groups = (int)(p.cols / p.group);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = i * per_row + at;
+        if (row >= p.rows || c >= pieces) continue;
+        const float raw = most[i] * r / kCodeMax;
+        const bool least = !(raw >= kLeastScale);
+        const float f = least ? r / kLeastScale : kCodeMax / most[i];
+        const int64_t to = row * groups + (whole ? 0 : c * 8 / p.group);
+        if ((c * 8) % p.group == 0 && EXL3_SPAN(to, 1, p.rows * groups)) p.scales[to] = least ? kLeastScale : raw;
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = to_e4m3x2(h[i].v[2 * e] * f, h[i].v[2 * e + 1] * f);
+        if (EXL3_SPAN(row * p.ldc + c * 8, 8, (p.rows - 1) * p.ldc + p.cols))
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.codes) + row * p.ldc + c * 8) =
+              make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+      }
+    }
+    if (p.y) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = i * per_row + at;
+        if (row >= p.rows || c >= pieces) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i].v[e] *= r;
+        if (EXL3_SPAN(row * p.ldy + c * 8, 8, (p.rows - 1) * p.ldy + p.cols))
+          h[i].store(static_cast<__half *>(p.y) + row * p.ldy + c * 8);
+      }
+    }
+  }
+}
+
+template <typename X, typename R, int V, bool CTA_ROW>
+cudaError_t launch(const exl3_norm &p, int threads, int lanes, int num_sms, cudaStream_t st) {
+  const int64_t ctas = CTA_ROW ? p.rows : ceil_div(p.rows, threads / lanes);
+  const int64_t most = (int64_t)num_sms * (2048 / threads);
+  return launch_overlapped(rms_norm_kernel<X, R, V, CTA_ROW>, dim3((unsigned)(ctas < most ? ctas : most)), threads, 0, st, 1, p, lanes);
+}
+
+template <typename X, typename R>
+cudaError_t by_size(const exl3_norm &p, int num_sms, cudaStream_t st) {
+  const int pieces = (int)(p.cols / 8);
+  if (pieces <= 128) {  // a row is a warp's, or a part's
+    int lanes = 16;
+    while (lanes < 32 && lanes < pieces) lanes *= 2;
+    if (pieces <= 32) return launch<X, R, 1, false>(p, 256, lanes, num_sms, st);
+    return pieces <= 64 ? launch<X, R, 2, false>(p, 256, lanes, num_sms, st) : launch<X, R, 4, false>(p, 256, lanes, num_sms, st);
+  }
+  const int most = p.rows <= num_sms ? 1024 : 512;
+  auto threads = [&](int v) { return (int)(ceil_div(ceil_div(pieces, v), 32) * 32); };
+  if (threads(1) <= most) return launch<X, R, 1, true>(p, threads(1), 32, num_sms, st);
+  if (threads(2) <= most) return launch<X, R, 2, true>(p, threads(2), 32, num_sms, st);
+  return launch<X, R, 4, true>(p, threads(4), 32, num_sms, st);
+}
+
+template <typename X>
+cudaError_t by_residual(const exl3_norm &p, int num_sms, cudaStream_t st) {
+  if (!p.residual) return by_size<X, void>(p, num_sms, st);
+  return p.residual_dtype == EXL3_F32 ? by_size<X, float>(p, num_sms, st) : by_size<X, __half>(p, num_sms, st);
+}
+
+template <typename X, typename R>
+cudaError_t load_kernels() {
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaSuccess;
+  for (const void *f : {(const void *)rms_norm_kernel<X, R, 1, false>, (const void *)rms_norm_kernel<X, R, 2, false>,
+                        (const void *)rms_norm_kernel<X, R, 4, false>, (const void *)rms_norm_kernel<X, R, 1, true>,
+                        (const void *)rms_norm_kernel<X, R, 2, true>, (const void *)rms_norm_kernel<X, R, 4, true>})
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, f);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const exl3_norm &p, int num_sms, cudaStream_t st) {
+  return p.x_dtype == EXL3_F32 ? by_residual<float>(p, num_sms, st) : by_residual<__half>(p, num_sms, st);
+}
+
+cudaError_t init_rms_norm_kernels(int *status) {
+  cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
+  if (e == cudaSuccess) e = load_kernels<__half, void>();
+  if (e == cudaSuccess) e = load_kernels<__half, __half>();
+  if (e == cudaSuccess) e = load_kernels<__half, float>();
+  if (e == cudaSuccess) e = load_kernels<float, void>();
+  if (e == cudaSuccess) e = load_kernels<float, __half>();
+  if (e == cudaSuccess) e = load_kernels<float, float>();
+  return e;
+}
+
+#if EXL3_DEBUG_BOUNDS
+cudaError_t bounds_probe_rms_norm(cudaStream_t st) { return launch_bounds_probe(st); }
+#endif
+
+}  // namespace exl3

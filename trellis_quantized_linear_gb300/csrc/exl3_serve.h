@@ -66,7 +66,52 @@ cudaError_t launch_kv8_weigh_chunk(const KvAttention &p, cudaStream_t st);
 cudaError_t launch_logits_adjust(const float *logits, int64_t ldl, int64_t M, int64_t n, const exl3_logits_rules &r,
                                  float *out, int64_t ldo, int32_t *argmax, int *status, int num_sms, cudaStream_t st);
 
+// What a step does around its projections (exl3_step_api.cu).
+struct PromptAttention {
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  int n_heads, n_kv_heads, head_dim;
+  const int32_t *q_start;
+  int n_seqs, rows;
+  float scale, softcap;
+  int causal;
+  void *out;
+  int64_t ldo;
+  float *lse;
+  int *status;
+};
+struct KvPlan {
+  const int32_t *tokens, *cached, *free_count;
+  int32_t *page_table, *kv_len, *q_start, *free_pages, *free_left, *position, *slot, *served;
+  int n_seqs, max_pages, rows, max_rows, free_capacity, n_pages;
+  int *status;
+};
+struct QkRotary {
+  const void *x;
+  void *out;
+  int64_t ldx, ldo;
+  int rows, q_heads, k_heads, head_dim;
+  const int32_t *position;
+  const float *cos_sin;
+  int n_positions, rot_dim, interleaved;
+  const void *q_weight, *k_weight;
+  float eps, weight_offset;
+  int *status;
+};
+cudaError_t init_prompt_attention_kernels(int *status);
+cudaError_t init_kv8_plan_kernels(int *status);
+cudaError_t init_rms_norm_kernels(int *status);
+cudaError_t init_qk_rotary_kernels(int *status);
+cudaError_t launch_prompt_attention(const PromptAttention &p, int num_sms, cudaStream_t st);
+cudaError_t launch_kv8_plan(const KvPlan &p, cudaStream_t st);
+cudaError_t launch_rms_norm(const exl3_norm &p, int num_sms, cudaStream_t st);
+cudaError_t launch_qk_rotary(const QkRotary &p, int num_sms, cudaStream_t st);
+
 #if EXL3_DEBUG_BOUNDS
+cudaError_t bounds_probe_prompt_attention(cudaStream_t st);
+cudaError_t bounds_probe_kv8_plan(cudaStream_t st);
+cudaError_t bounds_probe_rms_norm(cudaStream_t st);
+cudaError_t bounds_probe_qk_rotary(cudaStream_t st);
 cudaError_t bounds_probe_kv8_cache(cudaStream_t st);
 cudaError_t bounds_probe_kv8_attention(cudaStream_t st);
 cudaError_t bounds_probe_kv8_chunk(cudaStream_t st);

@@ -187,7 +187,8 @@ exl3_status exl3_selftest_bounds_serving(int *units_reported, int *units_total, 
   if (pending != EXL3_OK) return pending;
   cudaError_t (*const probes[])(cudaStream_t) = {bounds_probe_kv8_cache, bounds_probe_kv8_attention, bounds_probe_kv8_chunk,
                                                  bounds_probe_kv8_weigh_chunk,
-                                                 bounds_probe_logits_adjust};
+                                                 bounds_probe_logits_adjust, bounds_probe_kv8_plan, bounds_probe_rms_norm,
+                                                 bounds_probe_qk_rotary, bounds_probe_prompt_attention};
   for (auto *probe : probes) {
     ++*units_total;
     if (probe(static_cast<cudaStream_t>(stream)) != cudaSuccess) return EXL3_ERR_CUDA;
