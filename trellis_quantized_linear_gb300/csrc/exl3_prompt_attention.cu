@@ -5,22 +5,31 @@
 // 128 rows: floor(128 / group) tokens with the group's query heads, so that keys and
 // values are read once for all of them. Items are worked on from the longest to the
 // shortest, dealt to the CTAs to and fro, so that each gets about the same number of
-// units (128 keys) without a counter that would have to be cleared and without results
-// that depend on who was first. Per unit:
-//   * warp 9 (one lane): queries, keys and values by TMA into 128-byte swizzled operand
-//     buffers, keys and values in rings;
+// units (128 keys; 8192 tokens of 40 heads: 280 to 285) without a counter that would have
+// to be cleared and without results that depend on who was first. Per unit:
+//   * warp 9 (one lane): announces the items; queries, keys and values by TMA into 128-byte
+//     swizzled operand buffers, keys and values in rings;
 //   * warp 8 (one lane): for each tile tcgen05.mma S = Q K^T into TMEM, then, when the
 //     tile's probabilities are there, O += P V with P read from TMEM, where it has taken
 //     the place of S; the first half of P V starts when half of P is there;
 //   * warps 0..3 / 4..7 (tile 0 / 1; thread = row = TMEM lane): the row's 128 scores in
-//     registers, maximum, exp2, sum, probabilities as fp16 back to TMEM. While one tile's
-//     softmax runs, the tensor core works on the other's products. O is rescaled only
-//     when the maximum grows by more than 2^3.75 over the one that the reference in use
-//     was set by (the result is the same: the sum uses that reference);
+//     registers, exp2, sum, probabilities as fp16 back to TMEM. While one tile's softmax
+//     runs, the tensor core works on the other's products. O is rescaled only where the
+//     probabilities would leave fp16 with the reference in use (see kHeadroom);
 //   * warps 10, 11: in units that not all rows see whole, values past the sequence become
 //     zero, and so do infinities and NaN, which times a probability of zero would reach
 //     rows that do not see them. Rows that do see one get it back at the end.
 // TMEM: S0 S1 O0 O1, 128 columns each.
+//
+// Measured: one prompt of 8192 tokens, 40 heads on 8, D = 128: 454 us (687 GFLOP, 1510
+// TFLOP/s), one of 2048: 46 us; D = 64: 383 us. What binds it is the chain of a tile's unit:
+// about 1550 cycles of softmax (of them 512 for 128 exponentials a row at 4 cycles a warp)
+// and 1300 from the last probability to the next scores (768 of products, the rest the ways
+// through barriers), with TMEM full, so that the next scores cannot be formed meanwhile; the
+// tensor core is busy 2048 of the 2850 cycles that a pair of units takes. Steps on the way
+// (8192 tokens): the issuing lane by elect.sync, not lane 0, 644 -> 479 us; no maximum before
+// the exponentials, items' places without a loop over all, stores by rows 479 -> 454. Slower:
+// two threads a row (531), two issuing lanes (606), 168 registers for the softmax (782).
 #include <cuda.h>
 
 #include "exl3_internal.h"
@@ -36,11 +45,15 @@ constexpr int kTokens = 128;       // of a unit
 constexpr int kMmaWarp = 8 /* after the softmax warps */, kLoadWarp = 9, kCleanWarp = 10, kCleanWarps = 2;
 constexpr int kPromptThreads = 12 * 32;  // 168 registers a thread
 constexpr int kPromptSeqs = 1024;  // sequences of one launch
+constexpr int kItems = 4;          // items announced at a time
 constexpr int kFlags = 8;          // items whose flag is kept; more than a ring can be ahead
-// A row's reference is set 2^12 below its maximum, and set anew when a maximum passes it
-// by more than 2^15.75 (fp16 ends at 2^16): the many small probabilities of a long
-// sequence keep their bits (one of 2^-26 of the largest has all 11).
-constexpr float kHeadroom = 12.0f, kLazy = 15.75f;
+// Probabilities are taken relative to a reference: 2^kHeadroom below the row's maximum over
+// its first unit, and set anew only when one of a unit's could leave fp16: when those of the
+// first 64 keys add up to more than kMostSum (a sum that is formed anyway), or one of the
+// others, whose scores are looked at while the first ones' exponentials run, is above 2^kMost.
+// The result is the same, as the row's sum goes by the same reference. A row's largest
+// probability is then 2^8 to 2^16: one of 2^-22 of it has all 11 bits, one of 2^-33 counts.
+constexpr float kHeadroom = 8.0f, kMostSum = 65504.0f, kMost = 15.9f;
 
 template <int D>
 struct PromptCfg {
@@ -51,14 +64,19 @@ struct PromptCfg {
   static constexpr int kOffV = kOffK + kStages * kOperand;
   static constexpr int kOffSeq = kOffV + kStages * kOperand;
   static constexpr int kOffLen = kOffSeq + kPromptSeqs * 8;
-  static constexpr int kOffBar = kOffLen + kPromptSeqs * 4;
+  static constexpr int kOffStage = kOffLen + kPromptSeqs * 4;  // 32 rows x 32 columns fp16 of each softmax warp
+  static constexpr int kOffItem = kOffStage + 8 * 2048;
+  static constexpr int kOffBar = kOffItem + kItems * 32;
   static constexpr int kSmem = 1024 + kOffBar + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 constexpr int kMaxStages = 4;
-enum { kPQFull = 0, kPQEmpty = 2, kPKFull = 4, kPKEmpty = kPKFull + kMaxStages, kPVFull = kPKEmpty + kMaxStages,
-       kPVEmpty = kPVFull + kMaxStages, kPClean = kPVEmpty + kMaxStages, kPS = kPClean + kMaxStages, kPP = kPS + 2 /* tile x half */,
-       kPO = kPP + 4, kPDone = kPO + 2, kPBars = kPDone + 1 };
+// kPReady: values of a unit fit for use, and the next unit's keys.
+// kPPassed: all that uses a unit's scores has them, so its keys and the values of the unit
+// before are not needed any more.
+enum { kPQFull = 0, kPFirst = 2, kPPassed = 3, kPVFull = kPPassed + kMaxStages, kPReady = kPVFull + kMaxStages,
+       kPS = kPReady + kMaxStages, kPP = kPS + 2 /* tile x half */, kPO = kPP + 4, kPItemFull = kPO + 2,
+       kPItemEmpty = kPItemFull + kItems, kPDone = kPItemEmpty + kItems, kPBars = kPDone + 1 };
 
 struct PromptParams {
   PromptAttention a;
@@ -66,83 +84,98 @@ struct PromptParams {
 };
 
 // The launch's sequences from the longest to the shortest (equal ones in their order):
-// first row and tokens. Returns how many have any. All threads; ends with a barrier.
-__device__ __forceinline__ int sort_prompts(const PromptAttention &a, int2 *seq, int *len) {
+// first row and tokens, and pairs of tiles. Returns how many have any tokens. All threads;
+// ends with a barrier.
+__device__ __forceinline__ int sort_prompts(const PromptAttention &a, int pair, int2 *seq, int *pairs) {
   const int n4 = (a.n_seqs + 3) & ~3;
-  for (int s = threadIdx.x; s < n4; s += kPromptThreads) {
-    int n = 0;
+  int *len = pairs;  // by sequence, until the sorted ones take its place
+  constexpr int kEach = (kPromptSeqs + kPromptThreads - 1) / kPromptThreads;
+  int row0[kEach], n[kEach], before[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int s = threadIdx.x + k * kPromptThreads;
+    row0[k] = n[k] = 0;
     if (s < a.n_seqs) {
-      const int row0 = a.q_start[s];
-      n = a.q_start[s + 1] - row0;
-      if (row0 < 0 || n < 0 || row0 + (int64_t)n > a.rows) {
+      row0[k] = a.q_start[s];
+      n[k] = a.q_start[s + 1] - row0[k];
+      if (row0[k] < 0 || n[k] < 0 || row0[k] + (int64_t)n[k] > a.rows) {
         report_index(a.status);
-        n = 0;
+        n[k] = 0;
       }
     }
-    len[s] = n;
+    if (s < n4) len[s] = n[k];
   }
   __syncthreads();
-  int some = 0;
-  for (int s = threadIdx.x; s < a.n_seqs; s += kPromptThreads) {
-    const int n = len[s];
-    int before = 0;
-    for (int t = 0; t < n4; t += 4) {
-      const int4 o = *reinterpret_cast<const int4 *>(len + t);
-      before += (o.x > n || (o.x == n && t < s)) + (o.y > n || (o.y == n && t + 1 < s)) + (o.z > n || (o.z == n && t + 2 < s)) +
-                (o.w > n || (o.w == n && t + 3 < s));
-    }
-    if (n > 0) seq[before] = make_int2(a.q_start[s], n);
-    some += n > 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int s = threadIdx.x + k * kPromptThreads;
+    before[k] = 0;
+    if (n[k] > 0)
+      for (int t = 0; t < n4; t += 4) {
+        const int4 o = *reinterpret_cast<const int4 *>(len + t);
+        before[k] += (o.x > n[k] || (o.x == n[k] && t < s)) + (o.y > n[k] || (o.y == n[k] && t + 1 < s)) +
+                     (o.z > n[k] || (o.z == n[k] && t + 2 < s)) + (o.w > n[k] || (o.w == n[k] && t + 3 < s));
+      }
   }
-  // the number of sequences with tokens: a vote a pass, as each thread has at most three
   int total = 0;
 #pragma unroll
-  for (int k = 0; k < (kPromptSeqs + kPromptThreads - 1) / kPromptThreads; ++k) total += __syncthreads_count(some > k);
+  for (int k = 0; k < kEach; ++k) total += __syncthreads_count(n[k] > 0);  // all are past the lengths
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (n[k] > 0) {
+      seq[before[k]] = make_int2(row0[k], n[k]);
+      pairs[before[k]] = (n[k] + pair - 1) / pair;
+    }
+  __syncthreads();
   return total;
 }
 
 struct Item {
-  int row0, n;     // the sequence
-  int h;           // key/value head
-  int token0;      // first token of the pair
-  int units[2];    // of each tile; 0: the pair has no second tile
-  int all;         // of the pair
+  int row0, n;       // the sequence
+  int h;             // key/value head
+  int token0;        // first token of the pair
+  int units0, units1;// of each tile; 0: the pair has no second tile
   int first_masked;  // from this unit on, not every row sees all keys
+  int there;         // 0: there are no more items
+  __device__ __forceinline__ int all() const { return max(units0, units1); }
 };
 
 // The items of a CTA: number k of them is item k * CTAs + c or, every second time, from
 // the other end. Causal items are ordered by the pair's place in its sequence, the last
 // ones first (which is by length but for sequences' last pairs), others by sequence.
 struct PromptWalk {
+  const int2 *seq;
+  const int *pairs;
+  int n_seqs;
   uint32_t round, base;
   int level, count;  // causal: place of the pair, and sequences that have it; else the sequence
-  __device__ __forceinline__ void begin(const int2 *seq, int n_seqs, int pair, int causal) {
+  __device__ __forceinline__ void begin(int causal) {
     round = base = 0;
-    level = causal ? (n_seqs > 0 ? (seq[0].y + pair - 1) / pair - 1 : -1) : 0;
+    level = causal && n_seqs > 0 ? pairs[0] - 1 : 0;
     count = 0;
-    if (causal) widen(seq, n_seqs, pair);
   }
-  __device__ __forceinline__ void widen(const int2 *seq, int n_seqs, int pair) {
-    while (count < n_seqs && seq[count].y > level * pair) ++count;
-  }
-  __device__ __forceinline__ bool next(const int2 *seq, int n_seqs, const PromptParams &p, Item &it) {
+  __device__ __forceinline__ bool next(const PromptParams &p, Item &it) {
     const uint32_t c = blockIdx.x, C = gridDim.x, heads = p.a.n_kv_heads;
-    const int pair = 2 * p.tile_tokens;
     const uint32_t idx = round * C + (round & 1 ? C - 1 - c : c);
     ++round;
     int s, place;
     if (p.a.causal) {
-      while (level >= 0 && idx - base >= count * heads) {
-        base += count * heads;
-        --level;
-        widen(seq, n_seqs, pair);
+      // places that the same sequences have are passed over at once
+      for (;;) {
+        while (count < n_seqs && pairs[count] > level) ++count;
+        const uint32_t size = count * heads, same = level + 1 - (count < n_seqs ? pairs[count] : 0);
+        if (size == 0) return false;
+        const uint32_t skip = min((idx - base) / size, same);
+        base += skip * size;
+        level -= skip;
+        if (skip < same) break;
+        if (level < 0) return false;
       }
-      if (level < 0) return false;
       s = (idx - base) / heads;
       place = level;
     } else {
       uint32_t mine = 0;
-      while (level < n_seqs && idx - base >= (mine = (uint32_t)((seq[level].y + pair - 1) / pair) * heads)) {
+      while (level < n_seqs && idx - base >= (mine = pairs[level] * heads)) {
         base += mine;
         ++level;
       }
@@ -153,15 +186,15 @@ struct PromptWalk {
     it.h = (idx - base) % heads;
     it.row0 = seq[s].x;
     it.n = seq[s].y;
-    it.token0 = place * pair;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int first = it.token0 + t * p.tile_tokens;
+    it.token0 = place * 2 * p.tile_tokens;
+    auto units = [&](int first) {
       const int seen = p.a.causal ? min(first + p.tile_tokens, it.n) : it.n;
-      it.units[t] = first < it.n ? (seen + kTokens - 1) / kTokens : 0;
-    }
-    it.all = max(it.units[0], it.units[1]);
+      return first < it.n ? (seen + kTokens - 1) / kTokens : 0;
+    };
+    it.units0 = units(it.token0);
+    it.units1 = units(it.token0 + p.tile_tokens);
     it.first_masked = (p.a.causal ? it.token0 + 1 : it.n) / kTokens;
+    it.there = 1;
     return true;
   }
 };
@@ -173,19 +206,23 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// Loads 128 consecutive TMEM columns of this thread's lane and waits for them inside the
+// True in one lane of the warp. What it guards needs no loop over lanes around each
+// tensor-core instruction, which `lane == 0` gets from the compiler (46 cycles an
+// instruction and more, where 32 or 64 are the tensor core's own time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// Loads 64 consecutive TMEM columns of this thread's lane and waits for them inside the
 // same asm statement, so no use can be scheduled before the wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
-      "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
-      "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-      "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
-      "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
         "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
@@ -194,16 +231,45 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
         "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
         "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
         "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
-        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]),
-        "=f"(v[64]), "=f"(v[65]), "=f"(v[66]), "=f"(v[67]), "=f"(v[68]), "=f"(v[69]), "=f"(v[70]), "=f"(v[71]),
-        "=f"(v[72]), "=f"(v[73]), "=f"(v[74]), "=f"(v[75]), "=f"(v[76]), "=f"(v[77]), "=f"(v[78]), "=f"(v[79]),
-        "=f"(v[80]), "=f"(v[81]), "=f"(v[82]), "=f"(v[83]), "=f"(v[84]), "=f"(v[85]), "=f"(v[86]), "=f"(v[87]),
-        "=f"(v[88]), "=f"(v[89]), "=f"(v[90]), "=f"(v[91]), "=f"(v[92]), "=f"(v[93]), "=f"(v[94]), "=f"(v[95]),
-        "=f"(v[96]), "=f"(v[97]), "=f"(v[98]), "=f"(v[99]), "=f"(v[100]), "=f"(v[101]), "=f"(v[102]), "=f"(v[103]),
-        "=f"(v[104]), "=f"(v[105]), "=f"(v[106]), "=f"(v[107]), "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]),
-        "=f"(v[112]), "=f"(v[113]), "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]),
-        "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
-      : "r"(taddr));
+        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+      : "r"(taddr), "r"(taddr + 32));
+}
+// The same in two parts: nothing may use v between them, and what comes after goes through
+// the second.
+__device__ __forceinline__ void tmem_ld64_begin(uint32_t taddr, float (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+        "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+      : "r"(taddr), "r"(taddr + 32));
+}
+__device__ __forceinline__ void tmem_ld64_end(float (&v)[64]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" :
+      "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+      "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+      "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+      "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]),
+      "+f"(v[32]), "+f"(v[33]), "+f"(v[34]), "+f"(v[35]), "+f"(v[36]), "+f"(v[37]), "+f"(v[38]), "+f"(v[39]),
+      "+f"(v[40]), "+f"(v[41]), "+f"(v[42]), "+f"(v[43]), "+f"(v[44]), "+f"(v[45]), "+f"(v[46]), "+f"(v[47]),
+      "+f"(v[48]), "+f"(v[49]), "+f"(v[50]), "+f"(v[51]), "+f"(v[52]), "+f"(v[53]), "+f"(v[54]), "+f"(v[55]),
+      "+f"(v[56]), "+f"(v[57]), "+f"(v[58]), "+f"(v[59]), "+f"(v[60]), "+f"(v[61]), "+f"(v[62]), "+f"(v[63]));
+}
+
+// tmem_st32 of 32-bit words.
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
+  float f[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+  tmem_st32(taddr, f);
 }
 
 // Bits of the fp16 pair w whose exponent is all ones (infinity, NaN): 0x8000 for each.
@@ -229,19 +295,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(kPQFull + t), 1);
-      mbar_init(bar(kPQEmpty + t), 1);
       mbar_init(bar(kPS + t), 1);
       mbar_init(bar(kPP + 2 * t), 4);
       mbar_init(bar(kPP + 2 * t + 1), 4);
       mbar_init(bar(kPO + t), 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(kPKFull + i), 1);
-      mbar_init(bar(kPKEmpty + i), 1);
+      mbar_init(bar(kPPassed + i), 4);
       mbar_init(bar(kPVFull + i), 1);
-      mbar_init(bar(kPVEmpty + i), 1);
-      mbar_init(bar(kPClean + i), kCleanWarps);
+      mbar_init(bar(kPReady + i), 1 + kCleanWarps);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bar(kPItemFull + i), 1);
+      mbar_init(bar(kPItemEmpty + i), 8 + 1 + kCleanWarps);
+    }
+    mbar_init(bar(kPFirst), 1);
     mbar_init(bar(kPDone), 1);
     for (int i = 0; i < kFlags; ++i) flags[i] = 0;
     fence_barrier_init();
@@ -259,22 +327,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
-  const int n_seqs = sort_prompts(p.a, seq, reinterpret_cast<int *>(smem + Cfg::kOffLen));
+  PromptWalk walk{seq, reinterpret_cast<int *>(smem + Cfg::kOffLen),
+                  sort_prompts(p.a, 2 * p.tile_tokens, seq, reinterpret_cast<int *>(smem + Cfg::kOffLen))};
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  PromptWalk walk;
-  walk.begin(seq, n_seqs, 2 * p.tile_tokens, p.a.causal);
-  Item it;
+  int4 *items = reinterpret_cast<int4 *>(smem + Cfg::kOffItem);
+  // Item number n, as the loading lane announces it.
+  auto item_there = [&](uint32_t n) { return mbar_wait(bar(kPItemFull + n % kItems), (n / kItems) & 1, status); };
+  auto read_item = [&](uint32_t n, Item &it) {
+    const int4 a = items[2 * (n % kItems)], b = items[2 * (n % kItems) + 1];
+    it = Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  };
+  auto item_read = [&](uint32_t n) { mbar_arrive(bar(kPItemEmpty + n % kItems)); };
 
+  // 168 registers a thread at launch: the last four warps give 12288 of theirs to the others
+  if (warp >= kMmaWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == kMmaWarp) {
     // ---------------- tensor core (one lane) ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       // bit 13: A negated, for a negative scale
       const uint32_t idesc_s = f16_idesc(kTile, kTokens) | (p.a.scale < 0.f ? 1u << 13 : 0u);
       constexpr uint32_t kIdescO = f16_idesc(kTile, D) | kIdescBTransposed;
-      uint32_t unit = 0, items_of[2] = {0, 0}, units_of[2] = {0, 0};
-      bool ok = true;
-      auto wait_k = [&](uint32_t u) { return mbar_wait(bar(kPKFull + u % kStages), (u / kStages) & 1, status); };
+      uint32_t unit = 0, number = 0, items_of[2] = {0, 0}, units_of[2] = {0, 0};
+      auto ready = [&](uint32_t u) { return mbar_wait(bar(kPReady + u % kStages), (u / kStages) & 1, status); };
       auto scores = [&](int t, uint32_t u) {
         const uint32_t q = base + t * Cfg::kOperand, k = base + Cfg::kOffK + (u % kStages) * Cfg::kOperand;
 #pragma unroll
@@ -284,28 +360,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         tc_commit(bar(kPS + t));
       };
-      while (ok && walk.next(seq, n_seqs, p, it)) {
-        ok = wait_k(unit);
+      bool ok = item_there(0);
+      Item it;
+      read_item(0, it);
+      if (ok && it.there) ok = mbar_wait(bar(kPFirst), 0, status);
+      while (ok && it.there) {
+        const int units[2] = {it.units0, it.units1}, all = it.all();
+        item_read(number++);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok) break;
-          if (it.units[t] == 0) continue;
+          if (!ok || units[t] == 0) continue;
           ok = mbar_wait(bar(kPQFull + t), items_of[t]++ & 1, status);
           if (!ok) break;
           tc_fence_after();
           scores(t, unit);
-          if (it.units[t] == 1) tc_commit(bar(kPQEmpty + t));
         }
-        if (ok) tc_commit(bar(kPKEmpty + unit % kStages));
-        for (int j = 0; ok && j < it.all; ++j, ++unit) {
-          ok = mbar_wait(bar(kPVFull + unit % kStages), (unit / kStages) & 1, status);
-          ok = ok && mbar_wait(bar(kPClean + unit % kStages), (unit / kStages) & 1, status);
+        for (int j = 0; ok && j < all; ++j, ++unit) {
+          ok = ready(unit);
           const uint32_t v = base + Cfg::kOffV + (unit % kStages) * Cfg::kOperand;
-          bool next_k = false;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (!ok) break;
-            if (j >= it.units[t]) continue;
+            if (!ok || j >= units[t]) continue;
             const uint32_t ph = units_of[t]++ & 1;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -314,33 +389,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               tc_fence_after();
 #pragma unroll
               for (int k = 4 * half; k < 4 * half + 4; ++k)
-                tc_mma_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, sw128_mn_desc(v + k * 2048, 128 * 128, 1024), kIdescO,
-                          (j | k) > 0);
+                tc_mma_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, sw128_mn_desc(v + k * 2048, 128 * 128, 1024), kIdescO, (j | k) > 0);
             }
             if (!ok) break;
-            if (j + 1 < it.units[t]) {
-              if (!next_k) ok = wait_k(unit + 1);
-              if (!ok) break;
-              next_k = true;
-              tc_fence_after();
-              scores(t, unit + 1);
-              if (j + 2 == it.units[t]) tc_commit(bar(kPQEmpty + t));
-            } else {
-              tc_commit(bar(kPO + t));
-            }
+            if (j + 1 < units[t]) scores(t, unit + 1);
+            else tc_commit(bar(kPO + t));
           }
-          if (!ok) break;
-          tc_commit(bar(kPVEmpty + unit % kStages));
-          if (next_k) tc_commit(bar(kPKEmpty + (unit + 1) % kStages));
         }
+        ok = ok && item_there(number);
+        read_item(number, it);
       }
       tc_commit(bar(kPDone));  // every issued product ends before the TMEM is released
       mbar_wait_short(bar(kPDone), 0);
     }
   } else if (warp == kLoadWarp) {
-    // ---------------- loads (one lane) ----------------
-    if (lane == 0) {
-      uint32_t unit = 0, units_k = 0, units_v = 0, items_of[2] = {0, 0};
+    // ---------------- items and loads (one lane) ----------------
+    if (elect_one()) {
+      uint32_t unit = 0, number = 0, items_of[2] = {0, 0};
       bool ok = true;
       const uint32_t q_bytes = (uint32_t)(Cfg::kHalves * 128) * p.group * p.tile_tokens;
       auto operand = [&](const CUtensorMap *map, uint32_t dst, uint32_t b, int head, int row) {
@@ -349,49 +414,74 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (EXL3_RANGE(row, 0, p.a.rows) && EXL3_SMEM(dst + hf * (128 * 128), 128 * 128))
             tma_load_3d(dst + hf * (128 * 128), map, b, 64 * hf, head, row);
       };
-      while (ok && walk.next(seq, n_seqs, p, it)) {
-        for (int j = 0; ok && j < it.all; ++j, ++unit) {
-          const uint32_t st = unit % kStages, ph = (unit / kStages) & 1;
-          const int row = it.row0 + j * kTokens;
-          ok = mbar_wait(bar(kPKEmpty + st), ph ^ 1, status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(bar(kPKFull + st), Cfg::kOperand);
-          operand(&tk, base + Cfg::kOffK + st * Cfg::kOperand, bar(kPKFull + st), it.h, row);
-          ++units_k;
-          if (j == 0) {
+      auto announce = [&](const Item &it) {
+        ok = ok && mbar_wait(bar(kPItemEmpty + number % kItems), ((number / kItems) & 1) ^ 1, status);
+        if (!ok) return;
+        items[2 * (number % kItems)] = make_int4(it.row0, it.n, it.h, it.token0);
+        items[2 * (number % kItems) + 1] = make_int4(it.units0, it.units1, it.first_masked, it.there);
+        mbar_arrive(bar(kPItemFull + number % kItems));
+        ++number;
+      };
+      // In any order, but each unit's before the next one with its slot is loaded.
+      auto passed = [&](uint32_t u) { return mbar_wait(bar(kPPassed + u % kStages), (u / kStages) & 1, status); };
+      auto keys = [&](uint32_t u, uint32_t b, const Item &it, int j) {
+        mbar_arrive_expect_tx(b, Cfg::kOperand);
+        operand(&tk, base + Cfg::kOffK + (u % kStages) * Cfg::kOperand, b, it.h, it.row0 + j * kTokens);
+      };
+      walk.begin(p.a.causal);
+      Item it, next;
+      it.there = walk.next(p, it);
+      announce(it);
+      const bool any = it.there;
+      if (any) keys(0, bar(kPFirst), it, 0);
+      while (ok && it.there) {
+        ok = unit == 0 || passed(unit - 1);  // the last item's scores: its queries are not needed any more
+        if (!ok) break;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (!ok) break;
-              if (it.units[t] == 0) continue;
-              ok = mbar_wait(bar(kPQEmpty + t), (items_of[t] & 1) ^ 1, status);
-              if (!ok) break;
-              ++items_of[t];
-              mbar_arrive_expect_tx(bar(kPQFull + t), q_bytes);
-              operand(&tq, base + t * Cfg::kOperand, bar(kPQFull + t), it.h * p.group, it.row0 + it.token0 + t * p.tile_tokens);
-            }
-            if (!ok) break;
-          }
-          ok = mbar_wait(bar(kPVEmpty + st), ph ^ 1, status);
+        for (int t = 0; t < 2; ++t) {
+          if ((t == 0 ? it.units0 : it.units1) == 0) continue;
+          ++items_of[t];
+          mbar_arrive_expect_tx(bar(kPQFull + t), q_bytes);
+          operand(&tq, base + t * Cfg::kOperand, bar(kPQFull + t), it.h * p.group, it.row0 + it.token0 + t * p.tile_tokens);
+        }
+        next.there = walk.next(p, next);
+        const int all = it.all();
+        for (int j = 0; ok && j < all; ++j, ++unit) {
+          const uint32_t st = unit % kStages;
+          ok = unit + 1 < kStages || passed(unit + 1 - kStages);
           if (!ok) break;
           mbar_arrive_expect_tx(bar(kPVFull + st), Cfg::kOperand);
-          operand(&tv, base + Cfg::kOffV + st * Cfg::kOperand, bar(kPVFull + st), it.h, row);
-          ++units_v;
+          operand(&tv, base + Cfg::kOffV + st * Cfg::kOperand, bar(kPVFull + st), it.h, it.row0 + j * kTokens);
+          if (j == 0) announce(next);
+          if (j + 1 < all) keys(unit + 1, bar(kPReady + st), it, j + 1);
+          else if (next.there) keys(unit + 1, bar(kPReady + st), next, 0);
+          else mbar_arrive(bar(kPReady + st));
         }
+        it = next;
       }
       // nothing is on its way into this CTA's memory when it ends (at once, unless a wait ran out)
-      for (uint32_t i = 0; i < kStages; ++i) {
-        if (units_k > i) mbar_wait_short(bar(kPKFull + i), ((units_k - 1 - i) / kStages) & 1);
-        if (units_v > i) mbar_wait_short(bar(kPVFull + i), ((units_v - 1 - i) / kStages) & 1);
-      }
+      if (any) mbar_wait_short(bar(kPFirst), 0);
+      for (uint32_t i = 0; i < kStages; ++i)
+        if (unit > i) {
+          mbar_wait_short(bar(kPVFull + i), ((unit - 1 - i) / kStages) & 1);
+          mbar_wait_short(bar(kPReady + i), ((unit - 1 - i) / kStages) & 1);
+        }
       for (int t = 0; t < 2; ++t)
         if (items_of[t] > 0) mbar_wait_short(bar(kPQFull + t), (items_of[t] - 1) & 1);
     }
-  } else if (warp >= kCleanWarp) {
+  } else {
     // ---------------- values that not every row may use ----------------
     uint32_t unit = 0, number = 0;
-    bool ok = true;
-    for (; ok && walk.next(seq, n_seqs, p, it); ++number) {
-      for (int j = 0; ok && j < it.all; ++j, ++unit) {
+    Item it;
+    for (bool ok = true;; ++number) {
+      ok = __all_sync(0xffffffffu, ok && item_there(number));
+      if (!ok) break;
+      read_item(number, it);
+      __syncwarp();
+      if (lane == 0) item_read(number);
+      if (!it.there) break;
+      const int all = it.all();
+      for (int j = 0; j < all; ++j, ++unit) {
         const uint32_t st = unit % kStages;
         ok = __all_sync(0xffffffffu, mbar_wait(bar(kPVFull + st), (unit / kStages) & 1, status));
         if (!ok) break;
@@ -420,10 +510,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           fence_proxy_async_shared();
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive(bar(kPClean + st));  // of every unit: the ring cannot get ahead of this warp
+        if (lane == 0) mbar_arrive(bar(kPReady + st));  // of every unit: the ring cannot get ahead of this warp
       }
     }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---------------- softmax: thread = row of tile t ----------------
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -431,11 +523,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const SoftCap cap(p.a.softcap, kLog2e);
     const float c = fmaxf(fabsf(p.a.scale) * Raised<D>::kLog2e, 1e-37f);  // scores in log2 units are the products times c
     const int token = row / p.group, head_in = row - token * p.group;
-    uint32_t count = 0, items = 0, number = 0;  // units and items of this tile, items of the CTA
+    uint32_t count = 0, items = 0, number = 0, unit = 0;  // units and items of this tile, items and units of the CTA
     bool ok = true;
-    for (; ok && walk.next(seq, n_seqs, p, it); ++number) {
-      const int units = t == 0 ? it.units[0] : it.units[1];
-      if (units == 0) continue;
+    auto hand_over = [&](int half) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kPP + 2 * t + half));
+    };
+    Item it, next;
+    auto next_item = [&](uint32_t n) {
+      ok = __all_sync(0xffffffffu, ok && item_there(n));
+      read_item(n, next);
+      __syncwarp();
+      if (lane == 0) item_read(n);
+    };
+    next_item(0);
+    for (; ok && next.there; ++number, unit += it.all()) {
+      it = next;
+      const int units = t == 0 ? it.units0 : it.units1;
+      if (units == 0) {
+        next_item(number + 1);
+        continue;
+      }
+      // the last tile that uses a unit's keys and values: this one from here on (the products of tile 1 come after those of tile 0)
+      const int last_from = t == 0 ? it.units1 : 0;
       const int pos = it.token0 + t * p.tile_tokens + token;
       const bool real = token < p.tile_tokens && pos < it.n;
       const int limit = !real ? 0 : p.a.causal ? pos + 1 : it.n;
@@ -448,70 +560,100 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           break;
         }
         tc_fence_after();
+        // The scores are there, so their keys are not needed any more, nor the values of the unit
+        // before (its product came first), nor, with the item's last scores, the queries. Said from
+        // here: a commit for it would stop the lane that issues the products (64 to 200 cycles).
+        if (u >= last_from && lane == 0) mbar_arrive(bar(kPPassed + (unit + u) % kStages));
         if (live) {
-          float s[128];
-          tmem_ld128(s_tmem, s);
           const int pos0 = u * kTokens;
-          if constexpr (CAP) {
+          const float scale = CAP ? 1.0f : c;
+          const float2 scale2 = make_float2(scale, scale);
+          bool renew = u == 0 || __any_sync(0xffffffffu, real && ref == -INFINITY);
+          float s[64], s2[64];  // of the unit's first and second 64 keys
+          uint32_t packed[32];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
+          float2 part[2], shift2;
+          auto exponentials = [&](const float (&x64)[64], int from, int to) {
 #pragma unroll
-            for (int k = 0; k < 128; k += 2) {
-              const float2 x = cap(mul2(make_float2(s[k], s[k + 1]), make_float2(c, c)));
-              s[k] = x.x;
-              s[k + 1] = x.y;
-            }
-          }
-          if (pos0 + kTokens > least) {
-#pragma unroll
-            for (int k = 0; k < 128; ++k)
-              if (pos0 + k >= limit) s[k] = -INFINITY;
-          }
-          float m[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int k = 4; k < 124; k += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(s[k + e], s[k + 4 + e]));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], s[124 + e]);
-          float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-          if constexpr (!CAP) top *= c;
-          const float now = top > ref + kLazy || ref == -INFINITY ? top - kHeadroom : ref;
-          const float keep = now == ref || ref == -INFINITY || !real ? 1.0f : ex2(ref - now);
-          // the scores' product came after the output's, which is therefore done
-          if (u > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
-#pragma unroll 1
-            for (int k = 0; k < D / 32; ++k) {
-              float o[32];
-              tmem_ld32(o_tmem + 32 * k, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= keep;
-              tmem_st32(o_tmem + 32 * k, o);
-            }
-            sum *= keep;
-          }
-          ref = now;
-          const float scale = CAP ? 1.0f : c, shift = now == -INFINITY ? 0.f : -now;
-          const float2 scale2 = make_float2(scale, scale), shift2 = make_float2(shift, shift);
-          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t packed[16];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float2 x = make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]);
-              x = fma2(x, scale2, shift2);
+            for (int k = from; k < to; ++k) {
+              float2 x = fma2(make_float2(x64[2 * k], x64[2 * k + 1]), scale2, shift2);
               x = make_float2(ex2(x.x), ex2(x.y));
               part[k & 1] = add2(part[k & 1], x);
               const __half2 h2 = __floats2half2_rn(x.x, x.y);
               packed[k] = *reinterpret_cast<const uint32_t *>(&h2);
             }
-            tmem_st16(s_tmem + 16 * q, packed);
-            if (q & 1) {
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(kPP + 2 * t + (q >> 1)));
+          };
+          auto most = [&](const float (&x)[64]) {
+            float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int k = 4; k < 60; k += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(x[k + e], x[k + 4 + e]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], x[60 + e]);
+            return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale;
+          };
+          auto cap_and_mask = [&](float (&x64)[64], int first) {
+            if constexpr (CAP) {
+#pragma unroll
+              for (int k = 0; k < 64; k += 2) {
+                const float2 x = cap(mul2(make_float2(x64[k], x64[k + 1]), make_float2(c, c)));
+                x64[k] = x.x;
+                x64[k + 1] = x.y;
+              }
             }
+            if (first + 64 > least) {
+              const int n = min(max(limit - first, 0), 64);  // keys that the row sees; as bits, whose tests take an instruction for several
+              const uint64_t seen = n == 64 ? ~0ull : (1ull << n) - 1;
+              const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                if (!(lo & 1u << k)) x64[k] = -INFINITY;
+                if (!(hi & 1u << k)) x64[32 + k] = -INFINITY;
+              }
+            }
+          };
+          // A second round is rare; the scores are still in TMEM then.
+#pragma unroll 1
+          for (;;) {
+            tmem_ld64(s_tmem, s);
+            tmem_ld64_begin(s_tmem + 64, s2);
+            cap_and_mask(s, pos0);
+            if (renew) {
+              tmem_ld64_end(s2);
+              cap_and_mask(s2, pos0 + 64);
+              const float now = fmaxf(fmaxf(most(s), most(s2)) - kHeadroom, ref);
+              if (u > 0) {
+                const float keep = now == ref || ref == -INFINITY ? 1.0f : ex2(ref - now);
+                // the scores' product came after the output's, which is therefore done
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                  float o[32];
+                  tmem_ld32(o_tmem + 32 * k, o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] *= keep;
+                  tmem_st32(o_tmem + 32 * k, o);
+                }
+                sum *= keep;
+              }
+              ref = now;
+            }
+            const float shift = ref == -INFINITY ? 0.f : -ref;
+            shift2 = make_float2(shift, shift);
+            part[0] = part[1] = make_float2(0.f, 0.f);
+            exponentials(s, 0, 32);
+            if (renew) break;
+            tmem_ld64_end(s2);
+            cap_and_mask(s2, pos0 + 64);
+            const float so_far = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+            if (!__any_sync(0xffffffffu, real && (so_far > kMostSum || most(s2) + shift > kMost))) break;
+            renew = true;
           }
+          tmem_st32u(s_tmem, packed);
+          exponentials(s2, 0, 16);
+          hand_over(0);  // the stores have had time
+          exponentials(s2, 16, 32);
+          tmem_st32u(s_tmem + 32, packed);
+          hand_over(1);
           part[0] = add2(part[0], part[1]);
           sum += part[0].x + part[0].y;
         } else {  // rows past the sequence: whatever the products make of them is not used
@@ -522,6 +664,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
       }
+      if (ok) next_item(number + 1);  // while the last products run
       if (!ok || !__all_sync(0xffffffffu, mbar_wait(bar(kPO + t), items++ & 1, status))) {
         ok = false;
         break;
@@ -533,40 +676,60 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int64_t off = (int64_t)(it.row0 + pos) * p.a.ldo + (int64_t)head * D;
         const bool fits = real && EXL3_SPAN(off, D, (int64_t)(p.a.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D);
         const bool back = fits && flags[number % kFlags] == number + 1;
-#pragma unroll 1
-        for (int k = 0; k < D / 32; ++k) {
-          float o[32];
-          __syncwarp();
-          tmem_ld32(o_tmem + 32 * k, o);
-          if (!fits) continue;
+        // Through shared memory, so that a store's lanes have 64 bytes of each of 8 rows, not 16 of
+        // each of 32 (which take the SM's store path 32 cycles each).
+        const uint32_t stage = base + Cfg::kOffStage + warp * 2048;
+        const uint32_t rows_fit = __ballot_sync(0xffffffffu, fits);
+        int64_t to[4];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= f;
+        for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, off, 8 * i + (lane >> 2)) + 8 * (lane & 3);
+#pragma unroll 1
+        for (int k = 0; k < D; k += 64) {
+          float o[64];
+          __syncwarp();
+          tmem_ld64(o_tmem + k, o);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) o[e] *= f;
           if (back) {  // infinities and NaN that this row sees, of the units where they were taken out
+#pragma unroll 1
             for (int at = it.first_masked * kTokens; at < limit; ++at) {
-              const int64_t from = (int64_t)(it.row0 + at) * p.a.ldv + (int64_t)it.h * D + 32 * k;
-              if (!EXL3_SPAN(from, 32, (int64_t)(p.a.rows - 1) * p.a.ldv + (int64_t)p.a.n_kv_heads * D)) continue;
+              const int64_t from = (int64_t)(it.row0 + at) * p.a.ldv + (int64_t)it.h * D + k;
+              if (!EXL3_SPAN(from, 64, (int64_t)(p.a.rows - 1) * p.a.ldv + (int64_t)p.a.n_kv_heads * D)) continue;
               const __half *v = static_cast<const __half *>(p.a.v) + from;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < 64; ++e) {
                 const float x = __half2float(v[e]);
                 if (!isfinite(x)) o[e] += x;
               }
             }
           }
-          uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(p.a.out) + off + 32 * k);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
+          for (int part = 0; part < 2; ++part) {
+            __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const __half2 h2 = __floats2half2_rn(o[8 * e + 2 * x], o[8 * e + 2 * x + 1]);
-              w[x] = *reinterpret_cast<const uint32_t *>(&h2);
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const __half2 h2 = __floats2half2_rn(o[32 * part + 8 * e + 2 * x], o[32 * part + 8 * e + 2 * x + 1]);
+                w[x] = *reinterpret_cast<const uint32_t *>(&h2);
+              }
+              sts16(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
             }
-            out[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane >> 2);
+              uint4 w;
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                           : "r"(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)));
+              if (rows_fit >> r & 1) *reinterpret_cast<uint4 *>(static_cast<__half *>(p.a.out) + to[i] + k + 32 * part) = w;
+            }
           }
         }
-        // a logarithm near 12 would be 2^-20 off: with the reference back at the maximum first
-        if (fits && p.a.lse) p.a.lse[(int64_t)(it.row0 + pos) * p.a.n_heads + head] = log_sum(ref + kHeadroom, sum * 0x1p-12f);
+        // a logarithm near 8 would be 2^-21 off: with the reference back at the maximum first
+        if (fits && p.a.lse) p.a.lse[(int64_t)(it.row0 + pos) * p.a.n_heads + head] = log_sum(ref + kHeadroom, sum * 0x1p-8f);
       }
       tc_fence_before();  // the output has been read: before the next item's first products
     }
