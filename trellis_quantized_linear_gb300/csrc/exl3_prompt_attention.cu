@@ -22,14 +22,15 @@
 // TMEM: S0 S1 O0 O1, 128 columns each.
 //
 // Measured: one prompt of 8192 tokens, 40 heads on 8, D = 128: 454 us (687 GFLOP, 1510
-// TFLOP/s), one of 2048: 46 us; D = 64: 383 us. What binds it is the chain of a tile's unit:
+// TFLOP/s), one of 2048: 46 us; D = 64: 383 us; scores capped: 720 and 700 us. What binds it is the chain of a tile's unit:
 // about 1550 cycles of softmax (of them 512 for 128 exponentials a row at 4 cycles a warp)
 // and 1300 from the last probability to the next scores (768 of products, the rest the ways
 // through barriers), with TMEM full, so that the next scores cannot be formed meanwhile; the
 // tensor core is busy 2048 of the 2850 cycles that a pair of units takes. Steps on the way
 // (8192 tokens): the issuing lane by elect.sync, not lane 0, 644 -> 479 us; no maximum before
 // the exponentials, items' places without a loop over all, stores by rows 479 -> 454. Slower:
-// two threads a row (531), two issuing lanes (606), 168 registers for the softmax (782).
+// two threads a row (531), two issuing lanes (606), 168 registers for the softmax (782); at D
+// = 64, where TMEM has room, P apart from S and the next scores ahead of it (414 for 388).
 #include <cuda.h>
 
 #include "exl3_internal.h"
@@ -271,6 +272,59 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[3
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
   tmem_st32(taddr, f);
 }
+
+// A cap of the scores, in log2 units. Where x^2 < 1/4, x = score / cap, cap * tanh(x) is
+// score * p(x^2) with the polynomial p of degree 4 that is nearest to tanh(x) / x there (to
+// 1.5e-8, found by minimising the largest relative error): no exponential and no reciprocal,
+// which would cost three times the softmax's own. Those beyond go through
+// 1 - 2 / (exp(2 x) + 1), an absolute error near cap * 2^-22, in a pass of their own over
+// TMEM: in line with the softmax it would be too much code for the instruction cache. The
+// others have the same value there, so that a score's does not depend on its neighbours.
+struct PromptCap {
+  float k, cap, p[5];  // x = product * k; coefficients times what brings a product to log2 units
+  // A cap whose double leaves fp32 is lowered: no score comes near it.
+  __device__ __forceinline__ PromptCap(float softcap, float c)
+      : k(c / fmaxf(softcap * kLog2e, 1e-30f)), cap(fminf(softcap * kLog2e, 1.5e38f)),
+        p{c, c * -0.333331439f, c * 0.133258785f, c * -0.0530454412f, c * 0.0172413593f} {}
+  // N products to capped scores, those with x^2 < 1/4; `most` becomes the largest x^2.
+  template <int N>
+  __device__ __forceinline__ void near(float (&s)[N], float &most) const {
+    auto both = [](float v) { return make_float2(v, v); };
+    float m[4] = {most, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = make_float2(s[i], s[i + 1]), x = mul2(v, both(k)), y = mul2(x, x);
+      m[i / 2 % 4] = fmaxf(m[i / 2 % 4], fmaxf(y.x, y.y));
+      float2 t = fma2(y, both(p[4]), both(p[3]));
+      t = fma2(y, t, both(p[2]));
+      t = fma2(y, t, both(p[1]));
+      t = mul2(v, fma2(y, t, both(p[0])));
+      s[i] = t.x;
+      s[i + 1] = t.y;
+    }
+    most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  }
+  // A row's 128 products in TMEM, in place. Rows that are not real hold anything.
+  __device__ __forceinline__ void all(uint32_t scores, bool real) const {
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      float s[32], most = 0.f;
+      tmem_ld32(scores + 32 * q, s);
+      near(s, most);
+      if (__any_sync(0xffffffffu, real && most >= 0.25f)) {
+        float raw[32];
+        tmem_ld32(scores + 32 * q, raw);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float x = raw[i] * k, f = fmaf(-2.0f * cap, rcp(ex2(x * (2.0f * kLog2e)) + 1.0f), cap);
+          s[i] = x * x < 0.25f ? s[i] : f;
+        }
+      }
+      tmem_st32(scores + 32 * q, s);
+    }
+    tmem_wait_st();
+  }
+};
 
 // Bits of the fp16 pair w whose exponent is all ones (infinity, NaN): 0x8000 for each.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
@@ -520,8 +574,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_tmem = lane_base + 128 * t, o_tmem = lane_base + 256 + 128 * t;
-    const SoftCap cap(p.a.softcap, kLog2e);
     const float c = fmaxf(fabsf(p.a.scale) * Raised<D>::kLog2e, 1e-37f);  // scores in log2 units are the products times c
+    const PromptCap cap(p.a.softcap, c);
     const int token = row / p.group, head_in = row - token * p.group;
     uint32_t count = 0, items = 0, number = 0, unit = 0;  // units and items of this tile, items and units of the CTA
     bool ok = true;
@@ -554,6 +608,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int least = __reduce_min_sync(0xffffffffu, real ? limit : INT32_MAX);
       const bool live = __any_sync(0xffffffffu, real);
       float ref = -INFINITY, sum = 0.f;
+      bool far = false;  // scores beyond half the cap were seen
       for (int u = 0; u < units; ++u, ++count) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kPS + t), count & 1, status))) {
           ok = false;
@@ -592,15 +647,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], x[60 + e]);
             return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale;
           };
-          auto cap_and_mask = [&](float (&x64)[64], int first) {
-            if constexpr (CAP) {
-#pragma unroll
-              for (int k = 0; k < 64; k += 2) {
-                const float2 x = cap(mul2(make_float2(x64[k], x64[k + 1]), make_float2(c, c)));
-                x64[k] = x.x;
-                x64[k + 1] = x.y;
-              }
-            }
+          auto mask = [&](float (&x64)[64], int first) {
             if (first + 64 > least) {
               const int n = min(max(limit - first, 0), 64);  // keys that the row sees; as bits, whose tests take an instruction for several
               const uint64_t seen = n == 64 ? ~0ull : (1ull << n) - 1;
@@ -612,15 +659,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               }
             }
           };
+          bool capped = !CAP;  // the scores in TMEM
+          if (CAP && (renew || far)) {
+            cap.all(s_tmem, real);
+            capped = true;
+          }
           // A second round is rare; the scores are still in TMEM then.
 #pragma unroll 1
           for (;;) {
             tmem_ld64(s_tmem, s);
             tmem_ld64_begin(s_tmem + 64, s2);
-            cap_and_mask(s, pos0);
+            float most_x = 0.f;
+            if (CAP && !capped) cap.near(s, most_x);
+            mask(s, pos0);
             if (renew) {
               tmem_ld64_end(s2);
-              cap_and_mask(s2, pos0 + 64);
+              mask(s2, pos0 + 64);
               const float now = fmaxf(fmaxf(most(s), most(s2)) - kHeadroom, ref);
               if (u > 0) {
                 const float keep = now == ref || ref == -INFINITY ? 1.0f : ex2(ref - now);
@@ -643,9 +697,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             exponentials(s, 0, 32);
             if (renew) break;
             tmem_ld64_end(s2);
-            cap_and_mask(s2, pos0 + 64);
+            if (CAP && !capped) cap.near(s2, most_x);
+            mask(s2, pos0 + 64);
             const float so_far = (part[0].x + part[0].y) + (part[1].x + part[1].y);
-            if (!__any_sync(0xffffffffu, real && (so_far > kMostSum || most(s2) + shift > kMost))) break;
+            const bool beyond = CAP && real && most_x >= 0.25f;
+            if (!__any_sync(0xffffffffu, beyond || (real && (so_far > kMostSum || most(s2) + shift > kMost)))) break;
+            if (CAP && !capped) {
+              far = __any_sync(0xffffffffu, beyond);  // the item's other units at once
+              cap.all(s_tmem, real);
+              capped = true;
+            }
             renew = true;
           }
           tmem_st32u(s_tmem, packed);
