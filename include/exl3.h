@@ -638,8 +638,8 @@ exl3_status exl3_rms_norm(const exl3_norm *norm, void *stream);
  *   x, out:   rows x ((q_heads + k_heads) * head_dim) fp16: the query heads, then the key
  *             heads, as a fused projection gives them; leading dimensions ldx, ldo
  *             (multiples of 8). out may be x, with ldo = ldx; otherwise they must not overlap.
- *   position: rows int32, as exl3_kv8_plan gives them: a row with a negative one is neither
- *             read nor written; one of n_positions or more is recorded as
+ *   position: rows int32, as exl3_kv8_plan gives them: a row with a negative one is left
+ *             as it is in out; one of n_positions or more is recorded as
  *             EXL3_ERR_DEVICE_INDEX and treated so.
  *   cos_sin:  n_positions x rot_dim fp32, 16-byte aligned: for each position the cosines
  *             of the pairs' angles, then their sines. rot_dim: a multiple of 16, 16 .. head_dim.

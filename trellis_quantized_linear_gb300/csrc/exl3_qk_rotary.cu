@@ -10,12 +10,11 @@ namespace exl3 {
 
 namespace {
 
-constexpr int kRotaryThreads = 128;
+constexpr int kRotaryThreads = 128, kAhead = 3;
 
 struct Piece {
   float v[8];
-  __device__ __forceinline__ void load(const __half *p) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+  __device__ __forceinline__ explicit Piece(uint4 w) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -24,6 +23,7 @@ struct Piece {
       v[2 * i + 1] = f.y;
     }
   }
+  __device__ __forceinline__ Piece() {}
   __device__ __forceinline__ void store(__half *p) const {
     uint32_t x[4];
 #pragma unroll
@@ -35,7 +35,8 @@ struct Piece {
   }
 };
 
-// D / 16 lanes a head; blockIdx.y takes its share of the heads. `each`: heads of a CTA.
+// D / 16 lanes a head; blockIdx.y takes its share of the heads, `each` of them. A thread's
+// heads are loaded kAhead at a time, before the position is there.
 template <int D, bool INTERLEAVED, bool NORM>
 __global__ void __launch_bounds__(kRotaryThreads) qk_rotary_kernel(const QkRotary p, int each) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -47,81 +48,90 @@ __global__ void __launch_bounds__(kRotaryThreads) qk_rotary_kernel(const QkRotar
   // first elements of the two pieces
   const int a0 = INTERLEAVED || !turns ? 16 * l : 8 * l;
   const int b0 = INTERLEAVED || !turns ? 16 * l + 8 : p.rot_dim / 2 + 8 * l;
-  [[maybe_unused]] const int64_t size_x = (int64_t)(p.rows - 1) * p.ldx + (int64_t)heads * D, size_o = (int64_t)(p.rows - 1) * p.ldo + (int64_t)heads * D;
+  [[maybe_unused]] const int64_t size_x = (int64_t)(p.rows - 1) * p.ldx + (int64_t)heads * D;
+  [[maybe_unused]] const int64_t size_o = (int64_t)(p.rows - 1) * p.ldo + (int64_t)heads * D;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int pos = p.position[row];
-    if (pos < 0) continue;
-    if (pos >= p.n_positions) {
-      if (threadIdx.x == 0) report_index(p.status);
-      continue;
-    }
     float cs[8], sn[8];
+    bool known = false;
+    for (int first = h0; first < h1; first += kAhead * kAtOnce) {
+      uint4 ra[kAhead], rb[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
-    if (turns) {
-      const int64_t at = (int64_t)pos * p.rot_dim + 8 * l;
-      if (EXL3_SPAN(at, p.rot_dim / 2 + 8, (int64_t)p.n_positions * p.rot_dim)) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 c = *reinterpret_cast<const float4 *>(p.cos_sin + at + e);
-          const float4 s = *reinterpret_cast<const float4 *>(p.cos_sin + at + p.rot_dim / 2 + e);
-          cs[e] = c.x, cs[e + 1] = c.y, cs[e + 2] = c.z, cs[e + 3] = c.w;
-          sn[e] = s.x, sn[e + 1] = s.y, sn[e + 2] = s.z, sn[e + 3] = s.w;
+      for (int i = 0; i < kAhead; ++i) {
+        const int h = first + i * kAtOnce + slot;
+        const int64_t from = row * p.ldx + (int64_t)h * D;
+        ra[i] = rb[i] = make_uint4(0, 0, 0, 0);
+        if (h < h1 && EXL3_SPAN(from, D, size_x)) {
+          ra[i] = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.x) + from + a0);
+          rb[i] = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.x) + from + b0);
         }
       }
-    }
-    // all lanes of a warp go round as often as each other: the norm's shuffles
-    for (int first = h0; first < h1; first += kAtOnce) {
-      const int h = first + slot;
-      const int64_t from = row * p.ldx + (int64_t)h * D, to = row * p.ldo + (int64_t)h * D;
-      const bool there = h < h1 && EXL3_SPAN(from, D, size_x) && EXL3_SPAN(to, D, size_o);
-      Piece a, b;
-      if (there) {
-        a.load(static_cast<const __half *>(p.x) + from + a0);
-        b.load(static_cast<const __half *>(p.x) + from + b0);
-      } else {
+      if (!known) {  // the same in the whole CTA
+        known = true;
+        if (pos < 0) break;
+        if (pos >= p.n_positions) {
+          if (threadIdx.x == 0) report_index(p.status);
+          break;
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a.v[e] = b.v[e] = 0.f;
-      }
-      if constexpr (NORM) {
-        float sum = 0.f;
+        for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
+        if (turns) {
+          const int64_t at = (int64_t)pos * p.rot_dim + 8 * l;
+          if (EXL3_SPAN(at, p.rot_dim / 2 + 8, (int64_t)p.n_positions * p.rot_dim)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(a.v[e], a.v[e], fmaf(b.v[e], b.v[e], sum));
-#pragma unroll
-        for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float r = rsqrtf(sum / (float)D + p.eps);
-        if (there) {
-          const __half *w = static_cast<const __half *>(h < p.q_heads ? p.q_weight : p.k_weight);
-          Piece wa, wb;
-          wa.load(w + a0);
-          wb.load(w + b0);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a.v[e] *= r * (wa.v[e] + p.weight_offset);
-            b.v[e] *= r * (wb.v[e] + p.weight_offset);
+            for (int e = 0; e < 8; e += 4) {
+              const float4 c = *reinterpret_cast<const float4 *>(p.cos_sin + at + e);
+              const float4 s = *reinterpret_cast<const float4 *>(p.cos_sin + at + p.rot_dim / 2 + e);
+              cs[e] = c.x, cs[e + 1] = c.y, cs[e + 2] = c.z, cs[e + 3] = c.w;
+              sn[e] = s.x, sn[e + 1] = s.y, sn[e + 2] = s.z, sn[e + 3] = s.w;
+            }
           }
         }
       }
-      if (!there) continue;
-      Piece oa, ob;
-      if constexpr (INTERLEAVED) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          oa.v[2 * e] = a.v[2 * e] * cs[e] - a.v[2 * e + 1] * sn[e];
-          oa.v[2 * e + 1] = a.v[2 * e + 1] * cs[e] + a.v[2 * e] * sn[e];
-          ob.v[2 * e] = b.v[2 * e] * cs[4 + e] - b.v[2 * e + 1] * sn[4 + e];
-          ob.v[2 * e + 1] = b.v[2 * e + 1] * cs[4 + e] + b.v[2 * e] * sn[4 + e];
-        }
-      } else {
+      for (int i = 0; i < kAhead; ++i) {  // all lanes of a warp go round as often as each other: the norm's shuffles
+        const int h = first + i * kAtOnce + slot;
+        const int64_t to = row * p.ldo + (int64_t)h * D;
+        const bool there = h < h1 && EXL3_SPAN(to, D, size_o);
+        Piece a(ra[i]), b(rb[i]);
+        if constexpr (NORM) {
+          float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          oa.v[e] = a.v[e] * cs[e] - b.v[e] * sn[e];
-          ob.v[e] = b.v[e] * cs[e] + a.v[e] * sn[e];
+          for (int e = 0; e < 8; ++e) sum = fmaf(a.v[e], a.v[e], fmaf(b.v[e], b.v[e], sum));
+#pragma unroll
+          for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          const float r = rsqrtf(sum / (float)D + p.eps);
+          if (there) {
+            const __half *w = static_cast<const __half *>(h < p.q_heads ? p.q_weight : p.k_weight);
+            const Piece wa(*reinterpret_cast<const uint4 *>(w + a0)), wb(*reinterpret_cast<const uint4 *>(w + b0));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              a.v[e] *= r * (wa.v[e] + p.weight_offset);
+              b.v[e] *= r * (wb.v[e] + p.weight_offset);
+            }
+          }
         }
+        if (!there) continue;
+        Piece oa, ob;
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            oa.v[2 * e] = a.v[2 * e] * cs[e] - a.v[2 * e + 1] * sn[e];
+            oa.v[2 * e + 1] = a.v[2 * e + 1] * cs[e] + a.v[2 * e] * sn[e];
+            ob.v[2 * e] = b.v[2 * e] * cs[4 + e] - b.v[2 * e + 1] * sn[4 + e];
+            ob.v[2 * e + 1] = b.v[2 * e + 1] * cs[4 + e] + b.v[2 * e] * sn[4 + e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            oa.v[e] = a.v[e] * cs[e] - b.v[e] * sn[e];
+            ob.v[e] = b.v[e] * cs[e] + a.v[e] * sn[e];
+          }
+        }
+        // not rotated: as they are, also infinities and NaN, which 0 times would spread
+        (turns ? oa : a).store(static_cast<__half *>(p.out) + to + a0);
+        (turns ? ob : b).store(static_cast<__half *>(p.out) + to + b0);
       }
-      // not rotated: as they are, also infinities and NaN, which 0 times would spread
-      (turns ? oa : a).store(static_cast<__half *>(p.out) + to + a0);
-      (turns ? ob : b).store(static_cast<__half *>(p.out) + to + b0);
     }
   }
 }

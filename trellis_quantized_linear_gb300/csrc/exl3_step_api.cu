@@ -95,7 +95,7 @@ exl3_status exl3_rms_norm(const exl3_norm *norm, void *stream) {
     return EXL3_ERR_ALIGNMENT;
   const DeviceInfo *dev = initialized_device();
   if (!dev) return EXL3_ERR_NOT_INITIALIZED;
-  return from_cuda(launch_rms_norm(n, dev->num_sms, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_rms_norm(n, dev->num_sms, dev->status, static_cast<cudaStream_t>(stream)));
 }
 
 exl3_status exl3_qk_rotary(const void *x, int64_t ldx, void *out, int64_t ldo, int64_t rows, int32_t q_heads,
