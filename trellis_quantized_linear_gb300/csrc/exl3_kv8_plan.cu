@@ -1,11 +1,11 @@
 // Block tables, lengths, positions and slots of a step from its requests' lengths.
 // Contract in include/exl3.h.
 //
-// One cluster. Its first CTA takes the pages of ended sequences back, goes over the
-// sequences (prefix sums of rows and of pages, four sequences a thread) and hands pages out;
-// after the cluster's barrier all its CTAs write the rows' positions and slots, four rows a
-// thread, which finds the first one's sequence by a binary search in shared memory. All
-// latency: a few dependent loads one after the other.
+// One cluster. Its CTAs have a contiguous part of the sequences each (four a thread): prefix
+// sums of rows and of pages, joined through shared memory of the cluster, then the pages, a
+// thread each, and after a last barrier the rows' positions and slots, four rows a thread,
+// which finds the first one's sequence by a binary search in shared memory. All latency: a few
+// dependent loads and three barriers of the cluster one after the other.
 #include "exl3_internal.h"
 #include "exl3_kv8.cuh"
 
@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;  // at most
 constexpr int kEach = 4;               // sequences of a thread, one behind the other
+constexpr int kMaxRanks = 8;
 constexpr int kHeldSeqs = 11 * 1024;   // sequences whose row starts are held in shared memory
 constexpr uint32_t kFull = 1u << 30;   // sums stop here: above every bound that they are compared with
 
@@ -71,57 +72,105 @@ __device__ __forceinline__ int last_at_most(const uint32_t *v, int n, uint32_t x
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, int ranks) {
+// What the CTAs of the cluster tell each other.
+struct Told {
+  Sums all;        // of its sequences
+  int first_left;  // the first of them that is not served
+  Sums before;     // what comes before it
+};
+
+__global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, int ranks, int sharing) {
   extern __shared__ int2 held[];  // where the rows of a sequence end, and a row's distance to its position, where there is room
   __shared__ uint32_t page_at[kPlanThreads * kEach];  // pages before each sequence of a pass
   __shared__ int block_at[kPlanThreads * kEach];      // and its first block that one of them is for
   __shared__ Sums warp_sum[kPlanWarps];
-  __shared__ int first_left;     // the first sequence that is not served
-  __shared__ Sums at_left;       // rows and pages of those before it
+  __shared__ Told told[kMaxRanks];
+  __shared__ int first_left;      // of this CTA's sequences
+  __shared__ Sums at_left;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const uint32_t rank = ranks > 1 ? cluster_ctarank() : 0;
+  const int rank = ranks > 1 ? (int)cluster_ctarank() : 0;
+  const int threads = blockDim.x, at_once = threads * kEach;
   const bool holds = p.n_seqs <= kHeldSeqs;
   [[maybe_unused]] const int64_t table_size = (int64_t)p.n_seqs * p.max_pages;
   const int64_t room = (int64_t)p.max_pages * kKvBlock;
-  const int threads = blockDim.x, at_once = threads * kEach;
-  if (rank == 0) {
-    int count = *p.free_count;
-    if (threadIdx.x == 0) {
-      first_left = INT32_MAX;
-      p.q_start[0] = 0;
+  const int part = (p.n_seqs + sharing - 1) / sharing, part0 = min(rank * part, p.n_seqs), part1 = min(part0 + part, p.n_seqs);
+  const bool once = part <= at_once;  // a thread's sequences stay in registers
+  auto everyone = [&](int ctas) {  // the CTAs' threads; also what they wrote to memory before
+    if (ctas > 1) {
+      __threadfence();
+      cluster_sync_all();
+    } else {
+      __syncthreads();
     }
+  };
+  // thread r of the first warp stores to CTA r; `at` in words of Told
+  auto tell = [&](int at, const uint32_t *v, int n) {
+    if (threadIdx.x < (uint32_t)sharing)
+      for (int i = 0; i < n; ++i) {
+        const uint32_t dst = smem_u32(reinterpret_cast<uint32_t *>(told + rank) + at + i);
+        if (sharing > 1) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(dst, threadIdx.x)), "r"(v[i]) : "memory");
+        else reinterpret_cast<uint32_t *>(told + rank)[at + i] = v[i];
+      }
+  };
+
+  if (rank < sharing) {
+    int count = *p.free_count;
+    if (threadIdx.x == 0) first_left = INT32_MAX;
     // of the thread's sequences: tokens after the step, blocks before it, and what they add to the sums
     int len[kEach], blocks[kEach];
     bool valid[kEach], fits[kEach];
-    Sums adds[kEach], mine, total;
-    auto load = [&](int s0) {
+    Sums adds[kEach], mine, total, before;
+    auto load = [&](int c) {
+      const int s0 = c + (int)threadIdx.x * kEach;
       mine = {0, 0, 0};
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
-        const int tokens = s0 + k < p.n_seqs ? p.tokens[s0 + k] : 0, have = s0 + k < p.n_seqs ? p.cached[s0 + k] : 0, add = max(tokens, 0);
-        valid[k] = have >= 0 && have <= room;
-        fits[k] = valid[k] && add <= p.max_rows && have + (int64_t)add <= room;
-        blocks[k] = valid[k] ? blocks_of(have) : 0;
-        len[k] = tokens < 0 || !valid[k] ? 0 : have;
-        adds[k] = {(uint32_t)min(add, (int)kFull), fits[k] && add > 0 ? (uint32_t)(blocks_of(have + add) - blocks[k]) : 0u,
-                   tokens < 0 ? (uint32_t)blocks[k] : 0u};
-        mine = mine.plus(adds[k]);
+        valid[k] = fits[k] = true;
+        len[k] = blocks[k] = 0;
+        adds[k] = mine;
       }
+      if (s0 < part1) {  // whole warps have none, where rows need more threads than sequences
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int s = s0 + k, tokens = s < part1 ? p.tokens[s] : 0, have = s < part1 ? p.cached[s] : 0, add = max(tokens, 0);
+          valid[k] = have >= 0 && have <= room;
+          fits[k] = valid[k] && add <= p.max_rows && have + (int64_t)add <= room;
+          blocks[k] = valid[k] ? blocks_of(have) : 0;
+          len[k] = tokens < 0 || !valid[k] ? 0 : have;
+          adds[k] = {(uint32_t)min(add, (int)kFull), fits[k] && add > 0 ? (uint32_t)(blocks_of(have + add) - blocks[k]) : 0u,
+                     tokens < 0 ? (uint32_t)blocks[k] : 0u};
+          mine = mine.plus(adds[k]);
+        }
+      }
+      before = scan_before(mine, warp_sum, total);
     };
     if (count < 0 || count > p.free_capacity) {
-      if (threadIdx.x == 0) report_index(p.status);
+      if (rank == 0 && threadIdx.x == 0) report_index(p.status);
       count = min(max(count, 0), p.free_capacity);
     }
-    // The sums of up to at_once sequences are formed once; with more, those of the pages that come
-    // back are formed first, as they say how many there are to hand out.
-    const bool once = p.n_seqs <= at_once;
-    Sums before{0, 0, 0};
-    uint32_t given = 0;
-    for (int c = 0; c < p.n_seqs; c += at_once) {
-      const int s0 = c + (int)threadIdx.x * kEach;
-      load(s0);
-      before = scan_before(mine, warp_sum, total);
+    // 1. sums of the part
+    Sums sum{0, 0, 0};
+    for (int c = part0; c < part1; c += at_once) {
+      load(c);
+      sum = sum.plus(total);
+    }
+    if (sharing > 1) cluster_sync_all();  // every CTA runs before another stores to it
+    {
+      const uint32_t v[3] = {sum.rows, sum.need, sum.give};
+      tell(0, v, 3);
+    }
+    everyone(sharing);
+    Sums base{0, 0, 0}, whole{0, 0, 0};
+    for (int r = 0; r < sharing; ++r) {
+      if (r == rank) base = whole;
+      whole = whole.plus(told[r].all);
+    }
+    // 2. pages come back, and the first sequence of the part that does not fit
+    const int after = (int)min((uint32_t)count + whole.give, (uint32_t)p.free_capacity);
+    Sums carry = base;
+    for (int c = part0; c < part1; c += at_once) {
+      if (!once) load(c);
       if (total.give > 0) {  // the same in all threads
         uint32_t at = before.give;
 #pragma unroll
@@ -133,65 +182,71 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, 
         for (uint32_t j = threadIdx.x; j < total.give; j += threads) {
           const int i = last_at_most(page_at, at_once, j);
           const int64_t from = (int64_t)(c + i) * p.max_pages + (j - page_at[i]);
-          const uint32_t to = (uint32_t)count + sum_to_full(given, j);
+          const uint32_t to = (uint32_t)count + sum_to_full(carry.give, j);
           if (to >= (uint32_t)p.free_capacity) report_index(p.status);  // more pages than there are
           else if (EXL3_SPAN(from, 1, table_size)) p.free_pages[to] = p.page_table[from];
         }
-        __syncthreads();
       }
-      given = sum_to_full(given, total.give);
-    }
-    count = (int)min((uint32_t)count + given, (uint32_t)p.free_capacity);
-    Sums carry{0, 0, 0};
-    for (int c = 0; c < p.n_seqs; c += at_once) {
-      const int s0 = c + (int)threadIdx.x * kEach;
-      if (!once) {
-        load(s0);
-        before = scan_before(mine, warp_sum, total);
-      }
-      // sums before each of the thread's sequences
       Sums upto = carry.plus(before);
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
-        const int s = s0 + k;
+        const int s = c + (int)threadIdx.x * kEach + k;
         upto = upto.plus(adds[k]);
-        if (s < p.n_seqs) {
+        if (s < part1) {
           if (!valid[k]) report_index(p.status);
-          if (!(fits[k] && upto.rows <= (uint32_t)p.rows && upto.need <= (uint32_t)count)) atomicMin(&first_left, s);
+          if (!(fits[k] && upto.rows <= (uint32_t)p.rows && upto.need <= (uint32_t)after)) atomicMin(&first_left, s);
         }
       }
       __syncthreads();
       upto = carry.plus(before);
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) {  // those before the first that is left end where it begins
-        if (s0 + k == first_left) at_left = upto;
+      for (int k = 0; k < kEach; ++k) {
+        if (c + (int)threadIdx.x * kEach + k == first_left) at_left = upto;
         upto = upto.plus(adds[k]);
       }
-      upto = before;
+      carry = carry.plus(total);
+    }
+    __syncthreads();
+    {
+      const uint32_t v[4] = {(uint32_t)first_left, at_left.rows, at_left.need, 0};
+      tell(3, v, 4);
+    }
+    everyone(sharing);  // and the pages that came back are there
+    int left = INT32_MAX;  // of all
+    Sums ends = whole;     // the served ones' sums
+    for (int r = 0; r < sharing; ++r)
+      if (told[r].first_left < left) {
+        left = told[r].first_left;
+        ends = told[r].before;
+      }
+    // 3. lengths, row ranges, and pages from the top
+    carry = base;
+    for (int c = part0; c < part1; c += at_once) {
+      if (!once) load(c);
+      Sums upto = before;
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
         page_at[threadIdx.x * kEach + k] = upto.need;
         block_at[threadIdx.x * kEach + k] = blocks[k];
         upto.need = sum_to_full(upto.need, adds[k].need);
       }
-      __syncthreads();
       upto = carry.plus(before);
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
-        const int s = s0 + k;
-        const bool served = s < first_left;
+        const int s = c + (int)threadIdx.x * kEach + k;
+        const bool served = s < left;
         upto = upto.plus(adds[k]);
-        if (s < p.n_seqs) {
-          const int end = (int)(served ? upto.rows : at_left.rows), now = len[k] + (served ? (int)adds[k].rows : 0);
+        if (s < part1) {
+          const int end = (int)(served ? upto.rows : ends.rows), now = len[k] + (served ? (int)adds[k].rows : 0);
           p.kv_len[s] = now;
           p.q_start[s + 1] = end;
           if (holds) held[s] = make_int2(end, now - end);
         }
       }
-      // the pages of the served ones, one after the other from the top
-      const uint32_t all = first_left < c ? 0u : first_left < c + at_once ? at_left.need - carry.need : total.need;
+      __syncthreads();
+      const uint32_t all = left < c ? 0u : left < min(c + at_once, part1) ? ends.need - carry.need : total.need;
       for (uint32_t j = threadIdx.x; j < all; j += threads) {
-        const int i = last_at_most(page_at, at_once, j), from = count - 1 - (int)(carry.need + j);
+        const int i = last_at_most(page_at, at_once, j), from = after - 1 - (int)(carry.need + j);
         const int64_t to = (int64_t)(c + i) * p.max_pages + block_at[i] + (j - page_at[i]);
         int page = EXL3_SPAN(from, 1, p.free_capacity) ? p.free_pages[from] : -1;
         if (page < 0 || page >= p.n_pages) {
@@ -202,18 +257,17 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, 
       }
       carry = carry.plus(total);
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const bool all = first_left >= p.n_seqs;
-      *p.free_left = count - (int)(all ? carry.need : at_left.need);
-      *p.served = all ? p.n_seqs : first_left;
+    if (rank == 0 && threadIdx.x == 0) {
+      p.q_start[0] = 0;
+      *p.free_left = after - (int)ends.need;
+      *p.served = min(left, p.n_seqs);
     }
-    __threadfence();
   }
-  if (ranks > 1) cluster_sync_all();
-  else __syncthreads();
-  if (rank > 0 && holds) {
+  everyone(ranks);
+  // 4. the rows
+  if (ranks > 1 && holds) {
     for (int s = threadIdx.x; s < p.n_seqs; s += threads) {
+      if (s >= part0 && s < part1) continue;
       const int end = __ldcg(p.q_start + s + 1);
       held[s] = make_int2(end, __ldcg(p.kv_len + s) - end);
     }
@@ -222,7 +276,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, 
   auto end_of = [&](int s) { return holds ? held[s].x : __ldcg(p.q_start + s + 1); };
   const int used = p.n_seqs > 0 ? end_of(p.n_seqs - 1) : 0;
   constexpr int kRows = 4;  // of a thread
-  const bool whole = ((reinterpret_cast<uintptr_t>(p.position) | reinterpret_cast<uintptr_t>(p.slot)) & 15) == 0;
+  const bool by_four = ((reinterpret_cast<uintptr_t>(p.position) | reinterpret_cast<uintptr_t>(p.slot)) & 15) == 0;
   for (int64_t r0 = ((int64_t)rank * threads + threadIdx.x) * kRows; r0 < p.rows; r0 += (int64_t)ranks * threads * kRows) {
     int pos[kRows], slot[kRows], page[kRows];
     int lo = 0;
@@ -256,7 +310,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, 
       if (pos[k] >= 0 && !ok) report_index(p.status);
       slot[k] = pos[k] >= 0 && ok ? page[k] * kKvBlock + pos[k] % kKvBlock : -1;
     }
-    if (whole && r0 + kRows <= p.rows) {
+    if (by_four && r0 + kRows <= p.rows) {
       *reinterpret_cast<int4 *>(p.position + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       *reinterpret_cast<int4 *>(p.slot + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
     } else {
@@ -273,12 +327,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, 
 }  // namespace
 
 cudaError_t launch_kv8_plan(const KvPlan &p, cudaStream_t st) {
-  // No more threads than sequences and rows give work to: 1024 for 16 rows take 7.6 us, 64 of them 3.
-  const int ranks = p.rows > 4 * kPlanThreads ? 8 : 1;
-  const int64_t work = ceil_div(ceil_div(p.rows, ranks) > p.n_seqs ? ceil_div(p.rows, ranks) : p.n_seqs, kEach);
+  const int ranks = p.rows > 4 * kPlanThreads || p.n_seqs > kPlanThreads ? kMaxRanks : 1;
+  // No more threads than sequences and rows give work to: with 1024, 16 sequences take 7.6 us, with 64 of them 5.
+  // Up to 1024 sequences are one CTA's: shared by 8, 64 of them with prompts take 10.6 us for 8.5,
+  // 4096 sequences 13.8 for 15.9.
+  const int sharing = p.n_seqs > kPlanThreads ? ranks : 1;
+  const int64_t rows = ceil_div(p.rows, ranks), seqs = ceil_div(p.n_seqs, sharing);
+  const int64_t work = ceil_div(rows > seqs ? rows : seqs, kEach);
   const int threads = work >= kPlanThreads ? kPlanThreads : work <= 64 ? 64 : (int)(ceil_div(work, 32) * 32);
   const size_t smem = p.n_seqs <= kHeldSeqs ? (size_t)p.n_seqs * sizeof(int2) : 0;
-  return launch_overlapped(kv8_plan_kernel, dim3((unsigned)ranks), threads, smem, st, ranks, p, ranks);
+  return launch_overlapped(kv8_plan_kernel, dim3((unsigned)ranks), threads, smem, st, ranks, p, ranks, sharing);
 }
 
 cudaError_t init_kv8_plan_kernels(int *status) {
