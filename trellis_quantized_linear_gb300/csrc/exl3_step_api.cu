@@ -143,7 +143,7 @@ exl3_status exl3_prompt_attention(const void *q, int64_t ldq, const void *k, int
                                   int32_t n_seqs, int64_t rows, float scale, float softcap, int causal, void *out,
                                   int64_t ldo, float *lse, void *stream) {
   if ((head_dim != 64 && head_dim != 128) || n_heads < 1 || n_heads > 65535 || n_kv_heads < 1 || n_heads % n_kv_heads ||
-      n_heads / n_kv_heads > 128 || n_seqs < 0 || n_seqs > 65535 || rows < 0 || rows * n_heads > INT32_MAX || rows > INT32_MAX ||
+      n_heads / n_kv_heads > 128 || n_seqs < 0 || n_seqs > 65535 || rows < 0 || rows > INT32_MAX || rows * n_heads > INT32_MAX ||
       !isfinite(scale) || !(softcap == 0.f || (isfinite(softcap) && softcap >= 1e-30f)))
     return EXL3_ERR_INVALID_ARG;
   const int64_t width = (int64_t)n_heads * head_dim, kv_width = (int64_t)n_kv_heads * head_dim;
