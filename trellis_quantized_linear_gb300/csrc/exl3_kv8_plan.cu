@@ -96,13 +96,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, 
   const int64_t room = (int64_t)p.max_pages * kKvBlock;
   const int part = (p.n_seqs + sharing - 1) / sharing, part0 = min(rank * part, p.n_seqs), part1 = min(part0 + part, p.n_seqs);
   const bool once = part <= at_once;  // a thread's sequences stay in registers
-  auto everyone = [&](int ctas) {  // the CTAs' threads; also what they wrote to memory before
-    if (ctas > 1) {
-      __threadfence();
-      cluster_sync_all();
-    } else {
-      __syncthreads();
-    }
+  auto everyone = [&](int ctas) {  // the CTAs' threads; releases what they wrote before, memory included
+    if (ctas > 1) cluster_sync_all();
+    else __syncthreads();
   };
   // thread r of the first warp stores to CTA r; `at` in words of Told
   auto tell = [&](int at, const uint32_t *v, int n) {
