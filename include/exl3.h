@@ -668,6 +668,7 @@ exl3_status exl3_qk_rotary(const void *x, int64_t ldx, void *out, int64_t ldo, i
  * Rows of no sequence are left as they are in out and lse, and whatever they hold in q, k
  * and v reaches no other row; so it is with the rows that a row does not see, infinities and
  * NaN among them. A row that sees an infinity or NaN in v gets it in that column (or NaN).
+ * A row whose scores are all minus infinity gets zeros, and -inf in lse.
  * A sequence whose range is not in the rows is recorded as EXL3_ERR_DEVICE_INDEX and
  * left out.
  * Sums, maxima and the softmax are fp32; the probabilities enter the product with the

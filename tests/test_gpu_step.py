@@ -282,6 +282,33 @@ def test_norm_values_that_are_not_finite_stay_in_their_row():
     assert np.all(np.isnan(got[1][5])) and np.isnan(got[1][9, 639]) and np.all(got[1][9, :639] == 0)
 
 
+@pytest.mark.parametrize("rows,cols,x_type,r_type,group",
+                         [(305, 1032, np.float16, None, 0), (305, 1152, np.float32, None, 128), (641, 1032, np.float16, np.float16, 1032),
+                          (1300, 5120, np.float16, np.float16, 0), (777, 5120, np.float32, np.float32, 128), (700, 5120, np.float32, np.float16, 5120),
+                          (330, 8200, np.float16, np.float16, 8200), (310, 10240, np.float16, np.float32, 64), (457, 13824, np.float32, None, 13824),
+                          (400, 17408, np.float16, np.float16, 32), (306, 20480, np.float16, None, 20480), (306, 20488, np.float16, None, 0),
+                          (307, 27648, np.float16, None, 128), (305, 32768, np.float32, np.float32, 64)])
+def test_norm_many_rows(rows, cols, x_type, r_type, group):
+    """More rows than two for each SM: the rows of a CTA follow one another through shared memory."""
+    x, r, w = norm_inputs(rows, cols, x_type, r_type, rows + cols, gap=8)
+    check_norm(x, r, w, cols, run_norm(x, r, w, cols, offset=1.0, group=group), offset=1.0, group=group)
+
+
+@pytest.mark.parametrize("cols", [1032, 5120, 17408])
+def test_norm_many_rows_in_place_not_finite_and_repeated(cols):
+    x, r, w = norm_inputs(1500, cols, np.float16, np.float16, cols)
+    x[5, 7], x[309, cols - 1], r[1499, 100] = np.nan, np.inf, -np.inf
+    want = run_norm(x, r, w, cols, group=cols)
+    clean = np.delete(np.arange(1500), [5, 309, 1499])
+    check_norm(x[clean], r[clean], w, cols, [t[clean] for t in want], group=cols)
+    assert np.all(np.isnan(want[1][5])) and np.all(want[1][309, :-1] == 0) and np.isnan(want[1][1499, 100])
+    for _ in range(3):
+        xd, rd = dev(x), dev(r)
+        tql.exl3_rms_norm(xd, xd, weight=dev(w), residual=rd, residual_out=rd)
+        assert np.array_equal(xd.cpu().numpy().view(np.int16), want[1].view(np.int16))
+        assert np.array_equal(rd.cpu().numpy().view(np.int16), want[0].view(np.int16))
+
+
 def test_norm_in_place():
     import torch
     x, r, w = norm_inputs(200, 5120, np.float16, np.float16, 5)
@@ -390,3 +417,75 @@ def test_rotary_values_that_are_not_finite_stay_in_their_head():
     out = run_rotary(x, 3, 1, 64, [1, 2, 3, 4], tab, False, None, None)
     differs = ~((out == clean) | (np.isnan(out) & np.isnan(clean)))
     assert sorted(zip(*np.nonzero(differs))) == [(1, 3), (1, 19), (2, 100)]
+
+
+# --------------------------------------------------------------------------- together
+
+
+def test_two_of_each_at_once_and_captured():
+    """Calls on two streams at once, and a captured graph's, give what single calls give."""
+    import torch
+    rows, qh, kh, dim = 900, 10, 2, 128
+    cols = (qh + 2 * kh) * dim
+    tab, pos = dev(table(4000, dim)), dev(np.random.default_rng(1).integers(0, 4000, rows).astype(np.int32))
+    w = dev((1 + 0.3 * np.random.default_rng(2).standard_normal(dim)).astype(np.float16))
+
+    class Work:
+        def __init__(self, seed):
+            x, r, nw = norm_inputs(rows, cols, np.float16, np.float32, seed)
+            self.x, self.r, self.w = dev(x), dev(r), dev(nw)
+            self.y = torch.zeros((rows, cols), dtype=torch.float16, device="cuda")
+            self.so = torch.zeros((rows, cols), device="cuda")
+            self.codes = torch.zeros((rows, cols), dtype=torch.uint8, device="cuda")
+            self.scales = torch.zeros((rows, cols // 128), device="cuda")
+            self.out = torch.zeros((rows, (qh + kh) * dim), dtype=torch.float16, device="cuda")
+
+        def go(self, stream=None):
+            tql.exl3_rms_norm(self.x, self.y, weight=self.w, residual=self.r, residual_out=self.so, codes=self.codes, scales=self.scales,
+                              stream=stream)
+            tql.exl3_qk_rotary(self.y, self.out, qh, kh, dim, pos, tab, q_weight=w, k_weight=w, stream=stream)
+
+        def results(self):
+            got = [t.cpu().numpy() for t in (self.y, self.so, self.codes, self.scales, self.out)]
+            for t in (self.y, self.so, self.codes, self.scales, self.out):
+                t.zero_()
+            torch.cuda.synchronize()
+            return got
+
+    works = [Work(7), Work(8)]
+    want = []
+    for k in works:
+        k.go()
+        torch.cuda.synchronize()
+        want.append(k.results())
+        check_norm(k.x.cpu().numpy(), k.r.cpu().numpy(), k.w.cpu().numpy(), cols, [want[-1][1], *(want[-1][i] for i in (0, 2, 3))], group=128)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for k, st in zip(works, streams):
+            k.go(st)
+    torch.cuda.synchronize()
+    for k, a in zip(works, want):
+        assert all(np.array_equal(g, b) for g, b in zip(k.results(), a))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for k in works:
+            k.go()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, a in zip(works, want):
+            assert all(np.array_equal(g, b) for g, b in zip(k.results(), a))
+
+
+def test_two_plans_at_once():
+    import torch
+    plans = [Plan(*random_requests(n, 30, 700, n)) for n in (1500, 90)]
+    for p in plans:
+        p.call()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for p, st in zip(plans, streams):
+            p.again(st)
+    torch.cuda.synchronize()
+    for p in plans:
+        p.check()

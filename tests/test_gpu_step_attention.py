@@ -65,8 +65,7 @@ def check(x, q_start, heads, kv_heads, dim, scale, cap, causal, out, lse):
         n = int(z - a)
         if n <= 0:
             continue
-        qa = np.abs(np.nan_to_num(q[a:z].astype(np.float64))).reshape(n, heads, dim)
-        ka = np.abs(np.nan_to_num(k[a:z].astype(np.float64))).reshape(n, kv_heads, dim)
+        qa, ka = (np.abs(np.nan_to_num(t[a:z].astype(np.float64), posinf=0, neginf=0)).reshape(n, -1, dim) for t in (q, k))
         parts = np.stack([qa[:, h] @ ka[:, h // g].T for h in range(heads)], 1).max(2) * abs(scale)
         off = parts * (dim / 16) * 2.0 ** -22 + 2.0 ** -19 + (2.0 ** -19 * np.minimum(parts, cap) if cap else parts * 2.0 ** -22)
         vmax = np.abs(np.where(np.isfinite(v[a:z]), v[a:z], 0).astype(np.float64)).max(initial=0.0)
@@ -150,6 +149,48 @@ def test_keys_and_queries_that_are_not_finite(causal):
     x[200, 3] = np.nan                 # one query row
     out, lse = run(x, qs, heads, kv_heads, dim, dim ** -0.5, causal=causal)
     check(x, qs, heads, kv_heads, dim, dim ** -0.5, 0.0, causal, out, lse)
+
+
+@pytest.mark.parametrize("cap", [0.0, 3.0])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,at", [([200, 140], [5, 250]), ([400], [130]), ([1, 300], [1, 300])])
+def test_infinite_scores(cap, causal, lens, at):
+    """An infinite key: a score of infinity for half of the rows that see it (NaN), of minus
+    infinity for the others (no part in the sum); capped, plus and minus the cap."""
+    heads, kv_heads, dim = 6, 2, 64
+    x, qs = inputs(sum(lens), heads, kv_heads, dim, 21), starts(lens)
+    g = np.random.default_rng(3)
+    d = np.arange(heads) * dim + 9
+    x[:, d] = np.where(g.random((len(x), heads)) < 0.5, 1, -1) * (np.abs(x[:, d]) + 0.25)
+    for r in at:
+        x[r, d] = np.abs(x[r, d])  # else a row that sees nothing else has no score
+        x[r, heads * dim + 9::dim][:kv_heads] = np.inf
+    out, lse = run(x, qs, heads, kv_heads, dim, dim ** -0.5, cap, causal)
+    check(x, qs, heads, kv_heads, dim, dim ** -0.5, cap, causal, out, lse)
+
+
+def test_a_row_of_minus_infinity_alone():
+    x = inputs(131, 2, 1, 64, 22)
+    x[:, 5] = -1.0              # first head
+    x[:, 2 * 64 + 5] = np.inf   # every key
+    out, lse = run(x, [0, 1, 131], 2, 1, 64, 0.125)
+    assert not out[:, :64].any() and np.all(lse[:, 0] == -np.inf)
+
+
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 0.5, 8.0, 30.0, 1e38])
+@pytest.mark.parametrize("q_gain", [0.1, 3.0, 60.0])
+def test_caps_far_below_and_far_above_the_scores(cap, q_gain):
+    x, qs = inputs(700, 6, 2, 128, 23, q_gain=q_gain), starts([500, 200])
+    x[::7, :6 * 128] /= 16  # rows of small scores beside those of large ones
+    out, lse = run(x, qs, 6, 2, 128, 128 ** -0.5, cap)
+    check(x, qs, 6, 2, 128, 128 ** -0.5, cap, True, out, lse)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,lens", [(4, 2, 128, [1500, 3, 700]), (12, 2, 64, [1100, 1024])])
+def test_long_whole_sequences(heads, kv_heads, dim, lens):
+    x, qs = inputs(sum(lens), heads, kv_heads, dim, 24), starts(lens)
+    out, lse = run(x, qs, heads, kv_heads, dim, dim ** -0.5, 20.0, causal=False)
+    check(x, qs, heads, kv_heads, dim, dim ** -0.5, 20.0, False, out, lse)
 
 
 def test_heavy_and_growing_scores():

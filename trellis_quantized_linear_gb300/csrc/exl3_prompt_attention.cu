@@ -396,178 +396,178 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   // 168 registers a thread at launch: the last four warps give 12288 of theirs to the others
   if (warp >= kMmaWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == kMmaWarp) {
-    // ---------------- tensor core (one lane) ----------------
-    if (elect_one()) {
-      // bit 13: A negated, for a negative scale
-      const uint32_t idesc_s = f16_idesc(kTile, kTokens) | (p.a.scale < 0.f ? 1u << 13 : 0u);
-      constexpr uint32_t kIdescO = f16_idesc(kTile, D) | kIdescBTransposed;
-      uint32_t unit = 0, number = 0, items_of[2] = {0, 0}, units_of[2] = {0, 0};
-      auto ready = [&](uint32_t u) { return mbar_wait(bar(kPReady + u % kStages), (u / kStages) & 1, status); };
-      auto scores = [&](int t, uint32_t u) {
-        const uint32_t q = base + t * Cfg::kOperand, k = base + Cfg::kOffK + (u % kStages) * Cfg::kOperand;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const uint32_t off = (j >> 2) * (128 * 128) + (j & 3) * 32;
-          tc_mma(tmem + 128 * t, sw128_desc(q + off), sw128_desc(k + off), idesc_s, j > 0);
-        }
-        tc_commit(bar(kPS + t));
-      };
-      bool ok = item_there(0);
-      Item it;
-      read_item(0, it);
-      if (ok && it.there) ok = mbar_wait(bar(kPFirst), 0, status);
-      while (ok && it.there) {
-        const int units[2] = {it.units0, it.units1}, all = it.all();
-        item_read(number++);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || units[t] == 0) continue;
-          ok = mbar_wait(bar(kPQFull + t), items_of[t]++ & 1, status);
-          if (!ok) break;
-          tc_fence_after();
-          scores(t, unit);
-        }
-        for (int j = 0; ok && j < all; ++j, ++unit) {
-          ok = ready(unit);
-          const uint32_t v = base + Cfg::kOffV + (unit % kStages) * Cfg::kOperand;
-#pragma unroll
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kMmaWarp) {
+      // ---------------- tensor core (one lane) ----------------
+      if (elect_one()) {
+        // bit 13: A negated, for a negative scale
+        const uint32_t idesc_s = f16_idesc(kTile, kTokens) | (p.a.scale < 0.f ? 1u << 13 : 0u);
+        constexpr uint32_t kIdescO = f16_idesc(kTile, D) | kIdescBTransposed;
+        uint32_t unit = 0, number = 0, items_of[2] = {0, 0}, units_of[2] = {0, 0};
+        auto ready = [&](uint32_t u) { return mbar_wait(bar(kPReady + u % kStages), (u / kStages) & 1, status); };
+        auto scores = [&](int t, uint32_t u) {
+          const uint32_t q = base + t * Cfg::kOperand, k = base + Cfg::kOffK + (u % kStages) * Cfg::kOperand;
+  #pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const uint32_t off = (j >> 2) * (128 * 128) + (j & 3) * 32;
+            tc_mma(tmem + 128 * t, sw128_desc(q + off), sw128_desc(k + off), idesc_s, j > 0);
+          }
+          tc_commit(bar(kPS + t));
+        };
+        bool ok = item_there(0);
+        Item it;
+        read_item(0, it);
+        if (ok && it.there) ok = mbar_wait(bar(kPFirst), 0, status);
+        while (ok && it.there) {
+          const int units[2] = {it.units0, it.units1}, all = it.all();
+          item_read(number++);
+  #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (!ok || j >= units[t]) continue;
-            const uint32_t ph = units_of[t]++ & 1;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              ok = ok && mbar_wait(bar(kPP + 2 * t + half), ph, status);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                tc_mma_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, sw128_mn_desc(v + k * 2048, 128 * 128, 1024), kIdescO, (j | k) > 0);
-            }
+            if (!ok || units[t] == 0) continue;
+            ok = mbar_wait(bar(kPQFull + t), items_of[t]++ & 1, status);
             if (!ok) break;
-            if (j + 1 < units[t]) scores(t, unit + 1);
-            else tc_commit(bar(kPO + t));
+            tc_fence_after();
+            scores(t, unit);
           }
-        }
-        ok = ok && item_there(number);
-        read_item(number, it);
-      }
-      tc_commit(bar(kPDone));  // every issued product ends before the TMEM is released
-      mbar_wait_short(bar(kPDone), 0);
-    }
-  } else if (warp == kLoadWarp) {
-    // ---------------- items and loads (one lane) ----------------
-    if (elect_one()) {
-      uint32_t unit = 0, number = 0, items_of[2] = {0, 0};
-      bool ok = true;
-      const uint32_t q_bytes = (uint32_t)(Cfg::kHalves * 128) * p.group * p.tile_tokens;
-      auto operand = [&](const CUtensorMap *map, uint32_t dst, uint32_t b, int head, int row) {
-#pragma unroll
-        for (int hf = 0; hf < Cfg::kHalves; ++hf)
-          if (EXL3_RANGE(row, 0, p.a.rows) && EXL3_SMEM(dst + hf * (128 * 128), 128 * 128))
-            tma_load_3d(dst + hf * (128 * 128), map, b, 64 * hf, head, row);
-      };
-      auto announce = [&](const Item &it) {
-        ok = ok && mbar_wait(bar(kPItemEmpty + number % kItems), ((number / kItems) & 1) ^ 1, status);
-        if (!ok) return;
-        items[2 * (number % kItems)] = make_int4(it.row0, it.n, it.h, it.token0);
-        items[2 * (number % kItems) + 1] = make_int4(it.units0, it.units1, it.first_masked, it.there);
-        mbar_arrive(bar(kPItemFull + number % kItems));
-        ++number;
-      };
-      // In any order, but each unit's before the next one with its slot is loaded.
-      auto passed = [&](uint32_t u) { return mbar_wait(bar(kPPassed + u % kStages), (u / kStages) & 1, status); };
-      auto keys = [&](uint32_t u, uint32_t b, const Item &it, int j) {
-        mbar_arrive_expect_tx(b, Cfg::kOperand);
-        operand(&tk, base + Cfg::kOffK + (u % kStages) * Cfg::kOperand, b, it.h, it.row0 + j * kTokens);
-      };
-      walk.begin(p.a.causal);
-      Item it, next;
-      it.there = walk.next(p, it);
-      announce(it);
-      const bool any = it.there;
-      if (any) keys(0, bar(kPFirst), it, 0);
-      while (ok && it.there) {
-        ok = unit == 0 || passed(unit - 1);  // the last item's scores: its queries are not needed any more
-        if (!ok) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if ((t == 0 ? it.units0 : it.units1) == 0) continue;
-          ++items_of[t];
-          mbar_arrive_expect_tx(bar(kPQFull + t), q_bytes);
-          operand(&tq, base + t * Cfg::kOperand, bar(kPQFull + t), it.h * p.group, it.row0 + it.token0 + t * p.tile_tokens);
-        }
-        next.there = walk.next(p, next);
-        const int all = it.all();
-        for (int j = 0; ok && j < all; ++j, ++unit) {
-          const uint32_t st = unit % kStages;
-          ok = unit + 1 < kStages || passed(unit + 1 - kStages);
-          if (!ok) break;
-          mbar_arrive_expect_tx(bar(kPVFull + st), Cfg::kOperand);
-          operand(&tv, base + Cfg::kOffV + st * Cfg::kOperand, bar(kPVFull + st), it.h, it.row0 + j * kTokens);
-          if (j == 0) announce(next);
-          if (j + 1 < all) keys(unit + 1, bar(kPReady + st), it, j + 1);
-          else if (next.there) keys(unit + 1, bar(kPReady + st), next, 0);
-          else mbar_arrive(bar(kPReady + st));
-        }
-        it = next;
-      }
-      // nothing is on its way into this CTA's memory when it ends (at once, unless a wait ran out)
-      if (any) mbar_wait_short(bar(kPFirst), 0);
-      for (uint32_t i = 0; i < kStages; ++i)
-        if (unit > i) {
-          mbar_wait_short(bar(kPVFull + i), ((unit - 1 - i) / kStages) & 1);
-          mbar_wait_short(bar(kPReady + i), ((unit - 1 - i) / kStages) & 1);
-        }
-      for (int t = 0; t < 2; ++t)
-        if (items_of[t] > 0) mbar_wait_short(bar(kPQFull + t), (items_of[t] - 1) & 1);
-    }
-  } else {
-    // ---------------- values that not every row may use ----------------
-    uint32_t unit = 0, number = 0;
-    Item it;
-    for (bool ok = true;; ++number) {
-      ok = __all_sync(0xffffffffu, ok && item_there(number));
-      if (!ok) break;
-      read_item(number, it);
-      __syncwarp();
-      if (lane == 0) item_read(number);
-      if (!it.there) break;
-      const int all = it.all();
-      for (int j = 0; j < all; ++j, ++unit) {
-        const uint32_t st = unit % kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(kPVFull + st), (unit / kStages) & 1, status));
-        if (!ok) break;
-        if (j >= it.first_masked) {
-          const uint32_t v = base + Cfg::kOffV + st * Cfg::kOperand;
-          const int left = it.n - j * kTokens;  // tokens of the sequence from here
-          bool found = false;
-#pragma unroll 4
-          for (int i = (warp - kCleanWarp) * 32 + lane; i < Cfg::kHalves * 128 * 8; i += kCleanWarps * 32) {
-            const uint32_t addr = v + i * 16;
-            const bool there = ((i >> 3) & 127) < left;
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
-            const uint32_t bad = not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3]);
-            if (!there || bad) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t b = not_finite(w[e]);
-                w[e] = there ? w[e] & ~((b & 0x8000u ? 0xFFFFu : 0u) | (b & 0x80000000u ? 0xFFFF0000u : 0u)) : 0u;
+          for (int j = 0; ok && j < all; ++j, ++unit) {
+            ok = ready(unit);
+            const uint32_t v = base + Cfg::kOffV + (unit % kStages) * Cfg::kOperand;
+  #pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!ok || j >= units[t]) continue;
+              const uint32_t ph = units_of[t]++ & 1;
+  #pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                ok = ok && mbar_wait(bar(kPP + 2 * t + half), ph, status);
+                if (!ok) break;
+                tc_fence_after();
+  #pragma unroll
+                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                  tc_mma_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, sw128_mn_desc(v + k * 2048, 128 * 128, 1024), kIdescO, (j | k) > 0);
               }
-              sts16(addr, w[0], w[1], w[2], w[3]);
-              found = found || (there && bad);
+              if (!ok) break;
+              if (j + 1 < units[t]) scores(t, unit + 1);
+              else tc_commit(bar(kPO + t));
             }
           }
-          if (found) flags[number % kFlags] = number + 1;
-          fence_proxy_async_shared();
-          __syncwarp();
+          ok = ok && item_there(number);
+          read_item(number, it);
         }
-        if (lane == 0) mbar_arrive(bar(kPReady + st));  // of every unit: the ring cannot get ahead of this warp
+        tc_commit(bar(kPDone));  // every issued product ends before the TMEM is released
+        mbar_wait_short(bar(kPDone), 0);
+      }
+    } else if (warp == kLoadWarp) {
+      // ---------------- items and loads (one lane) ----------------
+      if (elect_one()) {
+        uint32_t unit = 0, number = 0, items_of[2] = {0, 0};
+        bool ok = true;
+        const uint32_t q_bytes = (uint32_t)(Cfg::kHalves * 128) * p.group * p.tile_tokens;
+        auto operand = [&](const CUtensorMap *map, uint32_t dst, uint32_t b, int head, int row) {
+  #pragma unroll
+          for (int hf = 0; hf < Cfg::kHalves; ++hf)
+            if (EXL3_RANGE(row, 0, p.a.rows) && EXL3_SMEM(dst + hf * (128 * 128), 128 * 128))
+              tma_load_3d(dst + hf * (128 * 128), map, b, 64 * hf, head, row);
+        };
+        auto announce = [&](const Item &it) {
+          ok = ok && mbar_wait(bar(kPItemEmpty + number % kItems), ((number / kItems) & 1) ^ 1, status);
+          if (!ok) return;
+          items[2 * (number % kItems)] = make_int4(it.row0, it.n, it.h, it.token0);
+          items[2 * (number % kItems) + 1] = make_int4(it.units0, it.units1, it.first_masked, it.there);
+          mbar_arrive(bar(kPItemFull + number % kItems));
+          ++number;
+        };
+        // In any order, but each unit's before the next one with its slot is loaded.
+        auto passed = [&](uint32_t u) { return mbar_wait(bar(kPPassed + u % kStages), (u / kStages) & 1, status); };
+        auto keys = [&](uint32_t u, uint32_t b, const Item &it, int j) {
+          mbar_arrive_expect_tx(b, Cfg::kOperand);
+          operand(&tk, base + Cfg::kOffK + (u % kStages) * Cfg::kOperand, b, it.h, it.row0 + j * kTokens);
+        };
+        walk.begin(p.a.causal);
+        Item it, next;
+        it.there = walk.next(p, it);
+        announce(it);
+        const bool any = it.there;
+        if (any) keys(0, bar(kPFirst), it, 0);
+        while (ok && it.there) {
+          ok = unit == 0 || passed(unit - 1);  // the last item's scores: its queries are not needed any more
+          if (!ok) break;
+  #pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if ((t == 0 ? it.units0 : it.units1) == 0) continue;
+            ++items_of[t];
+            mbar_arrive_expect_tx(bar(kPQFull + t), q_bytes);
+            operand(&tq, base + t * Cfg::kOperand, bar(kPQFull + t), it.h * p.group, it.row0 + it.token0 + t * p.tile_tokens);
+          }
+          next.there = walk.next(p, next);
+          const int all = it.all();
+          for (int j = 0; ok && j < all; ++j, ++unit) {
+            const uint32_t st = unit % kStages;
+            ok = unit + 1 < kStages || passed(unit + 1 - kStages);
+            if (!ok) break;
+            mbar_arrive_expect_tx(bar(kPVFull + st), Cfg::kOperand);
+            operand(&tv, base + Cfg::kOffV + st * Cfg::kOperand, bar(kPVFull + st), it.h, it.row0 + j * kTokens);
+            if (j == 0) announce(next);
+            if (j + 1 < all) keys(unit + 1, bar(kPReady + st), it, j + 1);
+            else if (next.there) keys(unit + 1, bar(kPReady + st), next, 0);
+            else mbar_arrive(bar(kPReady + st));
+          }
+          it = next;
+        }
+        // nothing is on its way into this CTA's memory when it ends (at once, unless a wait ran out)
+        if (any) mbar_wait_short(bar(kPFirst), 0);
+        for (uint32_t i = 0; i < kStages; ++i)
+          if (unit > i) {
+            mbar_wait_short(bar(kPVFull + i), ((unit - 1 - i) / kStages) & 1);
+            mbar_wait_short(bar(kPReady + i), ((unit - 1 - i) / kStages) & 1);
+          }
+        for (int t = 0; t < 2; ++t)
+          if (items_of[t] > 0) mbar_wait_short(bar(kPQFull + t), (items_of[t] - 1) & 1);
+      }
+    } else {
+      // ---------------- values that not every row may use ----------------
+      uint32_t unit = 0, number = 0;
+      Item it;
+      for (bool ok = true;; ++number) {
+        ok = __all_sync(0xffffffffu, ok && item_there(number));
+        if (!ok) break;
+        read_item(number, it);
+        __syncwarp();
+        if (lane == 0) item_read(number);
+        if (!it.there) break;
+        const int all = it.all();
+        for (int j = 0; j < all; ++j, ++unit) {
+          const uint32_t st = unit % kStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(kPVFull + st), (unit / kStages) & 1, status));
+          if (!ok) break;
+          if (j >= it.first_masked) {
+            const uint32_t v = base + Cfg::kOffV + st * Cfg::kOperand;
+            const int left = it.n - j * kTokens;  // tokens of the sequence from here
+            bool found = false;
+  #pragma unroll 4
+            for (int i = (warp - kCleanWarp) * 32 + lane; i < Cfg::kHalves * 128 * 8; i += kCleanWarps * 32) {
+              const uint32_t addr = v + i * 16;
+              const bool there = ((i >> 3) & 127) < left;
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+              const uint32_t bad = not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3]);
+              if (!there || bad) {
+  #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t b = not_finite(w[e]);
+                  w[e] = there ? w[e] & ~((b & 0x8000u ? 0xFFFFu : 0u) | (b & 0x80000000u ? 0xFFFF0000u : 0u)) : 0u;
+                }
+                sts16(addr, w[0], w[1], w[2], w[3]);
+                found = found || (there && bad);
+              }
+            }
+            if (found) flags[number % kFlags] = number + 1;
+            fence_proxy_async_shared();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(bar(kPReady + st));  // of every unit: the ring cannot get ahead of this warp
+        }
       }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---------------- softmax: thread = row of tile t ----------------
