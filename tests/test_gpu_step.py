@@ -287,9 +287,13 @@ def test_norm_values_that_are_not_finite_stay_in_their_row():
                           (1300, 5120, np.float16, np.float16, 0), (777, 5120, np.float32, np.float32, 128), (700, 5120, np.float32, np.float16, 5120),
                           (330, 8200, np.float16, np.float16, 8200), (310, 10240, np.float16, np.float32, 64), (457, 13824, np.float32, None, 13824),
                           (400, 17408, np.float16, np.float16, 32), (306, 20480, np.float16, None, 20480), (306, 20488, np.float16, None, 0),
-                          (307, 27648, np.float16, None, 128), (305, 32768, np.float32, np.float32, 64)])
+                          (307, 27648, np.float16, None, 128), (305, 32768, np.float32, np.float32, 64),
+                          (305, 264, np.float16, np.float16, 264), (1000, 512, np.float32, None, 64), (321, 520, np.float16, np.float32, 0),
+                          (3001, 640, np.float16, np.float16, 64), (400, 1024, np.float32, np.float16, 1024), (456, 5120, np.float16, None, 64),
+                          (153, 8200, np.float16, np.float16, 0), (500, 2048, np.float16, np.float16, 32), (500, 2056, np.float16, np.float32, 0),
+                          (1217, 2560, np.float16, np.float16, 128), (460, 17408, np.float16, np.float32, 0), (153, 17408, np.float32, np.float32, 0)])
 def test_norm_many_rows(rows, cols, x_type, r_type, group):
-    """More rows than two for each SM: the rows of a CTA follow one another through shared memory."""
+    """A row by a warp, by a CTA, and many rows of a CTA one behind the other through shared memory."""
     x, r, w = norm_inputs(rows, cols, x_type, r_type, rows + cols, gap=8)
     check_norm(x, r, w, cols, run_norm(x, r, w, cols, offset=1.0, group=group), offset=1.0, group=group)
 

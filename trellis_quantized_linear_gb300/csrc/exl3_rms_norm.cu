@@ -4,9 +4,14 @@
 // A row is read once and stays in registers until its outputs are stored: 8 elements a
 // thread and piece, the sum of squares by shuffles and, where a row has more than a warp, one
 // exchange through shared memory. Bound by the bytes, or by launch and one row's latency.
-// Many rows of more than a warp come by bulk copies into a ring of shared memory, several
-// rows ahead of the one that is worked on: loads into registers have a row at a time in
-// flight for each resident CTA.
+// Many rows of more than 2048 columns come by bulk copies into a ring of shared memory, the
+// next rows while one is worked on: loads into registers have a row at a time in flight for
+// each resident CTA.
+//
+// Measured (in a graph, residual read and written): one row of 5120 fp16 1.9 us; 8192 rows
+// 57 us (5.9 TB/s; loads into registers 67); 777 rows fp32 with E4M3 codes 11.6 us (4.5 TB/s:
+// 2.6 rows for each CTA of the ring, 3 for some); 2400 rows of 17408 58 us (5.8 TB/s, from
+// registers 94). The rules between the forms stand at by_size, with both sides.
 #include <math.h>
 
 #include <type_traits>
@@ -20,8 +25,8 @@ namespace {
 
 constexpr float kCodeMax = 448.0f, kLeastScale = 0x1p-40f;
 constexpr int kWarpRowThreads = 256;
-constexpr int kRingThreads = 640, kMaxStages = 8;  // two CTAs an SM with two pieces a thread, one with four
-constexpr int kRingBytes = 108 * 1024;
+constexpr int kRingThreads = 640, kMaxStages = 8;  // two CTAs an SM with two pieces a thread (more of fewer threads), one with four
+constexpr int kRingBytes = 220 * 1024, kRingOther = 2 * 1024;  // of an SM's shared memory; what a CTA has besides its stages
 
 struct Eight {
   float v[8];
@@ -296,7 +301,9 @@ __global__ void __launch_bounds__(kRingThreads, V <= 2 ? 2 : 1) rms_norm_ring_ke
 template <typename X, typename R, int V, bool CTA_ROW>
 cudaError_t launch(const exl3_norm &p, int threads, int lanes, int num_sms, cudaStream_t st) {
   const int64_t ctas = CTA_ROW ? p.rows : ceil_div(p.rows, threads / lanes);
-  const int64_t most = (int64_t)num_sms * (2048 / threads);
+  // Rows of one piece a thread have a CTA each: 8192 rows of 2048 fp16 take 23.7 us, 25.5 from CTAs that stay; the widest
+  // ones stay, with their weight (1000 rows of 17408 fp32: 54.1 us, 57.7 with a CTA each).
+  const int64_t most = CTA_ROW && V == 1 ? INT32_MAX : (int64_t)num_sms * (2048 / threads);
   return launch_overlapped(rms_norm_kernel<X, R, V, CTA_ROW>, dim3((unsigned)(ctas < most ? ctas : most)), threads, 0, st, 1, p, lanes);
 }
 
@@ -309,7 +316,9 @@ constexpr int element_bytes() {
 template <typename X, typename R>
 cudaError_t by_size(const exl3_norm &p, int num_sms, int *status, cudaStream_t st) {
   const int pieces = (int)(p.cols / 8);
-  if (pieces <= 128) {  // a row is a warp's, or a part's
+  // A row of at most 1024 columns is a warp's, or a part's; where rows are few, one of more than 256 is a CTA's: 304 rows of
+  // 1024 take 1.8 us, 2.3 by warps; 608 rows 2.8 and 2.3, 8192 rows 25 and 13.3.
+  if (pieces <= 32 || (pieces <= 128 && p.rows > 2 * num_sms)) {
     int lanes = 16;
     while (lanes < 32 && lanes < pieces) lanes *= 2;
     if (pieces <= 32) return launch<X, R, 1, false>(p, kWarpRowThreads, lanes, num_sms, st);
@@ -317,11 +326,19 @@ cudaError_t by_size(const exl3_norm &p, int num_sms, int *status, cudaStream_t s
                         : launch<X, R, 4, false>(p, kWarpRowThreads, lanes, num_sms, st);
   }
   auto threads = [&](int v) { return (int)(ceil_div(ceil_div(pieces, v), 32) * 32); };
-  const int stage = (int)p.cols * element_bytes<X, R>(), stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;
-  if (p.rows > 2 * num_sms && stages >= 2 && threads(4) <= kRingThreads) {
-    const int t = threads(2) <= kRingThreads ? threads(2) : threads(4);
-    return launch_overlapped(t == threads(2) ? rms_norm_ring_kernel<X, R, 2> : rms_norm_ring_kernel<X, R, 4>, t == threads(2) ? 2 * num_sms : num_sms, t,
-                             (size_t)stages * stage, st, 1, p, stages, stage, status);
+  // The ring, with as many CTAs as have two stages each: from three rows an SM on (fp16: 500 rows of 5120 3.9 us, 4.4 from
+  // registers; 400 rows 4.0 and 3.9; 8192 rows 57 and 67) and above 2048 columns (8192 rows of 2560: 29.7 and 33.7; of 2048:
+  // 24.6 and 23.7). Rows too wide for one piece a thread: from one an SM on (160 rows of 17408: 5.9 us and 9.2; 2400: 58 and 94).
+  if (pieces > 256 && p.rows > (threads(1) > 1024 ? 1 : 3) * num_sms && threads(4) <= kRingThreads) {
+    const bool two = threads(2) <= kRingThreads;
+    const int t = threads(two ? 2 : 4), stage = (int)p.cols * element_bytes<X, R>();
+    auto stages_of = [&](int ctas) { return ((kRingBytes + kRingOther) / ctas - kRingOther) / stage; };
+    int ctas = two ? 2 * kRingThreads / t : 1;
+    while (ctas > 1 && stages_of(ctas) < 2) --ctas;
+    const int stages = stages_of(ctas) < kMaxStages ? stages_of(ctas) : kMaxStages;
+    if (stages >= 2)
+      return launch_overlapped(two ? rms_norm_ring_kernel<X, R, 2> : rms_norm_ring_kernel<X, R, 4>, ctas * num_sms, t, (size_t)stages * stage, st, 1,
+                               p, stages, stage, status);
   }
   if (threads(1) <= 1024) return launch<X, R, 1, true>(p, threads(1), 32, num_sms, st);
   return launch<X, R, 4, true>(p, threads(4), 32, num_sms, st);
