@@ -405,6 +405,30 @@ def test_rotary_rows_and_far_positions(rows):
     check_rotary(x, out, 2, 1, 64, pos, tab, False, None, None)
 
 
+@pytest.mark.parametrize("dim,qh,kh", [(128, 1, 0), (128, 2, 1), (128, 8, 1), (128, 15, 1), (128, 16, 1), (64, 5, 5), (64, 31, 1), (64, 32, 1)])
+@pytest.mark.parametrize("rows", [1, 2, 31, 1217, 3001])
+def test_rotary_few_heads(dim, qh, kh, rows):
+    """Several rows of a CTA at once, with rows among them that are left as they are."""
+    g = np.random.default_rng(rows + qh)
+    x = g.standard_normal((rows, (qh + kh) * dim + 8)).astype(np.float16)
+    pos = g.integers(-300, 1000, rows)
+    qw, kw = ((1 + 0.3 * g.standard_normal(dim)).astype(np.float16) if n else None for n in (qh, kh))
+    for in_place in (False, True):
+        out = run_rotary(x, qh, kh, dim, pos, table(1000, dim // 2), False, qw, kw, in_place=in_place)
+        check_rotary(x, out, qh, kh, dim, pos, table(1000, dim // 2), False, qw, kw, in_place=in_place)
+    assert tql.exl3_get_device_status() == 0
+
+
+@pytest.mark.parametrize("qh,kh", [(2, 1), (40, 8)])
+def test_rotary_positions_past_the_table_among_others(qh, kh):
+    g = np.random.default_rng(qh)
+    x = g.standard_normal((100, (qh + kh) * 64 + 8)).astype(np.float16)
+    pos = g.integers(0, 130, 100)
+    out = run_rotary(x, qh, kh, 64, pos, table(100, 64), True, None, None)
+    check_rotary(x, out, qh, kh, 64, pos, table(100, 64), True, None, None)
+    assert tql.exl3_get_device_status() == 10
+
+
 def test_rotary_positions_past_the_table():
     x = np.random.default_rng(1).standard_normal((9, 128)).astype(np.float16)
     pos = [0, 99, 100, -1, 2**31 - 1, -2**31, 5, 98, 101]

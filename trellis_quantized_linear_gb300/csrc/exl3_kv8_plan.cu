@@ -1,11 +1,17 @@
 // Block tables, lengths, positions and slots of a step from its requests' lengths.
 // Contract in include/exl3.h.
 //
-// One cluster. Its CTAs have a contiguous part of the sequences each (four a thread): prefix
-// sums of rows and of pages, joined through shared memory of the cluster, then the pages, a
-// thread each, and after a last barrier the rows' positions and slots, four rows a thread,
-// which finds the first one's sequence by a binary search in shared memory. All latency: a few
-// dependent loads and three barriers of the cluster one after the other.
+// The prefix sums of rows and of pages over the sequences say everything: who is served, whose
+// pages are whose, where a row lies. One cluster: its CTAs have a contiguous part of the
+// sequences each (four a thread), join their sums through shared memory of the cluster, then
+// hand out the pages, a thread each, and after a last barrier the rows' positions and slots,
+// four rows a thread, which finds the first one's sequence by a binary search in shared memory.
+// Few sequences are one CTA's, and many rows are still shared by the cluster.
+//
+// All latency: the bytes are some hundred KB at most, and a few dependent loads stand one after
+// the other, with the barriers between them. Measured (in a graph): 16 sequences of one token
+// 5.0 us; 64 with 16 prompts, 16K rows 8.5; 4096 sequences, 18K rows 12.7 (15.9 by one CTA; a fence at
+// each of the cluster's barriers 13.2).
 #include "exl3_internal.h"
 #include "exl3_kv8.cuh"
 

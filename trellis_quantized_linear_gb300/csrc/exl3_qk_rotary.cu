@@ -1,8 +1,12 @@
 // Norm and rotation of query and key heads. Formulas in include/exl3.h.
 //
 // A thread has 16 elements of a head, in two pieces of 8 that hold both partners of its
-// 8 pairs, and the angles of those pairs in registers for all heads that it works on: a
-// row's table entry is read once a CTA. Bound by the bytes.
+// 8 pairs, and the angles of those pairs in registers for all heads of the row that it works
+// on. Bound by the bytes, or by launch and the way position - angles - store.
+//
+// Measured (in a graph, 48 heads of 128, normed): 16 rows 2.0 us, 6827 rows 27.8 us (6.0 TB/s;
+// loads after the position 33.8). 9 heads, a row at a time 12.7 us, several 8.0; 3 heads
+// 10.2 and 3.9.
 #include "exl3_internal.h"
 #include "exl3_kv8.cuh"
 
@@ -10,7 +14,7 @@ namespace exl3 {
 
 namespace {
 
-constexpr int kRotaryThreads = 128, kAhead = 3;
+constexpr int kRotaryThreads = 128, kFlatThreads = 256;
 
 struct Piece {
   float v[8];
@@ -36,24 +40,29 @@ struct Piece {
 };
 
 // D / 16 lanes a head; blockIdx.y takes its share of the heads, `each` of them. A thread's
-// heads are loaded kAhead at a time, before the position is there.
-template <int D, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kRotaryThreads) qk_rotary_kernel(const QkRotary p, int each) {
+// heads are loaded kAhead at a time, before the position is there. FLAT: a CTA has `tall` rows
+// at once, a head for each place.
+template <int D, bool INTERLEAVED, bool NORM, bool FLAT>
+__global__ void __launch_bounds__(FLAT ? kFlatThreads : kRotaryThreads) qk_rotary_kernel(const QkRotary p, int each, int tall) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kLanes = D / 16, kAtOnce = kRotaryThreads / kLanes;
-  const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
+  constexpr int kLanes = D / 16, kAtOnce = (FLAT ? kFlatThreads : kRotaryThreads) / kLanes, kAhead = FLAT ? 1 : 3;
+  const int l = threadIdx.x % kLanes, place = threadIdx.x / kLanes;
   const int heads = p.q_heads + p.k_heads, h0 = blockIdx.y * each, h1 = min(h0 + each, heads);
+  const int below = FLAT ? place / heads : 0, slot = place - below * heads;
   const bool turns = 16 * l < p.rot_dim;
   // first elements of the two pieces
   const int a0 = INTERLEAVED || !turns ? 16 * l : 8 * l;
   const int b0 = INTERLEAVED || !turns ? 16 * l + 8 : p.rot_dim / 2 + 8 * l;
   [[maybe_unused]] const int64_t size_x = (int64_t)(p.rows - 1) * p.ldx + (int64_t)heads * D;
   [[maybe_unused]] const int64_t size_o = (int64_t)(p.rows - 1) * p.ldo + (int64_t)heads * D;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const int pos = p.position[row];
+  const int rows_at_once = FLAT ? tall : 1;
+  for (int64_t first_row = (int64_t)blockIdx.x * rows_at_once; first_row < p.rows; first_row += (int64_t)gridDim.x * rows_at_once) {
+    const int64_t row = first_row + below;
+    const bool mine = !FLAT || (below < tall && row < p.rows);
+    const int pos = mine ? p.position[row] : -1;
     float cs[8], sn[8];
-    bool known = false;
+    bool known = false, turned = true;
     for (int first = h0; first < h1; first += kAhead * kAtOnce) {
       uint4 ra[kAhead], rb[kAhead];
 #pragma unroll
@@ -61,21 +70,19 @@ __global__ void __launch_bounds__(kRotaryThreads) qk_rotary_kernel(const QkRotar
         const int h = first + i * kAtOnce + slot;
         const int64_t from = row * p.ldx + (int64_t)h * D;
         ra[i] = rb[i] = make_uint4(0, 0, 0, 0);
-        if (h < h1 && EXL3_SPAN(from, D, size_x)) {
+        if (mine && h < h1 && EXL3_SPAN(from, D, size_x)) {
           ra[i] = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.x) + from + a0);
           rb[i] = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.x) + from + b0);
         }
       }
-      if (!known) {  // the same in the whole CTA
+      if (!known) {
         known = true;
-        if (pos < 0) break;
-        if (pos >= p.n_positions) {
-          if (threadIdx.x == 0) report_index(p.status);
-          break;
-        }
+        if (pos >= p.n_positions && slot == 0 && l == 0) report_index(p.status);
+        turned = pos >= 0 && pos < p.n_positions;
+        if (!FLAT && !turned) break;  // the same in the whole CTA
 #pragma unroll
         for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
-        if (turns) {
+        if (turned && turns) {
           const int64_t at = (int64_t)pos * p.rot_dim + 8 * l;
           if (EXL3_SPAN(at, p.rot_dim / 2 + 8, (int64_t)p.n_positions * p.rot_dim)) {
 #pragma unroll
@@ -92,7 +99,7 @@ __global__ void __launch_bounds__(kRotaryThreads) qk_rotary_kernel(const QkRotar
       for (int i = 0; i < kAhead; ++i) {  // all lanes of a warp go round as often as each other: the norm's shuffles
         const int h = first + i * kAtOnce + slot;
         const int64_t to = row * p.ldo + (int64_t)h * D;
-        const bool there = h < h1 && EXL3_SPAN(to, D, size_o);
+        const bool there = turned && h < h1 && EXL3_SPAN(to, D, size_o);
         Piece a(ra[i]), b(rb[i]);
         if constexpr (NORM) {
           float sum = 0.f;
@@ -138,15 +145,25 @@ __global__ void __launch_bounds__(kRotaryThreads) qk_rotary_kernel(const QkRotar
 
 template <int D, bool INTERLEAVED>
 cudaError_t rotary(const QkRotary &p, int num_sms, cudaStream_t st) {
-  constexpr int kAtOnce = kRotaryThreads * 16 / D;
   const int heads = p.q_heads + p.k_heads;
-  // few rows: the heads of a row are shared by CTAs, which finish at once
-  const bool few = p.rows < 4 * num_sms;
-  const int each = few ? kAtOnce : heads;
-  const int64_t most = (int64_t)num_sms * (2048 / kRotaryThreads);
+  const bool norm = p.q_weight || p.k_weight;
+  // Up to 2048 columns of heads leave most of a CTA without work, or a few rows of it: several rows at once, whose threads
+  // read the angles for one head each (6827 rows of 16 heads of 128 or fewer: 3 to 11 us, 10 to 14 by rows; 20 heads: 19 and 16).
+  if (heads * D <= 2048) {
+    const int tall = kFlatThreads * 16 / D / heads;
+    const int64_t ctas = ceil_div(p.rows, tall), most = (int64_t)num_sms * (2048 / kFlatThreads);
+    return launch_overlapped(norm ? qk_rotary_kernel<D, INTERLEAVED, true, true> : qk_rotary_kernel<D, INTERLEAVED, false, true>,
+                             dim3((unsigned)(ctas < most ? ctas : most)), kFlatThreads, 0, st, 1, p, heads, tall);
+  }
+  // Few rows: the heads of a row are shared by CTAs, as far as those are resident at once (48 heads of 128: 1 row 1.9 us, by
+  // one CTA 2.2; 304 rows 2.9 and 3.8; 700 rows, shared as if there were fewer, 5.1, not 4.3).
+  constexpr int kAtOnce = kRotaryThreads * 16 / D;
+  const int64_t most = (int64_t)num_sms * (2048 / kRotaryThreads), top = ceil_div(heads, kAtOnce), full = most / 2 / p.rows;
+  const int64_t shares = full < 1 ? 1 : full < top ? full : top;
+  const int each = (int)(ceil_div(ceil_div(heads, shares), kAtOnce) * kAtOnce);
   const dim3 grid((unsigned)(p.rows < most ? p.rows : most), (unsigned)ceil_div(heads, each));
-  return launch_overlapped(p.q_weight || p.k_weight ? qk_rotary_kernel<D, INTERLEAVED, true> : qk_rotary_kernel<D, INTERLEAVED, false>, grid,
-                           kRotaryThreads, 0, st, 1, p, each);
+  return launch_overlapped(norm ? qk_rotary_kernel<D, INTERLEAVED, true, false> : qk_rotary_kernel<D, INTERLEAVED, false, false>, grid,
+                           kRotaryThreads, 0, st, 1, p, each, 1);
 }
 
 }  // namespace
@@ -159,10 +176,14 @@ cudaError_t launch_qk_rotary(const QkRotary &p, int num_sms, cudaStream_t st) {
 cudaError_t init_qk_rotary_kernels(int *status) {
   cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
   cudaFuncAttributes attr;
-  for (const void *f : {(const void *)qk_rotary_kernel<64, false, false>, (const void *)qk_rotary_kernel<64, false, true>,
-                        (const void *)qk_rotary_kernel<64, true, false>, (const void *)qk_rotary_kernel<64, true, true>,
-                        (const void *)qk_rotary_kernel<128, false, false>, (const void *)qk_rotary_kernel<128, false, true>,
-                        (const void *)qk_rotary_kernel<128, true, false>, (const void *)qk_rotary_kernel<128, true, true>})
+  for (const void *f : {(const void *)qk_rotary_kernel<64, false, false, false>, (const void *)qk_rotary_kernel<64, false, true, false>,
+                        (const void *)qk_rotary_kernel<64, true, false, false>, (const void *)qk_rotary_kernel<64, true, true, false>,
+                        (const void *)qk_rotary_kernel<128, false, false, false>, (const void *)qk_rotary_kernel<128, false, true, false>,
+                        (const void *)qk_rotary_kernel<128, true, false, false>, (const void *)qk_rotary_kernel<128, true, true, false>,
+                        (const void *)qk_rotary_kernel<64, false, false, true>, (const void *)qk_rotary_kernel<64, false, true, true>,
+                        (const void *)qk_rotary_kernel<64, true, false, true>, (const void *)qk_rotary_kernel<64, true, true, true>,
+                        (const void *)qk_rotary_kernel<128, false, false, true>, (const void *)qk_rotary_kernel<128, false, true, true>,
+                        (const void *)qk_rotary_kernel<128, true, false, true>, (const void *)qk_rotary_kernel<128, true, true, true>})
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, f);
   return e;
 }
