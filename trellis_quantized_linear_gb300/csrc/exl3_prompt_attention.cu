@@ -274,29 +274,39 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[3
 }
 
 // A cap of the scores, in log2 units. Where x^2 < 1/4, x = score / cap, cap * tanh(x) is
-// score * p(x^2) with the polynomial p of degree 4 that is nearest to tanh(x) / x there (to
-// 1.5e-8, found by minimising the largest relative error): no exponential and no reciprocal,
-// which would cost three times the softmax's own. Those beyond go through
-// 1 - 2 / (exp(2 x) + 1), an absolute error near cap * 2^-22, in a pass of their own over
-// TMEM: in line with the softmax it would be too much code for the instruction cache. The
-// others have the same value there, so that a score's does not depend on its neighbours.
+// score * p(x^2) with the polynomial p of degree 3, p(0) = 1, that is nearest to tanh(x) / x
+// there (to 6.5e-7, found by minimising the largest relative error): no exponential and no
+// reciprocal, which would cost three times the softmax's own. It is of the product's square,
+// with coefficients that bring that to x^2, where they stay in fp32's range (`ready`). Scores
+// beyond go through 1 - 2 / (exp(2 x) + 1), an absolute error near cap * 2^-22, in a pass of
+// their own over TMEM: in line with the softmax it would be too much code for the instruction
+// cache. The others have the same value there, so that a score's does not depend on its
+// neighbours.
 struct PromptCap {
-  float k, cap, p[5];  // x = product * k; coefficients times what brings a product to log2 units
+  bool ready;               // else all scores take the pass over TMEM
+  float k, unit, cap, edge; // x = product * k; edge: what (product * unit)^2 is below, of those near
+  float p[4];               // of (product * unit)^2, times what brings a product to log2 units
   // A cap whose double leaves fp32 is lowered: no score comes near it.
-  __device__ __forceinline__ PromptCap(float softcap, float c)
-      : k(c / fmaxf(softcap * kLog2e, 1e-30f)), cap(fminf(softcap * kLog2e, 1.5e38f)),
-        p{c, c * -0.333331439f, c * 0.133258785f, c * -0.0530454412f, c * 0.0172413593f} {}
-  // N products to capped scores, those with x^2 < 1/4; `most` becomes the largest x^2.
-  template <int N>
+  __device__ __forceinline__ PromptCap(float softcap, float c) : k(c / fmaxf(softcap * kLog2e, 1e-30f)), cap(fminf(softcap * kLog2e, 1.5e38f)) {
+    ready = k > 0x1p-18f && k < 0x1p14f && c > 0x1p-10f && c < 0x1p14f;
+    unit = ready ? 1.0f : k;
+    const float k2 = ready ? k * k : 1.0f;
+    edge = 0.25f / k2;
+    p[0] = c;
+    p[1] = c * -0.333281593f * k2;
+    p[2] = c * 0.132053586f * (k2 * k2);
+    p[3] = c * -0.0447506050f * (k2 * k2 * k2);
+  }
+  // N products to capped scores, those with x^2 < 1/4; `most` becomes the largest (product * unit)^2.
+  template <bool READY, int N>
   __device__ __forceinline__ void near(float (&s)[N], float &most) const {
     auto both = [](float v) { return make_float2(v, v); };
     float m[4] = {most, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const float2 v = make_float2(s[i], s[i + 1]), x = mul2(v, both(k)), y = mul2(x, x);
+      const float2 v = make_float2(s[i], s[i + 1]), x = READY ? v : mul2(v, both(unit)), y = mul2(x, x);
       m[i / 2 % 4] = fmaxf(m[i / 2 % 4], fmaxf(y.x, y.y));
-      float2 t = fma2(y, both(p[4]), both(p[3]));
-      t = fma2(y, t, both(p[2]));
+      float2 t = fma2(y, both(p[3]), both(p[2]));
       t = fma2(y, t, both(p[1]));
       t = mul2(v, fma2(y, t, both(p[0])));
       s[i] = t.x;
@@ -310,14 +320,14 @@ struct PromptCap {
     for (int q = 0; q < 4; ++q) {
       float s[32], most = 0.f;
       tmem_ld32(scores + 32 * q, s);
-      near(s, most);
-      if (__any_sync(0xffffffffu, real && most >= 0.25f)) {
+      near<false>(s, most);
+      if (__any_sync(0xffffffffu, real && most >= edge)) {
         float raw[32];
         tmem_ld32(scores + 32 * q, raw);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float x = raw[i] * k, f = fmaf(-2.0f * cap, rcp(ex2(x * (2.0f * kLog2e)) + 1.0f), cap);
-          s[i] = x * x < 0.25f ? s[i] : f;
+          const float x = raw[i] * k, u = raw[i] * unit, f = fmaf(-2.0f * cap, rcp(ex2(x * (2.0f * kLog2e)) + 1.0f), cap);
+          s[i] = u * u < edge ? s[i] : f;
         }
       }
       tmem_st32(scores + 32 * q, s);
@@ -608,7 +618,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int least = __reduce_min_sync(0xffffffffu, real ? limit : INT32_MAX);
       const bool live = __any_sync(0xffffffffu, real);
       float ref = -INFINITY, sum = 0.f;
-      bool far = false;  // scores beyond half the cap were seen
+      bool far = !cap.ready;  // scores beyond half the cap were seen
       for (int u = 0; u < units; ++u, ++count) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kPS + t), count & 1, status))) {
           ok = false;
@@ -670,7 +680,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tmem_ld64(s_tmem, s);
             tmem_ld64_begin(s_tmem + 64, s2);
             float most_x = 0.f;
-            if (CAP && !capped) cap.near(s, most_x);
+            if (CAP && !capped) cap.near<true>(s, most_x);
             mask(s, pos0);
             if (renew) {
               tmem_ld64_end(s2);
@@ -697,10 +707,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             exponentials(s, 0, 32);
             if (renew) break;
             tmem_ld64_end(s2);
-            if (CAP && !capped) cap.near(s2, most_x);
+            if (CAP && !capped) cap.near<true>(s2, most_x);
             mask(s2, pos0 + 64);
             const float so_far = (part[0].x + part[0].y) + (part[1].x + part[1].y);
-            const bool beyond = CAP && real && most_x >= 0.25f;
+            const bool beyond = CAP && real && most_x >= cap.edge;
             if (!__any_sync(0xffffffffu, beyond || (real && (so_far > kMostSum || most(s2) + shift > kMost)))) break;
             if (CAP && !capped) {
               far = __any_sync(0xffffffffu, beyond);  // the item's other units at once
