@@ -21,9 +21,10 @@
 //     rows that do not see them. Rows that do see one get it back at the end.
 // TMEM: S0 S1 O0 O1, 128 columns each.
 //
-// Measured: one prompt of 8192 tokens, 40 heads on 8, D = 128: 454 us (687 GFLOP, 1510
-// TFLOP/s), one of 2048: 46 us; D = 64: 383 us; scores capped: 720 and 700 us. What binds it is the chain of a tile's unit:
-// about 1550 cycles of softmax (of them 512 for 128 exponentials a row at 4 cycles a warp)
+// Measured: one prompt of 8192 tokens, 40 heads on 8, D = 128: 454 to 467 us (687 GFLOP, up to
+// 1510 TFLOP/s; 485 to 504 in long runs, in which the clock falls), one of 2048: 46 us; D = 64:
+// 383 us; scores capped: 693 and 656 us. What binds it is the chain of a tile's unit: about
+// 1550 cycles of softmax (of them 512 for 128 exponentials a row at 4 cycles a warp)
 // and 1300 from the last probability to the next scores (768 of products, the rest the ways
 // through barriers), with TMEM full, so that the next scores cannot be formed meanwhile; the
 // tensor core is busy 2048 of the 2850 cycles that a pair of units takes. Steps on the way
