@@ -447,6 +447,34 @@ def test_rotary_values_that_are_not_finite_stay_in_their_head():
     assert sorted(zip(*np.nonzero(differs))) == [(1, 3), (1, 19), (2, 100)]
 
 
+@pytest.mark.parametrize("qh,kh", [(2, 1), (24, 8)])
+def test_rotary_past_32_bit_offsets(qh, kh):
+    import torch
+    rows, ld, cols = 2100, 1 << 20, (qh + kh) * 128
+    g = np.random.default_rng(qh)
+    x, pos = dev(g.standard_normal((rows, cols)).astype(np.float16)), dev(g.integers(0, 500, rows).astype(np.int32))
+    tab, want = dev(table(500, 128)), torch.empty((rows, cols), dtype=torch.float16, device="cuda")
+    tql.exl3_qk_rotary(x, want, qh, kh, 128, pos, tab)
+    big = torch.zeros((rows, ld), dtype=torch.float16, device="cuda")
+    big[:, -cols:] = x
+    tql.exl3_qk_rotary(big[:, -cols:], big[:, -cols:], qh, kh, 128, pos, tab)
+    assert torch.equal(big[:, -cols:], want) and not big[:, :-cols].any()
+
+
+def test_norm_ring_past_32_bit_offsets():
+    import torch
+    rows, ld, cols = 2100, 1 << 20, 4096
+    x = torch.randn((rows, cols), device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)).half()
+    want, codes, scales = torch.empty_like(x), torch.empty((rows, cols), dtype=torch.uint8, device="cuda"), torch.empty((rows, 32), device="cuda")
+    tql.exl3_rms_norm(x, want, residual=x, codes=codes, scales=scales)
+    big = torch.zeros((rows, ld), dtype=torch.float16, device="cuda")
+    big[:, -cols:] = x
+    far, far_scales = big[:, -cols:], torch.empty_like(scales)
+    far_codes = torch.zeros((rows, 2 * ld), dtype=torch.uint8, device="cuda")[:, -cols:]
+    tql.exl3_rms_norm(far, far, residual=far, codes=far_codes, scales=far_scales)
+    assert torch.equal(far, want) and torch.equal(far_codes, codes) and torch.equal(far_scales, scales) and not big[:, :-cols].any()
+
+
 # --------------------------------------------------------------------------- together
 
 

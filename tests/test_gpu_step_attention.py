@@ -240,6 +240,21 @@ def test_ranges_outside_the_rows_are_reported_and_left_out(q_start, good):
         assert np.all(out[:a] == 7.0) and np.all(out[z:] == 7.0)
 
 
+def test_past_32_bit_offsets():
+    """Queries, keys, values and outputs in the last columns of a matrix of more than 2^31 elements."""
+    import torch
+    heads, kv_heads, dim, rows, ld = 4, 2, 64, 2100, 1 << 20
+    x = torch.from_numpy(inputs(rows, heads, kv_heads, dim, 14)).cuda()
+    qs = torch.tensor([0, 1200, rows], dtype=torch.int32, device="cuda")
+    want = torch.empty((rows, heads * dim), dtype=torch.float16, device="cuda")
+    tql.exl3_prompt_attention(*split(x, heads, kv_heads, dim), heads, kv_heads, dim, qs, 0.125, want)
+    big = torch.zeros((rows, ld), dtype=torch.float16, device="cuda")
+    big[:, -x.shape[1]:] = x
+    out = big[:, -x.shape[1] - heads * dim:-x.shape[1]]
+    tql.exl3_prompt_attention(*split(big[:, -x.shape[1]:], heads, kv_heads, dim), heads, kv_heads, dim, qs, 0.125, out)
+    assert torch.equal(out, want) and torch.equal(big[:, -x.shape[1]:], x) and not big[:, :-x.shape[1] - heads * dim].any()
+
+
 def test_captured_call_serves_other_lengths():
     import torch
     heads, kv_heads, dim, rows = 10, 2, 128, 700
