@@ -189,3 +189,18 @@ def test_prompt_attention_looks_at_its_tensors(lib):
                dict(qs=torch.zeros(6, dtype=torch.int32)[::2]), dict(out=torch.zeros((8, 256)).half()), dict(out=torch.zeros((9, 256))),
                dict(lse=torch.zeros((8, 4))), dict(lse=torch.zeros((9, 4)).half()), dict(lse=torch.zeros((9, 8))[:, ::2])):
         refused(lambda: call(**kw))
+
+
+def test_tensors_of_another_device_are_refused(lib, monkeypatch):
+    import torch
+    monkeypatch.setattr(tql, "_ready", True)
+    monkeypatch.setattr(tql, "_raw_device", lambda: 0)
+    x, i, table = torch.zeros((3, 768)).half(), torch.zeros(9, dtype=torch.int32), torch.zeros((10, 64))
+    batch = tql.Exl3Kv8Batch(i[:2].view(2, 1), i[:2], i[:3], 3, 3)
+    for f in (lambda: tql.exl3_kv8_plan(batch, i, i, i, i, i, 10, i, i, i, stream=0), lambda: tql.exl3_rms_norm(x, x, stream=0),
+              lambda: tql.exl3_qk_rotary(x, x, 4, 2, 128, i, table, stream=0),
+              lambda: tql.exl3_prompt_attention(x[:, :256], x[:, 256:512], x[:, 512:], 4, 4, 64, i[:2], 0.1, torch.zeros((3, 256)).half(), stream=0)):
+        with pytest.raises(ValueError, match="current device"):
+            f()
+    monkeypatch.setattr(tql, "_raw_device", lambda: -1)  # where the tensors are
+    goes(lambda: tql.exl3_rms_norm(x, x, stream=0))
