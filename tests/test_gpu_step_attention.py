@@ -193,6 +193,93 @@ def test_long_whole_sequences(heads, kv_heads, dim, lens):
     check(x, qs, heads, kv_heads, dim, dim ** -0.5, 20.0, False, out, lse)
 
 
+# Few heads and long sequences: CTAs share an item's keys and join what they have of its rows.
+FEW = [(1, 1, 128), (1, 1, 64), (3, 3, 64), (5, 1, 128), (8, 2, 64), (8, 8, 128)]
+
+
+@pytest.mark.parametrize("lens", [[1024], [1153], [1600, 900], [2100, 1, 1000]])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("heads,kv_heads,dim", FEW)
+def test_few_heads(heads, kv_heads, dim, cap, causal, lens):
+    x, qs = inputs(sum(lens) + 5, heads, kv_heads, dim, 30, q_gain=3.0), starts(lens, first=2)
+    x[:2], x[qs[-1]:] = np.nan, np.inf
+    out, lse = run(x, qs, heads, kv_heads, dim, dim ** -0.5, cap, causal)
+    check(x, qs, heads, kv_heads, dim, dim ** -0.5, cap, causal, out, lse)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(1, 1, 128), (4, 2, 64), (8, 8, 128)])
+def test_few_heads_values_that_are_not_finite(heads, kv_heads, dim, causal):
+    lens = [1500, 1300]
+    x, qs = inputs(sum(lens), heads, kv_heads, dim, 31), starts(lens)
+    for i, r in enumerate([0, 700, 1279, 1280, 1499, 1500, 2600]):
+        x[r, (heads + kv_heads) * dim + 5 * i] = [np.inf, -np.inf, np.nan][i % 3]
+    out, lse = run(x, qs, heads, kv_heads, dim, dim ** -0.5, causal=causal)
+    q, k, v = split(x, heads, kv_heads, dim)
+    want, _ = step_ref.prompt_attention(q, k, v, qs, heads, kv_heads, dim, dim ** -0.5, 0.0, causal)
+    fine = np.isfinite(want)
+    # a row that sees one gets it or NaN there, and all else is as if it were not there
+    assert np.array_equal(np.isfinite(out), fine)
+    clean, clean_lse = run(np.where(np.isfinite(x), x, 0).astype(np.float16), qs, heads, kv_heads, dim, dim ** -0.5, causal=causal)
+    assert np.array_equal(out[fine], clean[fine]) and np.array_equal(lse, clean_lse)
+    assert tql.exl3_get_device_status() == 0
+
+
+def test_few_heads_growing_scores_and_rows_without_any():
+    """References that differ by far between the CTAs of an item; keys whose scores are minus
+    infinity for a CTA's whole range, and for all."""
+    heads, kv_heads, dim = 2, 1, 64
+    x, qs = inputs(1400, heads, kv_heads, dim, 32), starts([1400])
+    x[:, :heads * dim] = np.abs(x[:, :heads * dim])
+    k = slice(heads * dim, (heads + 1) * dim)
+    grow = (np.arange(1400)[:, None] / 50.0 + 0.1 * np.abs(x[:, k])).astype(np.float16)
+    for keys in (grow, grow[::-1]):
+        x[:, k] = keys
+        for scale in (0.125, -0.125):
+            out, lse = run(x, qs, heads, kv_heads, dim, scale)
+            check(x, qs, heads, kv_heads, dim, scale, 0.0, True, out, lse)
+    x[:, 3], x[:, dim + 3] = -1.0, -1.0
+    x[600:, heads * dim + 3] = np.inf  # minus infinity
+    out, lse = run(x, qs, heads, kv_heads, dim, 0.125, causal=False)
+    check(x, qs, heads, kv_heads, dim, 0.125, 0.0, False, out, lse)
+    x[:, heads * dim + 3] = np.inf
+    out, lse = run(x, qs, heads, kv_heads, dim, 0.125)
+    assert not out.any() and np.all(lse == -np.inf)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,lens", [(1, 1, 128, [2500]), (8, 8, 64, [1500]), (6, 3, 128, [1024, 1400])])
+def test_few_heads_twice_at_once_and_captured(heads, kv_heads, dim, lens):
+    import torch
+    rows, qs = sum(lens), torch.from_numpy(starts(lens)).cuda()
+    xs = [torch.from_numpy(inputs(rows, heads, kv_heads, dim, 33 + i)).cuda() for i in range(2)]
+    outs = [[(torch.zeros((rows, heads * dim), dtype=torch.float16, device="cuda"), torch.zeros((rows, heads), device="cuda")) for _ in range(7)] for _ in range(2)]
+
+    def go(i, o, stream=None):
+        tql.exl3_prompt_attention(*split(xs[i], heads, kv_heads, dim), heads, kv_heads, dim, qs, dim ** -0.5, outs[i][o][0], lse=outs[i][o][1], stream=stream)
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for o in range(5):
+        for i in range(2):
+            go(i, o, streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        go(i, 5)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(2):
+            go(i, 6)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in outs[i][1:]:
+            assert torch.equal(out, outs[i][0][0]) and torch.equal(lse, outs[i][0][1])
+    assert tql.exl3_get_device_status() == 0
+
+
 def test_heavy_and_growing_scores():
     """Maxima that grow along a row, so that its output is rescaled again and again."""
     lens, heads, kv_heads, dim = [1000], 2, 1, 64

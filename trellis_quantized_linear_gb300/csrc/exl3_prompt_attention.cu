@@ -21,6 +21,14 @@
 //     rows that do not see them. Rows that do see one get it back at the end.
 // TMEM: S0 S1 O0 O1, 128 columns each.
 //
+// Where there are fewer items than SMs can take (few heads, few sequences), the longest one's
+// units, one after the other, are what a call takes. Then a cluster of 2 or 4 CTAs has an item
+// together: each a range of its keys, and in the end references, sums and outputs go from CTA
+// to CTA through shared memory of the cluster (`join`), each CTA joining and storing its share of the
+// columns: no workspace, and the same result each time. By st.async, which counts its bytes at
+// the receiver: a released arrival waits for the stores to memory too, and took 20 us an item;
+// what it takes now is about 2. ranks_for has the rule and both sides.
+//
 // Measured: one prompt of 8192 tokens, 40 heads on 8, D = 128: 454 to 467 us (687 GFLOP, up to
 // 1510 TFLOP/s; 485 to 504 in long runs, in which the clock falls), one of 2048: 46 us; D = 64:
 // 383 us; scores capped: 693 and 656 us. What binds it is the chain of a tile's unit: about
@@ -47,6 +55,7 @@ constexpr int kTokens = 128;       // of a unit
 constexpr int kMmaWarp = 8 /* after the softmax warps */, kLoadWarp = 9, kCleanWarp = 10, kCleanWarps = 2;
 constexpr int kPromptThreads = 12 * 32;  // 168 registers a thread
 constexpr int kPromptSeqs = 1024;  // sequences of one launch
+constexpr int kMaxParts = 4, kSplitSeqs = 128;  // CTAs that share an item's keys, and sequences of such a launch
 constexpr int kItems = 4;          // items announced at a time
 constexpr int kFlags = 8;          // items whose flag is kept; more than a ring can be ahead
 // Probabilities are taken relative to a reference: 2^kHeadroom below the row's maximum over
@@ -57,19 +66,25 @@ constexpr int kFlags = 8;          // items whose flag is kept; more than a ring
 // probability is then 2^8 to 2^16: one of 2^-22 of it has all 11 bits, one of 2^-33 counts.
 constexpr float kHeadroom = 8.0f, kMostSum = 65504.0f, kMost = 15.9f;
 
-template <int D>
+template <int D, bool SPLIT>
 struct PromptCfg {
+  static constexpr int kSeqs = SPLIT ? kSplitSeqs : kPromptSeqs;
   static constexpr int kHalves = D / 64;
   static constexpr int kStages = D == 64 ? 4 : 2;        // of keys, and of values
   static constexpr int kOperand = kHalves * 128 * 128;   // 128 rows (or tokens) x D fp16
   static constexpr int kOffK = 2 * kOperand;             // two query tiles before it
   static constexpr int kOffV = kOffK + kStages * kOperand;
   static constexpr int kOffSeq = kOffV + kStages * kOperand;
-  static constexpr int kOffLen = kOffSeq + kPromptSeqs * 8;
-  static constexpr int kOffStage = kOffLen + kPromptSeqs * 4;  // 32 rows x 32 columns fp16 of each softmax warp
-  static constexpr int kOffItem = kOffStage + 8 * 2048;
+  static constexpr int kOffLen = kOffSeq + kSeqs * 8;
+  static constexpr int kOffStage = kOffLen + kSeqs * 4;
+  // of each softmax warp: 32 rows x 32 columns fp16 of the output, or what the other CTAs send: slabs of 32 rows x 8 columns
+  // fp32, and references and sums
+  static constexpr int kSlab = 32 * 8 * 4, kStats = 32 * 8, kSlabs = D == 64 ? 6 : 3;
+  static constexpr int kStage = SPLIT ? kSlabs * kSlab + (kMaxParts - 1) * kStats : 2048;
+  static constexpr int kOffItem = kOffStage + 8 * kStage;
   static constexpr int kOffBar = kOffItem + kItems * 32;
-  static constexpr int kSmem = 1024 + kOffBar + 512;
+  static constexpr int kOffJoin = kOffBar + 512;  // a warp's barriers with those of the other CTAs: kGates for each
+  static constexpr int kSmem = 1024 + kOffJoin + (SPLIT ? 8 * (kMaxParts - 1) * 3 * 8 : 0);
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 constexpr int kMaxStages = 4;
@@ -80,18 +95,23 @@ enum { kPQFull = 0, kPFirst = 2, kPPassed = 3, kPVFull = kPPassed + kMaxStages, 
        kPS = kPReady + kMaxStages, kPP = kPS + 2 /* tile x half */, kPO = kPP + 4, kPItemFull = kPO + 2,
        kPItemEmpty = kPItemFull + kItems, kPDone = kPItemEmpty + kItems, kPBars = kPDone + 1 };
 
+// Of a warp with the same one of another CTA: its slab and its references and sums are here; what was sent there has been read.
+enum { kSlabHere = 0, kStatsHere = 1, kSlabRead = 2, kGates = 3 };
+
 struct PromptParams {
   PromptAttention a;
   int group, tile_tokens;
+  int ranks;  // CTAs of a cluster, which share the keys of their items
 };
 
 // The launch's sequences from the longest to the shortest (equal ones in their order):
 // first row and tokens, and pairs of tiles. Returns how many have any tokens. All threads;
 // ends with a barrier.
+template <int SEQS>
 __device__ __forceinline__ int sort_prompts(const PromptAttention &a, int pair, int2 *seq, int *pairs) {
   const int n4 = (a.n_seqs + 3) & ~3;
   int *len = pairs;  // by sequence, until the sorted ones take its place
-  constexpr int kEach = (kPromptSeqs + kPromptThreads - 1) / kPromptThreads;
+  constexpr int kEach = (SEQS + kPromptThreads - 1) / kPromptThreads;
   int row0[kEach], n[kEach], before[kEach];
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
@@ -139,16 +159,31 @@ struct Item {
   int units0, units1;// of each tile; 0: the pair has no second tile
   int first_masked;  // from this unit on, not every row sees all keys
   int there;         // 0: there are no more items
+  // Where CTAs share an item: units0 and units1 are this one's of total0 and total1, from `from` on, `share` of them at most.
+  int from, share, total0, total1;
   __device__ __forceinline__ int all() const { return max(units0, units1); }
+  template <bool SPLIT>
+  __device__ __forceinline__ void take_part(int rank, int ranks) {
+    from = 0;
+    if constexpr (SPLIT) {
+      total0 = units0;
+      total1 = units1;
+      share = (all() + ranks - 1) / ranks;
+      from = rank * share;
+      units0 = min(max(units0 - from, 0), share);
+      units1 = min(max(units1 - from, 0), share);
+    }
+  }
 };
 
-// The items of a CTA: number k of them is item k * CTAs + c or, every second time, from
-// the other end. Causal items are ordered by the pair's place in its sequence, the last
+// The items of a CTA (or a cluster): number k of them is item k * CTAs + c or, every second
+// time, from the other end. Causal items are ordered by the pair's place in its sequence, the last
 // ones first (which is by length but for sequences' last pairs), others by sequence.
 struct PromptWalk {
   const int2 *seq;
   const int *pairs;
   int n_seqs;
+  uint32_t c, C;
   uint32_t round, base;
   int level, count;  // causal: place of the pair, and sequences that have it; else the sequence
   __device__ __forceinline__ void begin(int causal) {
@@ -157,7 +192,7 @@ struct PromptWalk {
     count = 0;
   }
   __device__ __forceinline__ bool next(const PromptParams &p, Item &it) {
-    const uint32_t c = blockIdx.x, C = gridDim.x, heads = p.a.n_kv_heads;
+    const uint32_t heads = p.a.n_kv_heads;
     const uint32_t idx = round * C + (round & 1 ? C - 1 - c : c);
     ++round;
     int s, place;
@@ -236,7 +271,14 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
         "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
       : "r"(taddr), "r"(taddr + 32));
 }
-// The same in two parts: nothing may use v between them, and what comes after goes through
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+      : "r"(taddr));
+}
+// tmem_ld64 in two parts: nothing may use v between them, and what comes after goes through
 // the second.
 __device__ __forceinline__ void tmem_ld64_begin(uint32_t taddr, float (&v)[64]) {
   asm volatile(
@@ -337,14 +379,26 @@ struct PromptCap {
   }
 };
 
+// Stores to another CTA of the cluster, whose bytes are counted on its barrier (both addresses
+// from map_to_rank): nothing has to be waited for here, as a release would, for stores to memory too.
+__device__ __forceinline__ void store_there(uint32_t dst, uint32_t bar, float a, float b, float c, float d) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst), "f"(a), "f"(b),
+               "f"(c), "f"(d), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void store_there(uint32_t dst, uint32_t bar, float a, float b) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(dst), "f"(a), "f"(b), "r"(bar)
+               : "memory");
+}
+
 // Bits of the fp16 pair w whose exponent is all ones (infinity, NaN): 0x8000 for each.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool SPLIT>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                             const __grid_constant__ CUtensorMap tv, const PromptParams p) {
-  using Cfg = PromptCfg<D>;
+  using Cfg = PromptCfg<D, SPLIT>;
   constexpr int kStages = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -356,6 +410,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kOffBar + 8 * kPBars);
   volatile uint32_t *flags = tmem_slot + 1;  // number + 1 of the last item of each slot that has an infinity or NaN to give back
   int *status = p.a.status;
+  const int ranks = SPLIT ? p.ranks : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -377,6 +432,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     mbar_init(bar(kPFirst), 1);
     mbar_init(bar(kPDone), 1);
     for (int i = 0; i < kFlags; ++i) flags[i] = 0;
+    if constexpr (SPLIT)
+      for (int i = 0; i < 8 * (kMaxParts - 1) * kGates; ++i) mbar_init(base + Cfg::kOffJoin + 8 * i, 1);
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -391,9 +448,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncwarp();
+  if constexpr (SPLIT) cluster_sync_all();  // every CTA runs, with its barriers, before another stores to it
   tc_fence_before();
   PromptWalk walk{seq, reinterpret_cast<int *>(smem + Cfg::kOffLen),
-                  sort_prompts(p.a, 2 * p.tile_tokens, seq, reinterpret_cast<int *>(smem + Cfg::kOffLen))};
+                  sort_prompts<Cfg::kSeqs>(p.a, 2 * p.tile_tokens, seq, reinterpret_cast<int *>(smem + Cfg::kOffLen)),
+                  blockIdx.x / ranks, gridDim.x / ranks};
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int4 *items = reinterpret_cast<int4 *>(smem + Cfg::kOffItem);
@@ -402,6 +462,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   auto read_item = [&](uint32_t n, Item &it) {
     const int4 a = items[2 * (n % kItems)], b = items[2 * (n % kItems) + 1];
     it = Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    it.take_part<SPLIT>(rank, ranks);
   };
   auto item_read = [&](uint32_t n) { mbar_arrive(bar(kPItemEmpty + n % kItems)); };
 
@@ -483,7 +544,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           ok = ok && mbar_wait(bar(kPItemEmpty + number % kItems), ((number / kItems) & 1) ^ 1, status);
           if (!ok) return;
           items[2 * (number % kItems)] = make_int4(it.row0, it.n, it.h, it.token0);
-          items[2 * (number % kItems) + 1] = make_int4(it.units0, it.units1, it.first_masked, it.there);
+          items[2 * (number % kItems) + 1] = make_int4(SPLIT ? it.total0 : it.units0, SPLIT ? it.total1 : it.units1, it.first_masked, it.there);
           mbar_arrive(bar(kPItemFull + number % kItems));
           ++number;
         };
@@ -491,11 +552,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         auto passed = [&](uint32_t u) { return mbar_wait(bar(kPPassed + u % kStages), (u / kStages) & 1, status); };
         auto keys = [&](uint32_t u, uint32_t b, const Item &it, int j) {
           mbar_arrive_expect_tx(b, Cfg::kOperand);
-          operand(&tk, base + Cfg::kOffK + (u % kStages) * Cfg::kOperand, b, it.h, it.row0 + j * kTokens);
+          operand(&tk, base + Cfg::kOffK + (u % kStages) * Cfg::kOperand, b, it.h, it.row0 + (it.from + j) * kTokens);
+        };
+        auto walk_on = [&](Item &it) {  // to the next item that this CTA has units of
+          do {
+            it.there = walk.next(p, it);
+            it.take_part<SPLIT>(rank, ranks);
+          } while (SPLIT && it.there && it.all() == 0);
         };
         walk.begin(p.a.causal);
         Item it, next;
-        it.there = walk.next(p, it);
+        walk_on(it);
         announce(it);
         const bool any = it.there;
         if (any) keys(0, bar(kPFirst), it, 0);
@@ -509,14 +576,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mbar_arrive_expect_tx(bar(kPQFull + t), q_bytes);
             operand(&tq, base + t * Cfg::kOperand, bar(kPQFull + t), it.h * p.group, it.row0 + it.token0 + t * p.tile_tokens);
           }
-          next.there = walk.next(p, next);
+          walk_on(next);
           const int all = it.all();
           for (int j = 0; ok && j < all; ++j, ++unit) {
             const uint32_t st = unit % kStages;
             ok = unit + 1 < kStages || passed(unit + 1 - kStages);
             if (!ok) break;
             mbar_arrive_expect_tx(bar(kPVFull + st), Cfg::kOperand);
-            operand(&tv, base + Cfg::kOffV + st * Cfg::kOperand, bar(kPVFull + st), it.h, it.row0 + j * kTokens);
+            operand(&tv, base + Cfg::kOffV + st * Cfg::kOperand, bar(kPVFull + st), it.h, it.row0 + (it.from + j) * kTokens);
             if (j == 0) announce(next);
             if (j + 1 < all) keys(unit + 1, bar(kPReady + st), it, j + 1);
             else if (next.there) keys(unit + 1, bar(kPReady + st), next, 0);
@@ -550,9 +617,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const uint32_t st = unit % kStages;
           ok = __all_sync(0xffffffffu, mbar_wait(bar(kPVFull + st), (unit / kStages) & 1, status));
           if (!ok) break;
-          if (j >= it.first_masked) {
+          if (it.from + j >= it.first_masked) {
             const uint32_t v = base + Cfg::kOffV + st * Cfg::kOperand;
-            const int left = it.n - j * kTokens;  // tokens of the sequence from here
+            const int left = it.n - (it.from + j) * kTokens;  // tokens of the sequence from here
             bool found = false;
   #pragma unroll 4
             for (int i = (warp - kCleanWarp) * 32 + lane; i < Cfg::kHalves * 128 * 8; i += kCleanWarps * 32) {
@@ -589,6 +656,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const PromptCap cap(p.a.softcap, c);
     const int token = row / p.group, head_in = row - token * p.group;
     uint32_t count = 0, items = 0, number = 0, unit = 0;  // units and items of this tile, items and units of the CTA
+    [[maybe_unused]] uint32_t stats_got = 0, got = 0, sent = 0;  // phases of the barriers with the other CTAs, a bit each
     bool ok = true;
     auto hand_over = [&](int half) {
       tmem_wait_st();
@@ -631,7 +699,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // here: a commit for it would stop the lane that issues the products (64 to 200 cycles).
         if (u >= last_from && lane == 0) mbar_arrive(bar(kPPassed + (unit + u) % kStages));
         if (live) {
-          const int pos0 = u * kTokens;
+          const int pos0 = (it.from + u) * kTokens;
           const float scale = CAP ? 1.0f : c;
           const float2 scale2 = make_float2(scale, scale);
           bool renew = u == 0 || __any_sync(0xffffffffu, real && ref == -INFINITY);
@@ -742,7 +810,138 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         break;
       }
       tc_fence_after();
-      if (live) {
+      // What the CTAs that share the item have of this tile's rows becomes one: first their
+      // references and sums, then the outputs, each CTA's share of the columns at that CTA, from warp
+      // to warp of the same rows.
+      [[maybe_unused]] auto join = [&]() -> bool {
+        const int parts = ((t == 0 ? it.total0 : it.total1) + it.share - 1) / it.share;  // CTAs that have some, the first ones
+        const uint32_t mail = base + Cfg::kOffStage + warp * Cfg::kStage, mail_stats = mail + Cfg::kSlabs * Cfg::kSlab;
+        auto place = [](int of, int at) { return of < at ? of : of - 1; };  // of a CTA among the others of CTA `at`
+        auto gate = [&](int place, int what) { return base + Cfg::kOffJoin + 8 * ((warp * (kMaxParts - 1) + place) * kGates + what); };
+        auto here = [&](int place, int what, uint32_t phase, int bytes) {
+          if (bytes > 0 && lane == 0) mbar_arrive_expect_tx(gate(place, what), bytes);
+          return __all_sync(0xffffffffu, mbar_wait(gate(place, what), phase >> place & 1, status));
+        };
+        // the sum's sign says whether infinities and NaN were taken out
+        const float told = flags[number % kFlags] == number + 1 ? __uint_as_float(__float_as_uint(sum) | 0x80000000u) : sum;
+        for (int q = 0; q < parts; ++q)
+          if (q != rank) {
+            // the last item's slab has been read there, and before it the last item's sums
+            if (!here(place(q, rank), kSlabRead, ~sent, 0)) return false;
+            const uint32_t to = mail_stats + place(rank, q) * Cfg::kStats + lane * 8;
+            if (EXL3_SMEM(to, 8)) store_there(map_to_rank(to, q), map_to_rank(gate(place(rank, q), kStatsHere), q), ref, told);
+          }
+        float refs[kMaxParts - 1], sums[kMaxParts - 1], top = ref;
+        uint32_t taken = __float_as_uint(told);
+#pragma unroll
+        for (int k = 0; k < kMaxParts - 1; ++k) {
+          refs[k] = -INFINITY;
+          sums[k] = 0.f;
+          if (k + (k >= rank) < parts) {
+            if (!here(k, kStatsHere, stats_got, Cfg::kStats)) return false;
+            stats_got ^= 1u << k;
+            uint32_t w;
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=f"(refs[k]), "=r"(w) : "r"(mail_stats + k * Cfg::kStats + lane * 8) : "memory");
+            sums[k] = __uint_as_float(w & 0x7fffffffu);
+            taken |= w;
+            top = fmaxf(top, refs[k]);
+          }
+        }
+        float mine = ref == -INFINITY ? 0.f : ex2(ref - top), total = mine * sum;
+#pragma unroll
+        for (int k = 0; k < kMaxParts - 1; ++k) {
+          refs[k] = refs[k] == -INFINITY ? 0.f : ex2(refs[k] - top);
+          total = fmaf(refs[k], sums[k], total);
+        }
+        const float f = total == 0.f ? 0.f : 1.0f / total;
+        mine *= f;
+#pragma unroll
+        for (int k = 0; k < kMaxParts - 1; ++k) refs[k] *= f;
+        const int head = it.h * p.group + head_in;
+        const int64_t off = (int64_t)(it.row0 + pos) * p.a.ldo + (int64_t)head * D;
+        const bool fits = real && EXL3_SPAN(off, D, (int64_t)(p.a.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D);
+        if (rank == 0 && fits && p.a.lse) p.a.lse[(int64_t)(it.row0 + pos) * p.a.n_heads + head] = log_sum(top + kHeadroom, total * 0x1p-8f);
+        const int wide = parts == 2 ? 2 * Cfg::kSlabs / 3 : Cfg::kSlabs / 3;  // slabs that go to a CTA at a time: one place for each other
+#pragma unroll 1
+        for (int first = 0; first < D; first += 8 * wide * parts) {
+          for (int i = 1; i < parts; ++i) {
+            const int q = rank + i < parts ? rank + i : rank + i - parts, at = place(q, rank), k = first + 8 * wide * q;
+            if (k >= D) continue;
+            if (!here(at, kSlabRead, ~sent, 0)) return false;
+            sent ^= 1u << at;
+            const uint32_t bar_there = map_to_rank(gate(place(rank, q), kSlabHere), q);
+            for (int c = 0; c < wide; ++c) {
+              float o[8];
+              tmem_ld8(o_tmem + k + 8 * c, o);
+              const uint32_t to = mail + (place(rank, q) * wide + c) * Cfg::kSlab + lane * 32;
+              if (EXL3_SMEM(to, 32)) {
+                const uint32_t there = map_to_rank(to, q);
+                store_there(there, bar_there, o[0], o[1], o[2], o[3]);
+                store_there(there + 16, bar_there, o[4], o[5], o[6], o[7]);
+              }
+            }
+          }
+          if (first + 8 * wide * rank >= D) continue;
+#pragma unroll
+          for (int i = 0; i < kMaxParts - 1; ++i) {
+            if (i + (i >= rank) >= parts) continue;
+            if (!here(i, kSlabHere, got, wide * Cfg::kSlab)) return false;
+            got ^= 1u << i;
+          }
+          for (int c = 0; c < wide; ++c) {
+            const int k = first + 8 * (wide * rank + c);
+            float o[8];
+            tmem_ld8(o_tmem + k, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= mine;
+#pragma unroll
+            for (int i = 0; i < kMaxParts - 1; ++i) {
+              if (i + (i >= rank) >= parts) continue;
+              float x[8];
+              const uint32_t from = mail + (i * wide + c) * Cfg::kSlab + lane * 32;
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(from) : "memory");
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]) : "r"(from + 16) : "memory");
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = fmaf(refs[i], x[e], o[e]);
+            }
+            if (fits && taken >> 31) {  // as below
+#pragma unroll 1
+              for (int at = it.first_masked * kTokens; at < limit; ++at) {
+                const int64_t from = (int64_t)(it.row0 + at) * p.a.ldv + (int64_t)it.h * D + k;
+                if (!EXL3_SPAN(from, 8, (int64_t)(p.a.rows - 1) * p.a.ldv + (int64_t)p.a.n_kv_heads * D)) continue;
+                const __half *v = static_cast<const __half *>(p.a.v) + from;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float x = __half2float(v[e]);
+                  if (!isfinite(x)) o[e] += x;
+                }
+              }
+            }
+            if (fits) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const __half2 h2 = __floats2half2_rn(o[2 * x], o[2 * x + 1]);
+                w[x] = *reinterpret_cast<const uint32_t *>(&h2);
+              }
+              *reinterpret_cast<uint4 *>(static_cast<__half *>(p.a.out) + off + k) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          // after the stores, which have used what was read; one arrival for the warp
+          __syncwarp();
+          if (lane < kMaxParts - 1 && lane + (lane >= rank) < parts) {
+            const int q = lane + (lane >= rank);
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(gate(place(rank, q), kSlabRead), q)) : "memory");
+          }
+        }
+        return true;
+      };
+      if constexpr (SPLIT) {
+        if (live && !join()) {
+          ok = false;
+          break;
+        }
+      } else if (live) {
         const float f = sum == 0.f ? 0.f : 1.0f / sum;
         const int head = it.h * p.group + head_in;
         const int64_t off = (int64_t)(it.row0 + pos) * p.a.ldo + (int64_t)head * D;
@@ -807,11 +1006,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if constexpr (SPLIT) cluster_sync_all();  // nothing comes from another CTA any more
+  else __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+}
+
+// Clusters of 2 and of 4 CTAs that run at once (D = 64, D = 128), as exl3_init finds them.
+int resident_clusters[2][2];
+
+// How many CTAs share an item's keys: what takes least, in units of a pair of tiles (1.4 us),
+// if the sequences are of one length. An item costs 2.8 units besides its own, sharing it 3.2
+// more (4.5 by four). Measured (us, one / two / four CTAs an item, D = 128): 8192 tokens of one
+// head (32 items) 97 / 55 / 36; 4096 of 5 heads on one (82) 53 / 35 / 47; 2984 of 4 (48) 40 / 28
+// / 30; 1024 of 4 (16) 18.1 / 17.3 / 16.3; 512 of 4 (8) 12.3 / 14.4 / 14.5; 1024 of 40 on 8
+// (168) 21 / 38 / 60.
+int ranks_for(const PromptAttention &a, int64_t items, int num_sms, const int *clusters) {
+  if (a.n_seqs > kSplitSeqs) return 1;
+  const float longest = (float)a.rows / (float)a.n_seqs / kTokens;
+  auto units = [&](int ranks, int at_once, float more) {
+    float rounds = (float)items / (float)at_once, share = longest / ranks;
+    if (rounds < 1.0f) rounds = 1.0f;
+    if (a.causal) return fmaxf(share, rounds * share * 0.5f) + rounds * (2.8f + more);  // half as long on average, dealt evenly
+    return ceilf(rounds) * (share + 2.8f + more);
+  };
+  const float one = units(1, num_sms, 0.f), two = units(2, clusters[0] > 0 ? clusters[0] : 1, 3.2f);
+  const float four = items <= clusters[1] ? units(4, clusters[1], 4.5f) : INFINITY;
+  return four < one && four < two ? 4 : two < one ? 2 : 1;
 }
 
 template <int D>
@@ -830,17 +1054,48 @@ cudaError_t prompt_attention(const PromptAttention &a, int num_sms, cudaStream_t
   if (!encode(&tq, a.q, a.n_heads, a.ldq, (uint32_t)p.group, (uint32_t)p.tile_tokens) ||
       !encode(&tk, a.k, a.n_kv_heads, a.ldk, 1, kTokens) || !encode(&tv, a.v, a.n_kv_heads, a.ldv, 1, kTokens))
     return cudaErrorInvalidValue;
+  // items at most
+  auto items = [&](int n_seqs) { return (ceil_div(a.rows, 2 * p.tile_tokens) + n_seqs) * a.n_kv_heads; };
+  p.ranks = ranks_for(a, items(a.n_seqs), num_sms, resident_clusters[D == 128]);
+  if (p.ranks > 1) {
+    const int64_t most = items(a.n_seqs), clusters = resident_clusters[D == 128][p.ranks == 4];
+    return launch_overlapped(a.softcap > 0.f ? prompt_attention_kernel<D, true, true> : prompt_attention_kernel<D, false, true>,
+                             dim3((unsigned)(p.ranks * (most < clusters ? most : clusters))), kPromptThreads, PromptCfg<D, true>::kSmem, st, p.ranks,
+                             tq, tk, tv, p);
+  }
   for (int s0 = 0; s0 < a.n_seqs; s0 += kPromptSeqs) {
     p.a.q_start = a.q_start + s0;
     p.a.n_seqs = a.n_seqs - s0 < kPromptSeqs ? a.n_seqs - s0 : kPromptSeqs;
-    // no more items than this
-    const int64_t most = (ceil_div(a.rows, 2 * p.tile_tokens) + p.a.n_seqs) * a.n_kv_heads;
+    const int64_t most = items(p.a.n_seqs);
     const cudaError_t e =
-        launch_overlapped(a.softcap > 0.f ? prompt_attention_kernel<D, true> : prompt_attention_kernel<D, false>,
-                          dim3((unsigned)(most < num_sms ? most : num_sms)), kPromptThreads, PromptCfg<D>::kSmem, st, 1, tq, tk, tv, p);
+        launch_overlapped(a.softcap > 0.f ? prompt_attention_kernel<D, true, false> : prompt_attention_kernel<D, false, false>,
+                          dim3((unsigned)(most < num_sms ? most : num_sms)), kPromptThreads, PromptCfg<D, false>::kSmem, st, 1, tq, tk, tv, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+template <int D>
+cudaError_t init_kernels() {
+  cudaError_t e = cudaSuccess;
+  for (const void *f : {(const void *)prompt_attention_kernel<D, false, false>, (const void *)prompt_attention_kernel<D, true, false>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptCfg<D, false>::kSmem);
+  for (const void *f : {(const void *)prompt_attention_kernel<D, false, true>, (const void *)prompt_attention_kernel<D, true, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptCfg<D, true>::kSmem);
+  for (int four = 0; four < 2 && e == cudaSuccess; ++four) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = four ? 4 : 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(attr.val.clusterDim.x);
+    cfg.blockDim = dim3(kPromptThreads);
+    cfg.dynamicSmemBytes = PromptCfg<D, true>::kSmem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&resident_clusters[D == 128][four], prompt_attention_kernel<D, false, true>, &cfg);
+  }
+  return e;
 }
 
 }  // namespace
@@ -851,10 +1106,8 @@ cudaError_t launch_prompt_attention(const PromptAttention &a, int num_sms, cudaS
 
 cudaError_t init_prompt_attention_kernels(int *status) {
   cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
-  for (const void *f : {(const void *)prompt_attention_kernel<64, false>, (const void *)prompt_attention_kernel<64, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptCfg<64>::kSmem);
-  for (const void *f : {(const void *)prompt_attention_kernel<128, false>, (const void *)prompt_attention_kernel<128, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptCfg<128>::kSmem);
+  if (e == cudaSuccess) e = init_kernels<64>();
+  if (e == cudaSuccess) e = init_kernels<128>();
   return e;
 }
 
