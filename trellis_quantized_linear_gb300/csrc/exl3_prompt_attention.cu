@@ -183,7 +183,6 @@ struct PromptWalk {
   const int2 *seq;
   const int *pairs;
   int n_seqs;
-  uint32_t c, C;
   uint32_t round, base;
   int level, count;  // causal: place of the pair, and sequences that have it; else the sequence
   __device__ __forceinline__ void begin(int causal) {
@@ -191,8 +190,8 @@ struct PromptWalk {
     level = causal && n_seqs > 0 ? pairs[0] - 1 : 0;
     count = 0;
   }
-  __device__ __forceinline__ bool next(const PromptParams &p, Item &it) {
-    const uint32_t heads = p.a.n_kv_heads;
+  __device__ __forceinline__ bool next(const PromptParams &p, Item &it, int ranks) {
+    const uint32_t c = blockIdx.x / ranks, C = gridDim.x / ranks, heads = p.a.n_kv_heads;
     const uint32_t idx = round * C + (round & 1 ? C - 1 - c : c);
     ++round;
     int s, place;
@@ -448,12 +447,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __syncwarp();
-  if constexpr (SPLIT) cluster_sync_all();  // every CTA runs, with its barriers, before another stores to it
+  if constexpr (SPLIT) {  // every CTA runs, with its barriers, before another stores to it
+    __syncwarp();
+    cluster_sync_all();
+  }
   tc_fence_before();
   PromptWalk walk{seq, reinterpret_cast<int *>(smem + Cfg::kOffLen),
-                  sort_prompts<Cfg::kSeqs>(p.a, 2 * p.tile_tokens, seq, reinterpret_cast<int *>(smem + Cfg::kOffLen)),
-                  blockIdx.x / ranks, gridDim.x / ranks};
+                  sort_prompts<Cfg::kSeqs>(p.a, 2 * p.tile_tokens, seq, reinterpret_cast<int *>(smem + Cfg::kOffLen))};
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int4 *items = reinterpret_cast<int4 *>(smem + Cfg::kOffItem);
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         auto walk_on = [&](Item &it) {  // to the next item that this CTA has units of
           do {
-            it.there = walk.next(p, it);
+            it.there = walk.next(p, it, ranks);
             it.take_part<SPLIT>(rank, ranks);
           } while (SPLIT && it.there && it.all() == 0);
         };
@@ -1006,9 +1006,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   }
   tc_fence_before();
-  __syncwarp();
-  if constexpr (SPLIT) cluster_sync_all();  // nothing comes from another CTA any more
-  else __syncthreads();
+  if constexpr (SPLIT) {  // nothing comes from another CTA any more
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
