@@ -280,6 +280,35 @@ def test_few_heads_twice_at_once_and_captured(heads, kv_heads, dim, lens):
     assert tql.exl3_get_device_status() == 0
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(2, 1, 64), (1, 1, 128), (8, 8, 64)])
+def test_few_heads_captured_call_serves_other_lengths(heads, kv_heads, dim):
+    """The rows that a call has room for say how many CTAs share an item; the lengths may be any."""
+    import torch
+    rows = 4000
+    x = inputs(rows, heads, kv_heads, dim, 35)
+    xd = torch.from_numpy(x).cuda()
+    out, lse = torch.empty((rows, heads * dim), dtype=torch.float16, device="cuda"), torch.empty((rows, heads), device="cuda")
+    qs = torch.zeros(4, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tql.exl3_prompt_attention(*split(xd, heads, kv_heads, dim), heads, kv_heads, dim, qs, dim ** -0.5, out, lse=lse)
+    for lens in ([1500, 0, 1200], [1, 2, 3], [0, 0, 0], [129, 700, 64], [0, 1281, 0], [385, 513, 641]):
+        s = starts(lens)
+        qs.copy_(torch.from_numpy(s))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        check(x, s, heads, kv_heads, dim, dim ** -0.5, 0.0, True, out.cpu().numpy(), lse.cpu().numpy())
+    qs.copy_(torch.tensor([100, 1200, 1100, 5000], dtype=torch.int32))  # a good range and two that are none
+    out.fill_(7.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert tql.exl3_get_device_status() == 10
+    check(x[100:1200], [0, 1100], heads, kv_heads, dim, dim ** -0.5, 0.0, True, out.cpu().numpy()[100:1200], lse.cpu().numpy()[100:1200])
+    assert torch.all(out[:100] == 7.0) and torch.all(out[1200:] == 7.0)
+
+
 def test_heavy_and_growing_scores():
     """Maxima that grow along a row, so that its output is rescaled again and again."""
     lens, heads, kv_heads, dim = [1000], 2, 1, 64
