@@ -9,8 +9,8 @@
 // each resident CTA.
 //
 // Measured (in a graph, residual read and written): one row of 5120 fp16 1.9 us; 8192 rows
-// 57 us (5.9 TB/s; loads into registers 67); 777 rows fp32 with E4M3 codes 11.6 us (4.5 TB/s:
-// 2.6 rows for each CTA of the ring, 3 for some); 2400 rows of 17408 58 us (5.8 TB/s, from
+// 57 us (5.9 TB/s; loads into registers 67); 777 rows fp32 with E4M3 codes 11.0 us (4.7 TB/s:
+// 2.6 rows for each CTA of the ring, 3 for some; with two lanes at a bank 11.4); 2400 rows of 17408 58 us (5.8 TB/s, from
 // registers 94). The rules between the forms stand at by_size, with both sides.
 #include <math.h>
 
@@ -42,6 +42,14 @@ struct Eight {
   }
   __device__ __forceinline__ void load(const float *p) {
     const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  // From shared memory: every other four lanes read the second half first, so that 8 lanes have all 32 banks.
+  __device__ __forceinline__ void load_shared(const __half *p) { load(p); }
+  __device__ __forceinline__ void load_shared(const float *p) {
+    const bool second = threadIdx.x & 4;
+    const float4 x = reinterpret_cast<const float4 *>(p)[second], y = reinterpret_cast<const float4 *>(p)[!second];
+    const float4 a = second ? y : x, b = second ? x : y;
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
   __device__ __forceinline__ void zero() {
@@ -274,10 +282,10 @@ __global__ void __launch_bounds__(kRingThreads, V <= 2 ? 2 : 1) rms_norm_ring_ke
     for (int i = 0; i < V; ++i) {
       const int c = i * per_row + at;
       if (c < pieces) {
-        h[i].load(reinterpret_cast<const X *>(smem + st * stage_bytes) + c * 8);
+        h[i].load_shared(reinterpret_cast<const X *>(smem + st * stage_bytes) + c * 8);
         if constexpr (kResidual) {
           Eight r;
-          r.load(reinterpret_cast<const Rt *>(smem + st * stage_bytes + x_bytes) + c * 8);
+          r.load_shared(reinterpret_cast<const Rt *>(smem + st * stage_bytes + x_bytes) + c * 8);
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[i].v[e] += r.v[e];
         }
