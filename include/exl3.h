@@ -673,7 +673,8 @@ exl3_status exl3_qk_rotary(const void *x, int64_t ldx, void *out, int64_t ldo, i
  * left out.
  * Sums, maxima and the softmax are fp32; the probabilities enter the product with the
  * values as fp16, scaled so that one of 2^-22 of a row's largest has all its 11 bits and
- * one of 2^-33 still counts. The result does not depend on scheduling.
+ * one of 2^-33 still counts. The result does not depend on scheduling. Scores of any size
+ * that fp32 holds are taken as they are; beyond it they are infinite.
  *   head_dim: 64 or 128; scale: finite; softcap: 0 (off) or finite and at least 1e-30 (a
  *   capped score has an error of 2^-19 of itself at most, besides that of the products);
  *   n_seqs: 0 .. 65535; rows * n_heads below 2^31. out must not overlap q, k or v.

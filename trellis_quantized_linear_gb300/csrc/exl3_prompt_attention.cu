@@ -65,6 +65,12 @@ constexpr int kFlags = 8;          // items whose flag is kept; more than a ring
 // The result is the same, as the row's sum goes by the same reference. A row's largest
 // probability is then 2^8 to 2^16: one of 2^-22 of it has all 11 bits, one of 2^-33 counts.
 constexpr float kHeadroom = 8.0f, kMostSum = 65504.0f, kMost = 15.9f;
+// The exponent is one fused operation, product * c - reference, which does not round the score
+// as the reference was rounded. Below kLarge the two are 2^-4 apart at most; at 2^28 they would be
+// 16 apart, which leaves fp16. Where a row's reference is past kLarge, every unit of the
+// item from there on sets references anew and then puts rounded scores less the reference in
+// the products' place (`less_reference`).
+constexpr float kLarge = 0x1p20f;
 
 template <int D, bool SPLIT>
 struct PromptCfg {
@@ -378,6 +384,20 @@ struct PromptCap {
   }
 };
 
+// A row's 128 products in TMEM, in place: (score - ref) / c for rows that want it.
+__device__ __forceinline__ void less_reference(uint32_t scores, bool wanted, float c, float ref) {
+  const float back = 1.0f / c;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    float s[32];
+    tmem_ld32(scores + 32 * q, s);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = wanted ? (__fmul_rn(s[i], c) - ref) * back : s[i];
+    tmem_st32(scores + 32 * q, s);
+  }
+  tmem_wait_st();
+}
+
 // Stores to another CTA of the cluster, whose bytes are counted on its barrier (both addresses
 // from map_to_rank): nothing has to be waited for here, as a release would, for stores to memory too.
 __device__ __forceinline__ void store_there(uint32_t dst, uint32_t bar, float a, float b, float c, float d) {
@@ -688,6 +708,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const bool live = __any_sync(0xffffffffu, real);
       float ref = -INFINITY, sum = 0.f;
       bool far = !cap.ready;  // scores beyond half the cap were seen
+      bool large = false;     // a reference past kLarge was
       for (int u = 0; u < units; ++u, ++count) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kPS + t), count & 1, status))) {
           ok = false;
@@ -702,7 +723,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const int pos0 = (it.from + u) * kTokens;
           const float scale = CAP ? 1.0f : c;
           const float2 scale2 = make_float2(scale, scale);
-          bool renew = u == 0 || __any_sync(0xffffffffu, real && ref == -INFINITY);
+          bool renew = u == 0 || large || __any_sync(0xffffffffu, real && ref == -INFINITY);
+          bool less = false;  // TMEM holds scores less the reference, of rows past kLarge
           float s[64], s2[64];  // of the unit's first and second 64 keys
           uint32_t packed[32];  // fp16 probabilities: 2^-12 on average, the size of the result's own rounding
           float2 part[2], shift2;
@@ -754,7 +776,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (renew) {
               tmem_ld64_end(s2);
               mask(s2, pos0 + 64);
-              const float now = fmaxf(fmaxf(most(s), most(s2)) - kHeadroom, ref);
+              const float now = fmaxf(__fsub_ru(fmaxf(most(s), most(s2)), kHeadroom), ref);  // up: 16 below would leave fp16
               if (u > 0) {
                 const float keep = now == ref || ref == -INFINITY ? 1.0f : ex2(ref - now);
                 // the scores' product came after the output's, which is therefore done
@@ -769,8 +791,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 sum *= keep;
               }
               ref = now;
+              const bool past = fabsf(ref) >= kLarge && ref > -INFINITY;
+              if (!CAP && __any_sync(0xffffffffu, real && past)) {
+                less_reference(s_tmem, past, c, ref);
+                large = less = true;
+                renew = false;
+                continue;  // none is above 2^kHeadroom now
+              }
             }
-            const float shift = ref == -INFINITY ? 0.f : -ref;
+            const float shift = ref == -INFINITY || (less && fabsf(ref) >= kLarge) ? 0.f : -ref;
             shift2 = make_float2(shift, shift);
             part[0] = part[1] = make_float2(0.f, 0.f);
             exponentials(s, 0, 32);
@@ -780,7 +809,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mask(s2, pos0 + 64);
             const float so_far = (part[0].x + part[0].y) + (part[1].x + part[1].y);
             const bool beyond = CAP && real && most_x >= cap.edge;
-            if (!__any_sync(0xffffffffu, beyond || (real && (so_far > kMostSum || most(s2) + shift > kMost)))) break;
+            if (!__any_sync(0xffffffffu, beyond || (real && (so_far > kMostSum || most(s2) + shift > kMost))) || less) break;
             if (CAP && !capped) {
               far = __any_sync(0xffffffffu, beyond);  // the item's other units at once
               cap.all(s_tmem, real);
