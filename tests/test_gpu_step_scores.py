@@ -74,3 +74,15 @@ def test_rows_of_large_scores_beside_usual_ones(heads, kv_heads, dim, rows):
         usual[:, heads * dim:] = x[:, heads * dim:]
         want, want_lse = run(usual, qs, heads, kv_heads, dim, 2.0, causal=causal)
         check(usual, qs, heads, kv_heads, dim, 2.0, 0.0, causal, np.where(few[:, None], out, want), np.where(few[:, None], lse, want_lse))
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,rows", [(6, 2, 64, 300), (1, 1, 128, 1500)])
+@pytest.mark.parametrize("scale,cap", [(1e30, 1e-30), (-1e30, 1e-28), (3.4e38, 0.0), (-3.4e38, 0.0), (3.4e38, 30.0), (3.4e38, 1e38)])
+def test_scores_of_zero_stay_zero_beside_any_scale(heads, kv_heads, dim, rows, scale, cap):
+    """Also where scale / cap or the scale in log2 units leaves fp32."""
+    x, qs = inputs(rows, heads, kv_heads, dim, 44), starts([rows])
+    x[:, :heads * dim] = 0
+    x[:, 1:heads * dim:2] = -0.0
+    for causal in (True, False):
+        out, lse = run(x, qs, heads, kv_heads, dim, scale, cap, causal)
+        check(x, qs, heads, kv_heads, dim, scale, cap, causal, out, lse)

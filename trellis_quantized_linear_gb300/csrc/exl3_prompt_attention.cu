@@ -334,8 +334,9 @@ struct PromptCap {
   bool ready;               // else all scores take the pass over TMEM
   float k, unit, cap, edge; // x = product * k; edge: what (product * unit)^2 is below, of those near
   float p[4];               // of (product * unit)^2, times what brings a product to log2 units
-  // A cap whose double leaves fp32 is lowered: no score comes near it.
-  __device__ __forceinline__ PromptCap(float softcap, float c) : k(c / fmaxf(softcap * kLog2e, 1e-30f)), cap(fminf(softcap * kLog2e, 1.5e38f)) {
+  // A cap whose double leaves fp32 is lowered: no score comes near it. So is k, which times 0 has to be 0.
+  __device__ __forceinline__ PromptCap(float softcap, float c)
+      : k(fminf(c / fmaxf(softcap * kLog2e, 1e-30f), 0x1p127f)), cap(fminf(softcap * kLog2e, 1.5e38f)) {
     ready = k > 0x1p-18f && k < 0x1p14f && c > 0x1p-10f && c < 0x1p14f;
     unit = ready ? 1.0f : k;
     const float k2 = ready ? k * k : 1.0f;
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_tmem = lane_base + 128 * t, o_tmem = lane_base + 256 + 128 * t;
-    const float c = fmaxf(fabsf(p.a.scale) * Raised<D>::kLog2e, 1e-37f);  // scores in log2 units are the products times c
+    const float c = fminf(fmaxf(fabsf(p.a.scale) * Raised<D>::kLog2e, 1e-37f), 0x1.fffffep127f);  // scores in log2 units are the products times c
     const PromptCap cap(p.a.softcap, c);
     const int token = row / p.group, head_in = row - token * p.group;
     uint32_t count = 0, items = 0, number = 0, unit = 0;  // units and items of this tile, items and units of the CTA
