@@ -117,7 +117,13 @@ class Exl3Kv8Batch(ctypes.Structure):
                 raise ValueError("Exl3Kv8Batch: tensors are contiguous int32")
         super().__init__(_ptr(page_table), _ptr(kv_len), _ptr(q_start), n, page_table.shape[1], rows, max_rows)
         self._keep = (page_table, kv_len, q_start)
+        devices = {t.get_device() for t in self._keep if t is not None}
+        self._device = devices.pop() if len(devices) == 1 else None  # None: not all on one
         self._ref = ctypes.byref(self)
+
+    def get_device(self):
+        """Index of the device that all its tensors are on, None where they are not on one."""
+        return self._device
 
 
 class _LogitsRules(ctypes.Structure):
@@ -262,14 +268,19 @@ def _stream(stream):
 _ready = False  # a device was initialized
 
 
-def _stream_beside(what, t, stream):
-    """_stream, if t is on the current device; its other tensors are not looked at (0.06 us each)."""
+def _stream_beside(what, stream, *tensors):
+    """_stream, if each of a call's tensors is on the current device (None and addresses: the caller's care)."""
     handle = _stream(stream)
     if _ready:
         if _raw_device is None:
             _stream(None)
-        if t.get_device() != _raw_device():
-            raise ValueError(f"{what}: the tensors have to be on the current device")
+        device = _raw_device()
+        try:
+            for t in tensors:
+                if t is not None and t.get_device() != device:
+                    raise ValueError(f"{what}: the tensors have to be on the current device ({device}), one is on {t.get_device()}")
+        except AttributeError:  # an address
+            return _stream_beside(what, stream, *(t for t in tensors if not isinstance(t, int)))
     return handle
 
 
@@ -562,7 +573,7 @@ def exl3_kv8_plan(batch: Exl3Kv8Batch, tokens, cached, free_pages, free_count, f
         _array("exl3_kv8_plan: free_pages", free_pages, i32, 0), free_pages.numel(), _array("exl3_kv8_plan: free_count", free_count, i32, 1),
         _array("exl3_kv8_plan: free_left", free_left, i32, 1), n_pages, _array("exl3_kv8_plan: position", position, i32, rows),
         _array("exl3_kv8_plan: slot", slot, i32, rows), _array("exl3_kv8_plan: served", served, i32, 1),
-        _stream_beside("exl3_kv8_plan: free_pages", free_pages, stream))
+        _stream_beside("exl3_kv8_plan", stream, batch, tokens, cached, free_pages, free_count, free_left, position, slot, served))
     if status:
         raise Exl3Error(status, "exl3_kv8_plan")
 
@@ -607,7 +618,7 @@ def exl3_rms_norm(x, y=None, weight=None, residual=None, residual_out=None, eps:
         ps = _array("exl3_rms_norm: scales", scales, _F32, rows * scales.shape[1])
     status = lib.exl3_rms_norm(_PACK_NORM(x.data_ptr(), r, ro, _array("exl3_rms_norm: weight", weight, f16, cols), py, pc, ps, rows, cols,
                                           ldx, ldr, ldro, ldy, ldc, x_type, r_type, group, eps, weight_offset),
-                               _stream_beside("exl3_rms_norm: x", x, stream))
+                               _stream_beside("exl3_rms_norm", stream, x, y, weight, residual, residual_out, codes, scales))
     if status:
         raise Exl3Error(status, "exl3_rms_norm")
 
@@ -629,7 +640,7 @@ def exl3_qk_rotary(x, out, q_heads: int, k_heads: int, head_dim: int, position, 
         x.data_ptr(), ldx, out.data_ptr(), ldo, rows, q_heads, k_heads, head_dim, _array("exl3_qk_rotary: position", position, _I32, rows),
         _array("exl3_qk_rotary: cos_sin", cos_sin, _F32, n_positions * rot_dim), n_positions, rot_dim, interleaved,
         _array("exl3_qk_rotary: q_weight", q_weight, f16, head_dim), _array("exl3_qk_rotary: k_weight", k_weight, f16, head_dim), eps,
-        weight_offset, _stream_beside("exl3_qk_rotary: x", x, stream))
+        weight_offset, _stream_beside("exl3_qk_rotary", stream, x, out, position, cos_sin, q_weight, k_weight))
     if status:
         raise Exl3Error(status, "exl3_qk_rotary")
 
@@ -650,7 +661,7 @@ def exl3_prompt_attention(q, k, v, n_heads: int, n_kv_heads: int, head_dim: int,
         _rows("exl3_prompt_attention: k", k, f16, rows, kv_width), v.data_ptr(), _rows("exl3_prompt_attention: v", v, f16, rows, kv_width),
         n_heads, n_kv_heads, head_dim, _array("exl3_prompt_attention: q_start", q_start, _I32, n_seqs + 1), n_seqs, rows, scale, softcap,
         causal, out.data_ptr(), _rows("exl3_prompt_attention: out", out, f16, rows, width),
-        _array("exl3_prompt_attention: lse", lse, _F32, rows * n_heads), _stream_beside("exl3_prompt_attention: q", q, stream))
+        _array("exl3_prompt_attention: lse", lse, _F32, rows * n_heads), _stream_beside("exl3_prompt_attention", stream, q, k, v, q_start, out, lse))
     if status:
         raise Exl3Error(status, "exl3_prompt_attention")
 
