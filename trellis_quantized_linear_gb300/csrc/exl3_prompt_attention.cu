@@ -108,6 +108,7 @@ struct PromptParams {
   PromptAttention a;
   int group, tile_tokens;
   int ranks;  // CTAs of a cluster, which share the keys of their items
+  uint32_t nothing;  // 0, which the compiler does not know
 };
 
 // The launch's sequences from the longest to the shortest (equal ones in their order):
@@ -850,7 +851,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         auto gate = [&](int place, int what) { return base + Cfg::kOffJoin + 8 * ((warp * (kMaxParts - 1) + place) * kGates + what); };
         auto here = [&](int place, int what, uint32_t phase, int bytes) {
           if (bytes > 0 && lane == 0) mbar_arrive_expect_tx(gate(place, what), bytes);
-          return __all_sync(0xffffffffu, mbar_wait(gate(place, what), phase >> place & 1, status));
+          return __all_sync(0xffffffffu, mbar_wait_cluster(gate(place, what), phase >> place & 1, status, kWaitLimitNs));
         };
         // the sum's sign says whether infinities and NaN were taken out
         const float told = flags[number % kFlags] == number + 1 ? __uint_as_float(__float_as_uint(sum) | 0x80000000u) : sum;
@@ -885,8 +886,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         const float f = total == 0.f ? 0.f : 1.0f / total;
         mine *= f;
+        uint32_t read = taken;  // bits of all that other CTAs sent
 #pragma unroll
-        for (int k = 0; k < kMaxParts - 1; ++k) refs[k] *= f;
+        for (int k = 0; k < kMaxParts - 1; ++k) {
+          refs[k] *= f;
+          read |= __float_as_uint(refs[k]);
+        }
         const int head = it.h * p.group + head_in;
         const int64_t off = (int64_t)(it.row0 + pos) * p.a.ldo + (int64_t)head * D;
         const bool fits = real && EXL3_SPAN(off, D, (int64_t)(p.a.rows - 1) * p.a.ldo + (int64_t)p.a.n_heads * D);
@@ -932,7 +937,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(from) : "memory");
               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]) : "r"(from + 16) : "memory");
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = fmaf(refs[i], x[e], o[e]);
+              for (int e = 0; e < 8; ++e) {
+                o[e] = fmaf(refs[i], x[e], o[e]);
+                read |= __float_as_uint(x[e]);
+              }
             }
             if (fits && taken >> 31) {  // as below
 #pragma unroll 1
@@ -957,11 +965,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               *reinterpret_cast<uint4 *>(static_cast<__half *>(p.a.out) + off + k) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          // after the stores, which have used what was read; one arrival for the warp
-          __syncwarp();
+          // One arrival for the warp. A release would wait for the stores to memory too (8192 tokens of one head:
+          // 39.6 us for 37.3); what orders the reads before the next slab is that the arrival's address
+          // depends on all of them.
+          const uint32_t seen = __reduce_or_sync(0xffffffffu, read) & p.nothing;
           if (lane < kMaxParts - 1 && lane + (lane >= rank) < parts) {
             const int q = lane + (lane >= rank);
-            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(gate(place(rank, q), kSlabRead), q)) : "memory");
+            asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(gate(place(rank, q), kSlabRead), q) + seen) : "memory");
           }
         }
         return true;
@@ -1077,6 +1087,7 @@ cudaError_t prompt_attention(const PromptAttention &a, int num_sms, cudaStream_t
   p.a = a;
   p.group = a.n_heads / a.n_kv_heads;
   p.tile_tokens = kTile / p.group;
+  p.nothing = 0;
   CUtensorMap tq, tk, tv;
   auto encode = [&](CUtensorMap *m, const void *ptr, int heads, int64_t ld, uint32_t box_heads, uint32_t box_rows) {
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)a.rows};
