@@ -253,7 +253,7 @@ exl3_status exl3_init(int device) {
       init_kv8_weigh_chunk_kernels(info.status) != cudaSuccess ||
       init_logits_adjust_kernels(info.status) != cudaSuccess || init_kv8_plan_kernels(info.status) != cudaSuccess ||
       init_rms_norm_kernels(info.status) != cudaSuccess || init_qk_rotary_kernels(info.status) != cudaSuccess ||
-      init_prompt_attention_kernels(info.status) != cudaSuccess)
+      init_prompt_attention_kernels(info.status, info.prompt_clusters) != cudaSuccess)
     return EXL3_ERR_CUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return EXL3_ERR_CUDA;
   info.ready = true;

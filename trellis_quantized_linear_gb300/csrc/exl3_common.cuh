@@ -389,6 +389,7 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t
 struct DeviceInfo {
   int num_sms = 0;
   int *status = nullptr;  // device address of the error word
+  int prompt_clusters[2][2] = {};  // of prompt attention, D = 64 and 128: clusters of 2 and of 4 CTAs that run at once
   bool ready = false;
 };
 

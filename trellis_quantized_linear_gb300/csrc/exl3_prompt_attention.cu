@@ -27,7 +27,7 @@
 // to CTA through shared memory of the cluster (`join`), each CTA joining and storing its share of the
 // columns: no workspace, and the same result each time. By st.async, which counts its bytes at
 // the receiver: a released arrival waits for the stores to memory too, and took 20 us an item;
-// what it takes now is about 2. ranks_for has the rule and both sides.
+// what it takes now is about 2. prompt_ranks has the rule and both sides.
 //
 // Measured: one prompt of 8192 tokens, 40 heads on 8, D = 128: 454 to 467 us (687 GFLOP, up to
 // 1510 TFLOP/s; 485 to 504 in long runs, in which the clock falls), one of 2048: 46 us; D = 64:
@@ -44,6 +44,7 @@
 
 #include "exl3_internal.h"
 #include "exl3_kv8.cuh"
+#include "exl3_prompt_ranks.h"
 #include "exl3_tcgen05.cuh"
 
 namespace exl3 {
@@ -55,7 +56,7 @@ constexpr int kTokens = 128;       // of a unit
 constexpr int kMmaWarp = 8 /* after the softmax warps */, kLoadWarp = 9, kCleanWarp = 10, kCleanWarps = 2;
 constexpr int kPromptThreads = 12 * 32;  // 168 registers a thread
 constexpr int kPromptSeqs = 1024;  // sequences of one launch
-constexpr int kMaxParts = 4, kSplitSeqs = 128;  // CTAs that share an item's keys, and sequences of such a launch
+constexpr int kMaxParts = 4;       // CTAs that share an item's keys
 constexpr int kItems = 4;          // items announced at a time
 constexpr int kFlags = 8;          // items whose flag is kept; more than a ring can be ahead
 // Probabilities are taken relative to a reference: 2^kHeadroom below the row's maximum over
@@ -1058,31 +1059,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
 }
 
-// Clusters of 2 and of 4 CTAs that run at once (D = 64, D = 128), as exl3_init finds them.
-int resident_clusters[2][2];
-
-// How many CTAs share an item's keys: what takes least, in units of a pair of tiles (1.4 us),
-// if the sequences are of one length. An item costs 2.8 units besides its own, sharing it 3.2
-// more (4.5 by four). Measured (us, one / two / four CTAs an item, D = 128): 8192 tokens of one
-// head (32 items) 97 / 55 / 36; 4096 of 5 heads on one (82) 53 / 35 / 47; 2984 of 4 (48) 40 / 28
-// / 30; 1024 of 4 (16) 18.1 / 17.3 / 16.3; 512 of 4 (8) 12.3 / 14.4 / 14.5; 1024 of 40 on 8
-// (168) 21 / 38 / 60.
-int ranks_for(const PromptAttention &a, int64_t items, int num_sms, const int *clusters) {
-  if (a.n_seqs > kSplitSeqs) return 1;
-  const float longest = (float)a.rows / (float)a.n_seqs / kTokens;
-  auto units = [&](int ranks, int at_once, float more) {
-    float rounds = (float)items / (float)at_once, share = longest / ranks;
-    if (rounds < 1.0f) rounds = 1.0f;
-    if (a.causal) return fmaxf(share, rounds * share * 0.5f) + rounds * (2.8f + more);  // half as long on average, dealt evenly
-    return ceilf(rounds) * (share + 2.8f + more);
-  };
-  const float one = units(1, num_sms, 0.f), two = units(2, clusters[0] > 0 ? clusters[0] : 1, 3.2f);
-  const float four = items <= clusters[1] ? units(4, clusters[1], 4.5f) : INFINITY;
-  return four < one && four < two ? 4 : two < one ? 2 : 1;
-}
-
+// clusters: of 2 and of 4 CTAs that run at once.
 template <int D>
-cudaError_t prompt_attention(const PromptAttention &a, int num_sms, cudaStream_t st) {
+cudaError_t prompt_attention(const PromptAttention &a, int num_sms, const int (&clusters)[2], cudaStream_t st) {
   PromptParams p;
   p.a = a;
   p.group = a.n_heads / a.n_kv_heads;
@@ -1100,11 +1079,11 @@ cudaError_t prompt_attention(const PromptAttention &a, int num_sms, cudaStream_t
     return cudaErrorInvalidValue;
   // items at most
   auto items = [&](int n_seqs) { return (ceil_div(a.rows, 2 * p.tile_tokens) + n_seqs) * a.n_kv_heads; };
-  p.ranks = ranks_for(a, items(a.n_seqs), num_sms, resident_clusters[D == 128]);
+  p.ranks = prompt_ranks(a.n_seqs, a.rows, a.causal, items(a.n_seqs), num_sms, clusters);
   if (p.ranks > 1) {
-    const int64_t most = items(a.n_seqs), clusters = resident_clusters[D == 128][p.ranks == 4];
+    const int64_t most = items(a.n_seqs), at_once = clusters[p.ranks == 4];
     return launch_overlapped(a.softcap > 0.f ? prompt_attention_kernel<D, true, true> : prompt_attention_kernel<D, false, true>,
-                             dim3((unsigned)(p.ranks * (most < clusters ? most : clusters))), kPromptThreads, PromptCfg<D, true>::kSmem, st, p.ranks,
+                             dim3((unsigned)(p.ranks * (most < at_once ? most : at_once))), kPromptThreads, PromptCfg<D, true>::kSmem, st, p.ranks,
                              tq, tk, tv, p);
   }
   for (int s0 = 0; s0 < a.n_seqs; s0 += kPromptSeqs) {
@@ -1120,7 +1099,7 @@ cudaError_t prompt_attention(const PromptAttention &a, int num_sms, cudaStream_t
 }
 
 template <int D>
-cudaError_t init_kernels() {
+cudaError_t init_kernels(int (&clusters)[2]) {
   cudaError_t e = cudaSuccess;
   for (const void *f : {(const void *)prompt_attention_kernel<D, false, false>, (const void *)prompt_attention_kernel<D, true, false>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptCfg<D, false>::kSmem);
@@ -1137,21 +1116,21 @@ cudaError_t init_kernels() {
     cfg.dynamicSmemBytes = PromptCfg<D, true>::kSmem;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&resident_clusters[D == 128][four], prompt_attention_kernel<D, false, true>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&clusters[four], prompt_attention_kernel<D, false, true>, &cfg);
   }
   return e;
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_attention(const PromptAttention &a, int num_sms, cudaStream_t st) {
-  return a.head_dim == 64 ? prompt_attention<64>(a, num_sms, st) : prompt_attention<128>(a, num_sms, st);
+cudaError_t launch_prompt_attention(const PromptAttention &a, int num_sms, const int (&clusters)[2][2], cudaStream_t st) {
+  return a.head_dim == 64 ? prompt_attention<64>(a, num_sms, clusters[0], st) : prompt_attention<128>(a, num_sms, clusters[1], st);
 }
 
-cudaError_t init_prompt_attention_kernels(int *status) {
+cudaError_t init_prompt_attention_kernels(int *status, int (&clusters)[2][2]) {
   cudaError_t e = EXL3_BIND_BOUNDS_WORD(status);
-  if (e == cudaSuccess) e = init_kernels<64>();
-  if (e == cudaSuccess) e = init_kernels<128>();
+  if (e == cudaSuccess) e = init_kernels<64>(clusters[0]);
+  if (e == cudaSuccess) e = init_kernels<128>(clusters[1]);
   return e;
 }
 

@@ -98,11 +98,11 @@ struct QkRotary {
   float eps, weight_offset;
   int *status;
 };
-cudaError_t init_prompt_attention_kernels(int *status);
+cudaError_t init_prompt_attention_kernels(int *status, int (&clusters)[2][2]);
 cudaError_t init_kv8_plan_kernels(int *status);
 cudaError_t init_rms_norm_kernels(int *status);
 cudaError_t init_qk_rotary_kernels(int *status);
-cudaError_t launch_prompt_attention(const PromptAttention &p, int num_sms, cudaStream_t st);
+cudaError_t launch_prompt_attention(const PromptAttention &p, int num_sms, const int (&clusters)[2][2], cudaStream_t st);
 cudaError_t launch_kv8_plan(const KvPlan &p, cudaStream_t st);
 cudaError_t launch_rms_norm(const exl3_norm &p, int num_sms, int *status, cudaStream_t st);
 cudaError_t launch_qk_rotary(const QkRotary &p, int num_sms, cudaStream_t st);

@@ -174,7 +174,7 @@ exl3_status exl3_prompt_attention(const void *q, int64_t ldq, const void *k, int
   p.ldo = ldo;
   p.lse = lse;
   p.status = dev->status;
-  return from_cuda(launch_prompt_attention(p, dev->num_sms, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_prompt_attention(p, dev->num_sms, dev->prompt_clusters, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
