@@ -2,7 +2,9 @@
 import numpy as np
 import pytest
 
+import step_ref
 import trellis_quantized_linear_gb300 as tql
+from test_gpu_step import Plan, random_requests
 from test_gpu_step_attention import check, gpu, inputs, split, starts  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -25,3 +27,39 @@ def test_shared_items_say_the_same_each_time(heads, kv_heads, dim, lens, causal)
     torch.cuda.synchronize()
     check(x, qs, heads, kv_heads, dim, dim ** -0.5, 0.0, causal, outs[0].cpu().numpy(), lses[0].cpu().numpy())
     assert torch.all(outs.view(torch.int16) == outs[:1].view(torch.int16)) and torch.all(lses == lses[:1])
+
+
+# --------------------------------------------------------------------------- plan
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n,most,cached", [(32768, 1, 130), (32769, 2, 70), (40000, 3, 200), (65535, 1, 65)])
+def test_plan_of_more_sequences_than_a_pass_takes(n, most, cached, in_place):
+    """From 32769 on each of the eight CTAs goes through its part several times."""
+    p = Plan(*random_requests(n, most, cached, n))
+    p.call(in_place)
+    p.check()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("where", [0, 4095, 4096, 4999, 5000, 9100, 39999])
+@pytest.mark.parametrize("why", ["pages", "rows", "max_rows", "width"])
+def test_plan_of_many_stops_at_the_first_that_does_not_fit(where, why, in_place):
+    """Before, at and after the ends of passes (4096) and of the CTAs' parts (5000)."""
+    t, c = random_requests(40000, 2, 100, 6, ended=0.02)
+    t[where], c[where] = 70, 64
+    kw = {}
+    if why == "rows":
+        kw = dict(rows=int(np.maximum(t[:where], 0).sum()) + 69)
+    elif why == "max_rows":
+        kw = dict(max_rows=69)
+    elif why == "width":
+        c[where] = 64 * 6 - 69
+        kw = dict(max_pages=6)
+    p = Plan(t, c, **kw)
+    if why == "pages":  # one of the two that it needs
+        p.tokens[:] = np.where(p.tokens < 0, 0, p.tokens)
+        p.count = 1 + sum(step_ref.blocks(int(x + y)) - step_ref.blocks(int(x)) for x, y in zip(c[:where], t[:where]) if y > 0)
+    p.call(in_place)
+    p.check()
+    assert p.d_served.item() == where
