@@ -4,7 +4,7 @@ import pytest
 
 import step_ref
 import trellis_quantized_linear_gb300 as tql
-from test_gpu_step import Plan, random_requests
+from test_gpu_step import Plan, norm_inputs, random_requests, run_norm
 from test_gpu_step_attention import check, gpu, inputs, split, starts  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +63,76 @@ def test_plan_of_many_stops_at_the_first_that_does_not_fit(where, why, in_place)
     p.call(in_place)
     p.check()
     assert p.d_served.item() == where
+
+
+# --------------------------------------------------------------------------- norm
+
+
+def check_codes(y, codes, group, scale=None):
+    """Each code is the nearest one, ties to even, of y / scale: of all that a quotient may be that is 2^-20
+    off (fp32: the sum, its product with the weight, the factor 448 / most and the product with it,
+    each half a step off, for the value and for the group's largest; the least scale brings the
+    root's reciprocal with 2 steps)."""
+    scale = step_ref.scales(y, group) if scale is None else scale
+    near, far = (step_ref.codes(y * (1 + d), scale, group) for d in (-2.0 ** -20, 2.0 ** -20))
+    nan = np.isnan(y)
+    assert np.array_equal(codes & 127 == 127, nan)
+    assert np.all((codes == near) | (codes == far) | nan)
+    assert (near != far).mean() < 2e-3  # hardly ever two choices
+
+
+@pytest.mark.parametrize("x_type,r_type", [(np.float16, None), (np.float32, np.float32), (np.float16, np.float32)])
+@pytest.mark.parametrize("rows,cols,group", [(1, 5120, 128), (40, 256, 256), (40, 640, 64), (333, 1024, 32), (777, 5120, 128), (160, 17408, 17408),
+                                             (310, 10240, 64), (40, 32768, 128)])
+def test_norm_codes_are_the_nearest(rows, cols, group, x_type, r_type):
+    x, r, w = norm_inputs(rows, cols, x_type, r_type, rows + cols)
+    if rows > 4:
+        x[3] = 0  # of the least scale, with a residual of the least, or without
+        x[4] *= np.float16(1e-3)
+        if r is not None:
+            r[3] = 1e-9
+            r[4] *= 1e-6
+    got = run_norm(x, r, w, cols, offset=1.0, group=group)
+    _, y = step_ref.rms_norm(x, r, w, 1.0, 1e-6)
+    check_codes(y, got[2], group)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 700])
+@pytest.mark.parametrize("cols,group", [(256, 64), (256, 256), (1024, 1024), (5120, 128), (8192, 8192)])
+def test_norm_codes_of_ties_are_even(rows, cols, group):
+    """The row's factor cancels in y / scale: with 448 as the largest value of each group, codes are those of h itself,
+    and h in the middle between two of them takes the even one, of either sign."""
+    values = step_ref.nearest_code.__globals__["VALUES"][:127]
+    middle = (values[1:] + values[:-1]) / 2  # exact in fp16
+    x = np.random.default_rng(cols + rows).choice(np.concatenate([middle, -middle, values]), (rows, cols)).astype(np.float16)
+    x[:, ::group] = 448.0
+    x[1::2, ::group] = -448.0
+    got = run_norm(x, None, None, cols, group=group)
+    want = step_ref.nearest_code(x.astype(np.float64))
+    assert np.array_equal(got[2], want)
+    up = np.isin(np.abs(x.astype(np.float64)), middle)
+    assert up.any() and np.all(got[2][up] % 2 == 0)
+
+
+@pytest.mark.parametrize("x_type", [np.float16, np.float32])
+def test_norm_codes_of_the_least_scale(x_type):
+    """Groups of values below 448 * 2^-40, whose codes are of y * 2^40; of zeros; and of values beside a NaN or an infinity."""
+    cols, group = 512, 64
+    g = np.random.default_rng(9)
+    h = g.standard_normal((6, cols))
+    w = np.ones(cols)
+    x = h.astype(x_type)
+    x[:, :64] = 0
+    if x_type is np.float32:
+        x[:, 64:128] *= np.float32(1e-12)
+        x[:, 128:192] *= np.float32(1e-11)
+    x[1, 200], x[2, 300], x[3, 400] = np.nan, np.inf, -np.inf
+    got = run_norm(x, None, w.astype(np.float16), cols, group=group)
+    _, y = step_ref.rms_norm(x, None, w, 0.0, 1e-6)
+    want = step_ref.scales(y, group)
+    assert np.all(np.abs(got[3] - want) <= want * 2.0 ** -18)
+    rows = [0, 4, 5]
+    check_codes(y[rows], got[2][rows], group)
+    assert np.all(got[2][1] & 127 == 127)
+    for r, at in ((2, 300), (3, 400)):
+        assert got[2][r, at] & 127 == 127 and not (np.delete(got[2][r], at) & 127).any()
