@@ -4,7 +4,7 @@ import pytest
 
 import step_ref
 import trellis_quantized_linear_gb300 as tql
-from test_gpu_step import Plan, norm_inputs, random_requests, run_norm
+from test_gpu_step import Plan, check_norm, norm_inputs, random_requests, run_norm
 from test_gpu_step_attention import check, gpu, inputs, split, starts  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -136,3 +136,13 @@ def test_norm_codes_of_the_least_scale(x_type):
     assert np.all(got[2][1] & 127 == 127)
     for r, at in ((2, 300), (3, 400)):
         assert got[2][r, at] & 127 == 127 and not (np.delete(got[2][r], at) & 127).any()
+
+
+@pytest.mark.parametrize("rows,cols,x_type,r_type,group", [(608, 512, np.float16, np.float16, 64), (609, 264, np.float16, np.float32, 264), (609, 520, np.float32, None, 0),
+                                                           (609, 1024, np.float32, np.float16, 1024), (640, 1024, np.float16, np.float16, 128),
+                                                           (700, 512, np.float16, None, 512), (1300, 768, np.float32, np.float32, 32)])
+def test_norm_rows_by_warps(rows, cols, x_type, r_type, group):
+    """On both sides of four rows an SM, from which on a row of 264 to 1024 columns is a warp's."""
+    x, r, w = norm_inputs(rows, cols, x_type, r_type, rows + cols, gap=8)
+    got = run_norm(x, r, w, cols, offset=1.0, group=group)
+    check_norm(x, r, w, cols, got, offset=1.0, group=group)

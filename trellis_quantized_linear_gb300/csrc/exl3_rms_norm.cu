@@ -325,8 +325,9 @@ template <typename X, typename R>
 cudaError_t by_size(const exl3_norm &p, int num_sms, int *status, cudaStream_t st) {
   const int pieces = (int)(p.cols / 8);
   // A row of at most 1024 columns is a warp's, or a part's; where rows are few, one of more than 256 is a CTA's: 304 rows of
-  // 1024 take 1.8 us, 2.3 by warps; 608 rows 2.8 and 2.3, 8192 rows 25 and 13.3.
-  if (pieces <= 32 || (pieces <= 128 && p.rows > 2 * num_sms)) {
+  // 1024 take 1.8 us, 2.3 by warps; 608 rows 2.0 and 2.3 (with codes 2.6 and 3.7), 1216 rows 2.7 and 2.4, 2400 rows 4.0 and
+  // 3.1, 8192 rows 11.8 and 13.4 (of 512: 8.6 and 5.1).
+  if (pieces <= 32 || (pieces <= 128 && p.rows > 4 * num_sms)) {
     int lanes = 16;
     while (lanes < 32 && lanes < pieces) lanes *= 2;
     if (pieces <= 32) return launch<X, R, 1, false>(p, kWarpRowThreads, lanes, num_sms, st);
