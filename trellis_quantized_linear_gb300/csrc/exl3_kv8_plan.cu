@@ -10,7 +10,7 @@
 //
 // All latency: the bytes are some hundred KB at most, and a few dependent loads stand one after
 // the other, with the barriers between them. Measured (in a graph): 16 sequences of one token
-// 5.0 us; 64 with 16 prompts, 16K rows 8.5; 4096 sequences, 18K rows 12.7 (15.9 by one CTA; a fence at
+// 4.9 us; 64 with 16 prompts, 16K rows 8.5; 4096 sequences, 18K rows 12.7 (15.9 by one CTA; a fence at
 // each of the cluster's barriers 13.2).
 #include "exl3_internal.h"
 #include "exl3_kv8.cuh"
@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(const KvPlan p, 
 cudaError_t launch_kv8_plan(const KvPlan &p, cudaStream_t st) {
   const int ranks = p.rows > 4 * kPlanThreads || p.n_seqs > kPlanThreads ? kMaxRanks : 1;
   // No more threads than sequences and rows give work to: with 1024, 16 sequences take 7.6 us, with 64 of them 5.
-  // Up to 1024 sequences are one CTA's: shared by 8, 64 of them with prompts take 10.6 us for 8.5,
-  // 4096 sequences 13.8 for 15.9.
+  // Up to 1024 sequences are one CTA's: shared by 8, 64 of them with prompts take 9.9 us for 8.5,
+  // 4096 sequences 12.7 for 15.9.
   const int sharing = p.n_seqs > kPlanThreads ? ranks : 1;
   const int64_t rows = ceil_div(p.rows, ranks), seqs = ceil_div(p.n_seqs, sharing);
   const int64_t work = ceil_div(rows > seqs ? rows : seqs, kEach);

@@ -12,9 +12,9 @@ constexpr int kSplitSeqs = 128;  // sequences of a launch whose items are shared
 // how long each is lies on the device, and sequences without rows count as well. An item costs 2.8 units
 // besides its own, sharing it 3.2 more (4.5 by four). `clusters`: those of 2 and of 4 CTAs that the
 // device runs at once. Measured (us, one / two / four CTAs an item, D = 128): 8192 tokens of one
-// head (32 items) 97 / 55 / 36; 4096 of 5 heads on one (82) 53 / 35 / 47; 2984 of 4 (48) 40 / 28
-// / 30; 1024 of 4 (16) 18.1 / 17.3 / 16.3; 512 of 4 (8) 12.3 / 14.4 / 14.5; 1024 of 40 on 8
-// (168) 21 / 38 / 60.
+// head (32 items) 97 / 57 / 38; 4096 of 5 heads on one (82) 54 / 37 / 50; 2984 of 4 (48) 41 / 29
+// / 32; 1024 of 4 (16) 18.6 / 18.3 / 17.4; 512 of 4 (8) 12.9 / 15.0 / 15.4; 1024 of 40 on 8
+// (168) 21 / 40 / 64.
 inline int prompt_ranks(int n_seqs, int64_t rows, int causal, int64_t items, int num_sms, const int *clusters) {
   if (n_seqs > kSplitSeqs) return 1;
   const float longest = (float)rows / (float)n_seqs / 128;

@@ -8,10 +8,10 @@
 // next rows while one is worked on: loads into registers have a row at a time in flight for
 // each resident CTA.
 //
-// Measured (in a graph, residual read and written): one row of 5120 fp16 1.9 us; 8192 rows
-// 57 us (5.9 TB/s; loads into registers 67); 777 rows fp32 with E4M3 codes 11.0 us (4.7 TB/s:
-// 2.6 rows for each CTA of the ring, 3 for some; with two lanes at a bank 11.4); 2400 rows of 17408 58 us (5.8 TB/s, from
-// registers 94). The rules between the forms stand at by_size, with both sides.
+// Measured (in a graph, over three sets of buffers, the sum in the residual's place; here and at the rules between
+// the forms, which stand at by_size with both sides): one row of 5120 fp16 2.0 us; 8192 rows 57 us (5.9 TB/s); 777 rows
+// fp32 with E4M3 codes 11.0 us (4.7 TB/s: 107 MB of buffers, of which the L2 holds a part; 12.1 us, 4.3 TB/s, with the sum apart,
+// 155 MB; 2.6 rows for each CTA of the ring, 3 for some); 2400 rows of 17408 58 us (5.8 TB/s, from registers 94).
 #include <math.h>
 
 #include <type_traits>
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(kRingThreads, V <= 2 ? 2 : 1) rms_norm_ring_ke
 template <typename X, typename R, int V, bool CTA_ROW>
 cudaError_t launch(const exl3_norm &p, int threads, int lanes, int num_sms, cudaStream_t st) {
   const int64_t ctas = CTA_ROW ? p.rows : ceil_div(p.rows, threads / lanes);
-  // Rows of one piece a thread have a CTA each: 8192 rows of 2048 fp16 take 23.7 us, 25.5 from CTAs that stay; the widest
-  // ones stay, with their weight (1000 rows of 17408 fp32: 54.1 us, 57.7 with a CTA each).
+  // Rows of one piece a thread have a CTA each: 8192 rows of 2048 fp16 take 21.7 us, 22.5 from CTAs that stay; the widest
+  // ones stay, with their weight (1000 rows of 32768 fp16: 62.3 us, 66.3 with a CTA each).
   const int64_t most = CTA_ROW && V == 1 ? INT32_MAX : (int64_t)num_sms * (2048 / threads);
   return launch_overlapped(rms_norm_kernel<X, R, V, CTA_ROW>, dim3((unsigned)(ctas < most ? ctas : most)), threads, 0, st, 1, p, lanes);
 }
@@ -336,8 +336,11 @@ cudaError_t by_size(const exl3_norm &p, int num_sms, int *status, cudaStream_t s
   }
   auto threads = [&](int v) { return (int)(ceil_div(ceil_div(pieces, v), 32) * 32); };
   // The ring, with as many CTAs as have two stages each: from three rows an SM on (fp16: 500 rows of 5120 3.9 us, 4.4 from
-  // registers; 400 rows 4.0 and 3.9; 8192 rows 57 and 67) and above 2048 columns (8192 rows of 2560: 29.7 and 33.7; of 2048:
-  // 24.6 and 23.7). Rows too wide for one piece a thread: from one an SM on (160 rows of 17408: 5.9 us and 9.2; 2400: 58 and 94).
+  // registers; 400 rows 4.0 and 3.5; 2400 rows 17.6 and 18.2, without a residual 10.7 and 14.8, fp32 with codes 27.5 and 30.4) and above
+  // 2048 columns (2400 rows of 2560: 8.1 and 9.3; 8192 of 2048: 23.4 and 21.7). What is read and written in equal parts by many rows
+  // would be a little better off in registers (8192 rows of 5120, fp16 57.0 and 55.3, fp32 95 and 86; without a residual 32 and 44).
+  // Rows too wide for one piece a thread: from one an SM on (160 rows of 17408: 5.9 us and 9.1; 2400: 58 and 94), as far as the
+  // threads reach: 2400 rows of 20480 columns 66 us, of 20488, from registers, 106.
   if (pieces > 256 && p.rows > (threads(1) > 1024 ? 1 : 3) * num_sms && threads(4) <= kRingThreads) {
     const bool two = threads(2) <= kRingThreads;
     const int t = threads(two ? 2 : 4), stage = (int)p.cols * element_bytes<X, R>();
