@@ -1,6 +1,7 @@
 """Continuous batching of requests with a small quantized model: requests join with a prompt,
 run token by token beside each other, and end; their cache pages come from one pool and go
-back to it.
+back to it. A step is of one kind: the prompts that join, while the running requests wait, or
+one token of each running request.
 
 A step's lengths, block tables, positions and row ranges are made on the device by
 exl3_kv8_plan from one number a sequence. Both kinds of step are the same calls (norm,

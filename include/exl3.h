@@ -558,7 +558,10 @@ exl3_status exl3_logits_adjust(const float *logits, int64_t ldl, int64_t M, int6
  * positions and slots; exl3_rms_norm stands before a projection; exl3_qk_rotary
  * between the projection of queries, keys and values and exl3_kv8_append;
  * exl3_prompt_attention attends over prompts that begin in this step, which have
- * all their keys and values at hand in fp16.
+ * all their keys and values at hand in fp16. It reads no cache: a sequence that has
+ * tokens there (a running one, or the rest of a prompt) would attend over this step's
+ * rows alone. A step that takes both kinds goes through exl3_kv8_attention as a whole,
+ * or is planned as two, prompts (the running ones with 0 tokens) and single tokens.
  * ---------------------------------------------------------------------------
  *
  * exl3_kv8_plan: the step's batch from its requests, on the device.
@@ -665,6 +668,7 @@ exl3_status exl3_qk_rotary(const void *x, int64_t ldx, void *out, int64_t ldo, i
  *            projection's output will do. Query head h reads key/value head
  *            h / (n_heads / n_kv_heads), at most 128 query heads one of them.
  *   lse:     rows x n_heads fp32, log sum_t exp(s[t]); or NULL.
+ * A sequence's rows are all that it attends over: one with tokens in the cache does not belong here.
  * Rows of no sequence are left as they are in out and lse, and whatever they hold in q, k
  * and v reaches no other row; so it is with the rows that a row does not see, infinities and
  * NaN among them. A row that sees an infinity or NaN in v gets it in that column (or NaN).
