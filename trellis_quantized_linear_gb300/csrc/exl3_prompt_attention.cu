@@ -29,9 +29,10 @@
 // the receiver: a released arrival waits for the stores to memory too, and took 20 us an item;
 // what it takes now is about 2. prompt_ranks has the rule and both sides.
 //
-// Measured: one prompt of 8192 tokens, 40 heads on 8, D = 128: 454 to 467 us (687 GFLOP, up to
-// 1510 TFLOP/s; 485 to 504 in long runs, in which the clock falls), one of 2048: 46 us; D = 64:
-// 383 us; scores capped: 693 and 656 us. What binds it is the chain of a tile's unit: about
+// Measured (in a graph): one prompt of 8192 tokens, 40 heads on 8, D = 128: 453 to 460 us (687
+// GFLOP, up to 1517 TFLOP/s; 500 among other calls in a long run, in which the clock falls: 1374),
+// one of 2048: 47 us; D = 64: 386 us; scores capped: 697 and 650 us; 4096 tokens, not causal: 250
+// us (1373 TFLOP/s), D = 64: 225. What binds it is the chain of a tile's unit: about
 // 1550 cycles of softmax (of them 512 for 128 exponentials a row at 4 cycles a warp)
 // and 1300 from the last probability to the next scores (768 of products, the rest the ways
 // through barriers), with TMEM full, so that the next scores cannot be formed meanwhile; the
